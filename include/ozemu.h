@@ -481,6 +481,97 @@ int ozemu_dgemm_mixed(int m, int n, int k, const double* A, int lda, const doubl
 int ozemu_dgemm_host_mixed(int m, int n, int k, const double* A, int lda, const double* B,
                            int ldb, double* C, int ldc, int r, cudaStream_t stream);
 
+/* ------------------------------------------------------------------------ */
+/* Layer operators: linear layer and layer norm                             */
+/* ------------------------------------------------------------------------ */
+
+/* The operators of a transformer layer round a matrix product, forward and
+ * backward, on 16-bit (layer norm: also 32-bit) floating-point data.  The
+ * source pages have no counterpart.
+ *
+ *   - Matrices are row-major with unit inner stride and a leading dimension
+ *     of at least the row length; vectors are dense.  Every pointer needs its
+ *     element type's natural alignment only; rows on 16-byte boundaries are
+ *     read in place, other operands of a product are copied into the
+ *     workspace first.
+ *   - Sums, statistics and products accumulate in fp32; each output is
+ *     rounded once to its type.  Results do not depend on anything but the
+ *     arguments: no atomics, a fixed order of every sum.
+ *   - The workspace is the CALLER'S (256-byte aligned, at least the bytes that
+ *     the query of the same name gives; NULL where that is 0): unlike the
+ *     calls above, these may overlap on different streams with workspaces of
+ *     their own.  Too small a one -> OZEMU_ERR_SCRATCH_TOO_SMALL.
+ *   - Outputs must not overlap inputs, except where a call says so.
+ *   - Infinities and NaN go through as the formulas take them, and set no
+ *     flag.  A product's pipeline wait that times out sets the flag that
+ *     ozemu_get_status reports. */
+typedef enum { OZEMU_BF16 = 0, OZEMU_F16 = 1, OZEMU_F32 = 2 } ozemu_type;
+
+/* none: z;  relu: max(z, 0);  gelu: z/2 (1 + erf(z/sqrt 2));  gelu_tanh:
+ * z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3)));  silu: z / (1 + exp(-z)). */
+typedef enum {
+  OZEMU_ACT_NONE = 0,
+  OZEMU_ACT_RELU = 1,
+  OZEMU_ACT_GELU = 2,
+  OZEMU_ACT_GELU_TANH = 3,
+  OZEMU_ACT_SILU = 4
+} ozemu_activation;
+
+/* Y = act(Z) + R with Z = X W^T + bias: X is m x k (ldx), W is n x k (ldw; row
+ * j holds the weights of output j), bias has n entries (NULL: none), R is
+ * m x n (ldr; NULL: none), Y is m x n (ldy).  pre (m x n, ldpre) receives Z
+ * rounded to the type, as the backward pass wants it (NULL: not written);
+ * act itself takes the unrounded Z.  type: OZEMU_BF16 or OZEMU_F16, of every
+ * operand.  Y may be R itself (same pointer and leading dimension).  k = 0
+ * gives Z = bias; m or n = 0 is a no-op. */
+int ozemu_linear(int m, int n, int k, int type, const void* X, int ldx, const void* W, int ldw, const void* bias,
+                 const void* R, int ldr, int activation, void* pre, int ldpre, void* Y, int ldy, void* workspace,
+                 size_t workspace_bytes, cudaStream_t stream);
+
+/* Workspace bytes of that call (only the alignment of the pointers is looked
+ * at); 0 on bad arguments, which the call itself rejects.  host. */
+size_t ozemu_linear_bytes(int m, int n, int k, const void* X, int ldx, const void* W, int ldw);
+
+/* Gradients of ozemu_linear: with dZ = dY act'(pre) (dZ = dY and pre unused
+ * for OZEMU_ACT_NONE; relu's slope at 0 is 0),
+ *   dX = dZ W (m x k, lddx),  dW = dZ^T X (n x k, lddw),  db = sum_i dZ_i (n);
+ * each of dX, dW, db may be NULL: not computed.  The gradient of R is dY.
+ * dZ is rounded to the type for the two products (the tensor cores take
+ * 16-bit operands); db sums it unrounded.  m = 0 zeroes dW and db, n = 0
+ * zeroes dX. */
+int ozemu_linear_backward(int m, int n, int k, int type, const void* dY, int lddy, const void* X, int ldx,
+                          const void* W, int ldw, int activation, const void* pre, int ldpre, void* dX, int lddx,
+                          void* dW, int lddw, void* db, void* workspace, size_t workspace_bytes,
+                          cudaStream_t stream);
+
+/* Workspace bytes of that call; 0 on bad arguments.  host. */
+size_t ozemu_linear_backward_bytes(int m, int n, int k, const void* dY, int lddy, const void* X, int ldx,
+                                   const void* W, int ldw, int activation);
+
+/* Y = (X - mean) rstd weight + bias for each row of X (rows x cols, ldx):
+ * mean = sum(X)/cols, rstd = (sum (X - mean)^2 / cols + eps)^(-1/2).  weight
+ * and bias have cols entries (NULL: 1 and 0), of param_type, which is type or
+ * OZEMU_F32.  mean and rstd (rows fp32 values each) are written unless NULL.
+ * eps >= 0.  Y (ldy) may be X itself (same leading dimension). */
+int ozemu_layer_norm(int rows, int cols, int type, const void* X, int ldx, int param_type, const void* weight,
+                     const void* bias, float eps, void* Y, int ldy, float* mean, float* rstd, cudaStream_t stream);
+
+/* Gradients of ozemu_layer_norm from its mean and rstd: with g = dY weight,
+ * xhat = (X - mean) rstd and row means over the columns,
+ *   dX = rstd (g - mean(g) - xhat mean(g xhat)) + dR,
+ *   dweight = sum over rows of dY xhat,  dbias = sum over rows of dY.
+ * dR (rows x cols, lddr; NULL: none) is the gradient that reaches X along a
+ * skip connection; dX may be dR or dY itself (same leading dimension).
+ * dweight and dbias have param_type; NULL: not computed.  rows = 0 zeroes
+ * them. */
+int ozemu_layer_norm_backward(int rows, int cols, int type, const void* dY, int lddy, const void* X, int ldx,
+                              int param_type, const void* weight, const float* mean, const float* rstd,
+                              const void* dR, int lddr, void* dX, int lddx, void* dweight, void* dbias,
+                              void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Workspace bytes of that call; 0 on bad arguments.  host. */
+size_t ozemu_layer_norm_backward_bytes(int rows, int cols);
+
 #ifdef __cplusplus
 }
 #endif

@@ -24,6 +24,16 @@ OZEMU_ERR_UNSUPPORTED = -7
 OZEMU_ERR_SCRATCH_TOO_SMALL = -8
 OZEMU_ERR_RANGE = -9
 
+OZEMU_BF16 = 0
+OZEMU_F16 = 1
+OZEMU_F32 = 2
+
+OZEMU_ACT_NONE = 0
+OZEMU_ACT_RELU = 1
+OZEMU_ACT_GELU = 2
+OZEMU_ACT_GELU_TANH = 3
+OZEMU_ACT_SILU = 4
+
 _STATUS_NAMES = {
     0: "OZEMU_OK", -1: "OZEMU_ERR_INVALID_ARG", -2: "OZEMU_ERR_K_OVERFLOW", -3: "OZEMU_ERR_ALLOC",
     -4: "OZEMU_ERR_CUDA", -5: "OZEMU_ERR_NONFINITE", -6: "OZEMU_ERR_TIMEOUT", -7: "OZEMU_ERR_UNSUPPORTED",
@@ -42,6 +52,7 @@ _lib = None
 _I = ctypes.c_int
 _P = ctypes.c_void_p
 _S = ctypes.c_size_t
+_F = ctypes.c_float
 
 _SIGNATURES = {
     "ozemu_igemm_s8": (_I, [_I, _I, _I, _P, _P, _P, _P]),
@@ -97,6 +108,15 @@ _SIGNATURES = {
     "ozemu_crt_f64_mixed": (_I, [_I, _I, _I, _P, _P, _P, _P, _I, _P]),
     "ozemu_dgemm_mixed": (_I, [_I, _I, _I, _P, _I, _P, _I, _P, _I, _I, _P]),
     "ozemu_dgemm_host_mixed": (_I, [_I, _I, _I, _P, _I, _P, _I, _P, _I, _I, _P]),
+    "ozemu_linear": (_I, [_I, _I, _I, _I, _P, _I, _P, _I, _P, _P, _I, _I, _P, _I, _P, _I, _P, _S, _P]),
+    "ozemu_linear_bytes": (_S, [_I, _I, _I, _P, _I, _P, _I]),
+    "ozemu_linear_backward": (_I, [_I, _I, _I, _I, _P, _I, _P, _I, _P, _I, _I, _P, _I, _P, _I, _P, _I, _P, _P, _S,
+                                   _P]),
+    "ozemu_linear_backward_bytes": (_S, [_I, _I, _I, _P, _I, _P, _I, _P, _I, _I]),
+    "ozemu_layer_norm": (_I, [_I, _I, _I, _P, _I, _I, _P, _P, _F, _P, _I, _P, _P, _P]),
+    "ozemu_layer_norm_backward": (_I, [_I, _I, _I, _P, _I, _P, _I, _I, _P, _P, _P, _P, _I, _P, _I, _P, _P, _P, _S,
+                                       _P]),
+    "ozemu_layer_norm_backward_bytes": (_S, [_I, _I]),
 }
 
 
@@ -362,6 +382,41 @@ def ozemu_dgemm_mixed(m, n, k, A, lda, B, ldb, C, ldc, r, stream):
 
 def ozemu_dgemm_host_mixed(m, n, k, A, lda, B, ldb, C, ldc, r, stream):
     return _call("ozemu_dgemm_host_mixed", m, n, k, A, lda, B, ldb, C, ldc, r, stream)
+
+
+def ozemu_linear(m, n, k, type, X, ldx, W, ldw, bias, R, ldr, activation, pre, ldpre, Y, ldy, workspace,
+                 workspace_bytes, stream):
+    return _call("ozemu_linear", m, n, k, type, X, ldx, W, ldw, bias, R, ldr, activation, pre, ldpre, Y, ldy,
+                 workspace, workspace_bytes, stream)
+
+
+def ozemu_linear_bytes(m, n, k, X, ldx, W, ldw):
+    return _call("ozemu_linear_bytes", m, n, k, X, ldx, W, ldw)
+
+
+def ozemu_linear_backward(m, n, k, type, dY, lddy, X, ldx, W, ldw, activation, pre, ldpre, dX, lddx, dW, lddw, db,
+                          workspace, workspace_bytes, stream):
+    return _call("ozemu_linear_backward", m, n, k, type, dY, lddy, X, ldx, W, ldw, activation, pre, ldpre, dX, lddx,
+                 dW, lddw, db, workspace, workspace_bytes, stream)
+
+
+def ozemu_linear_backward_bytes(m, n, k, dY, lddy, X, ldx, W, ldw, activation):
+    return _call("ozemu_linear_backward_bytes", m, n, k, dY, lddy, X, ldx, W, ldw, activation)
+
+
+def ozemu_layer_norm(rows, cols, type, X, ldx, param_type, weight, bias, eps, Y, ldy, mean, rstd, stream):
+    return _call("ozemu_layer_norm", rows, cols, type, X, ldx, param_type, weight, bias, eps, Y, ldy, mean, rstd,
+                 stream)
+
+
+def ozemu_layer_norm_backward(rows, cols, type, dY, lddy, X, ldx, param_type, weight, mean, rstd, dR, lddr, dX, lddx,
+                              dweight, dbias, workspace, workspace_bytes, stream):
+    return _call("ozemu_layer_norm_backward", rows, cols, type, dY, lddy, X, ldx, param_type, weight, mean, rstd, dR,
+                 lddr, dX, lddx, dweight, dbias, workspace, workspace_bytes, stream)
+
+
+def ozemu_layer_norm_backward_bytes(rows, cols):
+    return _call("ozemu_layer_norm_backward_bytes", rows, cols)
 
 
 # ------------------------------------------------------- torch marshalling
@@ -715,3 +770,203 @@ def crt_f64_mixed(m, n, r, residues, shifts_a, shifts_b, out=None, stream=None):
     _check(ozemu_crt_f64_mixed(m, n, r, residues.data_ptr(), shifts_a.data_ptr(), shifts_b.data_ptr(),
                                C.data_ptr(), _ld(C), _stream(stream)), "ozemu_crt_f64_mixed")
     return C
+
+
+# ------------------------------------- layer operators: linear, layer norm
+
+ACTIVATIONS = {"none": OZEMU_ACT_NONE, "relu": OZEMU_ACT_RELU, "gelu": OZEMU_ACT_GELU,
+               "gelu_tanh": OZEMU_ACT_GELU_TANH, "silu": OZEMU_ACT_SILU}
+_types = {}
+
+
+def _type(t, products=False):
+    """The library's number of a tensor's element type."""
+    if not _types:
+        torch = _torch()
+        _types.update({torch.bfloat16: OZEMU_BF16, torch.float16: OZEMU_F16, torch.float32: OZEMU_F32})
+    code = _types.get(t.dtype)
+    if code is None or (products and code == OZEMU_F32):
+        raise ValueError("expected bfloat16%s, got %s" % (" or float16" if products else ", float16 or float32",
+                                                          t.dtype))
+    return code
+
+
+def _matrix(t, rows, cols, like, name):
+    """(pointer, leading dimension) of an optional row-major matrix argument."""
+    if t is None:
+        return None, max(cols, 1)
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError("%s: expected a %d x %d matrix, got %s" % (name, rows, cols, tuple(t.shape)))
+    if t.dtype != like.dtype or t.device != like.device:
+        raise ValueError("%s: expected %s on %s" % (name, like.dtype, like.device))
+    if rows == 0 or cols == 0:
+        return None, max(cols, 1)
+    outer, inner = t.stride()
+    if (inner != 1 and cols > 1) or (outer < cols and rows > 1):
+        raise ValueError("%s: expected a row-major matrix, got strides %s" % (name, (outer, inner)))
+    return t.data_ptr(), outer if rows > 1 else cols
+
+
+def _vector(t, n, dtype, device, name):
+    """Pointer of an optional dense vector argument."""
+    if t is None:
+        return None
+    if t.dim() != 1 or t.shape[0] != n or t.dtype != dtype or t.device != device or (n > 1 and t.stride(0) != 1):
+        raise ValueError("%s: expected a dense vector of %d %s on %s" % (name, n, dtype, device))
+    return t.data_ptr()
+
+
+class _Launch:
+    """The stream of one call, and its outputs' and workspace's memory.  Memory is taken on that stream, and the
+    allocator learns of inputs that were made on another; ordering their values is the caller's (wait_stream)."""
+
+    def __init__(self, like, stream, inputs):
+        torch = _torch()
+        if not like.is_cuda:
+            raise ValueError("expected CUDA tensors")
+        if like.device.index != torch.cuda.current_device():
+            raise ValueError("expected tensors on the current device")
+        self.torch, self.device, self.given = torch, like.device, stream
+        if stream is not None:
+            for t in inputs:
+                if t is not None:
+                    t.record_stream(stream)
+        self.stream = _stream(stream)
+
+    def empty(self, shape, dtype):
+        if self.given is None:
+            return self.torch.empty(shape, dtype=dtype, device=self.device)
+        with self.torch.cuda.stream(self.given):
+            return self.torch.empty(shape, dtype=dtype, device=self.device)
+
+    def scratch(self, nbytes):
+        """(tensor that keeps it, pointer) of a workspace, 256-byte aligned."""
+        if nbytes == 0:
+            return None, None
+        t = self.empty(nbytes + 256, self.torch.uint8)
+        return t, (t.data_ptr() + 255) & ~255
+
+
+def linear(x, w, bias=None, residual=None, activation="none", save_pre=False, out=None, stream=None):
+    """act(x @ w.T + bias) + residual of bfloat16 or float16 cuda tensors: x m x k, w n x k, bias n, residual m x n.
+
+    With save_pre also the pre-activation x @ w.T + bias, rounded, for linear_backward: (y, pre).  out may be
+    residual itself."""
+    if activation not in ACTIVATIONS:
+        raise ValueError("activation: expected one of %s" % ", ".join(ACTIVATIONS))
+    code = _type(x, products=True)
+    if x.dim() != 2 or w.dim() != 2:
+        raise ValueError("expected 2-D tensors")
+    m, k = x.shape
+    n = w.shape[0]
+    xp, ldx = _matrix(x, m, k, x, "x")
+    wp, ldw = _matrix(w, n, k, x, "w")
+    bp = _vector(bias, n, x.dtype, x.device, "bias")
+    rp, ldr = _matrix(residual, m, n, x, "residual")
+    call = _Launch(x, stream, (x, w, bias, residual, out))
+    y = call.empty((m, n), x.dtype) if out is None else out
+    yp, ldy = _matrix(y, m, n, x, "out")
+    pre = call.empty((m, n), x.dtype) if save_pre else None
+    pp, ldp = _matrix(pre, m, n, x, "pre")
+    need = ozemu_linear_bytes(m, n, k, xp, ldx, wp, ldw)
+    keep, ws = call.scratch(need)
+    _check(ozemu_linear(m, n, k, code, xp, ldx, wp, ldw, bp, rp, ldr, ACTIVATIONS[activation], pp, ldp, yp, ldy, ws,
+                        need, call.stream), "ozemu_linear")
+    return (y, pre) if save_pre else y
+
+
+def linear_backward(dy, x, w, pre=None, activation="none", x_grad=True, w_grad=True, bias_grad=True, stream=None):
+    """(dx, dw, db) of linear for the gradient dy of its output (None for those not asked for).
+
+    pre is linear's saved pre-activation (not needed for "none").  The residual's gradient is dy."""
+    if activation not in ACTIVATIONS:
+        raise ValueError("activation: expected one of %s" % ", ".join(ACTIVATIONS))
+    code = _type(x, products=True)
+    if x.dim() != 2 or w.dim() != 2:
+        raise ValueError("expected 2-D tensors")
+    m, k = x.shape
+    n = w.shape[0]
+    if activation == "none":
+        pre = None
+    elif pre is None:
+        raise ValueError("pre: the pre-activation is needed for %s" % activation)
+    dyp, lddy = _matrix(dy, m, n, x, "dy")
+    xp, ldx = _matrix(x, m, k, x, "x")
+    wp, ldw = _matrix(w, n, k, x, "w")
+    pp, ldp = _matrix(pre, m, n, x, "pre")
+    call = _Launch(x, stream, (dy, x, w, pre))
+    dx = call.empty((m, k), x.dtype) if x_grad else None
+    dw = call.empty((n, k), x.dtype) if w_grad else None
+    db = call.empty((n,), x.dtype) if bias_grad else None
+    need = ozemu_linear_backward_bytes(m, n, k, dyp, lddy, xp, ldx, wp, ldw, ACTIVATIONS[activation])
+    keep, ws = call.scratch(need)
+    _check(ozemu_linear_backward(m, n, k, code, dyp, lddy, xp, ldx, wp, ldw, ACTIVATIONS[activation], pp, ldp,
+                                 dx.data_ptr() if x_grad else None, max(k, 1), dw.data_ptr() if w_grad else None,
+                                 max(k, 1), db.data_ptr() if bias_grad else None, ws, need, call.stream),
+           "ozemu_linear_backward")
+    return dx, dw, db
+
+
+def _params(x, cols, **named):
+    """The parameters' common type (their own or x's): (torch dtype, library's number)."""
+    dtype = next((t.dtype for t in named.values() if t is not None), x.dtype)
+    torch = _torch()
+    if dtype not in (x.dtype, torch.float32):
+        raise ValueError("expected parameters of %s or float32, got %s" % (x.dtype, dtype))
+    return dtype, OZEMU_F32 if dtype == torch.float32 else _type(x)
+
+
+def layer_norm(x, weight=None, bias=None, eps=1e-5, stats=False, out=None, stream=None):
+    """Layer norm of the rows of a bfloat16, float16 or float32 cuda matrix; weight and bias in x's type or float32.
+
+    With stats also the fp32 row statistics that layer_norm_backward takes: (y, mean, rstd).  out may be x itself."""
+    code = _type(x)
+    if x.dim() != 2:
+        raise ValueError("expected a 2-D tensor")
+    rows, cols = x.shape
+    pdtype, pcode = _params(x, cols, weight=weight, bias=bias)
+    xp, ldx = _matrix(x, rows, cols, x, "x")
+    wp = _vector(weight, cols, pdtype, x.device, "weight")
+    bp = _vector(bias, cols, pdtype, x.device, "bias")
+    call = _Launch(x, stream, (x, weight, bias, out))
+    y = call.empty((rows, cols), x.dtype) if out is None else out
+    yp, ldy = _matrix(y, rows, cols, x, "out")
+    mean = rstd = None
+    if stats:
+        mean, rstd = call.empty((2, rows), call.torch.float32).unbind(0)
+    _check(ozemu_layer_norm(rows, cols, code, xp, ldx, pcode, wp, bp, eps, yp, ldy,
+                            mean.data_ptr() if stats else None, rstd.data_ptr() if stats else None, call.stream),
+           "ozemu_layer_norm")
+    return (y, mean, rstd) if stats else y
+
+
+def layer_norm_backward(dy, x, mean, rstd, weight=None, dresidual=None, weight_grad=True, bias_grad=True, out=None,
+                        stream=None):
+    """(dx, dweight, dbias) of layer_norm from its saved statistics (None for those not asked for).
+
+    dresidual, the gradient that reaches x along a skip connection, is added to dx; out (dx's memory) may be
+    dresidual or dy itself.  dweight and dbias have weight's type (x's without a weight)."""
+    code = _type(x)
+    if x.dim() != 2:
+        raise ValueError("expected a 2-D tensor")
+    rows, cols = x.shape
+    pdtype, pcode = _params(x, cols, weight=weight)
+    f32 = _torch().float32
+    dyp, lddy = _matrix(dy, rows, cols, x, "dy")
+    xp, ldx = _matrix(x, rows, cols, x, "x")
+    drp, lddr = _matrix(dresidual, rows, cols, x, "dresidual")
+    wp = _vector(weight, cols, pdtype, x.device, "weight")
+    mp = _vector(mean, rows, f32, x.device, "mean")
+    sp = _vector(rstd, rows, f32, x.device, "rstd")
+    call = _Launch(x, stream, (dy, x, mean, rstd, weight, dresidual, out))
+    dx = call.empty((rows, cols), x.dtype) if out is None else out
+    dxp, lddx = _matrix(dx, rows, cols, x, "out")
+    dweight = call.empty((cols,), pdtype) if weight_grad else None
+    dbias = call.empty((cols,), pdtype) if bias_grad else None
+    need = ozemu_layer_norm_backward_bytes(rows, cols)
+    keep, ws = call.scratch(need)
+    _check(ozemu_layer_norm_backward(rows, cols, code, dyp, lddy, xp, ldx, pcode, wp, mp, sp, drp, lddr, dxp, lddx,
+                                     dweight.data_ptr() if weight_grad else None,
+                                     dbias.data_ptr() if bias_grad else None, ws, need, call.stream),
+           "ozemu_layer_norm_backward")
+    return dx, dweight, dbias

@@ -12,6 +12,7 @@
 #include "../../include/ozemu.h"
 #include "common.cuh"
 #include "kernels.h"
+#include "layer.cuh"
 
 namespace ozemu {
 namespace {
@@ -1458,6 +1459,147 @@ void ozemu_release(void) {
     d.ws = nullptr;
     d.ws_bytes = 0;
   }
+}
+
+// ------------------------------------------------------- layer operators
+static bool type_aligned(const void* p, int type) {
+  return (reinterpret_cast<uintptr_t>(p) & static_cast<uintptr_t>(type_bytes(type) - 1)) == 0;
+}
+
+// A matrix operand of `cols` columns: present, aligned to its type, ld wide
+// enough.  An optional one may be NULL, an empty one anything.
+static bool matrix_ok(const void* p, int rows, int cols, int ld, int type, bool optional = false) {
+  if (optional && !p) return true;
+  if (ld < (cols > 1 ? cols : 1)) return false;
+  if (rows == 0 || cols == 0) return true;
+  return p && type_aligned(p, type);
+}
+
+static bool vector_ok(const void* p, int type) { return !p || type_aligned(p, type); }
+
+static int scratch_ok(const void* ws, size_t have, size_t need) {
+  if (need == 0) return OZEMU_OK;
+  if (!ws || have < need) return OZEMU_ERR_SCRATCH_TOO_SMALL;
+  return (reinterpret_cast<uintptr_t>(ws) & 255u) == 0 ? OZEMU_OK : OZEMU_ERR_INVALID_ARG;
+}
+
+static bool product_type(int type) { return type == OZEMU_BF16 || type == OZEMU_F16; }
+static bool activation_ok(int a) { return a >= OZEMU_ACT_NONE && a <= OZEMU_ACT_SILU; }
+
+size_t ozemu_linear_bytes(int m, int n, int k, const void* X, int ldx, const void* W, int ldw) {
+  if (m <= 0 || n <= 0 || k <= 0 || ldx < k || ldw < k) return 0;
+  LinearCall c = {};
+  c.m = m;
+  c.n = n;
+  c.k = k;
+  c.x = X;
+  c.ldx = ldx;
+  c.w = W;
+  c.ldw = ldw;
+  return linear_workspace(c);
+}
+
+int ozemu_linear(int m, int n, int k, int type, const void* X, int ldx, const void* W, int ldw, const void* bias,
+                 const void* R, int ldr, int activation, void* pre, int ldpre, void* Y, int ldy, void* workspace,
+                 size_t workspace_bytes, cudaStream_t stream) {
+  if (m < 0 || n < 0 || k < 0 || !product_type(type) || !activation_ok(activation)) return OZEMU_ERR_INVALID_ARG;
+  if (!matrix_ok(X, m, k, ldx, type) || !matrix_ok(W, n, k, ldw, type) || !vector_ok(bias, type) ||
+      !matrix_ok(R, m, n, ldr, type, true) || !matrix_ok(pre, m, n, ldpre, type, true) ||
+      !matrix_ok(Y, m, n, ldy, type))
+    return OZEMU_ERR_INVALID_ARG;
+  if (m == 0 || n == 0) return OZEMU_OK;
+  LinearCall c = {m, n, k, type, X, ldx, W, ldw, bias, R, ldr, activation, pre, ldpre, Y, ldy, workspace, nullptr};
+  int s = scratch_ok(workspace, workspace_bytes, k > 0 ? linear_workspace(c) : 0);
+  if (s != OZEMU_OK) return s;
+  DeviceState* d = nullptr;
+  s = device_state(&d);
+  if (s != OZEMU_OK) return s;
+  c.flags = d->flags;
+  return cuda_status(launch_linear(c, stream));
+}
+
+size_t ozemu_linear_backward_bytes(int m, int n, int k, const void* dY, int lddy, const void* X, int ldx,
+                                   const void* W, int ldw, int activation) {
+  if (m <= 0 || n <= 0 || k < 0 || lddy < n || ldx < k || ldw < k || !activation_ok(activation)) return 0;
+  LinearGradCall c = {};
+  c.m = m;
+  c.n = n;
+  c.k = k;
+  c.dy = dY;
+  c.lddy = lddy;
+  c.x = X;
+  c.ldx = ldx;
+  c.w = W;
+  c.ldw = ldw;
+  c.act = activation;
+  return linear_backward_workspace(c);
+}
+
+int ozemu_linear_backward(int m, int n, int k, int type, const void* dY, int lddy, const void* X, int ldx,
+                          const void* W, int ldw, int activation, const void* pre, int ldpre, void* dX, int lddx,
+                          void* dW, int lddw, void* db, void* workspace, size_t workspace_bytes,
+                          cudaStream_t stream) {
+  if (m < 0 || n < 0 || k < 0 || !product_type(type) || !activation_ok(activation)) return OZEMU_ERR_INVALID_ARG;
+  const bool slope = activation != OZEMU_ACT_NONE;
+  if (!matrix_ok(dY, m, n, lddy, type) || !matrix_ok(X, m, k, ldx, type, !dW) ||
+      !matrix_ok(W, n, k, ldw, type, !dX) || (slope && !matrix_ok(pre, m, n, ldpre, type)) ||
+      !matrix_ok(dX, m, k, lddx, type, true) || !matrix_ok(dW, n, k, lddw, type, true) || !vector_ok(db, type))
+    return OZEMU_ERR_INVALID_ARG;
+  LinearGradCall c = {m, n, k, type, dY, lddy, X, ldx, W, ldw, activation, pre, ldpre, dX, lddx, dW, lddw, db,
+                      workspace, nullptr};
+  int s = scratch_ok(workspace, workspace_bytes, m > 0 && n > 0 ? linear_backward_workspace(c) : 0);
+  if (s != OZEMU_OK) return s;
+  if ((m == 0 && n == 0) || (k == 0 && n == 0) || (!dX && !dW && !db)) return OZEMU_OK;
+  DeviceState* d = nullptr;
+  s = device_state(&d);
+  if (s != OZEMU_OK) return s;
+  c.flags = d->flags;
+  return cuda_status(launch_linear_backward(c, stream));
+}
+
+static bool norm_types(int type, int param_type) {
+  return type >= OZEMU_BF16 && type <= OZEMU_F32 && (param_type == type || param_type == OZEMU_F32);
+}
+
+int ozemu_layer_norm(int rows, int cols, int type, const void* X, int ldx, int param_type, const void* weight,
+                     const void* bias, float eps, void* Y, int ldy, float* mean, float* rstd, cudaStream_t stream) {
+  if (rows < 0 || cols < 0 || !norm_types(type, param_type) || !(eps >= 0.0f)) return OZEMU_ERR_INVALID_ARG;
+  if (!matrix_ok(X, rows, cols, ldx, type) || !matrix_ok(Y, rows, cols, ldy, type) ||
+      !vector_ok(weight, param_type) || !vector_ok(bias, param_type) || !vector_ok(mean, OZEMU_F32) ||
+      !vector_ok(rstd, OZEMU_F32))
+    return OZEMU_ERR_INVALID_ARG;
+  if (rows == 0 || cols == 0) return OZEMU_OK;
+  DeviceState* d = nullptr;
+  const int s = device_state(&d);
+  if (s != OZEMU_OK) return s;
+  const NormCall c = {rows, cols, type, param_type, X, ldx, weight, bias, eps, Y, ldy, mean, rstd};
+  return cuda_status(launch_layer_norm(c, stream));
+}
+
+size_t ozemu_layer_norm_backward_bytes(int rows, int cols) {
+  if (rows <= 0 || cols <= 0) return 0;
+  return layer_norm_backward_workspace(rows, cols);
+}
+
+int ozemu_layer_norm_backward(int rows, int cols, int type, const void* dY, int lddy, const void* X, int ldx,
+                              int param_type, const void* weight, const float* mean, const float* rstd,
+                              const void* dR, int lddr, void* dX, int lddx, void* dweight, void* dbias,
+                              void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  if (rows < 0 || cols < 0 || !norm_types(type, param_type)) return OZEMU_ERR_INVALID_ARG;
+  if (!matrix_ok(dY, rows, cols, lddy, type) || !matrix_ok(X, rows, cols, ldx, type) ||
+      !matrix_ok(dX, rows, cols, lddx, type) || !matrix_ok(dR, rows, cols, lddr, type, true) ||
+      !vector_ok(weight, param_type) || !vector_ok(dweight, param_type) || !vector_ok(dbias, param_type) ||
+      (rows > 0 && cols > 0 && (!mean || !rstd)) || !vector_ok(mean, OZEMU_F32) || !vector_ok(rstd, OZEMU_F32))
+    return OZEMU_ERR_INVALID_ARG;
+  if (cols == 0) return OZEMU_OK;
+  int s = scratch_ok(workspace, workspace_bytes, rows > 0 ? layer_norm_backward_workspace(rows, cols) : 0);
+  if (s != OZEMU_OK) return s;
+  DeviceState* d = nullptr;
+  s = device_state(&d);
+  if (s != OZEMU_OK) return s;
+  const NormGradCall c = {rows, cols, type, param_type, dY, lddy, X, ldx, weight, mean, rstd, dR, lddr, dX, lddx,
+                          dweight, dbias, workspace};
+  return cuda_status(launch_layer_norm_backward(c, stream));
 }
 
 }  // extern "C"

@@ -96,6 +96,86 @@ cudaError_t launch_narrow_residues(const NarrowCall& call, cudaStream_t stream);
 cudaError_t launch_crt_f64(int m, int n, const uint8_t* residues, long long ldr, const int32_t* sa,
                            const int32_t* sb, double* C, long long ldc, const CrtModuli& cm, cudaStream_t stream);
 
+// Layer norm (layernorm.cu).  Types are numbered as in the C ABI (0 bf16,
+// 1 f16, 2 f32); leading dimensions in elements; NULL pointers mark absent
+// optional operands.
+struct NormCall {
+  int rows, cols, type, param_type;
+  const void* x;
+  long long ldx;
+  const void* weight;
+  const void* bias;
+  float eps;
+  void* y;
+  long long ldy;
+  float* mean;
+  float* rstd;
+};
+cudaError_t launch_layer_norm(const NormCall& call, cudaStream_t stream);
+
+struct NormGradCall {
+  int rows, cols, type, param_type;
+  const void* dy;
+  long long lddy;
+  const void* x;
+  long long ldx;
+  const void* weight;
+  const float* mean;
+  const float* rstd;
+  const void* dr;
+  long long lddr;
+  void* dx;
+  long long lddx;
+  void* dweight;
+  void* dbias;
+  void* ws;
+};
+size_t layer_norm_backward_workspace(int rows, int cols);
+cudaError_t launch_layer_norm_backward(const NormGradCall& call, cudaStream_t stream);
+
+// Linear layer (linear.cu): x is m x k, w is n x k.
+struct LinearCall {
+  int m, n, k, type;
+  const void* x;
+  long long ldx;
+  const void* w;
+  long long ldw;
+  const void* bias;
+  const void* res;
+  long long ldr;
+  int act;
+  void* pre;
+  long long ldpre;
+  void* y;
+  long long ldy;
+  void* ws;
+  uint32_t* flags;
+};
+size_t linear_workspace(const LinearCall& call);
+cudaError_t launch_linear(const LinearCall& call, cudaStream_t stream);
+
+struct LinearGradCall {
+  int m, n, k, type;
+  const void* dy;
+  long long lddy;
+  const void* x;
+  long long ldx;
+  const void* w;
+  long long ldw;
+  int act;
+  const void* pre;
+  long long ldpre;
+  void* dx;
+  long long lddx;
+  void* dw;
+  long long lddw;
+  void* db;
+  void* ws;
+  uint32_t* flags;
+};
+size_t linear_backward_workspace(const LinearGradCall& call);
+cudaError_t launch_linear_backward(const LinearGradCall& call, cudaStream_t stream);
+
 // Fill helpers.
 cudaError_t launch_zero_f64(double* C, int m, int n, long long ldc, cudaStream_t stream);
 cudaError_t launch_zero_s32(int32_t* C, int m, int n, long long ldc, cudaStream_t stream);
