@@ -777,74 +777,94 @@ def crt_f64_mixed(m, n, r, residues, shifts_a, shifts_b, out=None, stream=None):
 ACTIVATIONS = {"none": OZEMU_ACT_NONE, "relu": OZEMU_ACT_RELU, "gelu": OZEMU_ACT_GELU,
                "gelu_tanh": OZEMU_ACT_GELU_TANH, "silu": OZEMU_ACT_SILU}
 _types = {}
+_raw_stream = None
 
 
-def _type(t, products=False):
-    """The library's number of a tensor's element type."""
-    if not _types:
-        torch = _torch()
-        _types.update({torch.bfloat16: OZEMU_BF16, torch.float16: OZEMU_F16, torch.float32: OZEMU_F32})
-    code = _types.get(t.dtype)
-    if code is None or (products and code == OZEMU_F32):
-        raise ValueError("expected bfloat16%s, got %s" % (" or float16" if products else ", float16 or float32",
-                                                          t.dtype))
-    return code
+def _layer_setup():
+    """The torch side of the layer operators, resolved at the first call: a decoded token's calls are a few
+    microseconds of device work each, so they look up as little as they can."""
+    global _raw_stream
+    torch = _torch()
+    _types.update({torch.bfloat16: OZEMU_BF16, torch.float16: OZEMU_F16, torch.float32: OZEMU_F32})
+    # The current stream's handle without a Stream object round it, where this torch has that.
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda index: torch.cuda.current_stream(index).cuda_stream)
+    return load()
 
 
 def _matrix(t, rows, cols, like, name):
     """(pointer, leading dimension) of an optional row-major matrix argument."""
     if t is None:
-        return None, max(cols, 1)
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        return None, cols or 1
+    if t.dim() != 2 or tuple(t.shape) != (rows, cols):
         raise ValueError("%s: expected a %d x %d matrix, got %s" % (name, rows, cols, tuple(t.shape)))
-    if t.dtype != like.dtype or t.device != like.device:
+    if t.dtype is not like.dtype or t.get_device() != like.get_device():
         raise ValueError("%s: expected %s on %s" % (name, like.dtype, like.device))
     if rows == 0 or cols == 0:
-        return None, max(cols, 1)
+        return None, cols or 1
     outer, inner = t.stride()
     if (inner != 1 and cols > 1) or (outer < cols and rows > 1):
         raise ValueError("%s: expected a row-major matrix, got strides %s" % (name, (outer, inner)))
     return t.data_ptr(), outer if rows > 1 else cols
 
 
-def _vector(t, n, dtype, device, name):
+def _vector(t, n, dtype, like, name):
     """Pointer of an optional dense vector argument."""
     if t is None:
         return None
-    if t.dim() != 1 or t.shape[0] != n or t.dtype != dtype or t.device != device or (n > 1 and t.stride(0) != 1):
-        raise ValueError("%s: expected a dense vector of %d %s on %s" % (name, n, dtype, device))
+    if t.dim() != 1 or t.shape[0] != n or t.dtype is not dtype or t.get_device() != like.get_device() or (
+            n > 1 and t.stride(0) != 1):
+        raise ValueError("%s: expected a dense vector of %d %s on %s" % (name, n, dtype, like.device))
     return t.data_ptr()
 
 
-class _Launch:
-    """The stream of one call, and its outputs' and workspace's memory.  Memory is taken on that stream, and the
-    allocator learns of inputs that were made on another; ordering their values is the caller's (wait_stream)."""
+def _on(stream, like, inputs):
+    """The handle of the stream a call runs on.  For a given stream the allocator learns of the inputs' use there;
+    ordering their values is the caller's (wait_stream)."""
+    index = like.get_device()
+    if index < 0:
+        raise ValueError("expected CUDA tensors")
+    if index != _torch().cuda.current_device():
+        raise ValueError("expected tensors on the current device")
+    if stream is None:
+        return _raw_stream(index)
+    for t in inputs:
+        if t is not None:
+            t.record_stream(stream)
+    return stream.cuda_stream
 
-    def __init__(self, like, stream, inputs):
-        torch = _torch()
-        if not like.is_cuda:
-            raise ValueError("expected CUDA tensors")
-        if like.device.index != torch.cuda.current_device():
-            raise ValueError("expected tensors on the current device")
-        self.torch, self.device, self.given = torch, like.device, stream
-        if stream is not None:
-            for t in inputs:
-                if t is not None:
-                    t.record_stream(stream)
-        self.stream = _stream(stream)
 
-    def empty(self, shape, dtype):
-        if self.given is None:
-            return self.torch.empty(shape, dtype=dtype, device=self.device)
-        with self.torch.cuda.stream(self.given):
-            return self.torch.empty(shape, dtype=dtype, device=self.device)
+def _new(stream, like, shape, dtype=None):
+    """Memory of a call's output or workspace, taken on the stream it runs on."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    with _torch().cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
 
-    def scratch(self, nbytes):
-        """(tensor that keeps it, pointer) of a workspace, 256-byte aligned."""
-        if nbytes == 0:
-            return None, None
-        t = self.empty(nbytes + 256, self.torch.uint8)
-        return t, (t.data_ptr() + 255) & ~255
+
+def _scratch(stream, like, nbytes):
+    """(tensor that keeps it, pointer) of a workspace, 256-byte aligned."""
+    t = _new(stream, like, nbytes + 256, _torch().uint8)
+    return t, (t.data_ptr() + 255) & ~255
+
+
+def _sizes(t):
+    if t.dim() != 2:
+        raise ValueError("expected a 2-D tensor")
+    return t.shape
+
+
+def _linear_args(x, w, activation):
+    """(library, type, activation, m, n, k) of a linear layer's call."""
+    lib = _lib if _raw_stream else _layer_setup()
+    act = ACTIVATIONS.get(activation)
+    if act is None:
+        raise ValueError("activation: expected one of %s" % ", ".join(ACTIVATIONS))
+    code = _types.get(x.dtype, OZEMU_F32)
+    if code == OZEMU_F32:
+        raise ValueError("expected bfloat16 or float16, got %s" % x.dtype)
+    m, k = _sizes(x)
+    return lib, code, act, m, _sizes(w)[0], k
 
 
 def linear(x, w, bias=None, residual=None, activation="none", save_pre=False, out=None, stream=None):
@@ -852,41 +872,35 @@ def linear(x, w, bias=None, residual=None, activation="none", save_pre=False, ou
 
     With save_pre also the pre-activation x @ w.T + bias, rounded, for linear_backward: (y, pre).  out may be
     residual itself."""
-    if activation not in ACTIVATIONS:
-        raise ValueError("activation: expected one of %s" % ", ".join(ACTIVATIONS))
-    code = _type(x, products=True)
-    if x.dim() != 2 or w.dim() != 2:
-        raise ValueError("expected 2-D tensors")
-    m, k = x.shape
-    n = w.shape[0]
+    lib, code, act, m, n, k = _linear_args(x, w, activation)
     xp, ldx = _matrix(x, m, k, x, "x")
     wp, ldw = _matrix(w, n, k, x, "w")
-    bp = _vector(bias, n, x.dtype, x.device, "bias")
+    bp = _vector(bias, n, x.dtype, x, "bias")
     rp, ldr = _matrix(residual, m, n, x, "residual")
-    call = _Launch(x, stream, (x, w, bias, residual, out))
-    y = call.empty((m, n), x.dtype) if out is None else out
-    yp, ldy = _matrix(y, m, n, x, "out")
-    pre = call.empty((m, n), x.dtype) if save_pre else None
-    pp, ldp = _matrix(pre, m, n, x, "pre")
-    need = ozemu_linear_bytes(m, n, k, xp, ldx, wp, ldw)
-    keep, ws = call.scratch(need)
-    _check(ozemu_linear(m, n, k, code, xp, ldx, wp, ldw, bp, rp, ldr, ACTIVATIONS[activation], pp, ldp, yp, ldy, ws,
-                        need, call.stream), "ozemu_linear")
-    return (y, pre) if save_pre else y
+    handle = _on(stream, x, (x, w, bias, residual, out))
+    if out is None:
+        out = _new(stream, x, (m, n))
+    yp, ldy = _matrix(out, m, n, x, "out")
+    pre = pp = None
+    if save_pre:
+        pre = _new(stream, x, (m, n))
+        pp = pre.data_ptr()
+    keep = ws = None
+    need = lib.ozemu_linear_bytes(m, n, k, xp, ldx, wp, ldw)
+    if need:
+        keep, ws = _scratch(stream, x, need)
+    st = lib.ozemu_linear(m, n, k, code, xp, ldx, wp, ldw, bp, rp, ldr, act, pp, n or 1, yp, ldy, ws, need, handle)
+    if st:
+        raise OzemuError(st, "ozemu_linear")
+    return (out, pre) if save_pre else out
 
 
 def linear_backward(dy, x, w, pre=None, activation="none", x_grad=True, w_grad=True, bias_grad=True, stream=None):
     """(dx, dw, db) of linear for the gradient dy of its output (None for those not asked for).
 
     pre is linear's saved pre-activation (not needed for "none").  The residual's gradient is dy."""
-    if activation not in ACTIVATIONS:
-        raise ValueError("activation: expected one of %s" % ", ".join(ACTIVATIONS))
-    code = _type(x, products=True)
-    if x.dim() != 2 or w.dim() != 2:
-        raise ValueError("expected 2-D tensors")
-    m, k = x.shape
-    n = w.shape[0]
-    if activation == "none":
+    lib, code, act, m, n, k = _linear_args(x, w, activation)
+    if act == OZEMU_ACT_NONE:
         pre = None
     elif pre is None:
         raise ValueError("pre: the pre-activation is needed for %s" % activation)
@@ -894,50 +908,61 @@ def linear_backward(dy, x, w, pre=None, activation="none", x_grad=True, w_grad=T
     xp, ldx = _matrix(x, m, k, x, "x")
     wp, ldw = _matrix(w, n, k, x, "w")
     pp, ldp = _matrix(pre, m, n, x, "pre")
-    call = _Launch(x, stream, (dy, x, w, pre))
-    dx = call.empty((m, k), x.dtype) if x_grad else None
-    dw = call.empty((n, k), x.dtype) if w_grad else None
-    db = call.empty((n,), x.dtype) if bias_grad else None
-    need = ozemu_linear_backward_bytes(m, n, k, dyp, lddy, xp, ldx, wp, ldw, ACTIVATIONS[activation])
-    keep, ws = call.scratch(need)
-    _check(ozemu_linear_backward(m, n, k, code, dyp, lddy, xp, ldx, wp, ldw, ACTIVATIONS[activation], pp, ldp,
-                                 dx.data_ptr() if x_grad else None, max(k, 1), dw.data_ptr() if w_grad else None,
-                                 max(k, 1), db.data_ptr() if bias_grad else None, ws, need, call.stream),
-           "ozemu_linear_backward")
+    handle = _on(stream, x, (dy, x, w, pre))
+    dx = _new(stream, x, (m, k)) if x_grad else None
+    dw = _new(stream, x, (n, k)) if w_grad else None
+    db = _new(stream, x, (n,)) if bias_grad else None
+    keep = ws = None
+    need = lib.ozemu_linear_backward_bytes(m, n, k, dyp, lddy, xp, ldx, wp, ldw, act)
+    if need:
+        keep, ws = _scratch(stream, x, need)
+    st = lib.ozemu_linear_backward(m, n, k, code, dyp, lddy, xp, ldx, wp, ldw, act, pp, ldp,
+                                   dx.data_ptr() if x_grad else None, k or 1, dw.data_ptr() if w_grad else None,
+                                   k or 1, db.data_ptr() if bias_grad else None, ws, need, handle)
+    if st:
+        raise OzemuError(st, "ozemu_linear_backward")
     return dx, dw, db
 
 
-def _params(x, cols, **named):
-    """The parameters' common type (their own or x's): (torch dtype, library's number)."""
-    dtype = next((t.dtype for t in named.values() if t is not None), x.dtype)
-    torch = _torch()
-    if dtype not in (x.dtype, torch.float32):
+def _norm_args(x, *params):
+    """(library, type, parameters' dtype and type, rows, cols) of a layer norm's call."""
+    lib = _lib if _raw_stream else _layer_setup()
+    code = _types.get(x.dtype)
+    if code is None:
+        raise ValueError("expected bfloat16, float16 or float32, got %s" % x.dtype)
+    dtype = x.dtype
+    for p in params:
+        if p is not None:
+            dtype = p.dtype
+            break
+    pcode = _types.get(dtype)
+    if pcode != code and pcode != OZEMU_F32:
         raise ValueError("expected parameters of %s or float32, got %s" % (x.dtype, dtype))
-    return dtype, OZEMU_F32 if dtype == torch.float32 else _type(x)
+    rows, cols = _sizes(x)
+    return lib, code, dtype, pcode, rows, cols
 
 
 def layer_norm(x, weight=None, bias=None, eps=1e-5, stats=False, out=None, stream=None):
     """Layer norm of the rows of a bfloat16, float16 or float32 cuda matrix; weight and bias in x's type or float32.
 
     With stats also the fp32 row statistics that layer_norm_backward takes: (y, mean, rstd).  out may be x itself."""
-    code = _type(x)
-    if x.dim() != 2:
-        raise ValueError("expected a 2-D tensor")
-    rows, cols = x.shape
-    pdtype, pcode = _params(x, cols, weight=weight, bias=bias)
+    lib, code, pdtype, pcode, rows, cols = _norm_args(x, weight, bias)
     xp, ldx = _matrix(x, rows, cols, x, "x")
-    wp = _vector(weight, cols, pdtype, x.device, "weight")
-    bp = _vector(bias, cols, pdtype, x.device, "bias")
-    call = _Launch(x, stream, (x, weight, bias, out))
-    y = call.empty((rows, cols), x.dtype) if out is None else out
-    yp, ldy = _matrix(y, rows, cols, x, "out")
-    mean = rstd = None
+    wp = _vector(weight, cols, pdtype, x, "weight")
+    bp = _vector(bias, cols, pdtype, x, "bias")
+    handle = _on(stream, x, (x, weight, bias, out))
+    if out is None:
+        out = _new(stream, x, (rows, cols))
+    yp, ldy = _matrix(out, rows, cols, x, "out")
+    mean = rstd = mp = sp = None
     if stats:
-        mean, rstd = call.empty((2, rows), call.torch.float32).unbind(0)
-    _check(ozemu_layer_norm(rows, cols, code, xp, ldx, pcode, wp, bp, eps, yp, ldy,
-                            mean.data_ptr() if stats else None, rstd.data_ptr() if stats else None, call.stream),
-           "ozemu_layer_norm")
-    return (y, mean, rstd) if stats else y
+        f32 = _torch().float32
+        mean, rstd = _new(stream, x, (rows,), f32), _new(stream, x, (rows,), f32)
+        mp, sp = mean.data_ptr(), rstd.data_ptr()
+    st = lib.ozemu_layer_norm(rows, cols, code, xp, ldx, pcode, wp, bp, eps, yp, ldy, mp, sp, handle)
+    if st:
+        raise OzemuError(st, "ozemu_layer_norm")
+    return (out, mean, rstd) if stats else out
 
 
 def layer_norm_backward(dy, x, mean, rstd, weight=None, dresidual=None, weight_grad=True, bias_grad=True, out=None,
@@ -946,27 +971,27 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, dresidual=None, weight_g
 
     dresidual, the gradient that reaches x along a skip connection, is added to dx; out (dx's memory) may be
     dresidual or dy itself.  dweight and dbias have weight's type (x's without a weight)."""
-    code = _type(x)
-    if x.dim() != 2:
-        raise ValueError("expected a 2-D tensor")
-    rows, cols = x.shape
-    pdtype, pcode = _params(x, cols, weight=weight)
+    lib, code, pdtype, pcode, rows, cols = _norm_args(x, weight)
     f32 = _torch().float32
     dyp, lddy = _matrix(dy, rows, cols, x, "dy")
     xp, ldx = _matrix(x, rows, cols, x, "x")
     drp, lddr = _matrix(dresidual, rows, cols, x, "dresidual")
-    wp = _vector(weight, cols, pdtype, x.device, "weight")
-    mp = _vector(mean, rows, f32, x.device, "mean")
-    sp = _vector(rstd, rows, f32, x.device, "rstd")
-    call = _Launch(x, stream, (dy, x, mean, rstd, weight, dresidual, out))
-    dx = call.empty((rows, cols), x.dtype) if out is None else out
-    dxp, lddx = _matrix(dx, rows, cols, x, "out")
-    dweight = call.empty((cols,), pdtype) if weight_grad else None
-    dbias = call.empty((cols,), pdtype) if bias_grad else None
-    need = ozemu_layer_norm_backward_bytes(rows, cols)
-    keep, ws = call.scratch(need)
-    _check(ozemu_layer_norm_backward(rows, cols, code, dyp, lddy, xp, ldx, pcode, wp, mp, sp, drp, lddr, dxp, lddx,
-                                     dweight.data_ptr() if weight_grad else None,
-                                     dbias.data_ptr() if bias_grad else None, ws, need, call.stream),
-           "ozemu_layer_norm_backward")
-    return dx, dweight, dbias
+    wp = _vector(weight, cols, pdtype, x, "weight")
+    mp = _vector(mean, rows, f32, x, "mean")
+    sp = _vector(rstd, rows, f32, x, "rstd")
+    handle = _on(stream, x, (dy, x, mean, rstd, weight, dresidual, out))
+    if out is None:
+        out = _new(stream, x, (rows, cols))
+    dxp, lddx = _matrix(out, rows, cols, x, "out")
+    dweight = _new(stream, x, (cols,), pdtype) if weight_grad else None
+    dbias = _new(stream, x, (cols,), pdtype) if bias_grad else None
+    keep = ws = None
+    need = lib.ozemu_layer_norm_backward_bytes(rows, cols)
+    if need:
+        keep, ws = _scratch(stream, x, need)
+    st = lib.ozemu_layer_norm_backward(rows, cols, code, dyp, lddy, xp, ldx, pcode, wp, mp, sp, drp, lddr, dxp, lddx,
+                                       dweight.data_ptr() if weight_grad else None,
+                                       dbias.data_ptr() if bias_grad else None, ws, need, handle)
+    if st:
+        raise OzemuError(st, "ozemu_layer_norm_backward")
+    return out, dweight, dbias

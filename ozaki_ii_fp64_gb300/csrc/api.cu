@@ -1572,7 +1572,7 @@ int ozemu_layer_norm(int rows, int cols, int type, const void* X, int ldx, int p
   DeviceState* d = nullptr;
   const int s = device_state(&d);
   if (s != OZEMU_OK) return s;
-  const NormCall c = {rows, cols, type, param_type, X, ldx, weight, bias, eps, Y, ldy, mean, rstd};
+  const NormCall c = {rows, cols, type, param_type, X, ldx, weight, bias, eps, Y, ldy, mean, rstd, d->flags};
   return cuda_status(launch_layer_norm(c, stream));
 }
 
@@ -1598,7 +1598,7 @@ int ozemu_layer_norm_backward(int rows, int cols, int type, const void* dY, int 
   s = device_state(&d);
   if (s != OZEMU_OK) return s;
   const NormGradCall c = {rows, cols, type, param_type, dY, lddy, X, ldx, weight, mean, rstd, dR, lddr, dX, lddx,
-                          dweight, dbias, workspace};
+                          dweight, dbias, workspace, d->flags};
   return cuda_status(launch_layer_norm_backward(c, stream));
 }
 

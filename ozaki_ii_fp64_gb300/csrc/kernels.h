@@ -110,6 +110,7 @@ struct NormCall {
   long long ldy;
   float* mean;
   float* rstd;
+  uint32_t* flags;
 };
 cudaError_t launch_layer_norm(const NormCall& call, cudaStream_t stream);
 
@@ -129,6 +130,7 @@ struct NormGradCall {
   void* dweight;
   void* dbias;
   void* ws;
+  uint32_t* flags;
 };
 size_t layer_norm_backward_workspace(int rows, int cols);
 cudaError_t launch_layer_norm_backward(const NormGradCall& call, cudaStream_t stream);

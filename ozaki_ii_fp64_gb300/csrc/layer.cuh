@@ -33,6 +33,104 @@ __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float v) {
   return __float2bfloat16_rn(v);
 }
 
+// Two 16-bit elements in one word (the lower address in the low half).
+template <typename T>
+struct Pair;
+template <>
+struct Pair<__nv_bfloat16> {
+  static constexpr bool kBf16 = true;
+  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+  static __device__ __forceinline__ float2 unpack(uint32_t v) {  // bf16 is the upper half of an fp32
+    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+  }
+};
+template <>
+struct Pair<__half> {
+  static constexpr bool kBf16 = false;
+  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+  static __device__ __forceinline__ float2 unpack(uint32_t v) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&v));
+  }
+};
+
+// Arithmetic on two fp32 at once (each rounded as its scalar form).
+__device__ __forceinline__ unsigned long long f2_bits(float2 a) {
+  return static_cast<unsigned long long>(__float_as_uint(a.x)) |
+         (static_cast<unsigned long long>(__float_as_uint(a.y)) << 32);
+}
+__device__ __forceinline__ float2 f2_of(unsigned long long v) {
+  return make_float2(__uint_as_float(static_cast<uint32_t>(v)), __uint_as_float(static_cast<uint32_t>(v >> 32)));
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  unsigned long long r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(f2_bits(a)), "l"(f2_bits(b)));
+  return f2_of(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(f2_bits(a)), "l"(f2_bits(b)));
+  return f2_of(r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(f2_bits(a)), "l"(f2_bits(b)), "l"(f2_bits(c)));
+  return f2_of(r);
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// A 16-byte vector of elements and its floats, as pairs of consecutive ones.
+template <typename T>
+__device__ __forceinline__ void unpack16(const uint4& u, float2* v) {
+  if constexpr (sizeof(T) == 4) {
+    v[0] = make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
+    v[1] = make_float2(__uint_as_float(u.z), __uint_as_float(u.w));
+  } else {
+    v[0] = Pair<T>::unpack(u.x);
+    v[1] = Pair<T>::unpack(u.y);
+    v[2] = Pair<T>::unpack(u.z);
+    v[3] = Pair<T>::unpack(u.w);
+  }
+}
+template <typename T>
+__device__ __forceinline__ uint4 pack16(const float2* v) {
+  if constexpr (sizeof(T) == 4)
+    return make_uint4(__float_as_uint(v[0].x), __float_as_uint(v[0].y), __float_as_uint(v[1].x),
+                      __float_as_uint(v[1].y));
+  else
+    return make_uint4(Pair<T>::pack(v[0].x, v[0].y), Pair<T>::pack(v[1].x, v[1].y), Pair<T>::pack(v[2].x, v[2].y),
+                      Pair<T>::pack(v[3].x, v[3].y));
+}
+
+// A 16-byte vector of elements and its floats.
+template <typename T>
+__device__ __forceinline__ void unpack16(const uint4& u, float* v) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 4) {
+      v[i] = __uint_as_float(w[i]);
+    } else {
+      const float2 f = Pair<T>::unpack(w[i]);
+      v[2 * i] = f.x;
+      v[2 * i + 1] = f.y;
+    }
+  }
+}
+template <typename T>
+__device__ __forceinline__ uint4 pack16(const float* v) {
+  if constexpr (sizeof(T) == 4)
+    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+  else
+    return make_uint4(Pair<T>::pack(v[0], v[1]), Pair<T>::pack(v[2], v[3]), Pair<T>::pack(v[4], v[5]),
+                      Pair<T>::pack(v[6], v[7]));
+}
+
 constexpr float kGeluC = 0.7978845608028654f;  // sqrt(2 / pi)
 constexpr float kGeluA = 0.044715f;
 

@@ -72,44 +72,12 @@ __device__ __forceinline__ void settle_after_abort() {
   }
 }
 
-template <typename T>
-struct Pair;
-template <>
-struct Pair<__nv_bfloat16> {
-  static constexpr bool kBf16 = true;
-  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&v);
-  }
-  static __device__ __forceinline__ float2 unpack(uint32_t v) {
-    return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v));
-  }
-};
-template <>
-struct Pair<__half> {
-  static constexpr bool kBf16 = false;
-  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
-    const __half2 v = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&v);
-  }
-  static __device__ __forceinline__ float2 unpack(uint32_t v) {
-    return __half22float2(*reinterpret_cast<const __half2*>(&v));
-  }
-};
-
 // Eight consecutive elements p[0..7] of which `left` exist, as floats (0 past
 // the end); one 16-byte load where the address allows.
 template <typename T>
 __device__ __forceinline__ void load8(const T* p, int left, bool vec, float (&v)[8]) {
   if (vec && left >= 8) {
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = Pair<T>::unpack(w[i]);
-      v[2 * i] = f.x;
-      v[2 * i + 1] = f.y;
-    }
+    unpack16<T>(__ldg(reinterpret_cast<const uint4*>(p)), v);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = i < left ? to_float(p[i]) : 0.f;
@@ -134,9 +102,7 @@ __device__ __forceinline__ void store_rows(const float (&v)[64], uint8_t* stage,
   uint4* mine = reinterpret_cast<uint4*>(stage + lane * 128);
 #pragma unroll
   for (int c = 0; c < 8; ++c)
-    mine[c ^ (lane & 7)] =
-        make_uint4(Pair<T>::pack(v[8 * c], v[8 * c + 1]), Pair<T>::pack(v[8 * c + 2], v[8 * c + 3]),
-                   Pair<T>::pack(v[8 * c + 4], v[8 * c + 5]), Pair<T>::pack(v[8 * c + 6], v[8 * c + 7]));
+    mine[c ^ (lane & 7)] = pack16<T>(v + 8 * c);
   __syncwarp();
   if (vec && col0 + 64 <= n) {
     const int c = lane & 7;
@@ -442,9 +408,7 @@ __global__ void __launch_bounds__(256) slope_kernel(const T* dy, long long lddy,
 #pragma unroll
       for (int q = 0; q < 8; ++q) s[q] += v[q];
       if (dz) {  // rows of dz start on 16-byte boundaries and are padded to 8
-        *reinterpret_cast<uint4*>(dz + i * lddz + col) =
-            make_uint4(Pair<T>::pack(v[0], v[1]), Pair<T>::pack(v[2], v[3]), Pair<T>::pack(v[4], v[5]),
-                       Pair<T>::pack(v[6], v[7]));
+        *reinterpret_cast<uint4*>(dz + i * lddz + col) = pack16<T>(v);
       }
     }
   }
