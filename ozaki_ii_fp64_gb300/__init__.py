@@ -777,29 +777,30 @@ def crt_f64_mixed(m, n, r, residues, shifts_a, shifts_b, out=None, stream=None):
 ACTIVATIONS = {"none": OZEMU_ACT_NONE, "relu": OZEMU_ACT_RELU, "gelu": OZEMU_ACT_GELU,
                "gelu_tanh": OZEMU_ACT_GELU_TANH, "silu": OZEMU_ACT_SILU}
 _types = {}
-_raw_stream = None
+_raw_stream = _device = _float32 = _uint8 = None
 
 
 def _layer_setup():
     """The torch side of the layer operators, resolved at the first call: a decoded token's calls are a few
     microseconds of device work each, so they look up as little as they can."""
-    global _raw_stream
+    global _raw_stream, _device, _float32, _uint8
     torch = _torch()
     _types.update({torch.bfloat16: OZEMU_BF16, torch.float16: OZEMU_F16, torch.float32: OZEMU_F32})
+    _float32, _uint8, _device = torch.float32, torch.uint8, torch.cuda.current_device
     # The current stream's handle without a Stream object round it, where this torch has that.
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda index: torch.cuda.current_stream(index).cuda_stream)
     return load()
 
 
-def _matrix(t, rows, cols, like, name):
-    """(pointer, leading dimension) of an optional row-major matrix argument."""
+def _matrix(t, shape, dtype, index, name):
+    """(pointer, leading dimension) of an optional row-major matrix argument on device `index`."""
+    rows, cols = shape
     if t is None:
         return None, cols or 1
-    if t.dim() != 2 or tuple(t.shape) != (rows, cols):
-        raise ValueError("%s: expected a %d x %d matrix, got %s" % (name, rows, cols, tuple(t.shape)))
-    if t.dtype is not like.dtype or t.get_device() != like.get_device():
-        raise ValueError("%s: expected %s on %s" % (name, like.dtype, like.device))
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != index:
+        raise ValueError("%s: expected a %d x %d matrix of %s on device %d, got %s of %s on %s"
+                         % (name, rows, cols, dtype, index, tuple(t.shape), t.dtype, t.device))
     if rows == 0 or cols == 0:
         return None, cols or 1
     outer, inner = t.stride()
@@ -808,23 +809,21 @@ def _matrix(t, rows, cols, like, name):
     return t.data_ptr(), outer if rows > 1 else cols
 
 
-def _vector(t, n, dtype, like, name):
+def _vector(t, n, dtype, index, name):
     """Pointer of an optional dense vector argument."""
     if t is None:
         return None
-    if t.dim() != 1 or t.shape[0] != n or t.dtype is not dtype or t.get_device() != like.get_device() or (
-            n > 1 and t.stride(0) != 1):
-        raise ValueError("%s: expected a dense vector of %d %s on %s" % (name, n, dtype, like.device))
+    if t.shape != (n,) or t.dtype is not dtype or t.get_device() != index or (n > 1 and t.stride(0) != 1):
+        raise ValueError("%s: expected a dense vector of %d %s on device %d" % (name, n, dtype, index))
     return t.data_ptr()
 
 
-def _on(stream, like, inputs):
+def _on(stream, index, inputs):
     """The handle of the stream a call runs on.  For a given stream the allocator learns of the inputs' use there;
     ordering their values is the caller's (wait_stream)."""
-    index = like.get_device()
     if index < 0:
         raise ValueError("expected CUDA tensors")
-    if index != _torch().cuda.current_device():
+    if index != _device():
         raise ValueError("expected tensors on the current device")
     if stream is None:
         return _raw_stream(index)
@@ -844,7 +843,7 @@ def _new(stream, like, shape, dtype=None):
 
 def _scratch(stream, like, nbytes):
     """(tensor that keeps it, pointer) of a workspace, 256-byte aligned."""
-    t = _new(stream, like, nbytes + 256, _torch().uint8)
+    t = _new(stream, like, nbytes + 256, _uint8)
     return t, (t.data_ptr() + 255) & ~255
 
 
@@ -855,7 +854,7 @@ def _sizes(t):
 
 
 def _linear_args(x, w, activation):
-    """(library, type, activation, m, n, k) of a linear layer's call."""
+    """(library, type, activation, m, n, k, device) of a linear layer's call."""
     lib = _lib if _raw_stream else _layer_setup()
     act = ACTIVATIONS.get(activation)
     if act is None:
@@ -864,7 +863,7 @@ def _linear_args(x, w, activation):
     if code == OZEMU_F32:
         raise ValueError("expected bfloat16 or float16, got %s" % x.dtype)
     m, k = _sizes(x)
-    return lib, code, act, m, _sizes(w)[0], k
+    return lib, code, act, m, _sizes(w)[0], k, x.get_device()
 
 
 def linear(x, w, bias=None, residual=None, activation="none", save_pre=False, out=None, stream=None):
@@ -872,15 +871,18 @@ def linear(x, w, bias=None, residual=None, activation="none", save_pre=False, ou
 
     With save_pre also the pre-activation x @ w.T + bias, rounded, for linear_backward: (y, pre).  out may be
     residual itself."""
-    lib, code, act, m, n, k = _linear_args(x, w, activation)
-    xp, ldx = _matrix(x, m, k, x, "x")
-    wp, ldw = _matrix(w, n, k, x, "w")
-    bp = _vector(bias, n, x.dtype, x, "bias")
-    rp, ldr = _matrix(residual, m, n, x, "residual")
-    handle = _on(stream, x, (x, w, bias, residual, out))
+    lib, code, act, m, n, k, dev = _linear_args(x, w, activation)
+    dtype = x.dtype
+    xp, ldx = _matrix(x, (m, k), dtype, dev, "x")
+    wp, ldw = _matrix(w, (n, k), dtype, dev, "w")
+    bp = _vector(bias, n, dtype, dev, "bias")
+    rp, ldr = _matrix(residual, (m, n), dtype, dev, "residual")
+    handle = _on(stream, dev, (x, w, bias, residual, out))
     if out is None:
         out = _new(stream, x, (m, n))
-    yp, ldy = _matrix(out, m, n, x, "out")
+        yp, ldy = out.data_ptr(), n or 1
+    else:
+        yp, ldy = _matrix(out, (m, n), dtype, dev, "out")
     pre = pp = None
     if save_pre:
         pre = _new(stream, x, (m, n))
@@ -899,16 +901,17 @@ def linear_backward(dy, x, w, pre=None, activation="none", x_grad=True, w_grad=T
     """(dx, dw, db) of linear for the gradient dy of its output (None for those not asked for).
 
     pre is linear's saved pre-activation (not needed for "none").  The residual's gradient is dy."""
-    lib, code, act, m, n, k = _linear_args(x, w, activation)
+    lib, code, act, m, n, k, dev = _linear_args(x, w, activation)
+    dtype = x.dtype
     if act == OZEMU_ACT_NONE:
         pre = None
     elif pre is None:
         raise ValueError("pre: the pre-activation is needed for %s" % activation)
-    dyp, lddy = _matrix(dy, m, n, x, "dy")
-    xp, ldx = _matrix(x, m, k, x, "x")
-    wp, ldw = _matrix(w, n, k, x, "w")
-    pp, ldp = _matrix(pre, m, n, x, "pre")
-    handle = _on(stream, x, (dy, x, w, pre))
+    dyp, lddy = _matrix(dy, (m, n), dtype, dev, "dy")
+    xp, ldx = _matrix(x, (m, k), dtype, dev, "x")
+    wp, ldw = _matrix(w, (n, k), dtype, dev, "w")
+    pp, ldp = _matrix(pre, (m, n), dtype, dev, "pre")
+    handle = _on(stream, dev, (dy, x, w, pre))
     dx = _new(stream, x, (m, k)) if x_grad else None
     dw = _new(stream, x, (n, k)) if w_grad else None
     db = _new(stream, x, (n,)) if bias_grad else None
@@ -925,7 +928,7 @@ def linear_backward(dy, x, w, pre=None, activation="none", x_grad=True, w_grad=T
 
 
 def _norm_args(x, *params):
-    """(library, type, parameters' dtype and type, rows, cols) of a layer norm's call."""
+    """(library, type, parameters' dtype and type, rows, cols, device) of a layer norm's call."""
     lib = _lib if _raw_stream else _layer_setup()
     code = _types.get(x.dtype)
     if code is None:
@@ -939,25 +942,27 @@ def _norm_args(x, *params):
     if pcode != code and pcode != OZEMU_F32:
         raise ValueError("expected parameters of %s or float32, got %s" % (x.dtype, dtype))
     rows, cols = _sizes(x)
-    return lib, code, dtype, pcode, rows, cols
+    return lib, code, dtype, pcode, rows, cols, x.get_device()
 
 
 def layer_norm(x, weight=None, bias=None, eps=1e-5, stats=False, out=None, stream=None):
     """Layer norm of the rows of a bfloat16, float16 or float32 cuda matrix; weight and bias in x's type or float32.
 
     With stats also the fp32 row statistics that layer_norm_backward takes: (y, mean, rstd).  out may be x itself."""
-    lib, code, pdtype, pcode, rows, cols = _norm_args(x, weight, bias)
-    xp, ldx = _matrix(x, rows, cols, x, "x")
-    wp = _vector(weight, cols, pdtype, x, "weight")
-    bp = _vector(bias, cols, pdtype, x, "bias")
-    handle = _on(stream, x, (x, weight, bias, out))
+    lib, code, pdtype, pcode, rows, cols, dev = _norm_args(x, weight, bias)
+    dtype, shape = x.dtype, (rows, cols)
+    xp, ldx = _matrix(x, shape, dtype, dev, "x")
+    wp = _vector(weight, cols, pdtype, dev, "weight")
+    bp = _vector(bias, cols, pdtype, dev, "bias")
+    handle = _on(stream, dev, (x, weight, bias, out))
     if out is None:
-        out = _new(stream, x, (rows, cols))
-    yp, ldy = _matrix(out, rows, cols, x, "out")
+        out = _new(stream, x, shape)
+        yp, ldy = out.data_ptr(), cols or 1
+    else:
+        yp, ldy = _matrix(out, shape, dtype, dev, "out")
     mean = rstd = mp = sp = None
     if stats:
-        f32 = _torch().float32
-        mean, rstd = _new(stream, x, (rows,), f32), _new(stream, x, (rows,), f32)
+        mean, rstd = _new(stream, x, (rows,), _float32), _new(stream, x, (rows,), _float32)
         mp, sp = mean.data_ptr(), rstd.data_ptr()
     st = lib.ozemu_layer_norm(rows, cols, code, xp, ldx, pcode, wp, bp, eps, yp, ldy, mp, sp, handle)
     if st:
@@ -971,18 +976,20 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, dresidual=None, weight_g
 
     dresidual, the gradient that reaches x along a skip connection, is added to dx; out (dx's memory) may be
     dresidual or dy itself.  dweight and dbias have weight's type (x's without a weight)."""
-    lib, code, pdtype, pcode, rows, cols = _norm_args(x, weight)
-    f32 = _torch().float32
-    dyp, lddy = _matrix(dy, rows, cols, x, "dy")
-    xp, ldx = _matrix(x, rows, cols, x, "x")
-    drp, lddr = _matrix(dresidual, rows, cols, x, "dresidual")
-    wp = _vector(weight, cols, pdtype, x, "weight")
-    mp = _vector(mean, rows, f32, x, "mean")
-    sp = _vector(rstd, rows, f32, x, "rstd")
-    handle = _on(stream, x, (dy, x, mean, rstd, weight, dresidual, out))
+    lib, code, pdtype, pcode, rows, cols, dev = _norm_args(x, weight)
+    dtype, shape = x.dtype, (rows, cols)
+    dyp, lddy = _matrix(dy, shape, dtype, dev, "dy")
+    xp, ldx = _matrix(x, shape, dtype, dev, "x")
+    drp, lddr = _matrix(dresidual, shape, dtype, dev, "dresidual")
+    wp = _vector(weight, cols, pdtype, dev, "weight")
+    mp = _vector(mean, rows, _float32, dev, "mean")
+    sp = _vector(rstd, rows, _float32, dev, "rstd")
+    handle = _on(stream, dev, (dy, x, mean, rstd, weight, dresidual, out))
     if out is None:
-        out = _new(stream, x, (rows, cols))
-    dxp, lddx = _matrix(out, rows, cols, x, "out")
+        out = _new(stream, x, shape)
+        dxp, lddx = out.data_ptr(), cols or 1
+    else:
+        dxp, lddx = _matrix(out, shape, dtype, dev, "out")
     dweight = _new(stream, x, (cols,), pdtype) if weight_grad else None
     dbias = _new(stream, x, (cols,), pdtype) if bias_grad else None
     keep = ws = None

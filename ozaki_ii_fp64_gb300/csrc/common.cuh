@@ -138,6 +138,17 @@ __device__ __forceinline__ void mbar_arrive_expect_tx(uint64_t* bar, uint32_t by
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
+// The same without release semantics, for arrivals that publish no memory of
+// the thread: arming a barrier for copies, or handing back a buffer whose
+// reads have completed.  A release would first wait for the thread's own
+// outstanding stores and copies.
+__device__ __forceinline__ void mbar_arrive_expect_tx_relaxed(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.relaxed.cta.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
 __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -435,14 +446,16 @@ __device__ __forceinline__ void mma_f16_pair(uint32_t d_tmem, uint64_t a_desc, u
 // block holds 64 of the tile's M or N in its rows and 64 of K down them;
 // groups of 8 K rows 1024 bytes apart (stride), blocks 8192 bytes apart
 // (leading).
-__device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr, bool mn_major) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>(mn_major ? 8192u >> 4 : 1u) << 16;
-  d |= static_cast<uint64_t>(1024u >> 4) << 32;
-  d |= static_cast<uint64_t>(1u) << 46;  // version
-  d |= static_cast<uint64_t>(2u) << 61;  // 128-byte swizzle
-  return d;
+// Only the low word depends on the address, in units of 16 bytes: the issuing
+// thread adds offsets to it and joins the words.
+__device__ __forceinline__ uint32_t smem_desc_sw128_lo(uint32_t saddr, bool mn_major) {
+  return ((saddr & 0x3FFFFu) >> 4) | ((mn_major ? 8192u >> 4 : 1u) << 16);
+}
+constexpr uint32_t kSmemDescSw128Hi = (1024u >> 4)    // stride byte offset
+                                      | (1u << 14)    // version
+                                      | (2u << 29);   // 128-byte swizzle
+__device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t lo) {
+  return (static_cast<uint64_t>(kSmemDescSw128Hi) << 32) | lo;
 }
 
 // Instruction descriptor: kind::f16, fp32 accumulator, bf16 or f16 operands.

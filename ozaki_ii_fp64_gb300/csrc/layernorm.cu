@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(RingCfg<TPR, EPT, false>::kThreads, RingCfg<TP
     for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
     fence_mbar_init();
     for (long long row = first; issued < stages && row < c.rows; ++issued, row += step) {
-      mbar_arrive_expect_tx(&full[issued], bytes);
+      mbar_arrive_expect_tx_relaxed(&full[issued], bytes);
       bulk_load(slots + issued * bytes, x + row * c.ldx, bytes, &full[issued]);
     }
   }
@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(RingCfg<TPR, EPT, false>::kThreads, RingCfg<TP
     if (tid == 0) {
       const long long later = row + static_cast<long long>(stages) * step;
       if (later < c.rows) {
-        mbar_arrive_expect_tx(&full[slot], bytes);
+        mbar_arrive_expect_tx_relaxed(&full[slot], bytes);
         bulk_load(slots + slot * bytes, x + later * c.ldx, bytes, &full[slot]);
         ++issued;
       }
@@ -468,7 +468,7 @@ __global__ void __launch_bounds__(RingCfg<TPR, EPT, true>::kThreads, RingCfg<TPR
   int issued = 0;
   auto issue = [&](long long row, int slot) {
     uint8_t* to = slots + slot * slot_bytes;
-    mbar_arrive_expect_tx(&full[slot], slot_bytes);
+    mbar_arrive_expect_tx_relaxed(&full[slot], slot_bytes);
     bulk_load(to, static_cast<const T*>(c.x) + row * c.ldx, bytes, &full[slot]);
     bulk_load(to + bytes, static_cast<const T*>(c.dy) + row * c.lddy, bytes, &full[slot]);
     if (c.dr) bulk_load(to + 2 * bytes, static_cast<const T*>(c.dr) + row * c.lddr, bytes, &full[slot]);
@@ -612,28 +612,6 @@ __global__ void __launch_bounds__(cta_threads(TPR), TPR * NV > 4096 ? 1 : 1024 /
       if (q * TPR + tid < c.cols) dx[q * TPR + tid] = o[q];
   }
   sums.leave(part, parts, c.cols, sub);
-}
-
-// dweight and dbias from the partial sums: 32 columns a CTA, eight threads to
-// a column, each taking every eighth part in order.
-template <typename W>
-__global__ void __launch_bounds__(256) norm_param_kernel(const float* part, int used, int parts, int cols, W* dweight,
-                                                         W* dbias) {
-  __shared__ float red[8][33];
-  W* out = blockIdx.y == 0 ? dweight : dbias;
-  if (!out) return;
-  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5, j = blockIdx.x * 32 + tx;
-  const float* p = part + static_cast<long long>(blockIdx.y) * parts * cols;
-  float s = 0.f;
-  if (j < cols)
-    for (int k = ty; k < used; k += 8) s += p[static_cast<long long>(k) * cols + j];
-  red[ty][tx] = s;
-  __syncthreads();
-  if (ty == 0 && j < cols) {
-#pragma unroll
-    for (int y = 1; y < 8; ++y) s += red[y][tx];
-    out[j] = from_float<W>(s);
-  }
 }
 
 // Rows of any length: dx with a CTA per row, reading the row twice.
@@ -846,8 +824,8 @@ cudaError_t launch_layer_norm_backward(const NormGradCall& c, cudaStream_t strea
     const dim3 grid((c.cols + 31) / 32, 2);
     with_type(c.param_type, [&](auto w) {
       using W = decltype(w);
-      norm_param_kernel<W><<<grid, 256, 0, stream>>>(static_cast<const float*>(c.ws), l.used, l.parts, c.cols,
-                                                     static_cast<W*>(c.dweight), static_cast<W*>(c.dbias));
+      join_parts_kernel<W><<<grid, 1024, 0, stream>>>(static_cast<const float*>(c.ws), l.used, l.parts, c.cols,
+                                                      static_cast<W*>(c.dweight), static_cast<W*>(c.dbias));
       return cudaSuccess;
     });
   }

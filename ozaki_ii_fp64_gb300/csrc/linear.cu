@@ -12,6 +12,7 @@
 // in memory.
 #include <algorithm>
 #include <cstdint>
+#include <cstdlib>
 #include <cuda.h>
 
 #include "kernels.h"
@@ -37,14 +38,6 @@ struct Epilogue {
   long long ldo;
   int act;
   int vec;  // bits: 1 bias, 2 res, 4 pre, 8 out rows start on 16-byte boundaries
-};
-
-struct Product {
-  int m, n;        // rows and columns of D
-  int kb;          // 64-element blocks of the reduction
-  int a_mn, b_mn;  // the operand's reduction runs down its rows
-  int tiles_m, tiles_n;
-  Epilogue e;
 };
 
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_word,
@@ -84,10 +77,95 @@ __device__ __forceinline__ void load8(const T* p, int left, bool vec, float (&v)
   }
 }
 
-template <int kAct>
-__device__ __forceinline__ void activate_all(float (&z)[64]) {
+// The same for four, by plain loads (the memory may be the output's).
+template <typename T>
+__device__ __forceinline__ void load4(const T* p, int left, bool vec, float (&v)[4]) {
+  if (vec && left >= 4) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    const float2 a = Pair<T>::unpack(u.x), b = Pair<T>::unpack(u.y);
+    v[0] = a.x;
+    v[1] = a.y;
+    v[2] = b.x;
+    v[3] = b.y;
+  } else {
 #pragma unroll
-  for (int i = 0; i < 64; ++i) z[i] = activate(z[i], kAct);
+    for (int i = 0; i < 4; ++i) v[i] = i < left ? to_float(p[i]) : 0.f;
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store4(T* p, const float (&v)[4], int left, bool vec) {
+  if (vec && left >= 4) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(Pair<T>::pack(v[0], v[1]), Pair<T>::pack(v[2], v[3]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < left) p[i] = from_float<T>(v[i]);
+  }
+}
+
+template <int kAct, int N>
+__device__ __forceinline__ void activate_each(float (&z)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) z[i] = activate(z[i], kAct);
+}
+template <int N>
+__device__ __forceinline__ void activate_all(float (&z)[N], int act) {
+  switch (act) {
+    case kActRelu: activate_each<kActRelu>(z); break;
+    case kActGelu: activate_each<kActGelu>(z); break;
+    case kActGeluTanh: activate_each<kActGeluTanh>(z); break;
+    case kActSilu: activate_each<kActSilu>(z); break;
+    default: break;
+  }
+}
+
+// A warp's 32 rows x 64 columns of 16-bit elements on their way to or from
+// global memory, as this lane's share: eight 16-byte pieces, piece (lane % 8)
+// of row 4 i + lane / 8, so that a row moves as one 128-byte run; or, where
+// rows do not start on 16-byte boundaries, elements lane and lane + 32 of
+// each row, two rows to a word.
+template <typename T>
+__device__ __forceinline__ void read_rows(uint4 (&v)[8], const T* in, long long ld, int row0, int col0, int m, int n,
+                                          bool vec) {
+  const int lane = threadIdx.x & 31;
+  if (vec && col0 + 64 <= n) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = row0 + 4 * i + (lane >> 3);
+      v[i] = r < m ? *reinterpret_cast<const uint4*>(in + r * ld + col0 + 8 * (lane & 7)) : make_uint4(0, 0, 0, 0);
+    }
+  } else {
+    const uint16_t* p = reinterpret_cast<const uint16_t*>(in) + row0 * ld + col0 + lane;
+    uint32_t* w = reinterpret_cast<uint32_t*>(v);
+#pragma unroll
+    for (int r = 0; r < 32; ++r) {
+      const uint32_t a = row0 + r < m && col0 + lane < n ? p[r * ld] : 0;
+      const uint32_t b = row0 + r < m && col0 + lane + 32 < n ? p[r * ld + 32] : 0;
+      w[r] = a | (b << 16);
+    }
+  }
+}
+
+// That share into the warp's 4 KB of shared memory, where 16-byte piece c of
+// row r lies at piece c ^ (r % 8): no bank conflicts by rows or by pieces.
+template <typename T>
+__device__ __forceinline__ void stage_rows(const uint4 (&v)[8], uint8_t* stage, int col0, int n, bool vec) {
+  const int lane = threadIdx.x & 31;
+  if (vec && col0 + 64 <= n) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = 4 * i + (lane >> 3);
+      reinterpret_cast<uint4*>(stage + r * 128)[(lane & 7) ^ (r & 7)] = v[i];
+    }
+  } else {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(v);
+#pragma unroll
+    for (int r = 0; r < 32; ++r) {
+      uint16_t* row = reinterpret_cast<uint16_t*>(stage + r * 128);
+      row[((((lane >> 3)) ^ (r & 7)) << 3) + (lane & 7)] = static_cast<uint16_t>(w[r]);
+      row[((((lane >> 3) + 4) ^ (r & 7)) << 3) + (lane & 7)] = static_cast<uint16_t>(w[r] >> 16);
+    }
+  }
 }
 
 // A warp writes its 32 rows x 64 columns (one row a lane, in v) to rows
@@ -129,25 +207,29 @@ __device__ __forceinline__ void store_rows(const float (&v)[64], uint8_t* stage,
 }
 
 // ---------------------------------------------------------------------------
-// 256 x BN tiles on CTA pairs.
+// 256 x BN tiles on CTA pairs, BN = 64, 128, 192 or 256.
 //
 // Two CTAs of a cluster form one tile with the 2-SM MMA (M = 256): each stages
 // its 128 rows of A and BN / 2 rows of B, so an operand byte in shared memory
 // serves twice the multiplications of a single-CTA tile.  Persistent: each
 // pair walks the tiles.  Warp 0 issues the TMA loads, one thread of warp 1 the
 // MMAs (4 of K = 16 per 64-element stage), warps 2-9 take finished
-// accumulators out of TMEM; two accumulators of BN columns alternate, so the
-// next tile's MMAs run under this tile's epilogue.
+// accumulators out of TMEM; two accumulators alternate, so the next tile's
+// MMAs run under this tile's epilogue.
 // ---------------------------------------------------------------------------
-template <int BN>
-struct PairCfg {
-  static constexpr int kABytes = 2 * kBlockBytes;          // 128 rows
-  static constexpr int kBBlocks = BN / 2 / kBlock;         // 64-row blocks of B per CTA
-  static constexpr int kStage = kABytes + kBBlocks * kBlockBytes;
-  static constexpr int kStages = 192 * 1024 / kStage;
-  static constexpr int kSmem = 1024 + kStages * kStage + kEpiWarps * 4096 + 256;
-};
+constexpr int kStage = 4 * kBlockBytes;  // two blocks of A, up to two of B
+constexpr int kStages = 6;
+constexpr int kPairSmem = 1024 + kStages * kStage + kEpiWarps * 4096 + 256;
 constexpr int kGroupM = 8;  // tile rows swept together, for reuse of B's columns in L2
+
+struct Product {
+  int m, n;        // rows and columns of D
+  int kb;          // 64-element blocks of the reduction
+  int a_mn, b_mn;  // the operand's reduction runs down its rows
+  int bn;          // columns of a tile
+  int tiles_m, tiles_n;
+  Epilogue e;
+};
 
 __device__ __forceinline__ void tile_of(int t, const Product& p, int& tm, int& tn) {
   const int group = kGroupM * p.tiles_n;
@@ -157,17 +239,48 @@ __device__ __forceinline__ void tile_of(int t, const Product& p, int& tm, int& t
   tn = (t % group) / gm;
 }
 
-template <typename T, int BN>
+// One warp's 32 rows x 64 columns of accumulators, in z, through the epilogue.
+template <typename T>
+__device__ __forceinline__ void finish_rows(float (&z)[64], const uint4 (&res)[8], const Epilogue& e, uint8_t* stage,
+                                            int row0, int col0, int m, int n) {
+  const int lane = threadIdx.x & 31;
+  if (e.bias) {
+#pragma unroll
+    for (int q = 0; q < 64; q += 8) {
+      float b[8];
+      load8(static_cast<const T*>(e.bias) + col0 + q, n - col0 - q, e.vec & 1, b);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) z[q + i] += b[i];
+    }
+  }
+  if (e.pre) store_rows(z, stage, static_cast<T*>(e.pre), e.ldpre, row0, col0, m, n, (e.vec & 4) != 0);
+  activate_all(z, e.act);
+  if (e.res) {
+    stage_rows<T>(res, stage, col0, n, (e.vec & 2) != 0);
+    __syncwarp();
+    const uint4* mine = reinterpret_cast<const uint4*>(stage + lane * 128);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      float r[8];
+      unpack16<T>(mine[c ^ (lane & 7)], r);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) z[8 * c + i] += r[i];
+    }
+    __syncwarp();
+  }
+  store_rows(z, stage, static_cast<T*>(e.out), e.ldo, row0, col0, m, n, (e.vec & 8) != 0);
+}
+
+template <typename T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     product_pair_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
                         const __grid_constant__ Product p, uint32_t* flags) {
-  using C = PairCfg<BN>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* staging = smem + C::kStages * C::kStage;
+  uint8_t* staging = smem + kStages * kStage;
   uint64_t* full = reinterpret_cast<uint64_t*>(staging + kEpiWarps * 4096);
-  uint64_t* empty = full + C::kStages;
-  uint64_t* tfull = empty + C::kStages;
+  uint64_t* empty = full + kStages;
+  uint64_t* tfull = empty + kStages;
   uint64_t* tempty = tfull + 2;
   uint64_t* mma_done = tempty + 2;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(mma_done + 1);
@@ -179,7 +292,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int total = p.tiles_m * p.tiles_n;
 
   if (warp == 0 && lane == 0) {
-    for (int s = 0; s < C::kStages; ++s) {
+    for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);   // armed by the first CTA with both CTAs' bytes
       mbar_init(&empty[s], 1);  // one commit from the pair's MMA issuer
     }
@@ -205,31 +318,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     if (lane == 0) {
-      int it = 0;
+      // B's BN / 2 rows of this CTA, in whole blocks (a part block's last
+      // rows are loaded and not used).
+      const int b_blocks = p.bn > 128 ? 2 : 1;
+      const uint32_t bar0 = mapa_shared(&full[0], 0);
+      const uint32_t bytes = 2 * (2 + b_blocks) * kBlockBytes;
+      int s = 0;
+      uint32_t phase = 1;
       bool ok = true;
       for (int t = pair; t < total && ok; t += npairs) {
         int tm, tn;
         tile_of(t, p, tm, tn);
-        const int i0 = tm * 256 + rank * 128, j0 = tn * BN + rank * (BN / 2);
-        for (int kb = 0; kb < p.kb; ++kb, ++it) {
-          const int s = it % C::kStages;
-          if (!mbar_wait(&empty[s], ((it / C::kStages) & 1) ^ 1, abort_word, flags)) {
+        const int i0 = tm * 256 + rank * 128, j0 = tn * p.bn + rank * (p.bn / 2);
+        for (int kb = 0; kb < p.kb; ++kb) {
+          if (!mbar_wait(&empty[s], phase, abort_word, flags)) {
             ok = false;
             break;
           }
-          uint8_t* st = smem + s * C::kStage;
-          const uint32_t bar = mapa_shared(&full[s], 0);
-          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * C::kStage);
+          uint8_t* st = smem + s * kStage;
+          const uint32_t bar = bar0 + s * 8;
+          if (rank == 0) mbar_arrive_expect_tx_relaxed(&full[s], bytes);
           const int k0 = kb * kBlock;
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const int i = i0 + q * kBlock;
-            tma_load_2d_pair(st + q * kBlockBytes, &ma, bar, p.a_mn ? i : k0, p.a_mn ? k0 : i);
+          if (p.a_mn) {
+            tma_load_2d_pair(st, &ma, bar, i0, k0);
+            tma_load_2d_pair(st + kBlockBytes, &ma, bar, i0 + kBlock, k0);
+          } else {
+            tma_load_2d_pair(st, &ma, bar, k0, i0);
           }
-#pragma unroll
-          for (int q = 0; q < C::kBBlocks; ++q) {
-            const int j = j0 + q * kBlock;
-            tma_load_2d_pair(st + C::kABytes + q * kBlockBytes, &mb, bar, p.b_mn ? j : k0, p.b_mn ? k0 : j);
+          if (p.b_mn) {
+            tma_load_2d_pair(st + 2 * kBlockBytes, &mb, bar, j0, k0);
+            if (b_blocks == 2) tma_load_2d_pair(st + 3 * kBlockBytes, &mb, bar, j0 + kBlock, k0);
+          } else {
+            tma_load_2d_pair(st + 2 * kBlockBytes, &mb, bar, k0, j0);
+          }
+          if (++s == kStages) {
+            s = 0;
+            phase ^= 1;
           }
         }
       }
@@ -238,31 +362,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
-      const uint32_t idesc = idesc_f16(256, BN, Pair<T>::kBf16, p.a_mn != 0, p.b_mn != 0);
+      const uint32_t idesc = idesc_f16(256, p.bn, Pair<T>::kBf16, p.a_mn != 0, p.b_mn != 0);
       // One MMA takes 16 of the reduction: 32 bytes along a K-major row, 16
-      // rows of 128 bytes down an MN-major block.
-      const uint32_t a_step = p.a_mn ? 2048 : 32, b_step = p.b_mn ? 2048 : 32;
-      int it = 0, g = 0;
+      // rows of 128 bytes down an MN-major block (descriptors count 16 bytes).
+      const uint32_t a_step = p.a_mn ? 128 : 2, b_step = p.b_mn ? 128 : 2;
+      const uint32_t a_lo = smem_desc_sw128_lo(smem_u32(smem), p.a_mn != 0);
+      const uint32_t b_lo = smem_desc_sw128_lo(smem_u32(smem) + 2 * kBlockBytes, p.b_mn != 0);
+      int s = 0, g = 0;
+      uint32_t phase = 0;
       bool ok = true;
+      // Whether the next stage is known to be full: tested without blocking
+      // while this stage's MMAs are queued.
+      bool known = false;
       for (int t = pair; t < total && ok; t += npairs, ++g) {
         const int buf = g & 1, use = g >> 1;
         if (use > 0 && !mbar_wait(&tempty[buf], (use - 1) & 1, abort_word, flags)) break;
         tc_fence_after();
-        const uint32_t d = tbase + static_cast<uint32_t>(buf * BN);
-        for (int kb = 0; kb < p.kb; ++kb, ++it) {
-          const int s = it % C::kStages;
-          if (!mbar_wait(&full[s], (it / C::kStages) & 1, abort_word, flags)) {
+        const uint32_t d = tbase + static_cast<uint32_t>(buf * 256);
+        for (int kb = 0; kb < p.kb; ++kb) {
+          if (!known && !mbar_wait(&full[s], phase, abort_word, flags)) {
             ok = false;
             break;
           }
-          tc_fence_after();
-          const uint32_t st = smem_u32(smem + s * C::kStage);
+          const uint32_t at = s * (kStage / 16);
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks)
-            mma_f16_pair(d, smem_desc_sw128(st + ks * a_step, p.a_mn != 0),
-                         smem_desc_sw128(st + C::kABytes + ks * b_step, p.b_mn != 0), idesc,
-                         (kb | ks) != 0 ? 1u : 0u);
+            mma_f16_pair(d, smem_desc_sw128(a_lo + at + ks * a_step), smem_desc_sw128(b_lo + at + ks * b_step), idesc,
+                         ks != 0 ? 1u : (kb != 0 ? 1u : 0u));
           tc_commit_pair_multicast(&empty[s], 0x3);
+          if (++s == kStages) {
+            s = 0;
+            phase ^= 1;
+          }
+          known = mbar_test_wait(&full[s], phase);
         }
         if (ok) tc_commit_pair_multicast(&tfull[buf], 0x3);
       }
@@ -272,6 +404,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else {
+    // Lane quarter warp % 4; the quarter's two warps take alternate 64-column
+    // chunks.
     const int ew = warp - 2, quarter = warp & 3, half = ew >> 2;
     uint8_t* stage = staging + ew * 4096;
     const Epilogue& e = p.e;
@@ -280,67 +414,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int tm, tn;
       tile_of(t, p, tm, tn);
       const int buf = g & 1, use = g >> 1;
-      if (!warp_wait(&tfull[buf], use & 1, abort_word, flags)) break;
-      tc_fence_after();
-      const int row0 = tm * 256 + rank * 128 + quarter * 32, row = row0 + lane;
-      const uint32_t tcol = tbase + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(buf * BN);
+      const int row0 = tm * 256 + rank * 128 + quarter * 32;
+      // Columns of the tile that this warp has to take: none past D's edge.
+      const int cols = row0 < p.m ? min(p.bn, p.n - tn * p.bn) : 0;
+      const uint32_t tcol = tbase + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(buf * 256);
+      bool waited = false, live = true;
 #pragma unroll 1
-      for (int c = half * (BN / 2); c < (half + 1) * (BN / 2); c += 64) {
-        const int col0 = tn * BN + c;
-        const bool last = c + 64 == (half + 1) * (BN / 2);
-        if (row0 < p.m && col0 < p.n) {
-          float z[64];
-          {
-            uint32_t u[32], v[32];
-            tmem_ld32(tcol + c, u);
-            tmem_ld32(tcol + c + 32, v);
-            tmem_wait_ld();
+      for (int c = half * 64; c < cols; c += 128) {
+        const int col0 = tn * p.bn + c;
+        uint4 res[8];
+        if (e.res)
+          read_rows(res, static_cast<const T*>(e.res), e.ldr, row0, col0, p.m, p.n, (e.vec & 2) != 0);
+        if (!waited) {
+          live = warp_wait(&tfull[buf], use & 1, abort_word, flags);
+          if (!live) break;
+          tc_fence_after();
+          waited = true;
+        }
+        float z[64];
+        {
+          uint32_t u[32], v[32];
+          tmem_ld32(tcol + c, u);
+          tmem_ld32(tcol + c + 32, v);
+          tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              z[i] = __uint_as_float(u[i]);
-              z[32 + i] = __uint_as_float(v[i]);
-            }
+          for (int i = 0; i < 32; ++i) {
+            z[i] = __uint_as_float(u[i]);
+            z[32 + i] = __uint_as_float(v[i]);
           }
-          if (last) {  // all of this warp's columns are in registers
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(mapa_shared(&tempty[buf], 0));
-          }
-          if (e.bias) {
-#pragma unroll
-            for (int q = 0; q < 64; q += 8) {
-              float b[8];
-              load8(static_cast<const T*>(e.bias) + col0 + q, p.n - col0 - q, e.vec & 1, b);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) z[q + i] += b[i];
-            }
-          }
-          if (e.pre)
-            store_rows(z, stage, static_cast<T*>(e.pre), e.ldpre, row0, col0, p.m, p.n, (e.vec & 4) != 0);
-          switch (e.act) {
-            case kActRelu: activate_all<kActRelu>(z); break;
-            case kActGelu: activate_all<kActGelu>(z); break;
-            case kActGeluTanh: activate_all<kActGeluTanh>(z); break;
-            case kActSilu: activate_all<kActSilu>(z); break;
-            default: break;
-          }
-          if (e.res && row < p.m) {
-            const T* r = static_cast<const T*>(e.res) + row * e.ldr + col0;
-#pragma unroll
-            for (int q = 0; q < 64; q += 8) {
-              float b[8];
-              load8(r + q, p.n - col0 - q, (e.vec & 2) != 0, b);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) z[q + i] += b[i];
-            }
-          }
-          __syncwarp();  // every lane has read its part of r, which may be out
-          store_rows(z, stage, static_cast<T*>(e.out), e.ldo, row0, col0, p.m, p.n, (e.vec & 8) != 0);
-        } else if (last) {
+        }
+        if (c + 128 >= cols) {  // all of this warp's columns are in registers
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(mapa_shared(&tempty[buf], 0));
+          if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(&tempty[buf], 0));
         }
+        finish_rows<T>(z, res, e, stage, row0, col0, p.m, p.n);
+      }
+      if (!live) break;
+      if (half * 64 >= cols) {  // nothing to take: still let the buffer go, after the tile is done
+        if (!warp_wait(&tfull[buf], use & 1, abort_word, flags)) break;
+        if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(&tempty[buf], 0));
       }
     }
   }
@@ -351,6 +464,187 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tbase, 512);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Few rows (tokens being decoded): the other operand is all the traffic.
+//
+// The wide operand takes the MMA's 128 rows and the tokens its N = NT columns,
+// so every byte of a tile is one of the weights.  A cluster of S CTAs shares
+// the 128 columns of D: each takes a part of the reduction, leaves its fp32
+// sums in shared memory, and then adds up its share of the columns over the
+// cluster, in rank order, with the epilogue.  Two CTAs fit an SM, so one's
+// loads run under the other's start and end.
+// ---------------------------------------------------------------------------
+template <int NT>
+struct FewCfg {
+  static constexpr int kStage = 2 * kBlockBytes + NT * 128;
+  static constexpr int kStages = 108 * 1024 / kStage;
+  static constexpr int kSmem = 1024 + kStages * kStage + 256;
+  static constexpr int kTmemCols = NT < 32 ? 32 : NT;
+  static_assert(NT * 512 <= kStages * kStage, "the partial sums take the ring's memory");
+};
+constexpr int kFewThreads = 192;
+constexpr int kMaxSplit = 16;
+
+struct FewProduct {
+  int m, n;  // D: tokens x columns
+  int kb;
+  int w_mn;  // the wide operand's reduction runs down its rows
+  int split;
+  Epilogue e;
+};
+
+template <typename T, int NT>
+__global__ void __launch_bounds__(kFewThreads, 2)
+    product_few_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap mx,
+                       const __grid_constant__ FewProduct p, uint32_t* flags) {
+  using C = FewCfg<NT>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kStages * C::kStage);
+  uint64_t* empty = full + C::kStages;
+  uint64_t* tfull = empty + C::kStages;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(tfull + 1);
+  volatile int* abort_word = reinterpret_cast<volatile int*>(tmem_holder + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_rank());
+  const int j0 = blockIdx.x / p.split * 128, i0 = blockIdx.y * NT;
+  const int per = (p.kb + p.split - 1) / p.split;
+  const int kb0 = min(rank * per, p.kb), kb1 = min(kb0 + per, p.kb);
+
+  if (warp == 0 && lane == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(tfull, 1);
+    *abort_word = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&mw);
+    tma_prefetch_desc(&mx);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_holder, C::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = *tmem_holder;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      bool ok = true;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        const int it = kb - kb0, s = it % C::kStages;
+        if (!mbar_wait(&empty[s], ((it / C::kStages) & 1) ^ 1, abort_word, flags)) {
+          ok = false;
+          break;
+        }
+        uint8_t* st = smem + s * C::kStage;
+        mbar_arrive_expect_tx_relaxed(&full[s], C::kStage);
+        const int k0 = kb * kBlock;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const int j = j0 + q * kBlock;
+          tma_load_2d(st + q * kBlockBytes, &mw, &full[s], p.w_mn ? j : k0, p.w_mn ? k0 : j);
+        }
+        tma_load_2d(st + 2 * kBlockBytes, &mx, &full[s], k0, i0);
+      }
+      if (!ok) settle_after_abort();
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t idesc = idesc_f16(128, NT, Pair<T>::kBf16, p.w_mn != 0, false);
+      const uint32_t w_step = p.w_mn ? 128 : 2;
+      const uint32_t w_lo = smem_desc_sw128_lo(smem_u32(smem), p.w_mn != 0);
+      const uint32_t x_lo = smem_desc_sw128_lo(smem_u32(smem) + 2 * kBlockBytes, false);
+      int s = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!mbar_wait(&full[s], phase, abort_word, flags)) {
+          ok = false;
+          break;
+        }
+        const uint32_t at = s * (C::kStage / 16);
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+          mma_f16(tbase, smem_desc_sw128(w_lo + at + ks * w_step), smem_desc_sw128(x_lo + at + ks * 2), idesc,
+                  ks != 0 ? 1u : (kb != kb0 ? 1u : 0u));
+        tc_commit(&empty[s]);
+        if (++s == C::kStages) {
+          s = 0;
+          phase ^= 1;
+        }
+      }
+      tc_commit(tfull);  // also when giving up: the MMAs issued are waited for below
+      if (!ok) settle_after_abort();
+    }
+    __syncwarp();
+  } else {
+    const int quarter = warp & 3;
+    float* part = reinterpret_cast<float*>(smem);
+    if (kb0 == kb1) {
+      for (int i = 0; i < NT; ++i) part[i * 128 + quarter * 32 + lane] = 0.f;
+    } else if (warp_wait(tfull, 0, abort_word, flags)) {
+      tc_fence_after();
+#pragma unroll
+      for (int i = 0; i < NT; i += 16) {
+        uint32_t v[16];
+        tmem_ld16(tbase + (static_cast<uint32_t>(quarter * 32) << 16) + i, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int q = 0; q < 16; ++q) part[(i + q) * 128 + quarter * 32 + lane] = __uint_as_float(v[q]);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+
+  // This CTA's share of the columns: 128 / split of them, every token, four
+  // columns of a token at a time.
+  const Epilogue& e = p.e;
+  const int width = 32 / p.split, rows = min(NT, p.m - i0);
+  for (int at = threadIdx.x; at < rows * width; at += kFewThreads) {
+    const int i = at / width, jj = (rank * width + at % width) * 4, j = j0 + jj, left = p.n - j;
+    if (left <= 0) continue;
+    const float* mine = reinterpret_cast<const float*>(smem) + i * 128 + jj;
+    float z[4] = {};
+#pragma unroll 4
+    for (int s = 0; s < p.split; ++s) {
+      float v[4];
+      asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                   : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+                   : "r"(mapa_shared(mine, s)));
+#pragma unroll
+      for (int q = 0; q < 4; ++q) z[q] += v[q];
+    }
+    const long long row = i0 + i;
+    float v[4];
+    if (e.bias) {
+      load4(static_cast<const T*>(e.bias) + j, left, e.vec & 1, v);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) z[q] += v[q];
+    }
+    if (e.pre) store4(static_cast<T*>(e.pre) + row * e.ldpre + j, z, left, (e.vec & 4) != 0);
+    activate_all(z, e.act);
+    if (e.res) {
+      load4(static_cast<const T*>(e.res) + row * e.ldr + j, left, (e.vec & 2) != 0, v);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) z[q] += v[q];
+    }
+    store4(static_cast<T*>(e.out) + row * e.ldo + j, z, left, (e.vec & 8) != 0);
+  }
+  cluster_sync();  // peers have read this CTA's sums
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tbase, C::kTmemCols);
   }
 }
 
@@ -374,21 +668,57 @@ __global__ void __launch_bounds__(256) empty_product_kernel(const Product p) {
   }
 }
 
-// Rows of 16-bit elements copied to rows on 16-byte boundaries.
-__global__ void __launch_bounds__(256) align_rows_kernel(const uint16_t* in, long long ldi, uint16_t* out,
-                                                         long long ldo, int rows, int cols) {
-  for (int r = blockIdx.y; r < rows; r += gridDim.y)
-    for (int j = blockIdx.x * 256 + threadIdx.x; j < cols; j += gridDim.x * 256)
-      out[r * ldo + j] = in[r * ldi + j];
+// Copies of matrices of 16-bit elements with rows on 16-byte boundaries.  A
+// thread makes one 16-byte piece: from the aligned words its eight elements
+// lie in, moved by half a word where the row starts between two.
+struct AlignArgs {
+  const uint16_t* in;
+  uint16_t* out;
+  long long ldi, ldo;
+  int rows, cols;
+};
+struct AlignPair {
+  AlignArgs a[2];
+};
+__global__ void __launch_bounds__(256) align_rows_kernel(const AlignPair both) {
+  const AlignArgs& a = both.a[blockIdx.z];
+  const int pieces = (a.cols + 7) / 8;
+  for (long long at = blockIdx.x * 256LL + threadIdx.x; at < static_cast<long long>(a.rows) * pieces;
+       at += gridDim.x * 256LL) {
+    const long long r = at / pieces;
+    const int j = static_cast<int>(at % pieces) * 8, left = a.cols - j;
+    const uint16_t* p = a.in + r * a.ldi + j;
+    uint32_t w[4];
+    if (left >= 9) {  // the words that hold elements 0..8 lie within the row
+      const bool odd = (reinterpret_cast<uintptr_t>(p) & 2u) != 0;
+      const uint32_t* q = reinterpret_cast<const uint32_t*>(p - (odd ? 1 : 0));
+      // An odd start shares its first word with the element before it, which
+      // the row's first piece does not have: that one is read by itself.
+      uint32_t u[5];
+      u[0] = odd ? static_cast<uint32_t>(p[0]) << 16 : q[0];
+#pragma unroll
+      for (int i = 1; i < 4; ++i) u[i] = q[i];
+      u[4] = odd ? q[4] : 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = odd ? __funnelshift_r(u[i], u[i + 1], 16) : u[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t lo = 2 * i < left ? p[2 * i] : 0, hi = 2 * i + 1 < left ? p[2 * i + 1] : 0;
+        w[i] = lo | (hi << 16);
+      }
+    }
+    *reinterpret_cast<uint4*>(a.out + r * a.ldo + j) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
 }
 
 // dz = dy act'(pre) (where dz is given) and, per chunk of rows, the column
-// sums of the unrounded dz (where part is given).  A CTA takes 256 columns,
+// sums of the unrounded dz (to part, or to db where there is one chunk).  A CTA takes 256 columns,
 // eight to a thread, and `chunk` rows, eight at a time; the eight partial
 // sums of a column are joined in shared memory in a fixed order.
-template <typename T>
+template <typename T, int kAct>
 __global__ void __launch_bounds__(256) slope_kernel(const T* dy, long long lddy, const T* pre, long long ldpre, T* dz,
-                                                    long long lddz, float* part, int m, int n, int chunk, int act,
+                                                    long long lddz, float* part, T* db, int m, int n, int chunk,
                                                     int vec) {
   __shared__ float red[8][264];
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
@@ -399,11 +729,11 @@ __global__ void __launch_bounds__(256) slope_kernel(const T* dy, long long lddy,
     for (long long i = static_cast<long long>(blockIdx.y) * chunk + ty; i < end; i += 8) {
       float v[8];
       load8(dy + i * lddy + col, left, vec & 1, v);
-      if (act != kActNone) {
+      if constexpr (kAct != kActNone) {
         float z[8];
         load8(pre + i * ldpre + col, left, vec & 2, z);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) v[q] *= activation_slope(z[q], act);
+        for (int q = 0; q < 8; ++q) v[q] *= activation_slope(z[q], kAct);
       }
 #pragma unroll
       for (int q = 0; q < 8; ++q) s[q] += v[q];
@@ -412,7 +742,7 @@ __global__ void __launch_bounds__(256) slope_kernel(const T* dy, long long lddy,
       }
     }
   }
-  if (!part) return;
+  if (!part && !db) return;
 #pragma unroll
   for (int q = 0; q < 8; ++q) red[ty][tx * 8 + q] = s[q];
   __syncthreads();
@@ -421,18 +751,11 @@ __global__ void __launch_bounds__(256) slope_kernel(const T* dy, long long lddy,
     float sum = 0.f;
 #pragma unroll
     for (int y = 0; y < 8; ++y) sum += red[y][threadIdx.x];
-    part[static_cast<long long>(blockIdx.y) * n + j] = sum;
+    if (db)  // one chunk: the sum is whole
+      db[j] = from_float<T>(sum);
+    else
+      part[static_cast<long long>(blockIdx.y) * n + j] = sum;
   }
-}
-
-// out[j] = sum over the chunks of part[., j], in order.
-template <typename T>
-__global__ void __launch_bounds__(256) column_sum_kernel(const float* part, int chunks, int n, T* out) {
-  const int j = blockIdx.x * 256 + threadIdx.x;
-  if (j >= n) return;
-  float s = 0.f;
-  for (int c = 0; c < chunks; ++c) s += part[static_cast<long long>(c) * n + j];
-  out[j] = from_float<T>(s);
 }
 
 // ------------------------------------------------------------------- host
@@ -473,17 +796,25 @@ size_t aligned_copy_bytes(const Matrix& x) {
   return (static_cast<size_t>(x.rows) * pad8(x.cols) * 2 + 255) & ~static_cast<size_t>(255);
 }
 
-// Takes that copy (where one is needed) at *ws and moves *ws past it.
-Matrix aligned_copy(const Matrix& x, uint8_t** ws, cudaStream_t stream) {
-  const size_t bytes = aligned_copy_bytes(x);
-  if (bytes == 0) return x;
-  const Matrix y = {*ws, pad8(x.cols), x.rows, x.cols};
-  *ws += bytes;
-  const dim3 grid(std::min((x.cols + 255) / 256, 64), std::min(x.rows, 2048));
-  align_rows_kernel<<<grid, 256, 0, stream>>>(static_cast<const uint16_t*>(x.p), x.ld,
-                                              reinterpret_cast<uint16_t*>(const_cast<void*>(y.p)), y.ld, x.rows,
-                                              x.cols);
-  return y;
+// Makes those copies (where they are needed) of x and y at ws, in one launch,
+// and points x and y at them.
+void align_operands(Matrix* x, Matrix* y, uint8_t* ws, cudaStream_t stream) {
+  AlignPair both;
+  int count = 0;
+  long long most = 0;
+  for (Matrix* m : {x, y}) {
+    const size_t bytes = aligned_copy_bytes(*m);
+    if (bytes == 0 || m->rows == 0 || m->cols == 0) continue;
+    both.a[count++] = {static_cast<const uint16_t*>(m->p), reinterpret_cast<uint16_t*>(ws), m->ld, pad8(m->cols),
+                       m->rows, m->cols};
+    most = std::max(most, static_cast<long long>(m->rows) * (pad8(m->cols) / 8));
+    m->p = ws;
+    m->ld = pad8(m->cols);
+    ws += bytes;
+  }
+  if (count == 0) return;
+  align_rows_kernel<<<dim3(static_cast<unsigned>(std::min<long long>((most + 255) / 256, 152 * 16)), 1, count), 256,
+                      0, stream>>>(both);
 }
 
 // Map of an operand read in blocks of `box` rows of 64 elements; what lies
@@ -505,7 +836,7 @@ constexpr int kMaxDev = 64;
 
 // CTA pairs that can be resident at once (a persistent grid must not exceed
 // them); sets the kernel's shared-memory size on the way.
-template <typename T, int BN>
+template <typename T>
 cudaError_t resident_pairs(int* pairs) {
   static int known[kMaxDev] = {0};
   int dev = 0;
@@ -513,13 +844,13 @@ cudaError_t resident_pairs(int* pairs) {
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= kMaxDev) return cudaErrorInvalidDevice;
   if (known[dev] == 0) {
-    auto kern = product_pair_kernel<T, BN>;
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, PairCfg<BN>::kSmem);
+    auto kern = product_pair_kernel<T>;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2, 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = PairCfg<BN>::kSmem;
+    cfg.dynamicSmemBytes = kPairSmem;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = 2;
@@ -537,18 +868,82 @@ cudaError_t resident_pairs(int* pairs) {
   return cudaSuccess;
 }
 
-template <typename T, int BN>
+// Columns of a tile: the width whose tiles, in rounds over the pairs, take the
+// least time.  A 64-element block of the reduction takes a pair 2 BN clocks at
+// the tensor rate, and each CTA about 136 clocks for each 8 KB block that it
+// loads (60 bytes a clock from L2); a tile's start and end cost
+// about as much as 4 blocks of the widest.  An MN-major B comes in whole
+// blocks of 64 columns for each CTA.
+int tile_width(int m, int n, int kb, bool b_mn, int pairs) {
+  long long best = 0;
+  int width = 256;
+  for (int bn = 256; bn >= 64; bn -= b_mn ? 128 : 64) {
+    const long long tiles = static_cast<long long>((m + 255) / 256) * ((n + bn - 1) / bn);
+    const long long rounds = (tiles + pairs - 1) / pairs;
+    const int block = std::max(2 * bn, 136 * (bn > 128 ? 4 : 3));
+    const long long cost = rounds * (static_cast<long long>(kb) * block + 4 * bn) + 4 * bn;
+    if (best == 0 || cost < best) {
+      best = cost;
+      width = bn;
+    }
+  }
+  return width;
+}
+
+template <typename T>
 cudaError_t launch_pairs(const CUtensorMap& ma, const CUtensorMap& mb, Product p, uint32_t* flags,
                          cudaStream_t stream) {
   int pairs = 0;
-  const cudaError_t e = resident_pairs<T, BN>(&pairs);
+  const cudaError_t e = resident_pairs<T>(&pairs);
   if (e != cudaSuccess) return e;
+  p.bn = tile_width(p.m, p.n, p.kb, p.b_mn != 0, pairs);
   p.tiles_m = (p.m + 255) / 256;
-  p.tiles_n = (p.n + BN - 1) / BN;
+  p.tiles_n = (p.n + p.bn - 1) / p.bn;
   const int tiles = p.tiles_m * p.tiles_n;
-  product_pair_kernel<T, BN>
-      <<<2 * std::min(tiles, pairs), kThreads, PairCfg<BN>::kSmem, stream>>>(ma, mb, p, flags);
+  product_pair_kernel<T><<<2 * std::min(tiles, pairs), kThreads, kPairSmem, stream>>>(ma, mb, p, flags);
   return cudaGetLastError();
+}
+
+template <typename T, int NT>
+cudaError_t launch_few(const Matrix& w, bool w_mn, const Matrix& x, FewProduct p, uint32_t* flags,
+                       cudaStream_t stream) {
+  CUtensorMap mw, mx;
+  if (!make_map(&mw, w, Pair<T>::kBf16, kBlock) || !make_map(&mx, x, Pair<T>::kBf16, NT)) return cudaErrorInvalidValue;
+  auto kern = product_few_kernel<T, NT>;
+  static bool ready[kMaxDev] = {false};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDev) return cudaErrorInvalidDevice;
+  if (!ready[dev]) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, FewCfg<NT>::kSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    ready[dev] = true;
+  }
+  const int across = (p.n + 127) / 128, down = (p.m + NT - 1) / NT;
+  p.w_mn = w_mn;
+  // Two CTAs on each SM, and at least four blocks of the reduction for each.
+  p.split = 1;
+  while (p.split < kMaxSplit && 2 * p.split * across * down <= 304 && p.kb >= 8 * p.split) p.split *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(across * p.split, down, 1);
+  cfg.blockDim = dim3(kFewThreads, 1, 1);
+  cfg.dynamicSmemBytes = FewCfg<NT>::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = p.split;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, mw, mx, p, flags);
+}
+
+bool few_rows(int m, int n) {
+  static const int most = std::getenv("FEW") ? std::atoi(std::getenv("FEW")) : 64;
+  return m <= most;
 }
 
 // D = A B^T over `depth`, with the epilogue e.  a: m x depth (or depth x m
@@ -558,40 +953,49 @@ cudaError_t run_product(int m, int n, int depth, const Matrix& a, bool a_mn, con
                         uint32_t* flags, cudaStream_t stream) {
   e.vec = (e.bias && rows_aligned(e.bias, 0, 1) ? 1 : 0) | (e.res && rows_aligned(e.res, e.ldr, m) ? 2 : 0) |
           (e.pre && rows_aligned(e.pre, e.ldpre, m) ? 4 : 0) | (rows_aligned(e.out, e.ldo, m) ? 8 : 0);
-  Product p = {m, n, (depth + kBlock - 1) / kBlock, a_mn, b_mn, 0, 0, e};
+  const Product p = {m, n, (depth + kBlock - 1) / kBlock, a_mn, b_mn, 0, 0, 0, e};
   if (depth == 0) {
     const long long all = static_cast<long long>(m) * n;
     empty_product_kernel<T><<<static_cast<int>(std::min<long long>((all + 255) / 256, 4096)), 256, 0, stream>>>(p);
     return cudaGetLastError();
   }
+  if (few_rows(m, n) && !a_mn) {
+    const FewProduct f = {m, n, p.kb, 0, 1, e};
+    return m <= 16   ? launch_few<T, 16>(b, b_mn, a, f, flags, stream)
+           : m <= 32 ? launch_few<T, 32>(b, b_mn, a, f, flags, stream)
+           : m <= 64 ? launch_few<T, 64>(b, b_mn, a, f, flags, stream)
+                     : launch_few<T, 128>(b, b_mn, a, f, flags, stream);
+  }
+  int pairs = 0;
+  cudaError_t s = resident_pairs<T>(&pairs);
+  if (s != cudaSuccess) return s;
+  const int bn = tile_width(m, n, p.kb, b_mn, pairs);
   CUtensorMap ma, mb;
-  if (!make_map(&ma, a, Pair<T>::kBf16, kBlock) || !make_map(&mb, b, Pair<T>::kBf16, kBlock))
+  if (!make_map(&ma, a, Pair<T>::kBf16, a_mn ? kBlock : 128) || !make_map(&mb, b, Pair<T>::kBf16, b_mn ? kBlock : bn > 128 ? 128 : 64))
     return cudaErrorInvalidValue;
-  return n > 128 ? launch_pairs<T, 256>(ma, mb, p, flags, stream) : launch_pairs<T, 128>(ma, mb, p, flags, stream);
+  return launch_pairs<T>(ma, mb, p, flags, stream);
 }
 
 template <typename T>
 cudaError_t linear_t(const LinearCall& c, cudaStream_t stream) {
-  uint8_t* ws = static_cast<uint8_t*>(c.ws);
   Matrix x = {c.x, c.ldx, c.m, c.k}, w = {c.w, c.ldw, c.n, c.k};
-  if (c.k > 0) {
-    x = aligned_copy(x, &ws, stream);
-    w = aligned_copy(w, &ws, stream);
-  }
+  align_operands(&x, &w, static_cast<uint8_t*>(c.ws), stream);
   const Epilogue e = {c.bias, c.res, c.ldr, c.pre, c.ldpre, c.y, c.ldy, c.act, 0};
   return run_product<T>(c.m, c.n, c.k, x, false, w, false, e, c.flags, stream);
 }
 
-// Row chunks of the slope pass: enough CTAs to fill the GPU, at most 64 sums
-// to join per column.
+// Row chunks of the slope pass: one where that is quick, else enough CTAs to
+// fill the GPU.
 int slope_chunk(int m, int n) {
+  if (m <= 128) return 128;
   const int across = (n + 255) / 256;
-  const int chunks = std::max(1, std::min(64, 1216 / across));
-  return std::max(8, ((m + chunks - 1) / chunks + 7) / 8 * 8);
+  const int chunks = std::max(1, std::min(256, 1216 / across));
+  return std::max(32, ((m + chunks - 1) / chunks + 7) / 8 * 8);
 }
 
 struct BackwardPlan {
   bool own_dz;  // dz is written to the workspace (else it is dy itself)
+  int chunk, chunks;
   size_t dz, part, x, w;
 };
 BackwardPlan backward_plan(const LinearGradCall& c) {
@@ -599,54 +1003,61 @@ BackwardPlan backward_plan(const LinearGradCall& c) {
   p.own_dz = c.act != kActNone || !rows_aligned(c.dy, c.lddy, c.m);
   const size_t up = 255;
   p.dz = p.own_dz ? (static_cast<size_t>(c.m) * pad8(c.n) * 2 + up) & ~up : 0;
-  const int chunk = slope_chunk(c.m, c.n);
-  p.part = (static_cast<size_t>((c.m + chunk - 1) / chunk) * c.n * 4 + up) & ~up;
+  p.chunk = slope_chunk(c.m, c.n);
+  p.chunks = (c.m + p.chunk - 1) / p.chunk;
+  p.part = p.chunks > 1 ? (static_cast<size_t>(p.chunks) * c.n * 4 + up) & ~up : 0;
   p.x = aligned_copy_bytes({c.x, c.ldx, c.m, c.k});
   p.w = aligned_copy_bytes({c.w, c.ldw, c.n, c.k});
   return p;
 }
 
+template <typename T, int kAct>
+void run_slope(const LinearGradCall& c, const BackwardPlan& p, T* dz, float* part, cudaStream_t stream) {
+  const int vec = (rows_aligned(c.dy, c.lddy, c.m) ? 1 : 0) |
+                  (kAct != kActNone && rows_aligned(c.pre, c.ldpre, c.m) ? 2 : 0);
+  T* db = static_cast<T*>(c.db);
+  const bool whole = p.chunks == 1;
+  slope_kernel<T, kAct><<<dim3((c.n + 255) / 256, p.chunks), 256, 0, stream>>>(
+      static_cast<const T*>(c.dy), c.lddy, static_cast<const T*>(c.pre), c.ldpre, dz, pad8(c.n),
+      db && !whole ? part : nullptr, whole ? db : nullptr, c.m, c.n, p.chunk, vec);
+  if (db && !whole)
+    join_parts_kernel<T><<<(c.n + 31) / 32, 1024, 0, stream>>>(part, p.chunks, p.chunks, c.n, db, nullptr);
+}
+
 template <typename T>
 cudaError_t linear_backward_t(const LinearGradCall& c, cudaStream_t stream) {
-  const Epilogue none = {nullptr, nullptr, 0, nullptr, 0, nullptr, 0, kActNone, 0};
-  Matrix dz = {c.dy, c.lddy, c.m, c.n};
-  uint8_t* ws = static_cast<uint8_t*>(c.ws);
+  Matrix dz = {c.dy, c.lddy, c.m, c.n}, x = {c.x, c.ldx, c.m, c.k}, w = {c.w, c.ldw, c.n, c.k};
   if (c.m > 0 && c.n > 0) {
     const BackwardPlan plan = backward_plan(c);
+    uint8_t* ws = static_cast<uint8_t*>(c.ws);
     T* own = nullptr;
     if (plan.own_dz && (c.dx || c.dw)) {
       own = reinterpret_cast<T*>(ws);
       dz = {own, pad8(c.n), c.m, c.n};
     }
-    ws += plan.dz;
-    float* part = reinterpret_cast<float*>(ws);
-    ws += plan.part;
+    float* part = reinterpret_cast<float*>(ws + plan.dz);
     if (own || c.db) {
-      const int chunk = slope_chunk(c.m, c.n), chunks = (c.m + chunk - 1) / chunk;
-      const int vec = (rows_aligned(c.dy, c.lddy, c.m) ? 1 : 0) |
-                      (c.act != kActNone && rows_aligned(c.pre, c.ldpre, c.m) ? 2 : 0);
-      slope_kernel<T><<<dim3((c.n + 255) / 256, chunks), 256, 0, stream>>>(
-          static_cast<const T*>(c.dy), c.lddy, static_cast<const T*>(c.pre), c.ldpre, own, pad8(c.n),
-          c.db ? part : nullptr, c.m, c.n, chunk, c.act, vec);
-      if (c.db)
-        column_sum_kernel<T><<<(c.n + 255) / 256, 256, 0, stream>>>(part, chunks, c.n, static_cast<T*>(c.db));
+      switch (c.act) {
+        case kActRelu: run_slope<T, kActRelu>(c, plan, own, part, stream); break;
+        case kActGelu: run_slope<T, kActGelu>(c, plan, own, part, stream); break;
+        case kActGeluTanh: run_slope<T, kActGeluTanh>(c, plan, own, part, stream); break;
+        case kActSilu: run_slope<T, kActSilu>(c, plan, own, part, stream); break;
+        default: run_slope<T, kActNone>(c, plan, own, part, stream); break;
+      }
     }
+    Matrix none = {nullptr, 0, 0, 0};
+    align_operands(c.dw ? &x : &none, c.dx ? &w : &none, ws + plan.dz + plan.part, stream);
   } else if (c.db && c.n > 0) {
-    column_sum_kernel<T><<<(c.n + 255) / 256, 256, 0, stream>>>(nullptr, 0, c.n, static_cast<T*>(c.db));
+    join_parts_kernel<T><<<(c.n + 31) / 32, 1024, 0, stream>>>(nullptr, 0, 0, c.n, static_cast<T*>(c.db), nullptr);
   }
+  Epilogue e = {nullptr, nullptr, 0, nullptr, 0, nullptr, 0, kActNone, 0};
   cudaError_t s = cudaGetLastError();
   if (s == cudaSuccess && c.dx && c.m > 0 && c.k > 0) {
-    Matrix w = {c.w, c.ldw, c.n, c.k};
-    if (c.n > 0) w = aligned_copy(w, &ws, stream);
-    Epilogue e = none;
     e.out = c.dx;
     e.ldo = c.lddx;
     s = run_product<T>(c.m, c.k, c.n, dz, false, w, true, e, c.flags, stream);
   }
   if (s == cudaSuccess && c.dw && c.n > 0 && c.k > 0) {
-    Matrix x = {c.x, c.ldx, c.m, c.k};
-    if (c.m > 0) x = aligned_copy(x, &ws, stream);
-    Epilogue e = none;
     e.out = c.dw;
     e.ldo = c.lddw;
     s = run_product<T>(c.n, c.k, c.m, dz, true, x, true, e, c.flags, stream);
