@@ -3,7 +3,9 @@
 A thin ctypes layer over libozemu.so (``include/ozemu.h``).  The functions
 named ``ozemu_*`` mirror the C ABI one to one (ints for device pointers and
 streams); the short-named helpers (``dgemm``, ``igemm_s8``, ``split_rows_f64``
-...) only marshal torch CUDA tensors into those calls.  Every step of the
+...) only marshal torch CUDA tensors into those calls.  Those of the layer
+operators (``linear``, ``layer_norm`` and their ``_backward``) do so natively
+(``csrc/binding.cpp``): their calls for one token are a few microseconds.  Every step of the
 computation runs in the library's CUDA kernels; there is no fallback: if the
 library cannot be built or loaded, importing the binding's functions raises.
 """
@@ -776,198 +778,54 @@ def crt_f64_mixed(m, n, r, residues, shifts_a, shifts_b, out=None, stream=None):
 
 ACTIVATIONS = {"none": OZEMU_ACT_NONE, "relu": OZEMU_ACT_RELU, "gelu": OZEMU_ACT_GELU,
                "gelu_tanh": OZEMU_ACT_GELU_TANH, "silu": OZEMU_ACT_SILU}
-_types = {}
-_raw_stream = _device = _float32 = _uint8 = None
+_native = None
 
 
-def _layer_setup():
-    """The torch side of the layer operators, resolved at the first call: a decoded token's calls are a few
-    microseconds of device work each, so they look up as little as they can."""
-    global _raw_stream, _device, _float32, _uint8
-    torch = _torch()
-    _types.update({torch.bfloat16: OZEMU_BF16, torch.float16: OZEMU_F16, torch.float32: OZEMU_F32})
-    _float32, _uint8, _device = torch.float32, torch.uint8, torch.cuda.current_device
-    # The current stream's handle without a Stream object round it, where this torch has that.
-    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-        lambda index: torch.cuda.current_stream(index).cuda_stream)
-    return load()
+def _layer_calls():
+    """The native binding of the layer operators to torch tensors: argument checks, output memory and streams."""
+    global _native
+    import importlib.machinery
+    import importlib.util
+    _torch()
+    load()
+    if not os.path.exists(_build.binding_path()):
+        raise ImportError("%s is missing; run ozaki_ii_fp64_gb300.build.build()" % _build.binding_path())
+    loader = importlib.machinery.ExtensionFileLoader("_ozemu_torch", _build.binding_path())
+    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_ozemu_torch", loader))
+    loader.exec_module(module)
+    module.setup(OzemuError)
+    _native = module
+    return module
 
 
-def _matrix(t, shape, dtype, index, name):
-    """(pointer, leading dimension) of an optional row-major matrix argument on device `index`."""
-    rows, cols = shape
-    if t is None:
-        return None, cols or 1
-    if t.shape != shape or t.dtype is not dtype or t.get_device() != index:
-        raise ValueError("%s: expected a %d x %d matrix of %s on device %d, got %s of %s on %s"
-                         % (name, rows, cols, dtype, index, tuple(t.shape), t.dtype, t.device))
-    if rows == 0 or cols == 0:
-        return None, cols or 1
-    outer, inner = t.stride()
-    if (inner != 1 and cols > 1) or (outer < cols and rows > 1):
-        raise ValueError("%s: expected a row-major matrix, got strides %s" % (name, (outer, inner)))
-    return t.data_ptr(), outer if rows > 1 else cols
-
-
-def _vector(t, n, dtype, index, name):
-    """Pointer of an optional dense vector argument."""
-    if t is None:
-        return None
-    if t.shape != (n,) or t.dtype is not dtype or t.get_device() != index or (n > 1 and t.stride(0) != 1):
-        raise ValueError("%s: expected a dense vector of %d %s on device %d" % (name, n, dtype, index))
-    return t.data_ptr()
-
-
-def _on(stream, index, inputs):
-    """The handle of the stream a call runs on.  For a given stream the allocator learns of the inputs' use there;
-    ordering their values is the caller's (wait_stream)."""
-    if index < 0:
-        raise ValueError("expected CUDA tensors")
-    if index != _device():
-        raise ValueError("expected tensors on the current device")
-    if stream is None:
-        return _raw_stream(index)
-    for t in inputs:
-        if t is not None:
-            t.record_stream(stream)
-    return stream.cuda_stream
-
-
-def _new(stream, like, shape, dtype=None):
-    """Memory of a call's output or workspace, taken on the stream it runs on."""
-    if stream is None:
-        return like.new_empty(shape, dtype=dtype)
-    with _torch().cuda.stream(stream):
-        return like.new_empty(shape, dtype=dtype)
-
-
-def _scratch(stream, like, nbytes):
-    """(tensor that keeps it, pointer) of a workspace, 256-byte aligned."""
-    t = _new(stream, like, nbytes + 256, _uint8)
-    return t, (t.data_ptr() + 255) & ~255
-
-
-def _sizes(t):
-    if t.dim() != 2:
-        raise ValueError("expected a 2-D tensor")
-    return t.shape
-
-
-def _linear_args(x, w, activation):
-    """(library, type, activation, m, n, k, device) of a linear layer's call."""
-    lib = _lib if _raw_stream else _layer_setup()
-    act = ACTIVATIONS.get(activation)
+def _activation(name):
+    act = ACTIVATIONS.get(name)
     if act is None:
         raise ValueError("activation: expected one of %s" % ", ".join(ACTIVATIONS))
-    code = _types.get(x.dtype, OZEMU_F32)
-    if code == OZEMU_F32:
-        raise ValueError("expected bfloat16 or float16, got %s" % x.dtype)
-    m, k = _sizes(x)
-    return lib, code, act, m, _sizes(w)[0], k, x.get_device()
+    return act
 
 
 def linear(x, w, bias=None, residual=None, activation="none", save_pre=False, out=None, stream=None):
     """act(x @ w.T + bias) + residual of bfloat16 or float16 cuda tensors: x m x k, w n x k, bias n, residual m x n.
 
     With save_pre also the pre-activation x @ w.T + bias, rounded, for linear_backward: (y, pre).  out may be
-    residual itself."""
-    lib, code, act, m, n, k, dev = _linear_args(x, w, activation)
-    dtype = x.dtype
-    xp, ldx = _matrix(x, (m, k), dtype, dev, "x")
-    wp, ldw = _matrix(w, (n, k), dtype, dev, "w")
-    bp = _vector(bias, n, dtype, dev, "bias")
-    rp, ldr = _matrix(residual, (m, n), dtype, dev, "residual")
-    handle = _on(stream, dev, (x, w, bias, residual, out))
-    if out is None:
-        out = _new(stream, x, (m, n))
-        yp, ldy = out.data_ptr(), n or 1
-    else:
-        yp, ldy = _matrix(out, (m, n), dtype, dev, "out")
-    pre = pp = None
-    if save_pre:
-        pre = _new(stream, x, (m, n))
-        pp = pre.data_ptr()
-    keep = ws = None
-    need = lib.ozemu_linear_bytes(m, n, k, xp, ldx, wp, ldw)
-    if need:
-        keep, ws = _scratch(stream, x, need)
-    st = lib.ozemu_linear(m, n, k, code, xp, ldx, wp, ldw, bp, rp, ldr, act, pp, n or 1, yp, ldy, ws, need, handle)
-    if st:
-        raise OzemuError(st, "ozemu_linear")
-    return (out, pre) if save_pre else out
+    residual itself.  On a stream of its own (stream=), the caller orders the inputs' values (wait_stream)."""
+    return (_native or _layer_calls()).linear(x, w, bias, residual, _activation(activation), save_pre, out, stream)
 
 
 def linear_backward(dy, x, w, pre=None, activation="none", x_grad=True, w_grad=True, bias_grad=True, stream=None):
     """(dx, dw, db) of linear for the gradient dy of its output (None for those not asked for).
 
     pre is linear's saved pre-activation (not needed for "none").  The residual's gradient is dy."""
-    lib, code, act, m, n, k, dev = _linear_args(x, w, activation)
-    dtype = x.dtype
-    if act == OZEMU_ACT_NONE:
-        pre = None
-    elif pre is None:
-        raise ValueError("pre: the pre-activation is needed for %s" % activation)
-    dyp, lddy = _matrix(dy, (m, n), dtype, dev, "dy")
-    xp, ldx = _matrix(x, (m, k), dtype, dev, "x")
-    wp, ldw = _matrix(w, (n, k), dtype, dev, "w")
-    pp, ldp = _matrix(pre, (m, n), dtype, dev, "pre")
-    handle = _on(stream, dev, (dy, x, w, pre))
-    dx = _new(stream, x, (m, k)) if x_grad else None
-    dw = _new(stream, x, (n, k)) if w_grad else None
-    db = _new(stream, x, (n,)) if bias_grad else None
-    keep = ws = None
-    need = lib.ozemu_linear_backward_bytes(m, n, k, dyp, lddy, xp, ldx, wp, ldw, act)
-    if need:
-        keep, ws = _scratch(stream, x, need)
-    st = lib.ozemu_linear_backward(m, n, k, code, dyp, lddy, xp, ldx, wp, ldw, act, pp, ldp,
-                                   dx.data_ptr() if x_grad else None, k or 1, dw.data_ptr() if w_grad else None,
-                                   k or 1, db.data_ptr() if bias_grad else None, ws, need, handle)
-    if st:
-        raise OzemuError(st, "ozemu_linear_backward")
-    return dx, dw, db
-
-
-def _norm_args(x, *params):
-    """(library, type, parameters' dtype and type, rows, cols, device) of a layer norm's call."""
-    lib = _lib if _raw_stream else _layer_setup()
-    code = _types.get(x.dtype)
-    if code is None:
-        raise ValueError("expected bfloat16, float16 or float32, got %s" % x.dtype)
-    dtype = x.dtype
-    for p in params:
-        if p is not None:
-            dtype = p.dtype
-            break
-    pcode = _types.get(dtype)
-    if pcode != code and pcode != OZEMU_F32:
-        raise ValueError("expected parameters of %s or float32, got %s" % (x.dtype, dtype))
-    rows, cols = _sizes(x)
-    return lib, code, dtype, pcode, rows, cols, x.get_device()
+    return (_native or _layer_calls()).linear_backward(dy, x, w, pre, _activation(activation), x_grad, w_grad,
+                                                       bias_grad, stream)
 
 
 def layer_norm(x, weight=None, bias=None, eps=1e-5, stats=False, out=None, stream=None):
     """Layer norm of the rows of a bfloat16, float16 or float32 cuda matrix; weight and bias in x's type or float32.
 
     With stats also the fp32 row statistics that layer_norm_backward takes: (y, mean, rstd).  out may be x itself."""
-    lib, code, pdtype, pcode, rows, cols, dev = _norm_args(x, weight, bias)
-    dtype, shape = x.dtype, (rows, cols)
-    xp, ldx = _matrix(x, shape, dtype, dev, "x")
-    wp = _vector(weight, cols, pdtype, dev, "weight")
-    bp = _vector(bias, cols, pdtype, dev, "bias")
-    handle = _on(stream, dev, (x, weight, bias, out))
-    if out is None:
-        out = _new(stream, x, shape)
-        yp, ldy = out.data_ptr(), cols or 1
-    else:
-        yp, ldy = _matrix(out, shape, dtype, dev, "out")
-    mean = rstd = mp = sp = None
-    if stats:
-        mean, rstd = _new(stream, x, (rows,), _float32), _new(stream, x, (rows,), _float32)
-        mp, sp = mean.data_ptr(), rstd.data_ptr()
-    st = lib.ozemu_layer_norm(rows, cols, code, xp, ldx, pcode, wp, bp, eps, yp, ldy, mp, sp, handle)
-    if st:
-        raise OzemuError(st, "ozemu_layer_norm")
-    return (out, mean, rstd) if stats else out
+    return (_native or _layer_calls()).layer_norm(x, weight, bias, eps, stats, out, stream)
 
 
 def layer_norm_backward(dy, x, mean, rstd, weight=None, dresidual=None, weight_grad=True, bias_grad=True, out=None,
@@ -976,29 +834,5 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, dresidual=None, weight_g
 
     dresidual, the gradient that reaches x along a skip connection, is added to dx; out (dx's memory) may be
     dresidual or dy itself.  dweight and dbias have weight's type (x's without a weight)."""
-    lib, code, pdtype, pcode, rows, cols, dev = _norm_args(x, weight)
-    dtype, shape = x.dtype, (rows, cols)
-    dyp, lddy = _matrix(dy, shape, dtype, dev, "dy")
-    xp, ldx = _matrix(x, shape, dtype, dev, "x")
-    drp, lddr = _matrix(dresidual, shape, dtype, dev, "dresidual")
-    wp = _vector(weight, cols, pdtype, dev, "weight")
-    mp = _vector(mean, rows, _float32, dev, "mean")
-    sp = _vector(rstd, rows, _float32, dev, "rstd")
-    handle = _on(stream, dev, (dy, x, mean, rstd, weight, dresidual, out))
-    if out is None:
-        out = _new(stream, x, shape)
-        dxp, lddx = out.data_ptr(), cols or 1
-    else:
-        dxp, lddx = _matrix(out, shape, dtype, dev, "out")
-    dweight = _new(stream, x, (cols,), pdtype) if weight_grad else None
-    dbias = _new(stream, x, (cols,), pdtype) if bias_grad else None
-    keep = ws = None
-    need = lib.ozemu_layer_norm_backward_bytes(rows, cols)
-    if need:
-        keep, ws = _scratch(stream, x, need)
-    st = lib.ozemu_layer_norm_backward(rows, cols, code, dyp, lddy, xp, ldx, pcode, wp, mp, sp, drp, lddr, dxp, lddx,
-                                       dweight.data_ptr() if weight_grad else None,
-                                       dbias.data_ptr() if bias_grad else None, ws, need, handle)
-    if st:
-        raise OzemuError(st, "ozemu_layer_norm_backward")
-    return out, dweight, dbias
+    return (_native or _layer_calls()).layer_norm_backward(dy, x, mean, rstd, weight, dresidual, weight_grad,
+                                                           bias_grad, out, stream)

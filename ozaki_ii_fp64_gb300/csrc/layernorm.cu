@@ -185,9 +185,10 @@ struct RingCfg {
   // backward, their column sums) take.
   static constexpr int kResident = kBackward ? (EPT > 8 ? 512 : 1024) : (EPT > 16 ? 768 : 1024);
   static constexpr int kPerSm = kThreads >= kResident ? 1 : kResident / kThreads;
-  static constexpr int kBytes = 200 * 1024 / kPerSm / 128 * 128;  // shared memory of a CTA's ring
+  static constexpr int kBytes = 200 * 1024 / kPerSm / 128 * 128;  // shared memory of a CTA's ring, and kFront
 };
 constexpr int kMaxStages = 4;
+constexpr int kFront = 128;  // bytes before the first slot: a row's start may lie up to 15 before its slot
 
 // The 2 EPT parameters of one 16-byte vector, in the rows' type T or fp32.
 template <typename T, typename W>
@@ -213,86 +214,205 @@ __device__ __forceinline__ bool ring_wait(uint64_t* full, int turn, int slot, in
   return false;
 }
 
-template <typename T, typename W, int TPR, int EPT>
+// How a thread's EPT elements of a row are laid out.  Aligned rows: NV 16-byte
+// vectors, vector q at (q TPR + tid) VEC.  Rows that start anywhere: element i
+// of "vector" q is (q VEC + i) TPR + tid, so that a warp still reads and writes
+// consecutive elements.
+template <typename T, int TPR, int EPT, bool kAligned>
+struct Row {
+  static constexpr int VEC = 16 / sizeof(T), NV = EPT / VEC, H = VEC / 2;
+  static __device__ __forceinline__ int column(int tid, int q, int i) {
+    return kAligned ? (q * TPR + tid) * VEC + i : (q * VEC + i) * TPR + tid;
+  }
+};
+
+// The bulk copy of one row: 16-byte pieces that hold it, taken whole where
+// they lie within the matrix.  The first row's start and the last row's end
+// may lie in pieces that do not: those elements are read by themselves.
+struct RowCopy {
+  uintptr_t from;
+  uint32_t bytes;
+  int shift;  // byte of the slot where the row starts (negative: not copied)
+};
+template <typename T>
+__device__ __forceinline__ RowCopy row_copy(const void* base, long long ld, long long row, int rows, int cols) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(static_cast<const T*>(base) + row * ld);
+  const uintptr_t end = at + static_cast<uintptr_t>(cols) * sizeof(T);
+  const uintptr_t a = row > 0 ? at & ~uintptr_t(15) : (at + 15) & ~uintptr_t(15);
+  const uintptr_t b = row < rows - 1 ? (end + 15) & ~uintptr_t(15) : end & ~uintptr_t(15);
+  return {a, static_cast<uint32_t>(b - a), static_cast<int>(static_cast<intptr_t>(at - a))};
+}
+// Bytes of a slot for a row of `cols` elements.
+template <typename T, bool kAligned>
+__host__ __device__ __forceinline__ uint32_t slot_bytes_of(int cols) {
+  const uint32_t bytes = static_cast<uint32_t>(cols) * sizeof(T);
+  return kAligned ? bytes : (bytes + 30) & ~15u;
+}
+
+// Starts the copy of a row to its slot.
+template <typename T, bool kAligned>
+__device__ __forceinline__ uint32_t start_row(uint8_t* slot, const void* base, long long ld, long long row, int rows,
+                                              int cols, uint64_t* bar, bool go) {
+  if constexpr (kAligned) {
+    const uint32_t bytes = static_cast<uint32_t>(cols) * sizeof(T);
+    if (go) bulk_load(slot, static_cast<const T*>(base) + row * ld, bytes, bar);
+    return bytes;
+  } else {
+    const RowCopy c = row_copy<T>(base, ld, row, rows, cols);
+    if (go) bulk_load(slot, reinterpret_cast<const void*>(c.from), c.bytes, bar);
+    return c.bytes;
+  }
+}
+
+// A thread's elements of the row in a slot; 0 past the row's end.
+template <typename T, int TPR, int EPT, bool kAligned>
+__device__ __forceinline__ void take_row(const uint8_t* slot, const void* base, long long ld, long long row, int rows,
+                                         int cols, int tid, float2 (&v)[EPT / (16 / sizeof(T))][8 / sizeof(T)]) {
+  using L = Row<T, TPR, EPT, kAligned>;
+  if constexpr (kAligned) {
+#pragma unroll
+    for (int q = 0; q < L::NV; ++q) {
+      if (L::column(tid, q, 0) < cols) {
+        unpack16<T>(*reinterpret_cast<const uint4*>(slot + (q * TPR + tid) * 16), v[q]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < L::H; ++i) v[q][i] = make_float2(0.f, 0.f);
+      }
+    }
+  } else {
+    // Every element from the slot, those of the matrix's first and last bytes
+    // again from memory.
+    const RowCopy c = row_copy<T>(base, ld, row, rows, cols);
+    const uint8_t* mine = slot + c.shift + tid * static_cast<int>(sizeof(T));
+#pragma unroll
+    for (int q = 0; q < L::NV; ++q)
+#pragma unroll
+      for (int i = 0; i < L::VEC; ++i) {
+        const int j = L::column(tid, q, i);
+        const float f = j < cols ? to_float(*reinterpret_cast<const T*>(mine + (q * L::VEC + i) * TPR * sizeof(T))) : 0.f;
+        (i & 1 ? v[q][i / 2].y : v[q][i / 2].x) = f;
+      }
+    if (row == 0 || row == rows - 1) {
+      const T* whole = static_cast<const T*>(base) + row * ld;
+#pragma unroll
+      for (int q = 0; q < L::NV; ++q)
+#pragma unroll
+        for (int i = 0; i < L::VEC; ++i) {
+          const int j = L::column(tid, q, i), off = c.shift + j * static_cast<int>(sizeof(T));
+          if (j < cols && (off < 0 || off + static_cast<int>(sizeof(T)) > static_cast<int>(c.bytes)))
+            (i & 1 ? v[q][i / 2].y : v[q][i / 2].x) = to_float(whole[j]);
+        }
+    }
+  }
+}
+
+// A thread's parameters of vector q, and its store of one.
+template <typename T, typename W, int TPR, int EPT, bool kAligned>
+__device__ __forceinline__ void take_params(const void* base, int cols, int tid, int q, float2 (&v)[8 / sizeof(T)]) {
+  using L = Row<T, TPR, EPT, kAligned>;
+  if constexpr (kAligned) {
+    load_params16<T, W>(base, L::column(tid, q, 0), v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < L::VEC; ++i) {
+      const int j = L::column(tid, q, i);
+      (i & 1 ? v[i / 2].y : v[i / 2].x) = j < cols ? to_float(static_cast<const W*>(base)[j]) : 0.f;
+    }
+  }
+}
+template <typename T, int TPR, int EPT, bool kAligned>
+__device__ __forceinline__ void put_row(T* out, int cols, int tid, int q, const float2 (&v)[8 / sizeof(T)]) {
+  using L = Row<T, TPR, EPT, kAligned>;
+  if constexpr (kAligned) {
+    *reinterpret_cast<uint4*>(out + L::column(tid, q, 0)) = pack16<T>(v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < L::VEC; ++i) {
+      const int j = L::column(tid, q, i);
+      if (j < cols) out[j] = from_float<T>(i & 1 ? v[i / 2].y : v[i / 2].x);
+    }
+  }
+}
+
+template <typename T, typename W, int TPR, int EPT, bool kAligned>
 __global__ void __launch_bounds__(RingCfg<TPR, EPT, false>::kThreads, RingCfg<TPR, EPT, false>::kPerSm)
     norm_forward_ring_kernel(const NormCall c, int stages, float inv) {
-  constexpr int VEC = 16 / sizeof(T), NV = EPT / VEC, H = VEC / 2;
+  using L = Row<T, TPR, EPT, kAligned>;
   using R = RingCfg<TPR, EPT, false>;
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ __align__(16) float red[2][32];
   __shared__ uint64_t bars[R::kGroups][kMaxStages];
   __shared__ int abort_word;
   const int tid = threadIdx.x % TPR, group = threadIdx.x / TPR;
-  const uint32_t bytes = static_cast<uint32_t>(c.cols) * sizeof(T);
+  const uint32_t bytes = slot_bytes_of<T, kAligned>(c.cols);
   const float n = static_cast<float>(c.cols);
-  uint8_t* slots = ring + static_cast<size_t>(group) * stages * bytes;
+  uint8_t* slots = ring + kFront + static_cast<size_t>(group) * stages * bytes;
   uint64_t* full = bars[group];
   const int step = gridDim.x * R::kGroups, first = blockIdx.x * R::kGroups + group;
-  const T* x = static_cast<const T*>(c.x);
   int issued = 0;
+  auto issue = [&](long long row, int slot) {
+    uint64_t* bar = &full[slot];
+    mbar_arrive_expect_tx_relaxed(bar, start_row<T, kAligned>(nullptr, c.x, c.ldx, row, c.rows, c.cols, bar, false));
+    start_row<T, kAligned>(slots + slot * bytes, c.x, c.ldx, row, c.rows, c.cols, bar, true);
+    ++issued;
+  };
   if (threadIdx.x == 0) abort_word = 0;
   if (tid == 0) {
     for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
     fence_mbar_init();
-    for (long long row = first; issued < stages && row < c.rows; ++issued, row += step) {
-      mbar_arrive_expect_tx_relaxed(&full[issued], bytes);
-      bulk_load(slots + issued * bytes, x + row * c.ldx, bytes, &full[issued]);
-    }
+    for (long long row = first; issued < stages && row < c.rows; row += step) issue(row, issued);
   }
   __syncthreads();
   int slot = 0, turn = 0;
   for (long long row = first; row < c.rows; row += step, ++turn) {
     if (!ring_wait<TPR>(full, turn, slot, stages, issued, &abort_word, c.flags)) return;
-    const uint8_t* in = slots + slot * bytes + tid * 16;
-    float2 d[NV][H];
+    float2 d[L::NV][L::H];
+    take_row<T, TPR, EPT, kAligned>(slots + slot * bytes, c.x, c.ldx, row, c.rows, c.cols, tid, d);
     float2 s = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int q = 0; q < NV; ++q)
-      if ((q * TPR + tid) * VEC < c.cols) {
-        unpack16<T>(*reinterpret_cast<const uint4*>(in + q * TPR * 16), d[q]);
+    for (int q = 0; q < L::NV; ++q)
 #pragma unroll
-        for (int i = 0; i < H; ++i) s = add2(s, d[q][i]);
-      }
+      for (int i = 0; i < L::H; ++i) s = add2(s, d[q][i]);
     const float mean = mean_of(row_sum<TPR>(s.x + s.y, red[0]), n, inv);
     __syncwarp();
     if (tid == 0) {
       const long long later = row + static_cast<long long>(stages) * step;
-      if (later < c.rows) {
-        mbar_arrive_expect_tx_relaxed(&full[slot], bytes);
-        bulk_load(slots + slot * bytes, x + later * c.ldx, bytes, &full[slot]);
-        ++issued;
-      }
+      if (later < c.rows) issue(later, slot);
     }
     if (++slot == stages) slot = 0;
     s = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int q = 0; q < NV; ++q)
-      if ((q * TPR + tid) * VEC < c.cols)
+    for (int q = 0; q < L::NV; ++q)
 #pragma unroll
-        for (int i = 0; i < H; ++i) {
-          d[q][i] = add2(d[q][i], both(-mean));
-          s = fma2(d[q][i], d[q][i], s);
+      for (int i = 0; i < L::H; ++i) {
+        d[q][i] = add2(d[q][i], both(-mean));
+        if constexpr (kAligned) {
+          if (L::column(tid, q, 0) >= c.cols) break;
+        } else {
+          if (L::column(tid, q, 2 * i) >= c.cols) d[q][i].x = 0.f;
+          if (L::column(tid, q, 2 * i + 1) >= c.cols) d[q][i].y = 0.f;
         }
+        s = fma2(d[q][i], d[q][i], s);
+      }
     const float rstd = 1.f / sqrtf(mean_of(row_sum<TPR>(s.x + s.y, red[1]), n, inv) + c.eps);
-    T* y = static_cast<T*>(c.y) + row * c.ldy + tid * VEC;
+    T* y = static_cast<T*>(c.y) + row * c.ldy;
 #pragma unroll
-    for (int q = 0; q < NV; ++q) {
-      const int j = (q * TPR + tid) * VEC;
-      if (j >= c.cols) break;
+    for (int q = 0; q < L::NV; ++q) {
+      if (L::column(tid, q, 0) >= c.cols) break;
 #pragma unroll
-      for (int i = 0; i < H; ++i) d[q][i] = mul2(d[q][i], both(rstd));
-      float2 p[H];
+      for (int i = 0; i < L::H; ++i) d[q][i] = mul2(d[q][i], both(rstd));
+      float2 p[L::H];
       if (c.weight) {
-        load_params16<T, W>(c.weight, j, p);
+        take_params<T, W, TPR, EPT, kAligned>(c.weight, c.cols, tid, q, p);
 #pragma unroll
-        for (int i = 0; i < H; ++i) d[q][i] = mul2(d[q][i], p[i]);
+        for (int i = 0; i < L::H; ++i) d[q][i] = mul2(d[q][i], p[i]);
       }
       if (c.bias) {
-        load_params16<T, W>(c.bias, j, p);
+        take_params<T, W, TPR, EPT, kAligned>(c.bias, c.cols, tid, q, p);
 #pragma unroll
-        for (int i = 0; i < H; ++i) d[q][i] = add2(d[q][i], p[i]);
+        for (int i = 0; i < L::H; ++i) d[q][i] = add2(d[q][i], p[i]);
       }
-      *reinterpret_cast<uint4*>(y + q * TPR * VEC) = pack16<T>(d[q]);
+      put_row<T, TPR, EPT, kAligned>(y, c.cols, tid, q, d[q]);
     }
     if (tid == 0) {
       if (c.mean) c.mean[row] = mean;
@@ -335,8 +455,7 @@ __global__ void __launch_bounds__(kLong) norm_forward_long_kernel(const NormCall
 // ---------------------------------------------------------------------------
 // Backward.  One pass over x and dy gives dx and, per CTA, the column sums of
 // dy xhat and dy over the rows it took; a second kernel joins the CTAs' sums
-// in order.  A thread keeps the same columns for every row, its sums in
-// registers, or in shared memory (kShared) where a row takes up the
+// in order.  A thread keeps the same columns for every row, their sums in
 // registers.
 // ---------------------------------------------------------------------------
 
@@ -363,115 +482,38 @@ __device__ __forceinline__ float2 row_sum2(float2 s, float2* red) {
   return s;
 }
 
-// A thread's column sums and what happens to them.  Element i of vector q
-// stands for column (q TPR + tid) VEC + i.
-template <int VEC, int TPR, int NV, int kGroups, bool kShared>
-struct ColumnSums {
-  static constexpr int kWidth = NV * TPR * VEC;
-  static constexpr int kBytes = kShared ? 2 * kWidth * 4 : (kGroups > 1 ? 2 * kGroups * kWidth * 4 : 0);
-  alignas(8) float w[kShared ? 1 : NV][VEC];
-  alignas(8) float b[kShared ? 1 : NV][VEC];
-  float* mem;
-  int tid;
-
-  __device__ __forceinline__ ColumnSums(float* shared, int t) : mem(shared), tid(t) {
-#pragma unroll
-    for (int q = 0; q < (kShared ? 1 : NV); ++q)
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) w[q][i] = b[q][i] = 0.f;
-    if constexpr (kShared) {
-      // Each thread clears and keeps its own words.
-#pragma unroll
-      for (int q = 0; q < NV; ++q)
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) mem[(q * TPR + tid) * VEC + i] = mem[kWidth + (q * TPR + tid) * VEC + i] = 0.f;
-    }
-  }
-  // One element's dy xhat and dy.
-  __device__ __forceinline__ void add(int q, float xh, float dy) {
-    if constexpr (kShared) {
-      float* p = mem + (q * TPR + tid) * VEC;
-      p[0] += dy * xh;
-      p[kWidth] += dy;
-    } else {
-      w[q][0] += dy * xh;
-      b[q][0] += dy;
-    }
-  }
-  // The same for a vector.
-  __device__ __forceinline__ void add(int q, const float2* xh, const float2* dy) {
-    float2* pw = kShared ? reinterpret_cast<float2*>(mem + (q * TPR + tid) * VEC)
-                         : reinterpret_cast<float2*>(w[kShared ? 0 : q]);
-    float2* pb = kShared ? pw + kWidth / 2 : reinterpret_cast<float2*>(b[kShared ? 0 : q]);
-#pragma unroll
-    for (int i = 0; i < VEC / 2; ++i) {
-      pw[i] = fma2(dy[i], xh[i], pw[i]);
-      pb[i] = add2(pb[i], dy[i]);
-    }
-  }
-  // Writes the CTA's sums: part[0][cta][.] of dw, part[1][cta][.] of db.
-  __device__ __forceinline__ void leave(float* part, int parts, int cols, int group) {
-    float* pw = part + static_cast<long long>(blockIdx.x) * cols;
-    float* pb = pw + static_cast<long long>(parts) * cols;
-    if constexpr (kGroups > 1) {
-#pragma unroll
-      for (int q = 0; q < NV; ++q)
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          mem[(2 * group) * kWidth + (q * TPR + tid) * VEC + i] = w[q][i];
-          mem[(2 * group + 1) * kWidth + (q * TPR + tid) * VEC + i] = b[q][i];
-        }
-      __syncthreads();
-      for (int j = threadIdx.x; j < cols; j += kGroups * TPR) {
-        float a = 0.f, d = 0.f;
-#pragma unroll
-        for (int r = 0; r < kGroups; ++r) {
-          a += mem[(2 * r) * kWidth + j];
-          d += mem[(2 * r + 1) * kWidth + j];
-        }
-        pw[j] = a;
-        pb[j] = d;
-      }
-    } else {
-#pragma unroll
-      for (int q = 0; q < NV; ++q)
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          const int at = (q * TPR + tid) * VEC + i;
-          if (at >= cols) continue;
-          pw[at] = kShared ? mem[at] : w[kShared ? 0 : q][i];
-          pb[at] = kShared ? mem[kWidth + at] : b[kShared ? 0 : q][i];
-        }
-    }
-  }
-};
-
-// Rows through the ring (16-byte rows): a slot holds x, dy and, where given,
-// dr of one row.
-template <typename T, typename W, int TPR, int EPT, bool kShared>
+// Rows through the ring: a slot holds x, dy and, where given, dr of one row.
+template <typename T, typename W, int TPR, int EPT, bool kAligned>
 __global__ void __launch_bounds__(RingCfg<TPR, EPT, true>::kThreads, RingCfg<TPR, EPT, true>::kPerSm)
     norm_backward_ring_kernel(const NormGradCall c, float* part, int parts, int stages, float inv) {
-  constexpr int VEC = 16 / sizeof(T), NV = EPT / VEC, H = VEC / 2;
+  using L = Row<T, TPR, EPT, kAligned>;
   using R = RingCfg<TPR, EPT, true>;
-  using Sums = ColumnSums<VEC, TPR, NV, R::kGroups, kShared>;
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ __align__(16) float2 red[2][32];
   __shared__ uint64_t bars[R::kGroups][kMaxStages];
   __shared__ int abort_word;
   const int tid = threadIdx.x % TPR, group = threadIdx.x / TPR;
-  const uint32_t bytes = static_cast<uint32_t>(c.cols) * sizeof(T), slot_bytes = bytes * (c.dr ? 3 : 2);
+  const uint32_t bytes = slot_bytes_of<T, kAligned>(c.cols), slot_bytes = bytes * (c.dr ? 3 : 2);
   const float n = static_cast<float>(c.cols);
-  uint8_t* slots = ring + Sums::kBytes + static_cast<size_t>(group) * stages * slot_bytes;
+  uint8_t* slots = ring + kFront + static_cast<size_t>(group) * stages * slot_bytes;
   uint64_t* full = bars[group];
   const int step = gridDim.x * R::kGroups, first = blockIdx.x * R::kGroups + group;
-  Sums sums(reinterpret_cast<float*>(ring), tid);
+  float2 sw[L::NV][L::H], sb[L::NV][L::H];
+#pragma unroll
+  for (int q = 0; q < L::NV; ++q)
+#pragma unroll
+    for (int i = 0; i < L::H; ++i) sw[q][i] = sb[q][i] = make_float2(0.f, 0.f);
   int issued = 0;
   auto issue = [&](long long row, int slot) {
     uint8_t* to = slots + slot * slot_bytes;
-    mbar_arrive_expect_tx_relaxed(&full[slot], slot_bytes);
-    bulk_load(to, static_cast<const T*>(c.x) + row * c.ldx, bytes, &full[slot]);
-    bulk_load(to + bytes, static_cast<const T*>(c.dy) + row * c.lddy, bytes, &full[slot]);
-    if (c.dr) bulk_load(to + 2 * bytes, static_cast<const T*>(c.dr) + row * c.lddr, bytes, &full[slot]);
+    uint64_t* bar = &full[slot];
+    uint32_t all = start_row<T, kAligned>(nullptr, c.x, c.ldx, row, c.rows, c.cols, bar, false) +
+                   start_row<T, kAligned>(nullptr, c.dy, c.lddy, row, c.rows, c.cols, bar, false);
+    if (c.dr) all += start_row<T, kAligned>(nullptr, c.dr, c.lddr, row, c.rows, c.cols, bar, false);
+    mbar_arrive_expect_tx_relaxed(bar, all);
+    start_row<T, kAligned>(to, c.x, c.ldx, row, c.rows, c.cols, bar, true);
+    start_row<T, kAligned>(to + bytes, c.dy, c.lddy, row, c.rows, c.cols, bar, true);
+    if (c.dr) start_row<T, kAligned>(to + 2 * bytes, c.dr, c.lddr, row, c.rows, c.cols, bar, true);
     ++issued;
   };
   if (threadIdx.x == 0) abort_word = 0;
@@ -494,32 +536,34 @@ __global__ void __launch_bounds__(RingCfg<TPR, EPT, true>::kThreads, RingCfg<TPR
       next_rstd = c.rstd[row + step];
     }
     if (!ring_wait<TPR>(full, turn, slot, stages, issued, &abort_word, c.flags)) return;
-    const uint8_t* in = slots + slot * slot_bytes + tid * 16;
-    float2 xh[NV][H], g[NV][H];
-    uint4 dr[NV];
+    const uint8_t* in = slots + slot * slot_bytes;
+    float2 xh[L::NV][L::H], g[L::NV][L::H];
+    take_row<T, TPR, EPT, kAligned>(in, c.x, c.ldx, row, c.rows, c.cols, tid, xh);
+    take_row<T, TPR, EPT, kAligned>(in + bytes, c.dy, c.lddy, row, c.rows, c.cols, tid, g);
     float2 s1 = make_float2(0.f, 0.f), s2 = s1;
 #pragma unroll
-    for (int q = 0; q < NV; ++q) {
-      const int j = (q * TPR + tid) * VEC;
-      if (j >= c.cols) break;
-      unpack16<T>(*reinterpret_cast<const uint4*>(in + q * TPR * 16), xh[q]);
-      unpack16<T>(*reinterpret_cast<const uint4*>(in + bytes + q * TPR * 16), g[q]);
-      if (c.dr) dr[q] = *reinterpret_cast<const uint4*>(in + 2 * bytes + q * TPR * 16);
+    for (int q = 0; q < L::NV; ++q) {
+      if (L::column(tid, q, 0) >= c.cols) break;  // past the end dy is 0, and so are the sums
 #pragma unroll
-      for (int i = 0; i < H; ++i) xh[q][i] = mul2(add2(xh[q][i], both(-mean)), both(rstd));
-      sums.add(q, xh[q], g[q]);
+      for (int i = 0; i < L::H; ++i) {
+        xh[q][i] = mul2(add2(xh[q][i], both(-mean)), both(rstd));
+        sw[q][i] = fma2(g[q][i], xh[q][i], sw[q][i]);
+        sb[q][i] = add2(sb[q][i], g[q][i]);
+      }
       if (c.weight) {
-        float2 w[H];
-        load_params16<T, W>(c.weight, j, w);
+        float2 w[L::H];
+        take_params<T, W, TPR, EPT, kAligned>(c.weight, c.cols, tid, q, w);
 #pragma unroll
-        for (int i = 0; i < H; ++i) g[q][i] = mul2(g[q][i], w[i]);
+        for (int i = 0; i < L::H; ++i) g[q][i] = mul2(g[q][i], w[i]);
       }
 #pragma unroll
-      for (int i = 0; i < H; ++i) {
+      for (int i = 0; i < L::H; ++i) {
         s1 = add2(s1, g[q][i]);
         s2 = fma2(g[q][i], xh[q][i], s2);
       }
     }
+    float2 dr[L::NV][L::H];
+    if (c.dr) take_row<T, TPR, EPT, kAligned>(in + 2 * bytes, c.dr, c.lddr, row, c.rows, c.cols, tid, dr);
     const float2 s = row_sum2<TPR>(make_float2(s1.x + s1.y, s2.x + s2.y), red[turn & 1]);
     __syncwarp();
     if (tid == 0) {
@@ -528,138 +572,190 @@ __global__ void __launch_bounds__(RingCfg<TPR, EPT, true>::kThreads, RingCfg<TPR
     }
     if (++slot == stages) slot = 0;
     const float c1 = mean_of(s.x, n, inv), c2 = mean_of(s.y, n, inv);
-    T* dx = static_cast<T*>(c.dx) + row * c.lddx + tid * VEC;
+    T* dx = static_cast<T*>(c.dx) + row * c.lddx;
 #pragma unroll
-    for (int q = 0; q < NV; ++q) {
-      if ((q * TPR + tid) * VEC >= c.cols) break;
-      float2 extra[H];
+    for (int q = 0; q < L::NV; ++q) {
+      if (L::column(tid, q, 0) >= c.cols) break;
 #pragma unroll
-      for (int i = 0; i < H; ++i) extra[i] = make_float2(0.f, 0.f);
-      if (c.dr) unpack16<T>(dr[q], extra);
-#pragma unroll
-      for (int i = 0; i < H; ++i) {
+      for (int i = 0; i < L::H; ++i) {
         const float2 v = fma2(xh[q][i], both(-c2), add2(g[q][i], both(-c1)));
-        extra[i] = fma2(v, both(rstd), extra[i]);
+        g[q][i] = c.dr ? fma2(v, both(rstd), dr[q][i]) : mul2(v, both(rstd));
       }
-      *reinterpret_cast<uint4*>(dx + q * TPR * VEC) = pack16<T>(extra);
+      put_row<T, TPR, EPT, kAligned>(dx, c.cols, tid, q, g[q]);
     }
     mean = next_mean;
     rstd = next_rstd;
   }
-  sums.leave(part, parts, c.cols, group);
-}
 
-// The same on rows that no 16-byte access fits, element by element; the next
-// row is loaded before this row's sums meet.
-template <typename T, int TPR, int NV, bool kShared>
-__global__ void __launch_bounds__(cta_threads(TPR), TPR * NV > 4096 ? 1 : 1024 / cta_threads(TPR))
-    norm_backward_kernel(const NormGradCall c, float* part, int parts) {
-  constexpr int kRows = cta_threads(TPR) / TPR;
-  using Sums = ColumnSums<1, TPR, NV, kRows, kShared>;
-  __shared__ __align__(16) float2 red[2][32];
-  extern __shared__ float shared_sums[];
-  const int tid = threadIdx.x % TPR, sub = threadIdx.x / TPR;
-  const bool f32 = c.param_type == kF32;
-  Sums sums(shared_sums, tid);
-  const long long step = static_cast<long long>(gridDim.x) * kRows;
-  long long row = static_cast<long long>(blockIdx.x) * kRows + sub;
-  T x[NV], dy[NV];
-  auto load = [&](long long at) {
-    const T* px = static_cast<const T*>(c.x) + at * c.ldx;
-    const T* pd = static_cast<const T*>(c.dy) + at * c.lddy;
+  // This CTA's sums: part[0][cta][.] of dw, part[1][cta][.] of db.
+  float* pw = part + static_cast<long long>(blockIdx.x) * c.cols;
+  float* pb = pw + static_cast<long long>(parts) * c.cols;
+  if constexpr (R::kGroups > 1) {  // the groups' sums first, in order, in the ring's memory
+    constexpr int kWidth = TPR * EPT;
+    float* mem = reinterpret_cast<float*>(ring);
+    __syncthreads();
 #pragma unroll
-    for (int q = 0; q < NV; ++q) {
-      const int j = q * TPR + tid;
-      if (j < c.cols) {
-        x[q] = px[j];
-        dy[q] = pd[j];
+    for (int q = 0; q < L::NV; ++q)
+#pragma unroll
+      for (int i = 0; i < L::H; ++i) {
+        float* a = mem + (2 * group) * kWidth;
+        const int j = L::column(tid, q, 2 * i), k = L::column(tid, q, 2 * i + 1);
+        a[j] = sw[q][i].x;
+        a[k] = sw[q][i].y;
+        a[kWidth + j] = sb[q][i].x;
+        a[kWidth + k] = sb[q][i].y;
       }
-    }
-  };
-  if (row < c.rows) load(row);
-  for (int turn = 0; row < c.rows; row += step, turn ^= 1) {
-    const float mean = c.mean[row], rstd = c.rstd[row];
-    float2 s = make_float2(0.f, 0.f);
+    __syncthreads();
+    for (int j = threadIdx.x; j < c.cols; j += R::kThreads) {
+      float a = 0.f, b = 0.f;
 #pragma unroll
-    for (int q = 0; q < NV; ++q) {
-      const int j = q * TPR + tid;
-      if (j >= c.cols) break;
-      float w[1] = {1.f};
-      if (c.weight) load_params<T, 1>(c.weight, f32, true, j, 1, w);
-      const float d = to_float(dy[q]), xh = (to_float(x[q]) - mean) * rstd, g = d * w[0];
-      s.x += g;
-      s.y += g * xh;
-      sums.add(q, xh, d);
+      for (int r = 0; r < R::kGroups; ++r) {
+        a += mem[(2 * r) * kWidth + j];
+        b += mem[(2 * r + 1) * kWidth + j];
+      }
+      pw[j] = a;
+      pb[j] = b;
     }
-    s = row_sum2<TPR>(s, red[turn]);
-    const float c1 = s.x / static_cast<float>(c.cols), c2 = s.y / static_cast<float>(c.cols);
-    T* dx = static_cast<T*>(c.dx) + row * c.lddx;
-    const T* dr = c.dr ? static_cast<const T*>(c.dr) + row * c.lddr : nullptr;
-    T o[NV];
+  } else {
 #pragma unroll
-    for (int q = 0; q < NV; ++q) {
-      const int j = q * TPR + tid;
-      if (j >= c.cols) break;
-      float w[1] = {1.f};
-      if (c.weight) load_params<T, 1>(c.weight, f32, true, j, 1, w);
-      float v = rstd * (to_float(dy[q]) * w[0] - c1 - (to_float(x[q]) - mean) * rstd * c2);
-      if (dr) v += to_float(dr[j]);
-      o[q] = from_float<T>(v);
-    }
-    if (row + step < c.rows) load(row + step);
+    for (int q = 0; q < L::NV; ++q)
 #pragma unroll
-    for (int q = 0; q < NV; ++q)
-      if (q * TPR + tid < c.cols) dx[q * TPR + tid] = o[q];
+      for (int i = 0; i < L::H; ++i) {
+        const int j = L::column(tid, q, 2 * i), k = L::column(tid, q, 2 * i + 1);
+        if (j < c.cols) {
+          pw[j] = sw[q][i].x;
+          pb[j] = sb[q][i].x;
+        }
+        if (k < c.cols) {
+          pw[k] = sw[q][i].y;
+          pb[k] = sb[q][i].y;
+        }
+      }
   }
-  sums.leave(part, parts, c.cols, sub);
 }
 
-// Rows of any length: dx with a CTA per row, reading the row twice.
+// Rows of any length, in two passes: the row's mean(g) and mean(g xhat), a CTA
+// a row; then dx and the column sums, a CTA 256 columns of a chunk of rows.
+// The second reading of x and dy is the price of rows that no CTA can hold.
 template <typename T>
-__global__ void __launch_bounds__(kLong) norm_backward_long_kernel(const NormGradCall c) {
-  __shared__ __align__(16) float red[2][32];
+__global__ void __launch_bounds__(512) norm_backward_means_kernel(const NormGradCall c, float2* means, bool vec,
+                                                                  bool weight_vec) {
+  constexpr int VEC = 16 / sizeof(T);
+  __shared__ __align__(16) float2 red[2][32];
   const bool f32 = c.param_type == kF32;
-  for (long long row = blockIdx.x; row < c.rows; row += gridDim.x) {
+  int turn = 0;
+  for (long long row = blockIdx.x; row < c.rows; row += gridDim.x, turn ^= 1) {
     const T* x = static_cast<const T*>(c.x) + row * c.ldx;
     const T* dy = static_cast<const T*>(c.dy) + row * c.lddy;
-    const T* dr = c.dr ? static_cast<const T*>(c.dr) + row * c.lddr : nullptr;
-    T* dx = static_cast<T*>(c.dx) + row * c.lddx;
     const float mean = c.mean[row], rstd = c.rstd[row];
-    float s1 = 0.f, s2 = 0.f;
-    for (int j = threadIdx.x; j < c.cols; j += kLong) {
-      float w[1] = {1.f};
-      if (c.weight) load_params<T, 1>(c.weight, f32, false, j, 1, w);
-      const float g = to_float(dy[j]) * w[0];
-      s1 += g;
-      s2 += g * ((to_float(x[j]) - mean) * rstd);
+    float2 s = make_float2(0.f, 0.f);
+    auto add = [&](float d, float xv, float w) {
+      const float g = d * w;
+      s.x += g;
+      s.y += g * ((xv - mean) * rstd);
+    };
+    if (vec) {
+      for (int j = threadIdx.x * VEC; j < c.cols; j += 512 * VEC) {
+        const int left = c.cols - j;
+        float a[VEC], d[VEC], w[VEC];
+        load_vec<T, VEC>(x + j, left, a);
+        load_vec<T, VEC>(dy + j, left, d);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) w[i] = 1.f;
+        if (c.weight) load_params<T, VEC>(c.weight, f32, weight_vec, j, left, w);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+          if (i < left) add(d[i], a[i], w[i]);
+      }
+    } else {
+      for (int j = threadIdx.x; j < c.cols; j += 512) {
+        float w[1] = {1.f};
+        if (c.weight) load_params<T, 1>(c.weight, f32, true, j, 1, w);
+        add(to_float(dy[j]), to_float(x[j]), w[0]);
+      }
     }
-    s1 = row_sum<kLong>(s1, red[0]) / static_cast<float>(c.cols);
-    s2 = row_sum<kLong>(s2, red[1]) / static_cast<float>(c.cols);
-    for (int j = threadIdx.x; j < c.cols; j += kLong) {
-      float w[1] = {1.f};
-      if (c.weight) load_params<T, 1>(c.weight, f32, false, j, 1, w);
-      float v = rstd * (to_float(dy[j]) * w[0] - s1 - (to_float(x[j]) - mean) * rstd * s2);
-      if (dr) v += to_float(dr[j]);
-      dx[j] = from_float<T>(v);
-    }
+    s = row_sum2<512>(s, red[turn]);
+    if (threadIdx.x == 0) means[row] = make_float2(s.x / static_cast<float>(c.cols), s.y / static_cast<float>(c.cols));
   }
 }
 
-// Column sums over `chunk` rows, one column a thread, for those rows.
-template <typename T>
-__global__ void __launch_bounds__(256) norm_columns_long_kernel(const NormGradCall c, float* part, int parts,
-                                                                int chunk) {
-  const int j = blockIdx.x * 256 + threadIdx.x;
-  if (j >= c.cols) return;
-  float sw = 0.f, sb = 0.f;
-  const long long end = min(static_cast<long long>(c.rows), (blockIdx.y + 1LL) * chunk);
-  for (long long row = static_cast<long long>(blockIdx.y) * chunk; row < end; ++row) {
-    const float dy = to_float(static_cast<const T*>(c.dy)[row * c.lddy + j]);
-    sb += dy;
-    sw += dy * ((to_float(static_cast<const T*>(c.x)[row * c.ldx + j]) - c.mean[row]) * c.rstd[row]);
+template <typename T, bool kAligned>
+__global__ void __launch_bounds__(256) norm_backward_columns_kernel(const NormGradCall c, const float2* means,
+                                                                    float* part, int parts, int chunk) {
+  // Eight columns a thread, eight rows at a time.
+  __shared__ float red[2][8][264];
+  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5, col0 = blockIdx.x * 256;
+  const bool f32 = c.param_type == kF32;
+  float w[8], sw[8] = {}, sb[8] = {};
+  auto column = [&](int i) { return col0 + (kAligned ? tx * 8 + i : i * 32 + tx); };
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    w[i] = 1.f;
+    if (c.weight && column(i) < c.cols) {
+      float v[1];
+      load_params<T, 1>(c.weight, f32, true, column(i), 1, v);
+      w[i] = v[0];
+    }
   }
-  part[static_cast<long long>(blockIdx.y) * c.cols + j] = sw;
-  part[(static_cast<long long>(parts) + blockIdx.y) * c.cols + j] = sb;
+  auto take = [&](const void* base, long long ld, long long row, float (&v)[8]) {
+    const T* p = static_cast<const T*>(base) + row * ld;
+    constexpr int VEC = 16 / sizeof(T);
+    if constexpr (kAligned) {
+#pragma unroll
+      for (int q = 0; q < 8; q += VEC)
+        load_vec<T, VEC>(p + column(q), c.cols - column(q), reinterpret_cast<float(&)[VEC]>(v[q]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = column(i) < c.cols ? to_float(p[column(i)]) : 0.f;
+    }
+  };
+  const long long end = min(static_cast<long long>(c.rows), (blockIdx.y + 1LL) * chunk);
+#pragma unroll 2
+  for (long long row = static_cast<long long>(blockIdx.y) * chunk + ty; row < end; row += 8) {
+    float x[8], dy[8], dr[8];
+    take(c.x, c.ldx, row, x);
+    take(c.dy, c.lddy, row, dy);
+    if (c.dr) take(c.dr, c.lddr, row, dr);
+    const float mean = c.mean[row], rstd = c.rstd[row];
+    const float2 m = means[row];
+    T* out = static_cast<T*>(c.dx) + row * c.lddx;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float xh = (x[i] - mean) * rstd;
+      if (column(i) < c.cols) {
+        sw[i] += dy[i] * xh;
+        sb[i] += dy[i];
+      }
+      x[i] = rstd * (dy[i] * w[i] - m.x - xh * m.y) + (c.dr ? dr[i] : 0.f);
+    }
+    constexpr int VEC = 16 / sizeof(T);
+    if constexpr (kAligned) {
+#pragma unroll
+      for (int q = 0; q < 8; q += VEC)
+        store_vec<T, VEC>(out + column(q), reinterpret_cast<float(&)[VEC]>(x[q]), c.cols - column(q));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (column(i) < c.cols) out[column(i)] = from_float<T>(x[i]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    red[0][ty][column(i) - col0] = sw[i];
+    red[1][ty][column(i) - col0] = sb[i];
+  }
+  __syncthreads();
+  const int j = col0 + threadIdx.x;
+  if (j < c.cols) {
+    float a = 0.f, b = 0.f;
+#pragma unroll
+    for (int y = 0; y < 8; ++y) {
+      a += red[0][y][threadIdx.x];
+      b += red[1][y][threadIdx.x];
+    }
+    part[static_cast<long long>(blockIdx.y) * c.cols + j] = a;
+    part[(static_cast<long long>(parts) + blockIdx.y) * c.cols + j] = b;
+  }
 }
 
 // ------------------------------------------------------------------- host
@@ -710,24 +806,25 @@ struct ForwardLaunch {
 
   // Launches the ring for rows of at most TPR * EPT columns, if there are
   // enough rows to go round.
-  template <typename T, typename W, int TPR, int EPT>
+  template <typename T, typename W, int TPR, int EPT, bool kAligned>
   bool fits() {
     if (c.cols > TPR * EPT) return false;
     using R = RingCfg<TPR, EPT, false>;
-    const int bytes = c.cols * static_cast<int>(sizeof(T)), stages = ring_stages(R::kBytes, R::kGroups, bytes);
+    const int bytes = static_cast<int>(slot_bytes_of<T, kAligned>(c.cols));
+    const int stages = ring_stages(R::kBytes - kFront, R::kGroups, bytes);
     const int ctas = R::kPerSm * kSms;
     if (stages < 2 || c.rows <= ctas * R::kGroups) return false;
-    auto kern = norm_forward_ring_kernel<T, W, TPR, EPT>;
+    auto kern = norm_forward_ring_kernel<T, W, TPR, EPT, kAligned>;
     error = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, R::kBytes);
     if (error != cudaSuccess) return true;
-    kern<<<ctas, R::kThreads, R::kGroups * stages * bytes, stream>>>(c, stages, 1.f / static_cast<float>(c.cols));
+    kern<<<ctas, R::kThreads, kFront + R::kGroups * stages * bytes, stream>>>(c, stages, 1.f / static_cast<float>(c.cols));
     error = cudaGetLastError();
     return true;
   }
-  template <typename T, typename W>
+  template <typename T, typename W, bool kAligned>
   bool any() {
-    return fits<T, W, 32, 32>() || fits<T, W, 128, 32>() || fits<T, W, 256, 32>() || fits<T, W, 512, 32>() ||
-           fits<T, W, 1024, 32>();
+    return fits<T, W, 32, 32, kAligned>() || fits<T, W, 128, 32, kAligned>() || fits<T, W, 256, 32, kAligned>() ||
+           fits<T, W, 512, 32, kAligned>() || fits<T, W, 1024, 32, kAligned>();
   }
 };
 
@@ -738,50 +835,39 @@ struct BackwardLaunch {
   int used = 0;  // of which this many are written
   cudaError_t error = cudaSuccess;
 
-  template <typename T, typename W, int TPR, int EPT, bool kShared>
+  template <typename T, typename W, int TPR, int EPT, bool kAligned>
   bool ring() {
     if (c.cols > TPR * EPT) return false;
     using R = RingCfg<TPR, EPT, true>;
-    constexpr int VEC = 16 / sizeof(T);
-    constexpr int kSums = ColumnSums<VEC, TPR, EPT / VEC, R::kGroups, kShared>::kBytes;
-    const int slot = c.cols * static_cast<int>(sizeof(T)) * (c.dr ? 3 : 2);
-    const int stages = ring_stages(R::kBytes - kSums, R::kGroups, slot);
+    const int slot = static_cast<int>(slot_bytes_of<T, kAligned>(c.cols)) * (c.dr ? 3 : 2);
+    const int stages = ring_stages(R::kBytes - kFront, R::kGroups, slot);
     if (stages < 1) return false;
-    auto kern = norm_backward_ring_kernel<T, W, TPR, EPT, kShared>;
+    auto kern = norm_backward_ring_kernel<T, W, TPR, EPT, kAligned>;
     error = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, R::kBytes);
     if (error != cudaSuccess) return true;
     used = std::min({(c.rows + R::kGroups - 1) / R::kGroups, R::kPerSm * kSms, parts});
-    kern<<<used, R::kThreads, kSums + R::kGroups * stages * slot, stream>>>(
-        c, static_cast<float*>(c.ws), parts, stages, 1.f / static_cast<float>(c.cols));
+    // The groups' column sums meet in the ring's memory.
+    const int smem = std::max(kFront + R::kGroups * stages * slot, R::kGroups > 1 ? R::kGroups * TPR * EPT * 8 : 0);
+    kern<<<used, R::kThreads, smem, stream>>>(c, static_cast<float*>(c.ws), parts, stages,
+                                              1.f / static_cast<float>(c.cols));
     error = cudaGetLastError();
     return true;
   }
-  template <typename T, typename W>
+  template <typename T, typename W, bool kAligned>
   bool any() {
-    return ring<T, W, 32, 8, false>() || ring<T, W, 128, 16, false>() || ring<T, W, 256, 16, false>() ||
-           ring<T, W, 512, 16, false>() || ring<T, W, 1024, 16, true>();
-  }
-  template <typename T, int TPR, int NV, bool kShared>
-  bool plain() {
-    if (c.cols > TPR * NV) return false;
-    constexpr int kRows = cta_threads(TPR) / TPR;
-    constexpr int kSums = ColumnSums<1, TPR, NV, kRows, kShared>::kBytes;
-    auto kern = norm_backward_kernel<T, TPR, NV, kShared>;
-    if (kSums > 48 * 1024) error = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSums);
-    if (error != cudaSuccess) return true;
-    used = std::min({(c.rows + kRows - 1) / kRows, (TPR * NV > 4096 ? 1 : 1024 / cta_threads(TPR)) * kSms, parts});
-    kern<<<used, cta_threads(TPR), kSums, stream>>>(c, static_cast<float*>(c.ws), parts);
-    error = cudaGetLastError();
-    return true;
+    return ring<T, W, 32, 8, kAligned>() || ring<T, W, 128, 16, kAligned>() || ring<T, W, 256, 16, kAligned>() ||
+           ring<T, W, 512, 16, kAligned>();
   }
   template <typename T>
-  void any_length() {
-    const int chunk = (c.rows + parts - 1) / parts;
+  void two_passes(bool vec) {
+    float2* means = reinterpret_cast<float2*>(static_cast<float*>(c.ws) + 2LL * parts * c.cols);
+    norm_backward_means_kernel<T><<<std::min(c.rows, 65536), 512, 0, stream>>>(c, means, vec, aligned16(c.weight));
+    const int across = (c.cols + 255) / 256;
+    const int chunks = std::max(1, std::min({parts, 1216 / across, (c.rows + 7) / 8}));
+    const int chunk = (c.rows + chunks - 1) / chunks;
     used = (c.rows + chunk - 1) / chunk;
-    // The columns first: dx may be dy itself.
-    norm_columns_long_kernel<T><<<dim3((c.cols + 255) / 256, used), 256, 0, stream>>>(
-        c, static_cast<float*>(c.ws), parts, chunk);
-    norm_backward_long_kernel<T><<<std::min(c.rows, 65536), kLong, 0, stream>>>(c);
+    auto kern = vec ? norm_backward_columns_kernel<T, true> : norm_backward_columns_kernel<T, false>;
+    kern<<<dim3(across, used), 256, 0, stream>>>(c, means, static_cast<float*>(c.ws), parts, chunk);
     error = cudaGetLastError();
   }
 };
@@ -790,32 +876,38 @@ struct BackwardLaunch {
 
 cudaError_t launch_layer_norm(const NormCall& c, cudaStream_t stream) {
   const int size = type_bytes(c.type);
-  const bool vec = rows_aligned16(c.x, c.ldx, c.rows, size) && rows_aligned16(c.y, c.ldy, c.rows, size);
-  const bool ring = vec && static_cast<long long>(c.cols) * size % 16 == 0 && aligned16(c.weight) && aligned16(c.bias);
+  const long long bytes = static_cast<long long>(c.cols) * size;
+  const bool rows_vec = rows_aligned16(c.x, c.ldx, c.rows, size) && rows_aligned16(c.y, c.ldy, c.rows, size);
+  const bool whole = rows_vec && bytes % 16 == 0 && aligned16(c.weight) && aligned16(c.bias);
   ForwardLaunch l{c, stream};
   return with_type(c.type, [&](auto t) {
     using T = decltype(t);
-    if (!vec) return forward_vec<T, 1, 16>(c, stream);
-    if (ring && (c.param_type == kF32 ? l.any<T, float>() : l.any<T, T>())) return l.error;
-    return forward_vec<T, 16 / sizeof(T), 4>(c, stream);
+    const bool p32 = c.param_type == kF32;
+    if (whole ? (p32 ? l.any<T, float, true>() : l.any<T, T, true>())
+              : bytes >= 64 && (p32 ? l.any<T, float, false>() : l.any<T, T, false>()))
+      return l.error;
+    return rows_vec ? forward_vec<T, 16 / sizeof(T), 4>(c, stream) : forward_vec<T, 1, 16>(c, stream);
   });
 }
 
-size_t layer_norm_backward_workspace(int, int cols) { return static_cast<size_t>(2 * max_parts(cols)) * cols * 4; }
+size_t layer_norm_backward_workspace(int rows, int cols) {
+  return static_cast<size_t>(2 * max_parts(cols)) * cols * 4 + static_cast<size_t>(rows) * 8;
+}
 
 cudaError_t launch_layer_norm_backward(const NormGradCall& c, cudaStream_t stream) {
   BackwardLaunch l{c, stream, max_parts(c.cols)};
   if (c.rows > 0) {
     const int size = type_bytes(c.type);
-    const bool vec = static_cast<long long>(c.cols) * size % 16 == 0 && rows_aligned16(c.x, c.ldx, c.rows, size) &&
-                     rows_aligned16(c.dy, c.lddy, c.rows, size) && rows_aligned16(c.dr, c.lddr, c.rows, size) &&
-                     rows_aligned16(c.dx, c.lddx, c.rows, size) && aligned16(c.weight);
+    const long long bytes = static_cast<long long>(c.cols) * size;
+    const bool vec = rows_aligned16(c.x, c.ldx, c.rows, size) && rows_aligned16(c.dy, c.lddy, c.rows, size) &&
+                     rows_aligned16(c.dr, c.lddr, c.rows, size) && rows_aligned16(c.dx, c.lddx, c.rows, size);
+    const bool whole = vec && bytes % 16 == 0 && aligned16(c.weight);
     with_type(c.type, [&](auto t) {
       using T = decltype(t);
-      if (!(vec && (c.param_type == kF32 ? l.any<T, float>() : l.any<T, T>())) &&
-          !(l.plain<T, 32, 8, false>() || l.plain<T, 128, 8, false>() || l.plain<T, 256, 8, false>() ||
-            l.plain<T, 512, 8, false>() || l.plain<T, 512, 16, false>() || l.plain<T, 1024, 16, true>()))
-        l.any_length<T>();
+      const bool p32 = c.param_type == kF32;
+      if (!(whole ? (p32 ? l.any<T, float, true>() : l.any<T, T, true>())
+                  : bytes >= 64 && (p32 ? l.any<T, float, false>() : l.any<T, T, false>())))
+        l.two_passes<T>(vec);
       return l.error;
     });
     if (l.error != cudaSuccess) return l.error;

@@ -217,9 +217,9 @@ __device__ __forceinline__ void store_rows(const float (&v)[64], uint8_t* stage,
 // accumulators out of TMEM; two accumulators alternate, so the next tile's
 // MMAs run under this tile's epilogue.
 // ---------------------------------------------------------------------------
-constexpr int kStage = 4 * kBlockBytes;  // two blocks of A, up to two of B
-constexpr int kStages = 6;
-constexpr int kPairSmem = 1024 + kStages * kStage + kEpiWarps * 4096 + 256;
+constexpr int kRing = 192 * 1024;  // stages of two blocks of A and one or two of B: 8 or 6
+constexpr int kMaxStages = 8;
+constexpr int kPairSmem = 1024 + kRing + kEpiWarps * 4096 + 256;
 constexpr int kGroupM = 8;  // tile rows swept together, for reuse of B's columns in L2
 
 struct Product {
@@ -277,10 +277,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         const __grid_constant__ Product p, uint32_t* flags) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* staging = smem + kStages * kStage;
+  uint8_t* staging = smem + kRing;
   uint64_t* full = reinterpret_cast<uint64_t*>(staging + kEpiWarps * 4096);
-  uint64_t* empty = full + kStages;
-  uint64_t* tfull = empty + kStages;
+  uint64_t* empty = full + kMaxStages;
+  uint64_t* tfull = empty + kMaxStages;
   uint64_t* tempty = tfull + 2;
   uint64_t* mma_done = tempty + 2;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(mma_done + 1);
@@ -290,9 +290,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int rank = static_cast<int>(cluster_rank());
   const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
   const int total = p.tiles_m * p.tiles_n;
+  // B's BN / 2 rows of this CTA, in whole blocks (a part block's last rows
+  // are loaded and not used).
+  const int b_blocks = p.bn > 128 ? 2 : 1;
+  const int stage_bytes = (2 + b_blocks) * kBlockBytes, stages = kRing / stage_bytes;
 
   if (warp == 0 && lane == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < stages; ++s) {
       mbar_init(&full[s], 1);   // armed by the first CTA with both CTAs' bytes
       mbar_init(&empty[s], 1);  // one commit from the pair's MMA issuer
     }
@@ -318,11 +322,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     if (lane == 0) {
-      // B's BN / 2 rows of this CTA, in whole blocks (a part block's last
-      // rows are loaded and not used).
-      const int b_blocks = p.bn > 128 ? 2 : 1;
       const uint32_t bar0 = mapa_shared(&full[0], 0);
-      const uint32_t bytes = 2 * (2 + b_blocks) * kBlockBytes;
       int s = 0;
       uint32_t phase = 1;
       bool ok = true;
@@ -335,9 +335,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             ok = false;
             break;
           }
-          uint8_t* st = smem + s * kStage;
+          uint8_t* st = smem + s * stage_bytes;
           const uint32_t bar = bar0 + s * 8;
-          if (rank == 0) mbar_arrive_expect_tx_relaxed(&full[s], bytes);
+          if (rank == 0) mbar_arrive_expect_tx_relaxed(&full[s], 2 * stage_bytes);
           const int k0 = kb * kBlock;
           if (p.a_mn) {
             tma_load_2d_pair(st, &ma, bar, i0, k0);
@@ -351,7 +351,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           } else {
             tma_load_2d_pair(st + 2 * kBlockBytes, &mb, bar, k0, j0);
           }
-          if (++s == kStages) {
+          if (++s == stages) {
             s = 0;
             phase ^= 1;
           }
@@ -384,13 +384,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             ok = false;
             break;
           }
-          const uint32_t at = s * (kStage / 16);
+          const uint32_t at = s * (stage_bytes / 16);
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks)
             mma_f16_pair(d, smem_desc_sw128(a_lo + at + ks * a_step), smem_desc_sw128(b_lo + at + ks * b_step), idesc,
                          ks != 0 ? 1u : (kb != 0 ? 1u : 0u));
           tc_commit_pair_multicast(&empty[s], 0x3);
-          if (++s == kStages) {
+          if (++s == stages) {
             s = 0;
             phase ^= 1;
           }
