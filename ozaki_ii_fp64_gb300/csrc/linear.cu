@@ -12,7 +12,6 @@
 // in memory.
 #include <algorithm>
 #include <cstdint>
-#include <cstdlib>
 #include <cuda.h>
 
 #include "kernels.h"
@@ -119,11 +118,17 @@ __device__ __forceinline__ void activate_all(float (&z)[N], int act) {
   }
 }
 
-// A warp's 32 rows x 64 columns of 16-bit elements on their way to or from
-// global memory, as this lane's share: eight 16-byte pieces, piece (lane % 8)
-// of row 4 i + lane / 8, so that a row moves as one 128-byte run; or, where
-// rows do not start on 16-byte boundaries, elements lane and lane + 32 of
-// each row, two rows to a word.
+// A warp's 32 rows x 64 columns of 16-bit elements pass through its 4 KB of
+// shared memory (row r at byte 128 r, its 16-byte piece c at piece c ^ (r % 8):
+// no bank conflicts by rows or by pieces), so that a row moves as one 128-byte
+// run.  A lane's share on the way: piece lane % 8 of rows 4 i + lane / 8; or,
+// where rows do not start on 16-byte boundaries, elements 2 lane and
+// 2 lane + 1 of every row, moved by words, and between words where the row
+// starts on an odd element.
+__device__ __forceinline__ uint32_t* stage_word(uint8_t* stage, int r, int lane) {
+  return reinterpret_cast<uint32_t*>(stage + r * 128 + (((lane >> 2) ^ (r & 7)) << 4)) + (lane & 3);
+}
+
 template <typename T>
 __device__ __forceinline__ void read_rows(uint4 (&v)[8], const T* in, long long ld, int row0, int col0, int m, int n,
                                           bool vec) {
@@ -134,21 +139,36 @@ __device__ __forceinline__ void read_rows(uint4 (&v)[8], const T* in, long long 
       const int r = row0 + 4 * i + (lane >> 3);
       v[i] = r < m ? *reinterpret_cast<const uint4*>(in + r * ld + col0 + 8 * (lane & 7)) : make_uint4(0, 0, 0, 0);
     }
-  } else {
-    const uint16_t* p = reinterpret_cast<const uint16_t*>(in) + row0 * ld + col0 + lane;
-    uint32_t* w = reinterpret_cast<uint32_t*>(v);
+    return;
+  }
+  uint32_t* w = reinterpret_cast<uint32_t*>(v);
+  const uint16_t* p = reinterpret_cast<const uint16_t*>(in) + row0 * ld + col0;
+  if (col0 > 0 && col0 + 64 <= n) {  // the element before the run is the row's, too
+    // All loads first: the words, and for row `lane` the last element, which a
+    // row that starts on an odd element has in a 33rd word.
+    const uint32_t last = row0 + lane < m ? p[lane * ld + 63] : 0;
 #pragma unroll
     for (int r = 0; r < 32; ++r) {
-      const uint32_t a = row0 + r < m && col0 + lane < n ? p[r * ld] : 0;
-      const uint32_t b = row0 + r < m && col0 + lane + 32 < n ? p[r * ld + 32] : 0;
+      const uint16_t* q = p + r * ld;
+      w[r] = row0 + r < m ? *(reinterpret_cast<const uint32_t*>(reinterpret_cast<uintptr_t>(q) & ~uintptr_t(3)) + lane) : 0;
+    }
+#pragma unroll
+    for (int r = 0; r < 32; ++r) {
+      const uint32_t next = __shfl_down_sync(0xFFFFFFFFu, w[r], 1), tail = __shfl_sync(0xFFFFFFFFu, last, r);
+      const bool odd = (reinterpret_cast<uintptr_t>(p + r * ld) & 2u) != 0;
+      if (odd) w[r] = __funnelshift_r(w[r], lane == 31 ? tail : next, 16);
+    }
+  } else {
+#pragma unroll
+    for (int r = 0; r < 32; ++r) {
+      const uint16_t* q = p + r * ld + 2 * lane;
+      const uint32_t a = row0 + r < m && col0 + 2 * lane < n ? q[0] : 0;
+      const uint32_t b = row0 + r < m && col0 + 2 * lane + 1 < n ? q[1] : 0;
       w[r] = a | (b << 16);
     }
   }
 }
 
-// That share into the warp's 4 KB of shared memory, where 16-byte piece c of
-// row r lies at piece c ^ (r % 8): no bank conflicts by rows or by pieces.
-template <typename T>
 __device__ __forceinline__ void stage_rows(const uint4 (&v)[8], uint8_t* stage, int col0, int n, bool vec) {
   const int lane = threadIdx.x & 31;
   if (vec && col0 + 64 <= n) {
@@ -160,50 +180,48 @@ __device__ __forceinline__ void stage_rows(const uint4 (&v)[8], uint8_t* stage, 
   } else {
     const uint32_t* w = reinterpret_cast<const uint32_t*>(v);
 #pragma unroll
-    for (int r = 0; r < 32; ++r) {
-      uint16_t* row = reinterpret_cast<uint16_t*>(stage + r * 128);
-      row[((((lane >> 3)) ^ (r & 7)) << 3) + (lane & 7)] = static_cast<uint16_t>(w[r]);
-      row[((((lane >> 3) + 4) ^ (r & 7)) << 3) + (lane & 7)] = static_cast<uint16_t>(w[r] >> 16);
-    }
+    for (int r = 0; r < 32; ++r) *stage_word(stage, r, lane) = w[r];
   }
 }
 
-// A warp writes its 32 rows x 64 columns (one row a lane, in v) to rows
-// row0.. and columns col0.. of an m x n matrix, through its 4 KB of shared
-// memory so that each row leaves in 16-byte pieces of one 128-byte run.  The
-// 16-byte pieces of row i are stored at piece ^ (i % 8): neither side has
-// bank conflicts.
 template <typename T>
-__device__ __forceinline__ void store_rows(const float (&v)[64], uint8_t* stage, T* out, long long ldo, int row0,
-                                           int col0, int m, int n, bool vec) {
+__device__ __forceinline__ void write_rows(uint8_t* stage, T* out, long long ldo, int row0, int col0, int m, int n,
+                                           bool vec) {
   const int lane = threadIdx.x & 31;
-  uint4* mine = reinterpret_cast<uint4*>(stage + lane * 128);
-#pragma unroll
-  for (int c = 0; c < 8; ++c)
-    mine[c ^ (lane & 7)] = pack16<T>(v + 8 * c);
-  __syncwarp();
   if (vec && col0 + 64 <= n) {
-    const int c = lane & 7;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int r = 4 * i + (lane >> 3);
       if (row0 + r < m)
-        *reinterpret_cast<uint4*>(out + (row0 + r) * ldo + col0 + 8 * c) =
-            reinterpret_cast<const uint4*>(stage + r * 128)[c ^ (r & 7)];
+        *reinterpret_cast<uint4*>(out + (row0 + r) * ldo + col0 + 8 * (lane & 7)) =
+            reinterpret_cast<const uint4*>(stage + r * 128)[(lane & 7) ^ (r & 7)];
     }
-  } else {
-    const int rows = m - row0 < 32 ? m - row0 : 32;
-    for (int r = 0; r < rows; ++r) {
-      T* o = out + (row0 + r) * ldo + col0;
+    return;
+  }
+  uint16_t* p = reinterpret_cast<uint16_t*>(out) + row0 * ldo + col0;
+  const bool whole = col0 + 64 <= n;
+#pragma unroll 1
+  for (int r0 = 0; r0 < 32; r0 += 8) {
+    uint32_t a[8], b[8];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int j = 32 * h + lane;
-        if (col0 + j < n)
-          o[j] = reinterpret_cast<const T*>(stage + r * 128 + (((j >> 3) ^ (r & 7)) << 4))[j & 7];
+    for (int i = 0; i < 8; ++i) a[i] = *stage_word(stage, r0 + i, lane);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) b[i] = __shfl_down_sync(0xFFFFFFFFu, a[i], 1);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint16_t* q = p + (r0 + i) * ldo;
+      const bool odd = (reinterpret_cast<uintptr_t>(q) & 2u) != 0, in_m = row0 + r0 + i < m;
+      if (whole) {  // from an odd start: words of elements 2 lane + 1 and 2 lane + 2, and the two ends
+        const uint32_t word = odd ? __funnelshift_r(a[i], b[i], 16) : a[i];
+        if (in_m && !(odd && lane == 31)) *reinterpret_cast<uint32_t*>(q + 2 * lane + (odd ? 1 : 0)) = word;
+        if (in_m && odd && lane == 31) q[63] = static_cast<uint16_t>(a[i] >> 16);
+        if (in_m && odd && lane == 0) q[0] = static_cast<uint16_t>(a[i]);
+      } else {
+        if (in_m && col0 + 2 * lane < n) q[2 * lane] = static_cast<uint16_t>(a[i]);
+        if (in_m && col0 + 2 * lane + 1 < n) q[2 * lane + 1] = static_cast<uint16_t>(a[i] >> 16);
       }
     }
   }
-  __syncwarp();
 }
 
 // ---------------------------------------------------------------------------
@@ -239,36 +257,68 @@ __device__ __forceinline__ void tile_of(int t, const Product& p, int& tm, int& t
   tn = (t % group) / gm;
 }
 
-// One warp's 32 rows x 64 columns of accumulators, in z, through the epilogue.
-template <typename T>
-__device__ __forceinline__ void finish_rows(float (&z)[64], const uint4 (&res)[8], const Epilogue& e, uint8_t* stage,
-                                            int row0, int col0, int m, int n) {
+// One warp's 32 rows x 64 columns of accumulators, at TMEM address `taddr`,
+// through the epilogue; `done` is called once they have been read for the last
+// time.  Half of the columns at a time, in a loop: the code that a short
+// product has to fetch first is half as long.
+template <typename T, typename F>
+__device__ __forceinline__ void finish_rows(uint32_t taddr, const uint4 (&res)[8], const Epilogue& e, uint8_t* stage,
+                                            int row0, int col0, int m, int n, F done) {
   const int lane = threadIdx.x & 31;
-  if (e.bias) {
+  uint4* mine = reinterpret_cast<uint4*>(stage + lane * 128);
+  auto take = [&](int h, float (&z)[32]) {
+    uint32_t u[32];
+    tmem_ld32(taddr + 32 * h, u);
+    tmem_wait_ld();
 #pragma unroll
-    for (int q = 0; q < 64; q += 8) {
-      float b[8];
-      load8(static_cast<const T*>(e.bias) + col0 + q, n - col0 - q, e.vec & 1, b);
+    for (int i = 0; i < 32; ++i) z[i] = __uint_as_float(u[i]);
+    if (e.bias) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) z[q + i] += b[i];
+      for (int q = 0; q < 32; q += 8) {
+        float b[8];
+        load8(static_cast<const T*>(e.bias) + col0 + 32 * h + q, n - col0 - 32 * h - q, e.vec & 1, b);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z[q + i] += b[i];
+      }
     }
+  };
+  if (e.pre) {
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+      float z[32];
+      take(h, z);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) mine[(4 * h + c) ^ (lane & 7)] = pack16<T>(z + 8 * c);
+    }
+    __syncwarp();
+    write_rows(stage, static_cast<T*>(e.pre), e.ldpre, row0, col0, m, n, (e.vec & 4) != 0);
+    __syncwarp();
   }
-  if (e.pre) store_rows(z, stage, static_cast<T*>(e.pre), e.ldpre, row0, col0, m, n, (e.vec & 4) != 0);
-  activate_all(z, e.act);
   if (e.res) {
-    stage_rows<T>(res, stage, col0, n, (e.vec & 2) != 0);
-    __syncwarp();
-    const uint4* mine = reinterpret_cast<const uint4*>(stage + lane * 128);
-#pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      float r[8];
-      unpack16<T>(mine[c ^ (lane & 7)], r);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) z[8 * c + i] += r[i];
-    }
+    stage_rows(res, stage, col0, n, (e.vec & 2) != 0);
     __syncwarp();
   }
-  store_rows(z, stage, static_cast<T*>(e.out), e.ldo, row0, col0, m, n, (e.vec & 8) != 0);
+#pragma unroll 1
+  for (int h = 0; h < 2; ++h) {
+    float z[32];
+    take(h, z);
+    if (h == 1) done();
+    activate_all(z, e.act);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      uint4* at = mine + ((4 * h + c) ^ (lane & 7));
+      if (e.res) {
+        float r[8];
+        unpack16<T>(*at, r);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z[8 * c + i] += r[i];
+      }
+      *at = pack16<T>(z + 8 * c);
+    }
+  }
+  __syncwarp();
+  write_rows(stage, static_cast<T*>(e.out), e.ldo, row0, col0, m, n, (e.vec & 8) != 0);
+  __syncwarp();
 }
 
 template <typename T>
@@ -431,24 +481,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           tc_fence_after();
           waited = true;
         }
-        float z[64];
-        {
-          uint32_t u[32], v[32];
-          tmem_ld32(tcol + c, u);
-          tmem_ld32(tcol + c + 32, v);
-          tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            z[i] = __uint_as_float(u[i]);
-            z[32 + i] = __uint_as_float(v[i]);
+        finish_rows<T>(tcol + c, res, e, stage, row0, col0, p.m, p.n, [&] {
+          if (c + 128 >= cols) {  // this warp's last columns of the tile
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(&tempty[buf], 0));
           }
-        }
-        if (c + 128 >= cols) {  // all of this warp's columns are in registers
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(&tempty[buf], 0));
-        }
-        finish_rows<T>(z, res, e, stage, row0, col0, p.m, p.n);
+        });
       }
       if (!live) break;
       if (half * 64 >= cols) {  // nothing to take: still let the buffer go, after the tile is done
@@ -669,8 +708,9 @@ __global__ void __launch_bounds__(256) empty_product_kernel(const Product p) {
 }
 
 // Copies of matrices of 16-bit elements with rows on 16-byte boundaries.  A
-// thread makes one 16-byte piece: from the aligned words its eight elements
-// lie in, moved by half a word where the row starts between two.
+// thread makes 16-byte pieces: each from the two aligned pieces of the source
+// that its elements lie in, moved by the bytes that the row starts past a
+// boundary; element by element where those reach beyond the matrix.
 struct AlignArgs {
   const uint16_t* in;
   uint16_t* out;
@@ -680,27 +720,32 @@ struct AlignArgs {
 struct AlignPair {
   AlignArgs a[2];
 };
-__global__ void __launch_bounds__(256) align_rows_kernel(const AlignPair both) {
+__global__ void __launch_bounds__(256) align_rows_kernel(const __grid_constant__ AlignPair both) {
   const AlignArgs& a = both.a[blockIdx.z];
   const int pieces = (a.cols + 7) / 8;
-  for (long long at = blockIdx.x * 256LL + threadIdx.x; at < static_cast<long long>(a.rows) * pieces;
-       at += gridDim.x * 256LL) {
-    const long long r = at / pieces;
-    const int j = static_cast<int>(at % pieces) * 8, left = a.cols - j;
+  const uintptr_t begin = reinterpret_cast<uintptr_t>(a.in);
+  const uintptr_t end = reinterpret_cast<uintptr_t>(a.in + (a.rows - 1) * a.ldi + a.cols);
+  const int across = (pieces + 31) / 32;  // 32 pieces of a row to a warp
+  const long long all = static_cast<long long>(a.rows) * across;
+  for (long long at = blockIdx.x * 8LL + (threadIdx.x >> 5); at < all; at += gridDim.x * 8LL) {
+    const long long r = at / across;
+    const int j = (static_cast<int>(at % across) * 32 + (threadIdx.x & 31)) * 8, left = a.cols - j;
+    if (left <= 0) continue;
     const uint16_t* p = a.in + r * a.ldi + j;
+    const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 15u);
+    const uintptr_t from = reinterpret_cast<uintptr_t>(p) - off;
     uint32_t w[4];
-    if (left >= 9) {  // the words that hold elements 0..8 lie within the row
-      const bool odd = (reinterpret_cast<uintptr_t>(p) & 2u) != 0;
-      const uint32_t* q = reinterpret_cast<const uint32_t*>(p - (odd ? 1 : 0));
-      // An odd start shares its first word with the element before it, which
-      // the row's first piece does not have: that one is read by itself.
+    if (from >= begin && from + 32 <= end) {
+      const uint4 lo = *reinterpret_cast<const uint4*>(from), hi = *reinterpret_cast<const uint4*>(from + 16);
       uint32_t u[5];
-      u[0] = odd ? static_cast<uint32_t>(p[0]) << 16 : q[0];
+      switch (off >> 2) {  // the same for the whole warp
+        case 0: u[0] = lo.x, u[1] = lo.y, u[2] = lo.z, u[3] = lo.w, u[4] = hi.x; break;
+        case 1: u[0] = lo.y, u[1] = lo.z, u[2] = lo.w, u[3] = hi.x, u[4] = hi.y; break;
+        case 2: u[0] = lo.z, u[1] = lo.w, u[2] = hi.x, u[3] = hi.y, u[4] = hi.z; break;
+        default: u[0] = lo.w, u[1] = hi.x, u[2] = hi.y, u[3] = hi.z, u[4] = hi.w; break;
+      }
 #pragma unroll
-      for (int i = 1; i < 4; ++i) u[i] = q[i];
-      u[4] = odd ? q[4] : 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = odd ? __funnelshift_r(u[i], u[i + 1], 16) : u[i];
+      for (int i = 0; i < 4; ++i) w[i] = (off & 2) ? __funnelshift_r(u[i], u[i + 1], 16) : u[i];
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -807,13 +852,13 @@ void align_operands(Matrix* x, Matrix* y, uint8_t* ws, cudaStream_t stream) {
     if (bytes == 0 || m->rows == 0 || m->cols == 0) continue;
     both.a[count++] = {static_cast<const uint16_t*>(m->p), reinterpret_cast<uint16_t*>(ws), m->ld, pad8(m->cols),
                        m->rows, m->cols};
-    most = std::max(most, static_cast<long long>(m->rows) * (pad8(m->cols) / 8));
+    most = std::max(most, static_cast<long long>(m->rows) * ((m->cols + 255) / 256));
     m->p = ws;
     m->ld = pad8(m->cols);
     ws += bytes;
   }
   if (count == 0) return;
-  align_rows_kernel<<<dim3(static_cast<unsigned>(std::min<long long>((most + 255) / 256, 152 * 16)), 1, count), 256,
+  align_rows_kernel<<<dim3(static_cast<unsigned>(std::min<long long>((most + 7) / 8, 152 * 16)), 1, count), 256,
                       0, stream>>>(both);
 }
 
@@ -941,11 +986,6 @@ cudaError_t launch_few(const Matrix& w, bool w_mn, const Matrix& x, FewProduct p
   return cudaLaunchKernelEx(&cfg, kern, mw, mx, p, flags);
 }
 
-bool few_rows(int m, int n) {
-  static const int most = std::getenv("FEW") ? std::atoi(std::getenv("FEW")) : 64;
-  return m <= most;
-}
-
 // D = A B^T over `depth`, with the epilogue e.  a: m x depth (or depth x m
 // where a_mn), b likewise; rows on 16-byte boundaries.
 template <typename T>
@@ -959,7 +999,7 @@ cudaError_t run_product(int m, int n, int depth, const Matrix& a, bool a_mn, con
     empty_product_kernel<T><<<static_cast<int>(std::min<long long>((all + 255) / 256, 4096)), 256, 0, stream>>>(p);
     return cudaGetLastError();
   }
-  if (few_rows(m, n) && !a_mn) {
+  if (m <= 128 && !a_mn) {
     const FewProduct f = {m, n, p.kb, 0, 1, e};
     return m <= 16   ? launch_few<T, 16>(b, b_mn, a, f, flags, stream)
            : m <= 32 ? launch_few<T, 32>(b, b_mn, a, f, flags, stream)
