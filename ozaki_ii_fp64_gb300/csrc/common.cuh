@@ -123,6 +123,14 @@ __device__ __forceinline__ uint64_t globaltimer() {
   return t;
 }
 
+// Launches that follow each other on a stream may overlap: a kernel launched
+// with launch_chained starts once every CTA of the one before has said
+// chain_next (or ended), does what needs no memory of others, and waits with
+// chain_wait, before its first access to global memory, until that kernel is
+// complete and its writes are visible.
+__device__ __forceinline__ void chain_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void chain_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ---------------------------------------------------------------- mbarrier
 __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count) : "memory");

@@ -178,6 +178,28 @@ struct LinearGradCall {
 size_t linear_backward_workspace(const LinearGradCall& call);
 cudaError_t launch_linear_backward(const LinearGradCall& call, cudaStream_t stream);
 
+// Launches a kernel that begins with chain_wait (common.cuh).  cluster: CTAs
+// of a cluster, 0 where the kernel itself says.
+template <typename... K, typename... A>
+cudaError_t launch_chained(void (*kern)(K...), dim3 grid, int threads, size_t smem, cudaStream_t stream, int cluster,
+                           A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 0 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<K>(args)...);
+}
+
 // Fill helpers.
 cudaError_t launch_zero_f64(double* C, int m, int n, long long ldc, cudaStream_t stream);
 cudaError_t launch_zero_s32(int32_t* C, int m, int n, long long ldc, cudaStream_t stream);

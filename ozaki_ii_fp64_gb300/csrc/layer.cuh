@@ -7,6 +7,8 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include "common.cuh"
+
 namespace ozemu {
 
 // Element types and activations, numbered as in the C ABI.
@@ -204,6 +206,8 @@ template <typename W>
 static __global__ void __launch_bounds__(1024) join_parts_kernel(const float* part, int used, int parts, int cols, W* out0,
                                                           W* out1) {
   __shared__ float red[32][33];
+  chain_next();
+  chain_wait();
   W* out = blockIdx.y == 0 ? out0 : out1;
   if (!out) return;
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5, j = blockIdx.x * 32 + tx;

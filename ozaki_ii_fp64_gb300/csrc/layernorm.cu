@@ -119,6 +119,8 @@ constexpr int cta_threads(int tpr) { return tpr < 128 ? 128 : tpr; }
 template <typename T, int VEC, int TPR, int NV>
 __global__ void __launch_bounds__(cta_threads(TPR)) norm_forward_kernel(const NormCall c, int vec) {
   __shared__ __align__(16) float red[2][32];
+  chain_next();
+  chain_wait();
   constexpr int kRows = cta_threads(TPR) / TPR;
   const int tid = threadIdx.x % TPR;
   const long long row = static_cast<long long>(blockIdx.x) * kRows + threadIdx.x / TPR;
@@ -357,11 +359,14 @@ __global__ void __launch_bounds__(RingCfg<TPR, EPT, false>::kThreads, RingCfg<TP
     ++issued;
   };
   if (threadIdx.x == 0) abort_word = 0;
+  chain_next();
   if (tid == 0) {
     for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
     fence_mbar_init();
+    chain_wait();
     for (long long row = first; issued < stages && row < c.rows; row += step) issue(row, issued);
   }
+  chain_wait();
   __syncthreads();
   int slot = 0, turn = 0;
   for (long long row = first; row < c.rows; row += step, ++turn) {
@@ -426,6 +431,8 @@ constexpr int kLong = 1024;
 template <typename T>
 __global__ void __launch_bounds__(kLong) norm_forward_long_kernel(const NormCall c) {
   __shared__ __align__(16) float red[2][32];
+  chain_next();
+  chain_wait();
   const bool f32 = c.param_type == kF32;
   for (long long row = blockIdx.x; row < c.rows; row += gridDim.x) {
     const T* x = static_cast<const T*>(c.x) + row * c.ldx;
@@ -517,11 +524,14 @@ __global__ void __launch_bounds__(RingCfg<TPR, EPT, true>::kThreads, RingCfg<TPR
     ++issued;
   };
   if (threadIdx.x == 0) abort_word = 0;
+  chain_next();
   if (tid == 0) {
     for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
     fence_mbar_init();
+    chain_wait();
     for (long long row = first; issued < stages && row < c.rows; row += step) issue(row, issued);
   }
+  chain_wait();
   __syncthreads();
   int slot = 0, turn = 0;
   float mean = 0.f, rstd = 0.f;
@@ -642,6 +652,8 @@ __global__ void __launch_bounds__(512) norm_backward_means_kernel(const NormGrad
                                                                   bool weight_vec) {
   constexpr int VEC = 16 / sizeof(T);
   __shared__ __align__(16) float2 red[2][32];
+  chain_next();
+  chain_wait();
   const bool f32 = c.param_type == kF32;
   int turn = 0;
   for (long long row = blockIdx.x; row < c.rows; row += gridDim.x, turn ^= 1) {
@@ -684,6 +696,8 @@ __global__ void __launch_bounds__(256) norm_backward_columns_kernel(const NormGr
                                                                     float* part, int parts, int chunk) {
   // Eight columns a thread, eight rows at a time.
   __shared__ float red[2][8][264];
+  chain_next();
+  chain_wait();
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5, col0 = blockIdx.x * 256;
   const bool f32 = c.param_type == kF32;
   float w[8], sw[8] = {}, sb[8] = {};
@@ -779,18 +793,16 @@ cudaError_t forward_vec(const NormCall& c, cudaStream_t stream) {
   const int vec = (aligned16(c.weight) ? 1 : 0) | (aligned16(c.bias) ? 2 : 0);
   const int span = VEC * NV;  // elements per thread
   if (c.cols <= 32 * span)
-    norm_forward_kernel<T, VEC, 32, NV><<<(c.rows + 3) / 4, 128, 0, stream>>>(c, vec);
-  else if (c.cols <= 128 * span)
-    norm_forward_kernel<T, VEC, 128, NV><<<c.rows, 128, 0, stream>>>(c, vec);
-  else if (c.cols <= 256 * span)
-    norm_forward_kernel<T, VEC, 256, NV><<<c.rows, 256, 0, stream>>>(c, vec);
-  else if (c.cols <= 512 * span)
-    norm_forward_kernel<T, VEC, 512, NV><<<c.rows, 512, 0, stream>>>(c, vec);
-  else if (c.cols <= 1024 * span)
-    norm_forward_kernel<T, VEC, 1024, NV><<<c.rows, 1024, 0, stream>>>(c, vec);
-  else
-    norm_forward_long_kernel<T><<<std::min(c.rows, 65536), kLong, 0, stream>>>(c);
-  return cudaGetLastError();
+    return launch_chained(norm_forward_kernel<T, VEC, 32, NV>, dim3((c.rows + 3) / 4), 128, 0, stream, 0, c, vec);
+  if (c.cols <= 128 * span)
+    return launch_chained(norm_forward_kernel<T, VEC, 128, NV>, dim3(c.rows), 128, 0, stream, 0, c, vec);
+  if (c.cols <= 256 * span)
+    return launch_chained(norm_forward_kernel<T, VEC, 256, NV>, dim3(c.rows), 256, 0, stream, 0, c, vec);
+  if (c.cols <= 512 * span)
+    return launch_chained(norm_forward_kernel<T, VEC, 512, NV>, dim3(c.rows), 512, 0, stream, 0, c, vec);
+  if (c.cols <= 1024 * span)
+    return launch_chained(norm_forward_kernel<T, VEC, 1024, NV>, dim3(c.rows), 1024, 0, stream, 0, c, vec);
+  return launch_chained(norm_forward_long_kernel<T>, dim3(std::min(c.rows, 65536)), kLong, 0, stream, 0, c);
 }
 
 // Slots that a ring of `bytes` holds for each of its groups, and so whether it
@@ -817,8 +829,8 @@ struct ForwardLaunch {
     auto kern = norm_forward_ring_kernel<T, W, TPR, EPT, kAligned>;
     error = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, R::kBytes);
     if (error != cudaSuccess) return true;
-    kern<<<ctas, R::kThreads, kFront + R::kGroups * stages * bytes, stream>>>(c, stages, 1.f / static_cast<float>(c.cols));
-    error = cudaGetLastError();
+    error = launch_chained(kern, dim3(ctas), R::kThreads, kFront + R::kGroups * stages * bytes, stream, 0, c, stages,
+                           1.f / static_cast<float>(c.cols));
     return true;
   }
   template <typename T, typename W, bool kAligned>
@@ -848,9 +860,8 @@ struct BackwardLaunch {
     used = std::min({(c.rows + R::kGroups - 1) / R::kGroups, R::kPerSm * kSms, parts});
     // The groups' column sums meet in the ring's memory.
     const int smem = std::max(kFront + R::kGroups * stages * slot, R::kGroups > 1 ? R::kGroups * TPR * EPT * 8 : 0);
-    kern<<<used, R::kThreads, smem, stream>>>(c, static_cast<float*>(c.ws), parts, stages,
-                                              1.f / static_cast<float>(c.cols));
-    error = cudaGetLastError();
+    error = launch_chained(kern, dim3(used), R::kThreads, smem, stream, 0, c, static_cast<float*>(c.ws), parts, stages,
+                           1.f / static_cast<float>(c.cols));
     return true;
   }
   template <typename T, typename W, bool kAligned>
@@ -861,14 +872,15 @@ struct BackwardLaunch {
   template <typename T>
   void two_passes(bool vec) {
     float2* means = reinterpret_cast<float2*>(static_cast<float*>(c.ws) + 2LL * parts * c.cols);
-    norm_backward_means_kernel<T><<<std::min(c.rows, 65536), 512, 0, stream>>>(c, means, vec, aligned16(c.weight));
+    launch_chained(norm_backward_means_kernel<T>, dim3(std::min(c.rows, 65536)), 512, 0, stream, 0, c, means, vec,
+                   aligned16(c.weight));
     const int across = (c.cols + 255) / 256;
     const int chunks = std::max(1, std::min({parts, 1216 / across, (c.rows + 7) / 8}));
     const int chunk = (c.rows + chunks - 1) / chunks;
     used = (c.rows + chunk - 1) / chunk;
     auto kern = vec ? norm_backward_columns_kernel<T, true> : norm_backward_columns_kernel<T, false>;
-    kern<<<dim3(across, used), 256, 0, stream>>>(c, means, static_cast<float*>(c.ws), parts, chunk);
-    error = cudaGetLastError();
+    error = launch_chained(kern, dim3(across, used), 256, 0, stream, 0, c, means, static_cast<float*>(c.ws), parts,
+                           chunk);
   }
 };
 
@@ -916,9 +928,8 @@ cudaError_t launch_layer_norm_backward(const NormGradCall& c, cudaStream_t strea
     const dim3 grid((c.cols + 31) / 32, 2);
     with_type(c.param_type, [&](auto w) {
       using W = decltype(w);
-      join_parts_kernel<W><<<grid, 1024, 0, stream>>>(static_cast<const float*>(c.ws), l.used, l.parts, c.cols,
-                                                      static_cast<W*>(c.dweight), static_cast<W*>(c.dbias));
-      return cudaSuccess;
+      return launch_chained(join_parts_kernel<W>, grid, 1024, 0, stream, 0, static_cast<const float*>(c.ws), l.used,
+                            l.parts, c.cols, static_cast<W*>(c.dweight), static_cast<W*>(c.dbias));
     });
   }
   return cudaGetLastError();

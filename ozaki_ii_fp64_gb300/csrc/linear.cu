@@ -369,6 +369,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_sync();
   tc_fence_after();
   const uint32_t tbase = *tmem_holder;
+  chain_next();
+  chain_wait();
 
   if (warp == 0) {
     if (lane == 0) {
@@ -573,6 +575,8 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tmem_holder;
+  chain_next();
+  chain_wait();
 
   if (warp == 0) {
     if (lane == 0) {
@@ -694,6 +698,8 @@ __global__ void __launch_bounds__(kFewThreads, 2)
 // out = act(bias) + r: the product of an empty reduction.
 template <typename T>
 __global__ void __launch_bounds__(256) empty_product_kernel(const Product p) {
+  chain_next();
+  chain_wait();
   const Epilogue& e = p.e;
   const long long all = static_cast<long long>(p.m) * p.n;
   for (long long i = blockIdx.x * 256LL + threadIdx.x; i < all; i += gridDim.x * 256LL) {
@@ -721,6 +727,8 @@ struct AlignPair {
   AlignArgs a[2];
 };
 __global__ void __launch_bounds__(256) align_rows_kernel(const __grid_constant__ AlignPair both) {
+  chain_next();
+  chain_wait();
   const AlignArgs& a = both.a[blockIdx.z];
   const int pieces = (a.cols + 7) / 8;
   const uintptr_t begin = reinterpret_cast<uintptr_t>(a.in);
@@ -766,6 +774,8 @@ __global__ void __launch_bounds__(256) slope_kernel(const T* dy, long long lddy,
                                                     long long lddz, float* part, T* db, int m, int n, int chunk,
                                                     int vec) {
   __shared__ float red[8][264];
+  chain_next();
+  chain_wait();
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
   const int col = blockIdx.x * 256 + tx * 8, left = n - col;
   float s[8] = {};
@@ -858,8 +868,8 @@ void align_operands(Matrix* x, Matrix* y, uint8_t* ws, cudaStream_t stream) {
     ws += bytes;
   }
   if (count == 0) return;
-  align_rows_kernel<<<dim3(static_cast<unsigned>(std::min<long long>((most + 7) / 8, 152 * 16)), 1, count), 256,
-                      0, stream>>>(both);
+  launch_chained(align_rows_kernel, dim3(static_cast<unsigned>(std::min<long long>((most + 7) / 8, 152 * 16)), 1, count),
+                 256, 0, stream, 0, both);
 }
 
 // Map of an operand read in blocks of `box` rows of 64 elements; what lies
@@ -945,8 +955,8 @@ cudaError_t launch_pairs(const CUtensorMap& ma, const CUtensorMap& mb, Product p
   p.tiles_m = (p.m + 255) / 256;
   p.tiles_n = (p.n + p.bn - 1) / p.bn;
   const int tiles = p.tiles_m * p.tiles_n;
-  product_pair_kernel<T><<<2 * std::min(tiles, pairs), kThreads, kPairSmem, stream>>>(ma, mb, p, flags);
-  return cudaGetLastError();
+  return launch_chained(product_pair_kernel<T>, dim3(2 * std::min(tiles, pairs)), kThreads, kPairSmem, stream, 0, ma,
+                        mb, p, flags);
 }
 
 template <typename T, int NT>
@@ -971,19 +981,8 @@ cudaError_t launch_few(const Matrix& w, bool w_mn, const Matrix& x, FewProduct p
   // Two CTAs on each SM, and at least four blocks of the reduction for each.
   p.split = 1;
   while (p.split < kMaxSplit && 2 * p.split * across * down <= 304 && p.kb >= 8 * p.split) p.split *= 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(across * p.split, down, 1);
-  cfg.blockDim = dim3(kFewThreads, 1, 1);
-  cfg.dynamicSmemBytes = FewCfg<NT>::kSmem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = p.split;
-  attr.val.clusterDim.y = 1;
-  attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, mw, mx, p, flags);
+  return launch_chained(kern, dim3(across * p.split, down, 1), kFewThreads, FewCfg<NT>::kSmem, stream, p.split, mw, mx,
+                        p, flags);
 }
 
 // D = A B^T over `depth`, with the epilogue e.  a: m x depth (or depth x m
@@ -996,8 +995,8 @@ cudaError_t run_product(int m, int n, int depth, const Matrix& a, bool a_mn, con
   const Product p = {m, n, (depth + kBlock - 1) / kBlock, a_mn, b_mn, 0, 0, 0, e};
   if (depth == 0) {
     const long long all = static_cast<long long>(m) * n;
-    empty_product_kernel<T><<<static_cast<int>(std::min<long long>((all + 255) / 256, 4096)), 256, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch_chained(empty_product_kernel<T>, dim3(static_cast<unsigned>(std::min<long long>((all + 255) / 256, 4096))),
+                          256, 0, stream, 0, p);
   }
   if (m <= 128 && !a_mn) {
     const FewProduct f = {m, n, p.kb, 0, 1, e};
@@ -1057,11 +1056,12 @@ void run_slope(const LinearGradCall& c, const BackwardPlan& p, T* dz, float* par
                   (kAct != kActNone && rows_aligned(c.pre, c.ldpre, c.m) ? 2 : 0);
   T* db = static_cast<T*>(c.db);
   const bool whole = p.chunks == 1;
-  slope_kernel<T, kAct><<<dim3((c.n + 255) / 256, p.chunks), 256, 0, stream>>>(
-      static_cast<const T*>(c.dy), c.lddy, static_cast<const T*>(c.pre), c.ldpre, dz, pad8(c.n),
-      db && !whole ? part : nullptr, whole ? db : nullptr, c.m, c.n, p.chunk, vec);
+  launch_chained(slope_kernel<T, kAct>, dim3((c.n + 255) / 256, p.chunks), 256, 0, stream, 0,
+                 static_cast<const T*>(c.dy), c.lddy, static_cast<const T*>(c.pre), c.ldpre, dz, pad8(c.n),
+                 db && !whole ? part : nullptr, whole ? db : nullptr, c.m, c.n, p.chunk, vec);
   if (db && !whole)
-    join_parts_kernel<T><<<(c.n + 31) / 32, 1024, 0, stream>>>(part, p.chunks, p.chunks, c.n, db, nullptr);
+    launch_chained(join_parts_kernel<T>, dim3((c.n + 31) / 32), 1024, 0, stream, 0, part, p.chunks, p.chunks, c.n, db,
+                   nullptr);
 }
 
 template <typename T>
@@ -1088,7 +1088,8 @@ cudaError_t linear_backward_t(const LinearGradCall& c, cudaStream_t stream) {
     Matrix none = {nullptr, 0, 0, 0};
     align_operands(c.dw ? &x : &none, c.dx ? &w : &none, ws + plan.dz + plan.part, stream);
   } else if (c.db && c.n > 0) {
-    join_parts_kernel<T><<<(c.n + 31) / 32, 1024, 0, stream>>>(nullptr, 0, 0, c.n, static_cast<T*>(c.db), nullptr);
+    launch_chained(join_parts_kernel<T>, dim3((c.n + 31) / 32), 1024, 0, stream, 0, nullptr, 0, 0, c.n,
+                   static_cast<T*>(c.db), nullptr);
   }
   Epilogue e = {nullptr, nullptr, 0, nullptr, 0, nullptr, 0, kActNone, 0};
   cudaError_t s = cudaGetLastError();
