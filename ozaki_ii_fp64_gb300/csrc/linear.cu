@@ -234,6 +234,11 @@ __device__ __forceinline__ void write_rows(uint8_t* stage, T* out, long long ldo
 // MMAs (4 of K = 16 per 64-element stage), warps 2-9 take finished
 // accumulators out of TMEM; two accumulators alternate, so the next tile's
 // MMAs run under this tile's epilogue.
+//
+// Few tiles with a long reduction: `split` (2 or 4) pairs of a cluster share a
+// tile, each with a part of the reduction.  Each CTA leaves its fp32 sums in
+// the ring's shared memory, and the pairs take alternate 64-column chunks,
+// adding the parts up through distributed shared memory in order.
 // ---------------------------------------------------------------------------
 constexpr int kRing = 192 * 1024;  // stages of two blocks of A and one or two of B: 8 or 6
 constexpr int kMaxStages = 8;
@@ -245,6 +250,7 @@ struct Product {
   int kb;          // 64-element blocks of the reduction
   int a_mn, b_mn;  // the operand's reduction runs down its rows
   int bn;          // columns of a tile
+  int split;       // pairs that share a tile's reduction
   int tiles_m, tiles_n;
   Epilogue e;
 };
@@ -257,21 +263,32 @@ __device__ __forceinline__ void tile_of(int t, const Product& p, int& tm, int& t
   tn = (t % group) / gm;
 }
 
-// One warp's 32 rows x 64 columns of accumulators, at TMEM address `taddr`,
-// through the epilogue; `done` is called once they have been read for the last
-// time.  Half of the columns at a time, in a loop: the code that a short
-// product has to fetch first is half as long.
+// 16 bytes of shared memory of a CTA of the cluster.
+__device__ __forceinline__ float4 load_cluster16(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr));
+  return v;
+}
+
+// The sums that a pair of a split tile leaves: 128 rows of up to 256 fp32, the
+// 16-byte piece c of row r at piece c ^ (r % 32), so that a warp's rows meet
+// in no bank.
+__device__ __forceinline__ uint32_t part_piece(int r, int c) {
+  return static_cast<uint32_t>(r * 1024 + ((c ^ (r & 31)) << 4));
+}
+
+// One warp's 32 rows x 64 columns of accumulators through the epilogue: half
+// of the columns at a time, in a loop, from source(h, z) (the code that a
+// short product has to fetch first is half as long).
 template <typename T, typename F>
-__device__ __forceinline__ void finish_rows(uint32_t taddr, const uint4 (&res)[8], const Epilogue& e, uint8_t* stage,
-                                            int row0, int col0, int m, int n, F done) {
+__device__ __forceinline__ void finish_rows(F source, const uint4 (&res)[8], const Epilogue& e, uint8_t* stage,
+                                            int row0, int col0, int m, int n) {
   const int lane = threadIdx.x & 31;
   uint4* mine = reinterpret_cast<uint4*>(stage + lane * 128);
-  auto take = [&](int h, float (&z)[32]) {
-    uint32_t u[32];
-    tmem_ld32(taddr + 32 * h, u);
-    tmem_wait_ld();
-#pragma unroll
-    for (int i = 0; i < 32; ++i) z[i] = __uint_as_float(u[i]);
+  auto take = [&](int h, bool last, float (&z)[32]) {
+    source(h, last, z);
     if (e.bias) {
 #pragma unroll
       for (int q = 0; q < 32; q += 8) {
@@ -286,7 +303,7 @@ __device__ __forceinline__ void finish_rows(uint32_t taddr, const uint4 (&res)[8
 #pragma unroll 1
     for (int h = 0; h < 2; ++h) {
       float z[32];
-      take(h, z);
+      take(h, false, z);
 #pragma unroll
       for (int c = 0; c < 4; ++c) mine[(4 * h + c) ^ (lane & 7)] = pack16<T>(z + 8 * c);
     }
@@ -301,8 +318,7 @@ __device__ __forceinline__ void finish_rows(uint32_t taddr, const uint4 (&res)[8
 #pragma unroll 1
   for (int h = 0; h < 2; ++h) {
     float z[32];
-    take(h, z);
-    if (h == 1) done();
+    take(h, h == 1, z);
     activate_all(z, e.act);
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
@@ -322,7 +338,7 @@ __device__ __forceinline__ void finish_rows(uint32_t taddr, const uint4 (&res)[8
 }
 
 template <typename T>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     product_pair_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
                         const __grid_constant__ Product p, uint32_t* flags) {
   extern __shared__ uint8_t smem_raw[];
@@ -337,9 +353,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   volatile int* abort_word = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = static_cast<int>(cluster_rank());
-  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  const int place = static_cast<int>(cluster_rank()), rank = place & 1, lead = place & ~1;
+  const uint16_t both_ctas = static_cast<uint16_t>(0x3 << lead);
   const int total = p.tiles_m * p.tiles_n;
+  // A pair walks the tiles, or takes its part of one tile's reduction.
+  const int pair = blockIdx.x / (2 * p.split), npairs = p.split > 1 ? total : gridDim.x >> 1;
+  const int per = (p.kb + p.split - 1) / p.split;
+  const int kb0 = min((place >> 1) * per, p.kb), kb1 = min(kb0 + per, p.kb);
   // B's BN / 2 rows of this CTA, in whole blocks (a part block's last rows
   // are loaded and not used).
   const int b_blocks = p.bn > 128 ? 2 : 1;
@@ -374,7 +394,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     if (lane == 0) {
-      const uint32_t bar0 = mapa_shared(&full[0], 0);
+      const uint32_t bar0 = mapa_shared(&full[0], lead);
       int s = 0;
       uint32_t phase = 1;
       bool ok = true;
@@ -382,7 +402,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         int tm, tn;
         tile_of(t, p, tm, tn);
         const int i0 = tm * 256 + rank * 128, j0 = tn * p.bn + rank * (p.bn / 2);
-        for (int kb = 0; kb < p.kb; ++kb) {
+        for (int kb = kb0; kb < kb1; ++kb) {
           if (!mbar_wait(&empty[s], phase, abort_word, flags)) {
             ok = false;
             break;
@@ -431,7 +451,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (use > 0 && !mbar_wait(&tempty[buf], (use - 1) & 1, abort_word, flags)) break;
         tc_fence_after();
         const uint32_t d = tbase + static_cast<uint32_t>(buf * 256);
-        for (int kb = 0; kb < p.kb; ++kb) {
+        for (int kb = kb0; kb < kb1; ++kb) {
           if (!known && !mbar_wait(&full[s], phase, abort_word, flags)) {
             ok = false;
             break;
@@ -440,17 +460,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks)
             mma_f16_pair(d, smem_desc_sw128(a_lo + at + ks * a_step), smem_desc_sw128(b_lo + at + ks * b_step), idesc,
-                         ks != 0 ? 1u : (kb != 0 ? 1u : 0u));
-          tc_commit_pair_multicast(&empty[s], 0x3);
+                         ks != 0 ? 1u : (kb != kb0 ? 1u : 0u));
+          tc_commit_pair_multicast(&empty[s], both_ctas);
           if (++s == stages) {
             s = 0;
             phase ^= 1;
           }
           known = mbar_test_wait(&full[s], phase);
         }
-        if (ok) tc_commit_pair_multicast(&tfull[buf], 0x3);
+        if (ok) tc_commit_pair_multicast(&tfull[buf], both_ctas);
       }
-      tc_commit_pair_multicast(mma_done, 0x1);
+      tc_commit_pair_multicast(mma_done, static_cast<uint16_t>(1 << lead));
       drain_wait(mma_done, 0, flags);
       if (!ok) settle_after_abort();
     }
@@ -470,6 +490,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // Columns of the tile that this warp has to take: none past D's edge.
       const int cols = row0 < p.m ? min(p.bn, p.n - tn * p.bn) : 0;
       const uint32_t tcol = tbase + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(buf * 256);
+      if (p.split > 1) {  // leave the sums; the cluster joins them below
+        if (!warp_wait(&tfull[buf], use & 1, abort_word, flags)) break;
+        tc_fence_after();
+        const int r = quarter * 32 + lane;
+        for (int c = half * 32; c < cols; c += 64) {
+          uint32_t u[32];
+          if (kb0 < kb1) {
+            tmem_ld32(tcol + c, u);
+            tmem_wait_ld();
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) u[i] = 0;
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<uint4*>(smem + part_piece(r, c / 4 + i)) =
+                make_uint4(u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);
+        }
+        break;  // one tile
+      }
       bool waited = false, live = true;
 #pragma unroll 1
       for (int c = half * 64; c < cols; c += 128) {
@@ -483,18 +523,82 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           tc_fence_after();
           waited = true;
         }
-        finish_rows<T>(tcol + c, res, e, stage, row0, col0, p.m, p.n, [&] {
-          if (c + 128 >= cols) {  // this warp's last columns of the tile
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(&tempty[buf], 0));
-          }
-        });
+        finish_rows<T>(
+            [&](int h, bool last, float(&z)[32]) {
+              uint32_t u[32];
+              tmem_ld32(tcol + c + 32 * h, u);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) z[i] = __uint_as_float(u[i]);
+              if (last && c + 128 >= cols) {  // this warp's last columns of the tile
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(&tempty[buf], lead));
+              }
+            },
+            res, e, stage, row0, col0, p.m, p.n);
       }
       if (!live) break;
       if (half * 64 >= cols) {  // nothing to take: still let the buffer go, after the tile is done
         if (!warp_wait(&tfull[buf], use & 1, abort_word, flags)) break;
-        if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(&tempty[buf], 0));
+        if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(&tempty[buf], lead));
+      }
+    }
+  }
+
+  if (p.split > 1) {
+    __syncthreads();
+    cluster_sync();  // every pair's sums are in its shared memory
+    if (warp >= 2) {
+      // Sixteen rows a warp, a row's 64 columns to half a warp: shared memory
+      // of another CTA is read in contiguous runs, and so is global memory.
+      const Epilogue& e = p.e;
+      int tm, tn;
+      tile_of(pair, p, tm, tn);
+      const int row0 = (warp - 2) * 16 + (lane >> 4), cols = min(p.bn, p.n - tn * p.bn);
+      const long long grow0 = tm * 256 + rank * 128;
+      for (int c = (place >> 1) * 64; c < cols; c += 64 * p.split) {
+        const int piece = c / 4 + (lane & 15), col = tn * p.bn + c + (lane & 15) * 4, left = p.n - col;
+        if (left <= 0) continue;
+        float b[4] = {0.f, 0.f, 0.f, 0.f};
+        if (e.bias) load4(static_cast<const T*>(e.bias) + col, left, e.vec & 1, b);
+#pragma unroll 1
+        for (int r0 = row0; r0 < row0 + 16; r0 += 8) {
+          float z[4][4] = {};
+          for (int q = 0; q < p.split; q += 2) {
+            float4 v[2][4];  // all loads before the first sum
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                v[k][i] = load_cluster16(mapa_shared(smem, 2 * (q + k) + rank) + part_piece(r0 + 2 * i, piece));
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                z[i][0] += v[k][i].x;
+                z[i][1] += v[k][i].y;
+                z[i][2] += v[k][i].z;
+                z[i][3] += v[k][i].w;
+              }
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const long long row = grow0 + r0 + 2 * i;
+            if (row >= p.m) continue;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) z[i][k] += b[k];
+            if (e.pre) store4(static_cast<T*>(e.pre) + row * e.ldpre + col, z[i], left, (e.vec & 4) != 0);
+            activate_all(z[i], e.act);
+            if (e.res) {
+              float r[4];
+              load4(static_cast<const T*>(e.res) + row * e.ldr + col, left, (e.vec & 2) != 0, r);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) z[i][k] += r[k];
+            }
+            store4(static_cast<T*>(e.out) + row * e.ldo + col, z[i], left, (e.vec & 8) != 0);
+          }
+        }
       }
     }
   }
@@ -659,14 +763,19 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     if (left <= 0) continue;
     const float* mine = reinterpret_cast<const float*>(smem) + i * 128 + jj;
     float z[4] = {};
-#pragma unroll 4
-    for (int s = 0; s < p.split; ++s) {
-      float v[4];
-      asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                   : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
-                   : "r"(mapa_shared(mine, s)));
+    for (int s0 = 0; s0 < p.split; s0 += 8) {
+      float4 u[8];  // all loads before the first sum
 #pragma unroll
-      for (int q = 0; q < 4; ++q) z[q] += v[q];
+      for (int s = 0; s < 8; ++s)
+        if (s0 + s < p.split) u[s] = load_cluster16(mapa_shared(mine, s0 + s));
+#pragma unroll
+      for (int s = 0; s < 8; ++s)
+        if (s0 + s < p.split) {
+          z[0] += u[s].x;
+          z[1] += u[s].y;
+          z[2] += u[s].z;
+          z[3] += u[s].w;
+        }
     }
     const long long row = i0 + i;
     float v[4];
@@ -766,22 +875,26 @@ __global__ void __launch_bounds__(256) align_rows_kernel(const __grid_constant__
 }
 
 // dz = dy act'(pre) (where dz is given) and, per chunk of rows, the column
-// sums of the unrounded dz (to part, or to db where there is one chunk).  A CTA takes 256 columns,
-// eight to a thread, and `chunk` rows, eight at a time; the eight partial
-// sums of a column are joined in shared memory in a fixed order.
-template <typename T, int kAct>
+// sums of the unrounded dz (to part, or to db where there is one chunk).  A
+// CTA takes 8 TX columns, eight to a thread, and `chunk` rows, 256 / TX at a
+// time; the partial sums of a column are joined in shared memory in a fixed
+// order.  TX = 4 for few rows (64 at a time, so that one or two turns read
+// them all), else 32.
+template <typename T, int kAct, int TX>
 __global__ void __launch_bounds__(256) slope_kernel(const T* dy, long long lddy, const T* pre, long long ldpre, T* dz,
                                                     long long lddz, float* part, T* db, int m, int n, int chunk,
                                                     int vec) {
-  __shared__ float red[8][264];
+  constexpr int TY = 256 / TX, kCols = 8 * TX;
+  __shared__ float red[TY][kCols + 8];
   chain_next();
   chain_wait();
-  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-  const int col = blockIdx.x * 256 + tx * 8, left = n - col;
+  const int tx = threadIdx.x % TX, ty = threadIdx.x / TX;
+  const int col = blockIdx.x * kCols + tx * 8, left = n - col;
   float s[8] = {};
   const long long end = min(static_cast<long long>(m), (blockIdx.y + 1LL) * chunk);
   if (left > 0) {
-    for (long long i = static_cast<long long>(blockIdx.y) * chunk + ty; i < end; i += 8) {
+#pragma unroll 1
+    for (long long i = static_cast<long long>(blockIdx.y) * chunk + ty; i < end; i += TY) {
       float v[8];
       load8(dy + i * lddy + col, left, vec & 1, v);
       if constexpr (kAct != kActNone) {
@@ -801,11 +914,11 @@ __global__ void __launch_bounds__(256) slope_kernel(const T* dy, long long lddy,
 #pragma unroll
   for (int q = 0; q < 8; ++q) red[ty][tx * 8 + q] = s[q];
   __syncthreads();
-  const int j = blockIdx.x * 256 + threadIdx.x;
-  if (j < n) {
+  const int j = blockIdx.x * kCols + threadIdx.x;
+  if (threadIdx.x < kCols && j < n) {
     float sum = 0.f;
-#pragma unroll
-    for (int y = 0; y < 8; ++y) sum += red[y][threadIdx.x];
+#pragma unroll 8
+    for (int y = 0; y < TY; ++y) sum += red[y][threadIdx.x];
     if (db)  // one chunk: the sum is whole
       db[j] = from_float<T>(sum);
     else
@@ -889,74 +1002,84 @@ bool make_map(CUtensorMap* map, const Matrix& x, bool bf16, int box) {
 
 constexpr int kMaxDev = 64;
 
-// CTA pairs that can be resident at once (a persistent grid must not exceed
-// them); sets the kernel's shared-memory size on the way.
+// Tiles that can be worked on at once by clusters of one, two or four CTA
+// pairs (a persistent grid must not exceed the first; the GPCs leave some SMs
+// out of the larger clusters: 76, 36 and 15 on this GPU); sets the kernel's
+// shared-memory size on the way.
+struct Resident {
+  int tiles[3] = {0, 0, 0};
+};
 template <typename T>
-cudaError_t resident_pairs(int* pairs) {
-  static int known[kMaxDev] = {0};
+cudaError_t resident_clusters(Resident* out) {
+  static Resident known[kMaxDev];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= kMaxDev) return cudaErrorInvalidDevice;
-  if (known[dev] == 0) {
+  if (known[dev].tiles[0] == 0) {
     auto kern = product_pair_kernel<T>;
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2, 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = kPairSmem;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = 2;
-    attr.val.clusterDim.y = 1;
-    attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    int n = 0;
-    e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
-    if (e != cudaSuccess) return e;
-    if (n < 1) return cudaErrorInvalidConfiguration;
-    known[dev] = n;
+    Resident r;
+    for (int i = 2; i >= 0; --i) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(2 << i, 1, 1);
+      cfg.blockDim = dim3(kThreads, 1, 1);
+      cfg.dynamicSmemBytes = kPairSmem;
+      cudaLaunchAttribute attr;
+      attr.id = cudaLaunchAttributeClusterDimension;
+      attr.val.clusterDim.x = 2 << i;
+      attr.val.clusterDim.y = 1;
+      attr.val.clusterDim.z = 1;
+      cfg.attrs = &attr;
+      cfg.numAttrs = 1;
+      e = cudaOccupancyMaxActiveClusters(&r.tiles[i], kern, &cfg);
+      if (e != cudaSuccess) return e;
+    }
+    if (r.tiles[0] < 1) return cudaErrorInvalidConfiguration;
+    known[dev] = r;
   }
-  *pairs = known[dev];
+  *out = known[dev];
   return cudaSuccess;
 }
 
-// Columns of a tile: the width whose tiles, in rounds over the pairs, take the
-// least time.  A 64-element block of the reduction takes a pair 2 BN clocks at
-// the tensor rate, and each CTA about 136 clocks for each 8 KB block that it
-// loads (60 bytes a clock from L2); a tile's start and end cost
-// about as much as 4 blocks of the widest.  An MN-major B comes in whole
-// blocks of 64 columns for each CTA.
-int tile_width(int m, int n, int kb, bool b_mn, int pairs) {
-  long long best = 0;
-  int width = 256;
-  for (int bn = 256; bn >= 64; bn -= b_mn ? 128 : 64) {
-    const long long tiles = static_cast<long long>((m + 255) / 256) * ((n + bn - 1) / bn);
-    const long long rounds = (tiles + pairs - 1) / pairs;
-    const int block = std::max(2 * bn, 136 * (bn > 128 ? 4 : 3));
-    const long long cost = rounds * (static_cast<long long>(kb) * block + 4 * bn) + 4 * bn;
-    if (best == 0 || cost < best) {
-      best = cost;
-      width = bn;
+// The tiling of a product: the columns of a tile, and the pairs that share a
+// tile's reduction, whose estimated time in clocks is least.  Measured at
+// 2 GHz on 256-row tiles: a 64-element block of the reduction takes 0.30 us
+// at 256 and 192 columns and 0.27 us at 128 and 64 (a CTA's loads, not the
+// MMAs, which would take 2 BN clocks); joining a split tile's sums takes 4.5 us
+// at 256 columns and 3 us at 128.  2048 x 8192 -> 512: 40 us unsplit, 27 us by
+// two pairs, 18 us by four.  An MN-major B comes in whole blocks of 64 columns
+// for each CTA.
+struct Tiling {
+  int bn, split;
+};
+Tiling tiling(int m, int n, int kb, bool b_mn, const Resident& resident) {
+  long long best = -1;
+  Tiling t = {256, 1};
+  for (int bn = 256; bn >= 64; bn -= b_mn ? 128 : 64)
+    for (int i = 0; i < 3 && (64 << i) <= bn && resident.tiles[i] > 0; ++i) {
+      const int split = 1 << i;
+      const long long tiles = static_cast<long long>((m + 255) / 256) * ((n + bn - 1) / bn);
+      const long long rounds = (tiles + resident.tiles[i] - 1) / resident.tiles[i];
+      const long long round = static_cast<long long>((kb + split - 1) / split) * (bn > 128 ? 600 : 540) + 4 * bn;
+      const long long cost = rounds * (round + (split > 1 ? 2500 + 25 * bn : 0)) + 4 * bn;
+      if (best < 0 || cost < best) {
+        best = cost;
+        t = {bn, split};
+      }
     }
-  }
-  return width;
+  return t;
 }
 
 template <typename T>
-cudaError_t launch_pairs(const CUtensorMap& ma, const CUtensorMap& mb, Product p, uint32_t* flags,
+cudaError_t launch_pairs(const CUtensorMap& ma, const CUtensorMap& mb, Product p, int pairs, uint32_t* flags,
                          cudaStream_t stream) {
-  int pairs = 0;
-  const cudaError_t e = resident_pairs<T>(&pairs);
-  if (e != cudaSuccess) return e;
-  p.bn = tile_width(p.m, p.n, p.kb, p.b_mn != 0, pairs);
   p.tiles_m = (p.m + 255) / 256;
   p.tiles_n = (p.n + p.bn - 1) / p.bn;
   const int tiles = p.tiles_m * p.tiles_n;
-  return launch_chained(product_pair_kernel<T>, dim3(2 * std::min(tiles, pairs)), kThreads, kPairSmem, stream, 0, ma,
-                        mb, p, flags);
+  return launch_chained(product_pair_kernel<T>, dim3(2 * (p.split > 1 ? tiles * p.split : std::min(tiles, pairs))),
+                        kThreads, kPairSmem, stream, 2 * p.split, ma, mb, p, flags);
 }
 
 template <typename T, int NT>
@@ -980,7 +1103,8 @@ cudaError_t launch_few(const Matrix& w, bool w_mn, const Matrix& x, FewProduct p
   p.w_mn = w_mn;
   // Two CTAs on each SM, and at least four blocks of the reduction for each.
   p.split = 1;
-  while (p.split < kMaxSplit && 2 * p.split * across * down <= 304 && p.kb >= 8 * p.split) p.split *= 2;
+  while (p.split < (NT > 32 ? kMaxSplit / 2 : kMaxSplit) && 2 * p.split * across * down <= 304 && p.kb >= 8 * p.split)
+    p.split *= 2;
   return launch_chained(kern, dim3(across * p.split, down, 1), kFewThreads, FewCfg<NT>::kSmem, stream, p.split, mw, mx,
                         p, flags);
 }
@@ -992,27 +1116,37 @@ cudaError_t run_product(int m, int n, int depth, const Matrix& a, bool a_mn, con
                         uint32_t* flags, cudaStream_t stream) {
   e.vec = (e.bias && rows_aligned(e.bias, 0, 1) ? 1 : 0) | (e.res && rows_aligned(e.res, e.ldr, m) ? 2 : 0) |
           (e.pre && rows_aligned(e.pre, e.ldpre, m) ? 4 : 0) | (rows_aligned(e.out, e.ldo, m) ? 8 : 0);
-  const Product p = {m, n, (depth + kBlock - 1) / kBlock, a_mn, b_mn, 0, 0, 0, e};
+  Product p = {m, n, (depth + kBlock - 1) / kBlock, a_mn, b_mn, 0, 1, 0, 0, e};
   if (depth == 0) {
     const long long all = static_cast<long long>(m) * n;
     return launch_chained(empty_product_kernel<T>, dim3(static_cast<unsigned>(std::min<long long>((all + 255) / 256, 4096))),
                           256, 0, stream, 0, p);
   }
-  if (m <= 128 && !a_mn) {
+  // Up to 128 rows, and up to 76 tiles of 128 x 128 with a reduction worth
+  // sharing, go to the kernel for few rows: 128 rows of 4096 -> 4096 take it
+  // 15.5 us (pairs 18), 256 rows of 8192 -> 1024 15.7 (19.5); but 256 rows of
+  // 4096 -> 16384 41.7 (30).
+  const long long squares = static_cast<long long>((m + 127) / 128) * ((n + 127) / 128);
+  if (!a_mn && (m <= 128 || (squares <= 76 && p.kb >= 32))) {
     const FewProduct f = {m, n, p.kb, 0, 1, e};
     return m <= 16   ? launch_few<T, 16>(b, b_mn, a, f, flags, stream)
            : m <= 32 ? launch_few<T, 32>(b, b_mn, a, f, flags, stream)
            : m <= 64 ? launch_few<T, 64>(b, b_mn, a, f, flags, stream)
                      : launch_few<T, 128>(b, b_mn, a, f, flags, stream);
   }
-  int pairs = 0;
-  cudaError_t s = resident_pairs<T>(&pairs);
+  Resident resident;
+  const cudaError_t s = resident_clusters<T>(&resident);
   if (s != cudaSuccess) return s;
-  const int bn = tile_width(m, n, p.kb, b_mn, pairs);
+  const Tiling t = tiling(m, n, p.kb, b_mn, resident);
+  p.bn = t.bn;
+  p.split = t.split;
+  // Operand tiles of 128 rows come as one box where the reduction runs along
+  // them, as boxes of 64 x 64 where it runs down.
   CUtensorMap ma, mb;
-  if (!make_map(&ma, a, Pair<T>::kBf16, a_mn ? kBlock : 128) || !make_map(&mb, b, Pair<T>::kBf16, b_mn ? kBlock : bn > 128 ? 128 : 64))
+  if (!make_map(&ma, a, Pair<T>::kBf16, a_mn ? kBlock : 2 * kBlock) ||
+      !make_map(&mb, b, Pair<T>::kBf16, b_mn || t.bn <= 128 ? kBlock : 2 * kBlock))
     return cudaErrorInvalidValue;
-  return launch_pairs<T>(ma, mb, p, flags, stream);
+  return launch_pairs<T>(ma, mb, p, resident.tiles[0], flags, stream);
 }
 
 template <typename T>
@@ -1025,8 +1159,9 @@ cudaError_t linear_t(const LinearCall& c, cudaStream_t stream) {
 
 // Row chunks of the slope pass: one where that is quick, else enough CTAs to
 // fill the GPU.
+constexpr int kFewSlopeRows = 256;
 int slope_chunk(int m, int n) {
-  if (m <= 128) return 128;
+  if (m <= kFewSlopeRows) return kFewSlopeRows;
   const int across = (n + 255) / 256;
   const int chunks = std::max(1, std::min(256, 1216 / across));
   return std::max(32, ((m + chunks - 1) / chunks + 7) / 8 * 8);
@@ -1056,9 +1191,11 @@ void run_slope(const LinearGradCall& c, const BackwardPlan& p, T* dz, float* par
                   (kAct != kActNone && rows_aligned(c.pre, c.ldpre, c.m) ? 2 : 0);
   T* db = static_cast<T*>(c.db);
   const bool whole = p.chunks == 1;
-  launch_chained(slope_kernel<T, kAct>, dim3((c.n + 255) / 256, p.chunks), 256, 0, stream, 0,
-                 static_cast<const T*>(c.dy), c.lddy, static_cast<const T*>(c.pre), c.ldpre, dz, pad8(c.n),
-                 db && !whole ? part : nullptr, whole ? db : nullptr, c.m, c.n, p.chunk, vec);
+  const int tx = c.m <= kFewSlopeRows ? 4 : 32;
+  launch_chained(tx == 4 ? slope_kernel<T, kAct, 4> : slope_kernel<T, kAct, 32>,
+                 dim3((c.n + 8 * tx - 1) / (8 * tx), p.chunks), 256, 0, stream, 0, static_cast<const T*>(c.dy), c.lddy,
+                 static_cast<const T*>(c.pre), c.ldpre, dz, pad8(c.n), db && !whole ? part : nullptr,
+                 whole ? db : nullptr, c.m, c.n, p.chunk, vec);
   if (db && !whole)
     launch_chained(join_parts_kernel<T>, dim3((c.n + 31) / 32), 1024, 0, stream, 0, part, p.chunks, p.chunks, c.n, db,
                    nullptr);

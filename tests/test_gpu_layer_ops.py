@@ -63,6 +63,21 @@ def test_linear_shapes(oz, shape, dtype):
     assert worst(y, ref, tol) <= 1
 
 
+# Small outputs of long reductions, which several CTAs share; uneven shares, shares of nothing, edges on both sides.
+@pytest.mark.parametrize("m, k, n", [(200, 8192, 136), (513, 4100, 300), (150, 20000, 64), (129, 577, 65), (640, 3000, 256),
+                                     (256, 16384, 1024), (100, 9000, 130), (20, 30000, 24), (300, 2000, 2051)])
+def test_linear_long_reductions(oz, m, k, n):
+    x, w = rnd(m, k, BF16, 101), rnd(n, k, BF16, 102, k ** -0.5)
+    b, r = vec(n, BF16, 103), rnd(m, n, BF16, 104)
+    y, pre = oz.linear(x, w, b, r, activation="silu", save_pre=True)
+    ref, tol, z, tolz = linear64(x, w, b, r, "silu")
+    assert worst(y, ref, tol) <= 1 and worst(pre, z, tolz) <= 1
+    # The weight gradient's reduction runs over the rows: here k of them.
+    dy, x2, w2 = rnd(k, n, BF16, 105, 0.1), rnd(k, m, BF16, 106), rnd(n, m, BF16, 107, 0.1)
+    for g, v, e in zip(oz.linear_backward(dy, x2, w2), *linear_backward64(dy, x2, w2)):
+        assert worst(g, v, e) <= 1
+
+
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("m", [1, 5, 200])
 def test_linear_activations(oz, act, m):
