@@ -86,15 +86,21 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
+// Barrier of the TPR threads of a row, one of the CTA's groups of that many.
+template <int TPR>
+__device__ __forceinline__ void row_barrier() {
+  asm volatile("bar.sync %0, %1;" ::"r"(static_cast<int>(threadIdx.x) / TPR + 1), "n"(TPR) : "memory");
+}
+
 // Sum over the TPR threads of a row.  TPR = 32: one warp, no barrier.  Else
-// the whole CTA; `red` (one word per warp) is not used again before another
-// barrier.
+// through `red` (one word per warp of the group), which is not used again
+// before another barrier.
 template <int TPR>
 __device__ __forceinline__ float row_sum(float v, float* red) {
   v = warp_sum(v);
   if constexpr (TPR > 32) {
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x % TPR >> 5] = v;
+    row_barrier<TPR>();
     float2 s = make_float2(0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < TPR / 32; w += 4) {
@@ -173,31 +179,53 @@ __global__ void __launch_bounds__(cta_threads(TPR)) norm_forward_kernel(const No
 }
 
 // ---------------------------------------------------------------------------
-// Rows through a ring in shared memory.  A group of TPR threads (a warp, or the
-// CTA) takes every step-th row; bulk copies bring its next `stages` rows while
-// it works on one, so that memory stays busy through the two sums and the
+// Rows through a ring in shared memory.  A CTA fills an SM with groups of TPR
+// threads (a warp, or several with a barrier of their own); each group takes
+// every step-th row, and bulk copies bring its next `stages` rows while it
+// works on one, so that memory stays busy through the two sums and the
 // barriers of a row.  A slot is free again once every thread holds its part of
-// the row in registers, which the first sum's barrier says.
+// the row in registers, which the first sum's barrier says.  The parameters
+// lie in shared memory too, once for all groups: read through L1, what the
+// ring leaves of it did not hold them (16384 x 8192 bf16: 107 us, 84 % of the
+// stalls on those loads).
 // ---------------------------------------------------------------------------
 template <int TPR, int EPT, bool kBackward>
 struct RingCfg {
-  static constexpr int kThreads = TPR < 128 ? 256 : TPR;
-  static constexpr int kGroups = kThreads / TPR;
   // Threads an SM holds: by the registers that a thread's EPT elements (and,
   // backward, their column sums) take.
   static constexpr int kResident = kBackward ? (EPT > 8 ? 512 : 1024) : (EPT > 16 ? 768 : 1024);
-  static constexpr int kPerSm = kThreads >= kResident ? 1 : kResident / kThreads;
-  static constexpr int kBytes = 200 * 1024 / kPerSm / 128 * 128;  // shared memory of a CTA's ring, and kFront
+  static constexpr int kGroups = kResident > TPR ? kResident / TPR : 1;
+  static constexpr int kThreads = kGroups * TPR;
 };
+constexpr int kRingBytes = 216 * 1024;  // shared memory of a CTA: parameters, kFront, the slots
 constexpr int kMaxStages = 4;
 constexpr int kFront = 128;  // bytes before the first slot: a row's start may lie up to 15 before its slot
+
+// Copies n parameters to shared memory.
+template <typename W, bool kAligned>
+__device__ __forceinline__ void keep_params(W* to, const void* from, int n) {
+  if constexpr (kAligned) {
+    const int pieces = n * static_cast<int>(sizeof(W)) / 16;
+#pragma unroll 4
+    for (int j = threadIdx.x; j < pieces; j += blockDim.x)
+      reinterpret_cast<uint4*>(to)[j] = static_cast<const uint4*>(from)[j];
+  } else {
+#pragma unroll 8
+    for (int j = threadIdx.x; j < n; j += blockDim.x) to[j] = static_cast<const W*>(from)[j];
+  }
+}
+// Bytes that n parameters of type W take there.
+template <typename W>
+__host__ __device__ __forceinline__ int param_bytes(int n) {
+  return (n * static_cast<int>(sizeof(W)) + 127) & ~127;
+}
 
 // The 2 EPT parameters of one 16-byte vector, in the rows' type T or fp32.
 template <typename T, typename W>
 __device__ __forceinline__ void load_params16(const void* base, int j, float2* v) {
   const uint4* p = reinterpret_cast<const uint4*>(static_cast<const W*>(base) + j);
-  unpack16<W>(__ldg(p), v);
-  if constexpr (sizeof(W) > sizeof(T)) unpack16<W>(__ldg(p + 1), v + 2);
+  unpack16<W>(p[0], v);
+  if constexpr (sizeof(W) > sizeof(T)) unpack16<W>(p[1], v + 2);
 }
 
 // Waits for a slot.  False: give up (this thread leaves the kernel; the thread
@@ -337,20 +365,25 @@ __device__ __forceinline__ void put_row(T* out, int cols, int tid, int q, const 
 }
 
 template <typename T, typename W, int TPR, int EPT, bool kAligned>
-__global__ void __launch_bounds__(RingCfg<TPR, EPT, false>::kThreads, RingCfg<TPR, EPT, false>::kPerSm)
+__global__ void __launch_bounds__(RingCfg<TPR, EPT, false>::kThreads, 1)
     norm_forward_ring_kernel(const NormCall c, int stages, float inv) {
   using L = Row<T, TPR, EPT, kAligned>;
   using R = RingCfg<TPR, EPT, false>;
   extern __shared__ __align__(128) uint8_t ring[];
-  __shared__ __align__(16) float red[2][32];
+  __shared__ __align__(16) float red_all[R::kGroups][2][TPR < 128 ? 4 : TPR / 32];
   __shared__ uint64_t bars[R::kGroups][kMaxStages];
   __shared__ int abort_word;
   const int tid = threadIdx.x % TPR, group = threadIdx.x / TPR;
   const uint32_t bytes = slot_bytes_of<T, kAligned>(c.cols);
   const float n = static_cast<float>(c.cols);
-  uint8_t* slots = ring + kFront + static_cast<size_t>(group) * stages * bytes;
+  W* weight = reinterpret_cast<W*>(ring);
+  W* bias = reinterpret_cast<W*>(ring + (c.weight ? param_bytes<W>(c.cols) : 0));
+  uint8_t* slots = reinterpret_cast<uint8_t*>(bias) + (c.bias ? param_bytes<W>(c.cols) : 0) + kFront +
+                   static_cast<size_t>(group) * stages * bytes;
   uint64_t* full = bars[group];
-  const int step = gridDim.x * R::kGroups, first = blockIdx.x * R::kGroups + group;
+  float(*red)[TPR < 128 ? 4 : TPR / 32] = red_all[group];
+  // The CTAs' first groups take the first rows, so that few rows spread.
+  const int step = gridDim.x * R::kGroups, first = group * gridDim.x + blockIdx.x;
   int issued = 0;
   auto issue = [&](long long row, int slot) {
     uint64_t* bar = &full[slot];
@@ -367,6 +400,8 @@ __global__ void __launch_bounds__(RingCfg<TPR, EPT, false>::kThreads, RingCfg<TP
     for (long long row = first; issued < stages && row < c.rows; row += step) issue(row, issued);
   }
   chain_wait();
+  if (c.weight) keep_params<W, kAligned>(weight, c.weight, c.cols);
+  if (c.bias) keep_params<W, kAligned>(bias, c.bias, c.cols);
   __syncthreads();
   int slot = 0, turn = 0;
   for (long long row = first; row < c.rows; row += step, ++turn) {
@@ -408,12 +443,12 @@ __global__ void __launch_bounds__(RingCfg<TPR, EPT, false>::kThreads, RingCfg<TP
       for (int i = 0; i < L::H; ++i) d[q][i] = mul2(d[q][i], both(rstd));
       float2 p[L::H];
       if (c.weight) {
-        take_params<T, W, TPR, EPT, kAligned>(c.weight, c.cols, tid, q, p);
+        take_params<T, W, TPR, EPT, kAligned>(weight, c.cols, tid, q, p);
 #pragma unroll
         for (int i = 0; i < L::H; ++i) d[q][i] = mul2(d[q][i], p[i]);
       }
       if (c.bias) {
-        take_params<T, W, TPR, EPT, kAligned>(c.bias, c.cols, tid, q, p);
+        take_params<T, W, TPR, EPT, kAligned>(bias, c.cols, tid, q, p);
 #pragma unroll
         for (int i = 0; i < L::H; ++i) d[q][i] = add2(d[q][i], p[i]);
       }
@@ -466,9 +501,8 @@ __global__ void __launch_bounds__(kLong) norm_forward_long_kernel(const NormCall
 // registers.
 // ---------------------------------------------------------------------------
 
-// CTAs that leave partial sums, at most: what fits the GPU at once, fewer for
-// long rows, whose CTAs are large.
-int max_parts(int cols) { return cols <= 2048 ? 608 : (cols <= 4096 ? 304 : 152); }
+// CTAs that leave partial sums, at most: one to an SM.
+constexpr int kMaxParts = 152;
 
 // The sums of one row: (sum g, sum g xhat) over its TPR threads.
 template <int TPR>
@@ -477,8 +511,8 @@ __device__ __forceinline__ float2 row_sum2(float2 s, float2* red) {
   for (int o = 16; o > 0; o >>= 1)
     s = add2(s, make_float2(__shfl_xor_sync(0xFFFFFFFFu, s.x, o), __shfl_xor_sync(0xFFFFFFFFu, s.y, o)));
   if constexpr (TPR > 32) {
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
-    __syncthreads();
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x % TPR >> 5] = s;
+    row_barrier<TPR>();
     s = make_float2(0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < TPR / 32; w += 2) {
@@ -491,20 +525,23 @@ __device__ __forceinline__ float2 row_sum2(float2 s, float2* red) {
 
 // Rows through the ring: a slot holds x, dy and, where given, dr of one row.
 template <typename T, typename W, int TPR, int EPT, bool kAligned>
-__global__ void __launch_bounds__(RingCfg<TPR, EPT, true>::kThreads, RingCfg<TPR, EPT, true>::kPerSm)
+__global__ void __launch_bounds__(RingCfg<TPR, EPT, true>::kThreads, 1)
     norm_backward_ring_kernel(const NormGradCall c, float* part, int parts, int stages, float inv) {
   using L = Row<T, TPR, EPT, kAligned>;
   using R = RingCfg<TPR, EPT, true>;
   extern __shared__ __align__(128) uint8_t ring[];
-  __shared__ __align__(16) float2 red[2][32];
+  __shared__ __align__(16) float2 red_all[R::kGroups][2][TPR < 128 ? 4 : TPR / 32];
   __shared__ uint64_t bars[R::kGroups][kMaxStages];
   __shared__ int abort_word;
   const int tid = threadIdx.x % TPR, group = threadIdx.x / TPR;
   const uint32_t bytes = slot_bytes_of<T, kAligned>(c.cols), slot_bytes = bytes * (c.dr ? 3 : 2);
   const float n = static_cast<float>(c.cols);
-  uint8_t* slots = ring + kFront + static_cast<size_t>(group) * stages * slot_bytes;
+  W* weight = reinterpret_cast<W*>(ring);
+  uint8_t* slots =
+      ring + (c.weight ? param_bytes<W>(c.cols) : 0) + kFront + static_cast<size_t>(group) * stages * slot_bytes;
   uint64_t* full = bars[group];
-  const int step = gridDim.x * R::kGroups, first = blockIdx.x * R::kGroups + group;
+  float2(*red)[TPR < 128 ? 4 : TPR / 32] = red_all[group];
+  const int step = gridDim.x * R::kGroups, first = group * gridDim.x + blockIdx.x;
   float2 sw[L::NV][L::H], sb[L::NV][L::H];
 #pragma unroll
   for (int q = 0; q < L::NV; ++q)
@@ -532,6 +569,7 @@ __global__ void __launch_bounds__(RingCfg<TPR, EPT, true>::kThreads, RingCfg<TPR
     for (long long row = first; issued < stages && row < c.rows; row += step) issue(row, issued);
   }
   chain_wait();
+  if (c.weight) keep_params<W, kAligned>(weight, c.weight, c.cols);
   __syncthreads();
   int slot = 0, turn = 0;
   float mean = 0.f, rstd = 0.f;
@@ -562,7 +600,7 @@ __global__ void __launch_bounds__(RingCfg<TPR, EPT, true>::kThreads, RingCfg<TPR
       }
       if (c.weight) {
         float2 w[L::H];
-        take_params<T, W, TPR, EPT, kAligned>(c.weight, c.cols, tid, q, w);
+        take_params<T, W, TPR, EPT, kAligned>(weight, c.cols, tid, q, w);
 #pragma unroll
         for (int i = 0; i < L::H; ++i) g[q][i] = mul2(g[q][i], w[i]);
       }
@@ -805,10 +843,11 @@ cudaError_t forward_vec(const NormCall& c, cudaStream_t stream) {
   return launch_chained(norm_forward_long_kernel<T>, dim3(std::min(c.rows, 65536)), kLong, 0, stream, 0, c);
 }
 
-// Slots that a ring of `bytes` holds for each of its groups, and so whether it
-// is worth running.
-int ring_stages(int bytes, int groups, int slot_bytes) {
-  return std::min(kMaxStages, bytes / (groups * std::max(slot_bytes, 16)));
+// Slots of each of a ring's groups, with `params` bytes of parameters before
+// them.
+int ring_stages(int params, int groups, int slot_bytes) {
+  const int room = kRingBytes - params - kFront;
+  return room <= 0 ? 0 : std::min(kMaxStages, room / (groups * std::max(slot_bytes, 16)));
 }
 
 struct ForwardLaunch {
@@ -823,14 +862,14 @@ struct ForwardLaunch {
     if (c.cols > TPR * EPT) return false;
     using R = RingCfg<TPR, EPT, false>;
     const int bytes = static_cast<int>(slot_bytes_of<T, kAligned>(c.cols));
-    const int stages = ring_stages(R::kBytes - kFront, R::kGroups, bytes);
-    const int ctas = R::kPerSm * kSms;
-    if (stages < 2 || c.rows <= ctas * R::kGroups) return false;
+    const int params = param_bytes<W>(c.cols) * ((c.weight ? 1 : 0) + (c.bias ? 1 : 0));
+    const int stages = ring_stages(params, R::kGroups, bytes);
+    if (stages < 2 || c.rows <= kSms * R::kGroups) return false;
     auto kern = norm_forward_ring_kernel<T, W, TPR, EPT, kAligned>;
-    error = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, R::kBytes);
+    error = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
     if (error != cudaSuccess) return true;
-    error = launch_chained(kern, dim3(ctas), R::kThreads, kFront + R::kGroups * stages * bytes, stream, 0, c, stages,
-                           1.f / static_cast<float>(c.cols));
+    error = launch_chained(kern, dim3(kSms), R::kThreads, params + kFront + R::kGroups * stages * bytes, stream, 0, c,
+                           stages, 1.f / static_cast<float>(c.cols));
     return true;
   }
   template <typename T, typename W, bool kAligned>
@@ -843,8 +882,7 @@ struct ForwardLaunch {
 struct BackwardLaunch {
   const NormGradCall& c;
   cudaStream_t stream;
-  int parts;     // room for partial sums
-  int used = 0;  // of which this many are written
+  int used = 0;  // parts written, of kMaxParts
   cudaError_t error = cudaSuccess;
 
   template <typename T, typename W, int TPR, int EPT, bool kAligned>
@@ -852,16 +890,17 @@ struct BackwardLaunch {
     if (c.cols > TPR * EPT) return false;
     using R = RingCfg<TPR, EPT, true>;
     const int slot = static_cast<int>(slot_bytes_of<T, kAligned>(c.cols)) * (c.dr ? 3 : 2);
-    const int stages = ring_stages(R::kBytes - kFront, R::kGroups, slot);
+    const int params = c.weight ? param_bytes<W>(c.cols) : 0;
+    const int stages = ring_stages(params, R::kGroups, slot);
     if (stages < 1) return false;
     auto kern = norm_backward_ring_kernel<T, W, TPR, EPT, kAligned>;
-    error = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, R::kBytes);
+    error = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
     if (error != cudaSuccess) return true;
-    used = std::min({(c.rows + R::kGroups - 1) / R::kGroups, R::kPerSm * kSms, parts});
+    used = std::min(c.rows, kMaxParts);
     // The groups' column sums meet in the ring's memory.
-    const int smem = std::max(kFront + R::kGroups * stages * slot, R::kGroups > 1 ? R::kGroups * TPR * EPT * 8 : 0);
-    error = launch_chained(kern, dim3(used), R::kThreads, smem, stream, 0, c, static_cast<float*>(c.ws), parts, stages,
-                           1.f / static_cast<float>(c.cols));
+    const int smem = std::max(params + kFront + R::kGroups * stages * slot, R::kGroups > 1 ? R::kThreads * EPT * 8 : 0);
+    error = launch_chained(kern, dim3(used), R::kThreads, smem, stream, 0, c, static_cast<float*>(c.ws), kMaxParts,
+                           stages, 1.f / static_cast<float>(c.cols));
     return true;
   }
   template <typename T, typename W, bool kAligned>
@@ -871,15 +910,15 @@ struct BackwardLaunch {
   }
   template <typename T>
   void two_passes(bool vec) {
-    float2* means = reinterpret_cast<float2*>(static_cast<float*>(c.ws) + 2LL * parts * c.cols);
+    float2* means = reinterpret_cast<float2*>(static_cast<float*>(c.ws) + 2LL * kMaxParts * c.cols);
     launch_chained(norm_backward_means_kernel<T>, dim3(std::min(c.rows, 65536)), 512, 0, stream, 0, c, means, vec,
                    aligned16(c.weight));
     const int across = (c.cols + 255) / 256;
-    const int chunks = std::max(1, std::min({parts, 1216 / across, (c.rows + 7) / 8}));
+    const int chunks = std::max(1, std::min({kMaxParts, 1216 / across, (c.rows + 7) / 8}));
     const int chunk = (c.rows + chunks - 1) / chunks;
     used = (c.rows + chunk - 1) / chunk;
     auto kern = vec ? norm_backward_columns_kernel<T, true> : norm_backward_columns_kernel<T, false>;
-    error = launch_chained(kern, dim3(across, used), 256, 0, stream, 0, c, means, static_cast<float*>(c.ws), parts,
+    error = launch_chained(kern, dim3(across, used), 256, 0, stream, 0, c, means, static_cast<float*>(c.ws), kMaxParts,
                            chunk);
   }
 };
@@ -903,11 +942,11 @@ cudaError_t launch_layer_norm(const NormCall& c, cudaStream_t stream) {
 }
 
 size_t layer_norm_backward_workspace(int rows, int cols) {
-  return static_cast<size_t>(2 * max_parts(cols)) * cols * 4 + static_cast<size_t>(rows) * 8;
+  return static_cast<size_t>(2 * kMaxParts) * cols * 4 + static_cast<size_t>(rows) * 8;
 }
 
 cudaError_t launch_layer_norm_backward(const NormGradCall& c, cudaStream_t stream) {
-  BackwardLaunch l{c, stream, max_parts(c.cols)};
+  BackwardLaunch l{c, stream};
   if (c.rows > 0) {
     const int size = type_bytes(c.type);
     const long long bytes = static_cast<long long>(c.cols) * size;
@@ -929,7 +968,7 @@ cudaError_t launch_layer_norm_backward(const NormGradCall& c, cudaStream_t strea
     with_type(c.param_type, [&](auto w) {
       using W = decltype(w);
       return launch_chained(join_parts_kernel<W>, grid, 1024, 0, stream, 0, static_cast<const float*>(c.ws), l.used,
-                            l.parts, c.cols, static_cast<W*>(c.dweight), static_cast<W*>(c.dbias));
+                            kMaxParts, c.cols, static_cast<W*>(c.dweight), static_cast<W*>(c.dbias));
     });
   }
   return cudaGetLastError();
