@@ -24,7 +24,7 @@ namespace {
 constexpr int kBlock = 64;               // elements of an operand block: 64 rows of 64 (128 bytes)
 constexpr int kBlockBytes = 64 * 128;
 constexpr int kEpiWarps = 8;
-constexpr int kThreads = 32 * (2 + kEpiWarps);
+constexpr int kThreads = 32 * (3 + kEpiWarps);
 
 // What happens to an accumulator on its way out.
 struct Epilogue {
@@ -44,6 +44,19 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   int ok = 0;
   if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, abort_word, flags) ? 1 : 0;
   return __shfl_sync(0xFFFFFFFFu, ok, 0) != 0;
+}
+
+// The loops that issue loads and MMAs are run by a whole warp, so that their
+// addresses and descriptors stay in uniform registers, which these
+// instructions take; one elected lane, always the same, issues.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(one));
+  return one != 0;
+}
+__device__ __forceinline__ bool all_wait(uint64_t* bar, uint32_t parity, volatile int* abort_word, uint32_t* flags) {
+  const bool ok = mbar_wait(bar, parity, abort_word, flags);
+  return __all_sync(0xFFFFFFFFu, ok);
 }
 
 // Bounded wait that ignores the abort word (used while draining).
@@ -230,9 +243,9 @@ __device__ __forceinline__ void write_rows(uint8_t* stage, T* out, long long ldo
 // Two CTAs of a cluster form one tile with the 2-SM MMA (M = 256): each stages
 // its 128 rows of A and BN / 2 rows of B, so an operand byte in shared memory
 // serves twice the multiplications of a single-CTA tile.  Persistent: each
-// pair walks the tiles.  Warp 0 issues the TMA loads, one thread of warp 1 the
-// MMAs (4 of K = 16 per 64-element stage), warps 2-9 take finished
-// accumulators out of TMEM; two accumulators alternate, so the next tile's
+// pair walks the tiles.  A thread of warp 0 issues the TMA loads of A, one of
+// warp 10 those of B, one of warp 1 the MMAs (4 of K = 16 per 64-element
+// stage), warps 2-9 take finished accumulators out of TMEM; two accumulators alternate, so the next tile's
 // MMAs run under this tile's epilogue.
 //
 // Few tiles with a long reduction: `split` (2 or 4) pairs of a cluster share a
@@ -253,6 +266,14 @@ struct Product {
   int split;       // pairs that share a tile's reduction
   int tiles_m, tiles_n;
   Epilogue e;
+};
+
+// One product, or two whose tiles follow each other in one launch (the
+// gradients dx and dw).
+struct Products {
+  Product p[2];
+  int count;
+  int stage_bytes;
 };
 
 __device__ __forceinline__ void tile_of(int t, const Product& p, int& tm, int& tn) {
@@ -339,8 +360,9 @@ __device__ __forceinline__ void finish_rows(F source, const uint4 (&res)[8], con
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 1)
-    product_pair_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
-                        const __grid_constant__ Product p, uint32_t* flags) {
+    product_pair_kernel(const __grid_constant__ CUtensorMap ma0, const __grid_constant__ CUtensorMap mb0,
+                        const __grid_constant__ CUtensorMap ma1, const __grid_constant__ CUtensorMap mb1,
+                        const __grid_constant__ Products g, uint32_t* flags) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* staging = smem + kRing;
@@ -355,15 +377,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int place = static_cast<int>(cluster_rank()), rank = place & 1, lead = place & ~1;
   const uint16_t both_ctas = static_cast<uint16_t>(0x3 << lead);
-  const int total = p.tiles_m * p.tiles_n;
-  // A pair walks the tiles, or takes its part of one tile's reduction.
-  const int pair = blockIdx.x / (2 * p.split), npairs = p.split > 1 ? total : gridDim.x >> 1;
-  const int per = (p.kb + p.split - 1) / p.split;
-  const int kb0 = min((place >> 1) * per, p.kb), kb1 = min(kb0 + per, p.kb);
-  // B's BN / 2 rows of this CTA, in whole blocks (a part block's last rows
-  // are loaded and not used).
-  const int b_blocks = p.bn > 128 ? 2 : 1;
-  const int stage_bytes = (2 + b_blocks) * kBlockBytes, stages = kRing / stage_bytes;
+  const int first = g.p[0].tiles_m * g.p[0].tiles_n;  // tiles of the first product
+  const int total = first + (g.count > 1 ? g.p[1].tiles_m * g.p[1].tiles_n : 0);
+  // A pair walks the tiles, or takes its part of one tile's reduction (of one
+  // product).
+  const int split = g.p[0].split;
+  const int pair = blockIdx.x / (2 * split), npairs = split > 1 ? total : gridDim.x >> 1;
+  const int stage_bytes = g.stage_bytes, stages = kRing / stage_bytes;
+  // This pair's blocks of a product's reduction.
+  auto part = [&](const Product& p, int& kb0, int& kb1) {
+    const int per = (p.kb + split - 1) / split;
+    kb0 = min((place >> 1) * per, p.kb);
+    kb1 = min(kb0 + per, p.kb);
+  };
 
   if (warp == 0 && lane == 0) {
     for (int s = 0; s < stages; ++s) {
@@ -377,8 +403,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(mma_done, 1);
     *abort_word = 0;
     fence_mbar_init();
-    tma_prefetch_desc(&ma);
-    tma_prefetch_desc(&mb);
+    tma_prefetch_desc(&ma0);
+    tma_prefetch_desc(&mb0);
   }
   if (warp == 1) {
     tmem_alloc_pair(tmem_holder, 512);
@@ -392,87 +418,97 @@ __global__ void __launch_bounds__(kThreads, 1)
   chain_next();
   chain_wait();
 
-  if (warp == 0) {
-    if (lane == 0) {
-      const uint32_t bar0 = mapa_shared(&full[0], lead);
-      int s = 0;
-      uint32_t phase = 1;
-      bool ok = true;
-      for (int t = pair; t < total && ok; t += npairs) {
-        int tm, tn;
-        tile_of(t, p, tm, tn);
-        const int i0 = tm * 256 + rank * 128, j0 = tn * p.bn + rank * (p.bn / 2);
-        for (int kb = kb0; kb < kb1; ++kb) {
-          if (!mbar_wait(&empty[s], phase, abort_word, flags)) {
-            ok = false;
-            break;
-          }
-          uint8_t* st = smem + s * stage_bytes;
-          const uint32_t bar = bar0 + s * 8;
-          if (rank == 0) mbar_arrive_expect_tx_relaxed(&full[s], 2 * stage_bytes);
-          const int k0 = kb * kBlock;
-          if (p.a_mn) {
-            tma_load_2d_pair(st, &ma, bar, i0, k0);
-            tma_load_2d_pair(st + kBlockBytes, &ma, bar, i0 + kBlock, k0);
-          } else {
-            tma_load_2d_pair(st, &ma, bar, k0, i0);
-          }
-          if (p.b_mn) {
-            tma_load_2d_pair(st + 2 * kBlockBytes, &mb, bar, j0, k0);
-            if (b_blocks == 2) tma_load_2d_pair(st + 3 * kBlockBytes, &mb, bar, j0 + kBlock, k0);
-          } else {
-            tma_load_2d_pair(st + 2 * kBlockBytes, &mb, bar, k0, j0);
-          }
-          if (++s == stages) {
-            s = 0;
-            phase ^= 1;
-          }
+  if (warp == 0 || warp == 2 + kEpiWarps) {
+    // One thread loads A, one B: a stage's loads, issued by one thread, took
+    // longer than its MMAs.
+    const bool loads_a = warp == 0;
+    const uint32_t bar0 = mapa_shared(&full[0], lead);
+    int s = 0;
+    uint32_t phase = 1;
+    bool ok = true;
+    for (int t = pair; t < total && ok; t += npairs) {
+      const bool second = t >= first;
+      const Product& p = g.p[second];
+      const CUtensorMap* map = loads_a ? (second ? &ma1 : &ma0) : (second ? &mb1 : &mb0);
+      int tm, tn, kb0, kb1;
+      tile_of(second ? t - first : t, p, tm, tn);
+      part(p, kb0, kb1);
+      // B's BN / 2 rows of this CTA come in whole blocks (a part block's last
+      // rows are loaded and not used).
+      const int b_blocks = p.bn > 128 ? 2 : 1;
+      const uint32_t bytes = 2 * (2 + b_blocks) * kBlockBytes;
+      const bool arms = loads_a && rank == 0;  // for both CTAs and operands
+      const bool down = loads_a ? p.a_mn != 0 : p.b_mn != 0;
+      const bool two = down && (loads_a || b_blocks == 2);
+      const int at = loads_a ? tm * 256 + rank * 128 : tn * p.bn + rank * (p.bn / 2);
+      const uint32_t to = loads_a ? 0 : 2 * kBlockBytes;
+      for (int k = kb0 * kBlock; k < kb1 * kBlock; k += kBlock) {
+        if (!all_wait(&empty[s], phase, abort_word, flags)) {
+          ok = false;
+          break;
+        }
+        uint8_t* st = smem + s * stage_bytes + to;
+        const uint32_t bar = bar0 + s * 8;
+        if (elect_one()) {
+          if (arms) mbar_arrive_expect_tx_relaxed(&full[s], bytes);
+          tma_load_2d_pair(st, map, bar, down ? at : k, down ? k : at);
+          if (two) tma_load_2d_pair(st + kBlockBytes, map, bar, at + kBlock, k);
+        }
+        __syncwarp();
+        if (++s == stages) {
+          s = 0;
+          phase ^= 1;
         }
       }
-      if (!ok) settle_after_abort();
     }
+    if (!ok) settle_after_abort();
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
-      const uint32_t idesc = idesc_f16(256, p.bn, Pair<T>::kBf16, p.a_mn != 0, p.b_mn != 0);
-      // One MMA takes 16 of the reduction: 32 bytes along a K-major row, 16
-      // rows of 128 bytes down an MN-major block (descriptors count 16 bytes).
-      const uint32_t a_step = p.a_mn ? 128 : 2, b_step = p.b_mn ? 128 : 2;
-      const uint32_t a_lo = smem_desc_sw128_lo(smem_u32(smem), p.a_mn != 0);
-      const uint32_t b_lo = smem_desc_sw128_lo(smem_u32(smem) + 2 * kBlockBytes, p.b_mn != 0);
-      int s = 0, g = 0;
+    if (rank == 0) {
+      int s = 0, n_tiles = 0;
       uint32_t phase = 0;
       bool ok = true;
-      // Whether the next stage is known to be full: tested without blocking
-      // while this stage's MMAs are queued.
-      bool known = false;
-      for (int t = pair; t < total && ok; t += npairs, ++g) {
-        const int buf = g & 1, use = g >> 1;
-        if (use > 0 && !mbar_wait(&tempty[buf], (use - 1) & 1, abort_word, flags)) break;
+      for (int t = pair; t < total && ok; t += npairs, ++n_tiles) {
+        const Product& p = g.p[t >= first];
+        const uint32_t idesc = idesc_f16(256, p.bn, Pair<T>::kBf16, p.a_mn != 0, p.b_mn != 0);
+        // One MMA takes 16 of the reduction: 32 bytes along a K-major row, 16
+        // rows of 128 bytes down an MN-major block (descriptors count 16 bytes).
+        const uint32_t a_step = p.a_mn ? 128 : 2, b_step = p.b_mn ? 128 : 2;
+        const uint32_t a_lo = smem_desc_sw128_lo(smem_u32(smem), p.a_mn != 0);
+        const uint32_t b_lo = smem_desc_sw128_lo(smem_u32(smem) + 2 * kBlockBytes, p.b_mn != 0);
+        int kb0, kb1;
+        part(p, kb0, kb1);
+        const int buf = n_tiles & 1, use = n_tiles >> 1;
+        if (use > 0 && !all_wait(&tempty[buf], (use - 1) & 1, abort_word, flags)) break;
         tc_fence_after();
         const uint32_t d = tbase + static_cast<uint32_t>(buf * 256);
         for (int kb = kb0; kb < kb1; ++kb) {
-          if (!known && !mbar_wait(&full[s], phase, abort_word, flags)) {
+          if (!all_wait(&full[s], phase, abort_word, flags)) {
             ok = false;
             break;
           }
           const uint32_t at = s * (stage_bytes / 16);
+          if (elect_one()) {
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            mma_f16_pair(d, smem_desc_sw128(a_lo + at + ks * a_step), smem_desc_sw128(b_lo + at + ks * b_step), idesc,
-                         ks != 0 ? 1u : (kb != kb0 ? 1u : 0u));
-          tc_commit_pair_multicast(&empty[s], both_ctas);
+            for (int ks = 0; ks < 4; ++ks)
+              mma_f16_pair(d, smem_desc_sw128(a_lo + at + ks * a_step), smem_desc_sw128(b_lo + at + ks * b_step), idesc,
+                           ks != 0 ? 1u : (kb != kb0 ? 1u : 0u));
+            tc_commit_pair_multicast(&empty[s], both_ctas);
+          }
+          __syncwarp();
           if (++s == stages) {
             s = 0;
             phase ^= 1;
           }
-          known = mbar_test_wait(&full[s], phase);
         }
-        if (ok) tc_commit_pair_multicast(&tfull[buf], both_ctas);
+        if (ok && elect_one()) tc_commit_pair_multicast(&tfull[buf], both_ctas);
+        __syncwarp();
       }
-      tc_commit_pair_multicast(mma_done, static_cast<uint16_t>(1 << lead));
-      drain_wait(mma_done, 0, flags);
-      if (!ok) settle_after_abort();
+      if (elect_one()) {
+        tc_commit_pair_multicast(mma_done, static_cast<uint16_t>(1 << lead));
+        drain_wait(mma_done, 0, flags);
+        if (!ok) settle_after_abort();
+      }
     }
     __syncwarp();
   } else {
@@ -480,17 +516,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     // chunks.
     const int ew = warp - 2, quarter = warp & 3, half = ew >> 2;
     uint8_t* stage = staging + ew * 4096;
-    const Epilogue& e = p.e;
-    int g = 0;
-    for (int t = pair; t < total; t += npairs, ++g) {
+    int n_tiles = 0;
+    for (int t = pair; t < total; t += npairs, ++n_tiles) {
+      const bool second = t >= first;
+      const Product& p = g.p[second];
+      const Epilogue& e = p.e;
       int tm, tn;
-      tile_of(t, p, tm, tn);
-      const int buf = g & 1, use = g >> 1;
+      tile_of(second ? t - first : t, p, tm, tn);
+      const int buf = n_tiles & 1, use = n_tiles >> 1;
       const int row0 = tm * 256 + rank * 128 + quarter * 32;
       // Columns of the tile that this warp has to take: none past D's edge.
       const int cols = row0 < p.m ? min(p.bn, p.n - tn * p.bn) : 0;
       const uint32_t tcol = tbase + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(buf * 256);
-      if (p.split > 1) {  // leave the sums; the cluster joins them below
+      if (split > 1) {  // leave the sums; the cluster joins them below
+        int kb0, kb1;
+        part(p, kb0, kb1);
         if (!warp_wait(&tfull[buf], use & 1, abort_word, flags)) break;
         tc_fence_after();
         const int r = quarter * 32 + lane;
@@ -546,10 +586,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
 
-  if (p.split > 1) {
+  if (split > 1) {
+    const Product& p = g.p[0];
     __syncthreads();
     cluster_sync();  // every pair's sums are in its shared memory
-    if (warp >= 2) {
+    if (warp >= 2 && warp < 2 + kEpiWarps) {
       // Sixteen rows a warp, a row's 64 columns to half a warp: shared memory
       // of another CTA is read in contiguous runs, and so is global memory.
       const Epilogue& e = p.e;
@@ -683,52 +724,62 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   chain_wait();
 
   if (warp == 0) {
-    if (lane == 0) {
-      bool ok = true;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        const int it = kb - kb0, s = it % C::kStages;
-        if (!mbar_wait(&empty[s], ((it / C::kStages) & 1) ^ 1, abort_word, flags)) {
-          ok = false;
-          break;
-        }
-        uint8_t* st = smem + s * C::kStage;
+    int s = 0;
+    uint32_t phase = 1;
+    bool ok = true;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      if (!all_wait(&empty[s], phase, abort_word, flags)) {
+        ok = false;
+        break;
+      }
+      uint8_t* st = smem + s * C::kStage;
+      const int k0 = kb * kBlock;
+      if (elect_one()) {
         mbar_arrive_expect_tx_relaxed(&full[s], C::kStage);
-        const int k0 = kb * kBlock;
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const int j = j0 + q * kBlock;
-          tma_load_2d(st + q * kBlockBytes, &mw, &full[s], p.w_mn ? j : k0, p.w_mn ? k0 : j);
+        if (p.w_mn) {
+          tma_load_2d(st, &mw, &full[s], j0, k0);
+          tma_load_2d(st + kBlockBytes, &mw, &full[s], j0 + kBlock, k0);
+        } else {
+          tma_load_2d(st, &mw, &full[s], k0, j0);
         }
         tma_load_2d(st + 2 * kBlockBytes, &mx, &full[s], k0, i0);
       }
-      if (!ok) settle_after_abort();
+      __syncwarp();
+      if (++s == C::kStages) {
+        s = 0;
+        phase ^= 1;
+      }
     }
+    if (!ok) settle_after_abort();
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t idesc = idesc_f16(128, NT, Pair<T>::kBf16, p.w_mn != 0, false);
-      const uint32_t w_step = p.w_mn ? 128 : 2;
-      const uint32_t w_lo = smem_desc_sw128_lo(smem_u32(smem), p.w_mn != 0);
-      const uint32_t x_lo = smem_desc_sw128_lo(smem_u32(smem) + 2 * kBlockBytes, false);
-      int s = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (!mbar_wait(&full[s], phase, abort_word, flags)) {
-          ok = false;
-          break;
-        }
-        const uint32_t at = s * (C::kStage / 16);
+    const uint32_t idesc = idesc_f16(128, NT, Pair<T>::kBf16, p.w_mn != 0, false);
+    const uint32_t w_step = p.w_mn ? 128 : 2;
+    const uint32_t w_lo = smem_desc_sw128_lo(smem_u32(smem), p.w_mn != 0);
+    const uint32_t x_lo = smem_desc_sw128_lo(smem_u32(smem) + 2 * kBlockBytes, false);
+    int s = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      if (!all_wait(&full[s], phase, abort_word, flags)) {
+        ok = false;
+        break;
+      }
+      const uint32_t at = s * (C::kStage / 16);
+      if (elect_one()) {
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
           mma_f16(tbase, smem_desc_sw128(w_lo + at + ks * w_step), smem_desc_sw128(x_lo + at + ks * 2), idesc,
                   ks != 0 ? 1u : (kb != kb0 ? 1u : 0u));
         tc_commit(&empty[s]);
-        if (++s == C::kStages) {
-          s = 0;
-          phase ^= 1;
-        }
       }
+      __syncwarp();
+      if (++s == C::kStages) {
+        s = 0;
+        phase ^= 1;
+      }
+    }
+    if (elect_one()) {
       tc_commit(tfull);  // also when giving up: the MMAs issued are waited for below
       if (!ok) settle_after_abort();
     }
@@ -881,9 +932,9 @@ __global__ void __launch_bounds__(256) align_rows_kernel(const __grid_constant__
 // order.  TX = 4 for few rows (64 at a time, so that one or two turns read
 // them all), else 32.
 template <typename T, int kAct, int TX>
-__global__ void __launch_bounds__(256) slope_kernel(const T* dy, long long lddy, const T* pre, long long ldpre, T* dz,
-                                                    long long lddz, float* part, T* db, int m, int n, int chunk,
-                                                    int vec) {
+__global__ void __launch_bounds__(256, 4) slope_kernel(const T* dy, long long lddy, const T* pre, long long ldpre,
+                                                       T* dz, long long lddz, float* part, T* db, int m, int n,
+                                                       int chunk, int vec) {
   constexpr int TY = 256 / TX, kCols = 8 * TX;
   __shared__ float red[TY][kCols + 8];
   chain_next();
@@ -893,7 +944,7 @@ __global__ void __launch_bounds__(256) slope_kernel(const T* dy, long long lddy,
   float s[8] = {};
   const long long end = min(static_cast<long long>(m), (blockIdx.y + 1LL) * chunk);
   if (left > 0) {
-#pragma unroll 1
+#pragma unroll 2
     for (long long i = static_cast<long long>(blockIdx.y) * chunk + ty; i < end; i += TY) {
       float v[8];
       load8(dy + i * lddy + col, left, vec & 1, v);
@@ -1053,40 +1104,94 @@ cudaError_t resident_clusters(Resident* out) {
 // for each CTA.
 struct Tiling {
   int bn, split;
+  long long cost;
 };
-Tiling tiling(int m, int n, int kb, bool b_mn, const Resident& resident) {
-  long long best = -1;
-  Tiling t = {256, 1};
-  for (int bn = 256; bn >= 64; bn -= b_mn ? 128 : 64)
+// A round of a tile: its blocks of the reduction and its own epilogue.
+long long round_cost(int kb, int bn) { return static_cast<long long>(kb) * (bn > 128 ? 600 : 540) + 4 * bn; }
+long long tiles_of(int m, int n, int bn) { return static_cast<long long>((m + 255) / 256) * ((n + bn - 1) / bn); }
+
+Tiling tiling(const Product& p, const Resident& resident) {
+  Tiling t = {256, 1, -1};
+  for (int bn = 256; bn >= 64; bn -= p.b_mn ? 128 : 64)
     for (int i = 0; i < 3 && (64 << i) <= bn && resident.tiles[i] > 0; ++i) {
       const int split = 1 << i;
-      const long long tiles = static_cast<long long>((m + 255) / 256) * ((n + bn - 1) / bn);
-      const long long rounds = (tiles + resident.tiles[i] - 1) / resident.tiles[i];
-      const long long round = static_cast<long long>((kb + split - 1) / split) * (bn > 128 ? 600 : 540) + 4 * bn;
-      const long long cost = rounds * (round + (split > 1 ? 2500 + 25 * bn : 0)) + 4 * bn;
-      if (best < 0 || cost < best) {
-        best = cost;
-        t = {bn, split};
-      }
+      const long long rounds = (tiles_of(p.m, p.n, bn) + resident.tiles[i] - 1) / resident.tiles[i];
+      const long long cost =
+          rounds * (round_cost((p.kb + split - 1) / split, bn) + (split > 1 ? 2500 + 25 * bn : 0)) + 4 * bn;
+      if (t.cost < 0 || cost < t.cost) t = {bn, split, cost};
     }
   return t;
 }
 
+// The widths of two products whose tiles the pairs walk in one launch (pair i
+// takes tiles i, i + pairs, ...), and the longest pair's time.
+constexpr int kLaunch = 8000;  // clocks that a launch of its own costs
+struct TwoTilings {
+  int bn[2];
+  long long cost;
+};
+TwoTilings together(const Product& a, const Product& b, int pairs) {
+  TwoTilings best = {{256, 256}, -1};
+  for (int x = 256; x >= 128; x -= 128)
+    for (int y = 256; y >= 128; y -= 128) {
+      const long long na = tiles_of(a.m, a.n, x), nb = tiles_of(b.m, b.n, y);
+      const long long ca = round_cost(a.kb, x), cb = round_cost(b.kb, y);
+      long long longest = 0;
+      for (int p = 0; p < pairs; ++p) {
+        const long long mine_a = na > p ? (na - p + pairs - 1) / pairs : 0;
+        const long long all = na + nb > p ? (na + nb - p + pairs - 1) / pairs : 0;
+        longest = std::max(longest, mine_a * ca + (all - mine_a) * cb);
+      }
+      if (best.cost < 0 || longest < best.cost) best = {{x, y}, longest};
+    }
+  best.cost += 4 * 256;
+  return best;
+}
+
+// A product and its operands' maps, ready to launch.
+struct Ready {
+  Product p;
+  Matrix a, b;
+};
 template <typename T>
-cudaError_t launch_pairs(const CUtensorMap& ma, const CUtensorMap& mb, Product p, int pairs, uint32_t* flags,
-                         cudaStream_t stream) {
-  p.tiles_m = (p.m + 255) / 256;
-  p.tiles_n = (p.n + p.bn - 1) / p.bn;
-  const int tiles = p.tiles_m * p.tiles_n;
-  return launch_chained(product_pair_kernel<T>, dim3(2 * (p.split > 1 ? tiles * p.split : std::min(tiles, pairs))),
-                        kThreads, kPairSmem, stream, 2 * p.split, ma, mb, p, flags);
+bool make_maps(const Ready& r, CUtensorMap* ma, CUtensorMap* mb) {
+  // Operand tiles of 128 rows come as one box where the reduction runs along
+  // them, as boxes of 64 x 64 where it runs down.
+  return make_map(ma, r.a, Pair<T>::kBf16, r.p.a_mn ? kBlock : 2 * kBlock) &&
+         make_map(mb, r.b, Pair<T>::kBf16, r.p.b_mn || r.p.bn <= 128 ? kBlock : 2 * kBlock);
+}
+template <typename T>
+cudaError_t launch_pairs(Ready* r, int count, int pairs, uint32_t* flags, cudaStream_t stream) {
+  CUtensorMap m[4];
+  Products g;
+  g.count = count;
+  g.stage_bytes = 3 * kBlockBytes;
+  int tiles = 0;
+  for (int i = 0; i < count; ++i) {
+    Product& p = r[i].p;
+    p.tiles_m = (p.m + 255) / 256;
+    p.tiles_n = (p.n + p.bn - 1) / p.bn;
+    tiles += p.tiles_m * p.tiles_n;
+    if (p.bn > 128) g.stage_bytes = 4 * kBlockBytes;
+    if (!make_maps<T>(r[i], &m[2 * i], &m[2 * i + 1])) return cudaErrorInvalidValue;
+    g.p[i] = p;
+  }
+  if (count == 1) {
+    g.p[1] = g.p[0];
+    m[2] = m[0];
+    m[3] = m[1];
+  }
+  const int split = g.p[0].split;
+  return launch_chained(product_pair_kernel<T>, dim3(2 * (split > 1 ? tiles * split : std::min(tiles, pairs))), kThreads,
+                        kPairSmem, stream, 2 * split, m[0], m[1], m[2], m[3], g, flags);
 }
 
 template <typename T, int NT>
 cudaError_t launch_few(const Matrix& w, bool w_mn, const Matrix& x, FewProduct p, uint32_t* flags,
                        cudaStream_t stream) {
   CUtensorMap mw, mx;
-  if (!make_map(&mw, w, Pair<T>::kBf16, kBlock) || !make_map(&mx, x, Pair<T>::kBf16, NT)) return cudaErrorInvalidValue;
+  if (!make_map(&mw, w, Pair<T>::kBf16, w_mn ? kBlock : 2 * kBlock) || !make_map(&mx, x, Pair<T>::kBf16, NT))
+    return cudaErrorInvalidValue;
   auto kern = product_few_kernel<T, NT>;
   static bool ready[kMaxDev] = {false};
   int dev = 0;
@@ -1109,44 +1214,66 @@ cudaError_t launch_few(const Matrix& w, bool w_mn, const Matrix& x, FewProduct p
                         p, flags);
 }
 
-// D = A B^T over `depth`, with the epilogue e.  a: m x depth (or depth x m
-// where a_mn), b likewise; rows on 16-byte boundaries.
-template <typename T>
-cudaError_t run_product(int m, int n, int depth, const Matrix& a, bool a_mn, const Matrix& b, bool b_mn, Epilogue e,
-                        uint32_t* flags, cudaStream_t stream) {
+// The product D = A B^T over `depth`, with the epilogue e.  a: m x depth (or
+// depth x m where a_mn), b likewise; rows on 16-byte boundaries.
+Ready ready(int m, int n, int depth, const Matrix& a, bool a_mn, const Matrix& b, bool b_mn, Epilogue e) {
   e.vec = (e.bias && rows_aligned(e.bias, 0, 1) ? 1 : 0) | (e.res && rows_aligned(e.res, e.ldr, m) ? 2 : 0) |
           (e.pre && rows_aligned(e.pre, e.ldpre, m) ? 4 : 0) | (rows_aligned(e.out, e.ldo, m) ? 8 : 0);
-  Product p = {m, n, (depth + kBlock - 1) / kBlock, a_mn, b_mn, 0, 1, 0, 0, e};
-  if (depth == 0) {
-    const long long all = static_cast<long long>(m) * n;
-    return launch_chained(empty_product_kernel<T>, dim3(static_cast<unsigned>(std::min<long long>((all + 255) / 256, 4096))),
-                          256, 0, stream, 0, p);
+  return {{m, n, (depth + kBlock - 1) / kBlock, a_mn, b_mn, 256, 1, 0, 0, e}, a, b};
+}
+
+// Whether the kernel for few rows takes a product: up to 128 rows, and up to
+// 76 tiles of 128 x 128 with a reduction worth sharing.  128 rows of 4096 ->
+// 4096 take it 15.5 us (pairs 18), 256 rows of 8192 -> 1024 15.7 (19.5); but
+// 256 rows of 4096 -> 16384 41.7 (30).
+bool few_rows(const Product& p) {
+  const long long squares = static_cast<long long>((p.m + 127) / 128) * ((p.n + 127) / 128);
+  return !p.a_mn && (p.m <= 128 || (squares <= 76 && p.kb >= 32));
+}
+
+template <typename T>
+cudaError_t run_product(Ready r, uint32_t* flags, cudaStream_t stream) {
+  Product& p = r.p;
+  if (p.kb == 0) {
+    const long long all = static_cast<long long>(p.m) * p.n;
+    return launch_chained(empty_product_kernel<T>,
+                          dim3(static_cast<unsigned>(std::min<long long>((all + 255) / 256, 4096))), 256, 0, stream, 0, p);
   }
-  // Up to 128 rows, and up to 76 tiles of 128 x 128 with a reduction worth
-  // sharing, go to the kernel for few rows: 128 rows of 4096 -> 4096 take it
-  // 15.5 us (pairs 18), 256 rows of 8192 -> 1024 15.7 (19.5); but 256 rows of
-  // 4096 -> 16384 41.7 (30).
-  const long long squares = static_cast<long long>((m + 127) / 128) * ((n + 127) / 128);
-  if (!a_mn && (m <= 128 || (squares <= 76 && p.kb >= 32))) {
-    const FewProduct f = {m, n, p.kb, 0, 1, e};
-    return m <= 16   ? launch_few<T, 16>(b, b_mn, a, f, flags, stream)
-           : m <= 32 ? launch_few<T, 32>(b, b_mn, a, f, flags, stream)
-           : m <= 64 ? launch_few<T, 64>(b, b_mn, a, f, flags, stream)
-                     : launch_few<T, 128>(b, b_mn, a, f, flags, stream);
+  if (few_rows(p)) {
+    const FewProduct f = {p.m, p.n, p.kb, 0, 1, p.e};
+    return p.m <= 16   ? launch_few<T, 16>(r.b, p.b_mn, r.a, f, flags, stream)
+           : p.m <= 32 ? launch_few<T, 32>(r.b, p.b_mn, r.a, f, flags, stream)
+           : p.m <= 64 ? launch_few<T, 64>(r.b, p.b_mn, r.a, f, flags, stream)
+                       : launch_few<T, 128>(r.b, p.b_mn, r.a, f, flags, stream);
   }
   Resident resident;
   const cudaError_t s = resident_clusters<T>(&resident);
   if (s != cudaSuccess) return s;
-  const Tiling t = tiling(m, n, p.kb, b_mn, resident);
+  const Tiling t = tiling(p, resident);
   p.bn = t.bn;
   p.split = t.split;
-  // Operand tiles of 128 rows come as one box where the reduction runs along
-  // them, as boxes of 64 x 64 where it runs down.
-  CUtensorMap ma, mb;
-  if (!make_map(&ma, a, Pair<T>::kBf16, a_mn ? kBlock : 2 * kBlock) ||
-      !make_map(&mb, b, Pair<T>::kBf16, b_mn || t.bn <= 128 ? kBlock : 2 * kBlock))
-    return cudaErrorInvalidValue;
-  return launch_pairs<T>(ma, mb, p, resident.tiles[0], flags, stream);
+  return launch_pairs<T>(&r, 1, resident.tiles[0], flags, stream);
+}
+
+// Two products, in one launch where that is quicker: their tiles together fill
+// the pairs better.  (1328 x 2048 -> 1024, dx and dw: 21.7 us apart.)
+template <typename T>
+cudaError_t run_products(Ready a, Ready b, uint32_t* flags, cudaStream_t stream) {
+  if (a.p.kb > 0 && b.p.kb > 0 && !few_rows(a.p) && !few_rows(b.p)) {
+    Resident resident;
+    const cudaError_t s = resident_clusters<T>(&resident);
+    if (s != cudaSuccess) return s;
+    if (a.p.kb < b.p.kb) std::swap(a, b);  // the longer tiles first
+    const TwoTilings t = together(a.p, b.p, resident.tiles[0]);
+    if (t.cost < tiling(a.p, resident).cost + tiling(b.p, resident).cost + kLaunch) {
+      a.p.bn = t.bn[0];
+      b.p.bn = t.bn[1];
+      Ready both[2] = {a, b};
+      return launch_pairs<T>(both, 2, resident.tiles[0], flags, stream);
+    }
+  }
+  const cudaError_t s = run_product<T>(a, flags, stream);
+  return s != cudaSuccess ? s : run_product<T>(b, flags, stream);
 }
 
 template <typename T>
@@ -1154,7 +1281,7 @@ cudaError_t linear_t(const LinearCall& c, cudaStream_t stream) {
   Matrix x = {c.x, c.ldx, c.m, c.k}, w = {c.w, c.ldw, c.n, c.k};
   align_operands(&x, &w, static_cast<uint8_t*>(c.ws), stream);
   const Epilogue e = {c.bias, c.res, c.ldr, c.pre, c.ldpre, c.y, c.ldy, c.act, 0};
-  return run_product<T>(c.m, c.n, c.k, x, false, w, false, e, c.flags, stream);
+  return run_product<T>(ready(c.m, c.n, c.k, x, false, w, false, e), c.flags, stream);
 }
 
 // Row chunks of the slope pass: one where that is quick, else enough CTAs to
@@ -1163,7 +1290,7 @@ constexpr int kFewSlopeRows = 256;
 int slope_chunk(int m, int n) {
   if (m <= kFewSlopeRows) return kFewSlopeRows;
   const int across = (n + 255) / 256;
-  const int chunks = std::max(1, std::min(256, 1216 / across));
+  const int chunks = std::max(1, std::min(256, 608 / across));
   return std::max(32, ((m + chunks - 1) / chunks + 7) / 8 * 8);
 }
 
@@ -1228,19 +1355,17 @@ cudaError_t linear_backward_t(const LinearGradCall& c, cudaStream_t stream) {
     launch_chained(join_parts_kernel<T>, dim3((c.n + 31) / 32), 1024, 0, stream, 0, nullptr, 0, 0, c.n,
                    static_cast<T*>(c.db), nullptr);
   }
-  Epilogue e = {nullptr, nullptr, 0, nullptr, 0, nullptr, 0, kActNone, 0};
-  cudaError_t s = cudaGetLastError();
-  if (s == cudaSuccess && c.dx && c.m > 0 && c.k > 0) {
-    e.out = c.dx;
-    e.ldo = c.lddx;
-    s = run_product<T>(c.m, c.k, c.n, dz, false, w, true, e, c.flags, stream);
-  }
-  if (s == cudaSuccess && c.dw && c.n > 0 && c.k > 0) {
-    e.out = c.dw;
-    e.ldo = c.lddw;
-    s = run_product<T>(c.n, c.k, c.m, dz, true, x, true, e, c.flags, stream);
-  }
-  return s;
+  const cudaError_t s = cudaGetLastError();
+  if (s != cudaSuccess) return s;
+  Epilogue to_dx = {nullptr, nullptr, 0, nullptr, 0, c.dx, c.lddx, kActNone, 0}, to_dw = to_dx;
+  to_dw.out = c.dw;
+  to_dw.ldo = c.lddw;
+  const bool want_dx = c.dx && c.m > 0 && c.k > 0, want_dw = c.dw && c.n > 0 && c.k > 0;
+  const Ready dx = ready(c.m, c.k, c.n, dz, false, w, true, to_dx), dw = ready(c.n, c.k, c.m, dz, true, x, true, to_dw);
+  if (want_dx && want_dw) return run_products<T>(dx, dw, c.flags, stream);
+  if (want_dx) return run_product<T>(dx, c.flags, stream);
+  if (want_dw) return run_product<T>(dw, c.flags, stream);
+  return cudaSuccess;
 }
 
 }  // namespace
