@@ -255,7 +255,7 @@ __device__ __forceinline__ void write_rows(uint8_t* stage, T* out, long long ldo
 // ---------------------------------------------------------------------------
 constexpr int kRing = 192 * 1024;  // stages of two blocks of A and one or two of B: 8 or 6
 constexpr int kMaxStages = 8;
-constexpr int kPairSmem = 1024 + kRing + kEpiWarps * 4096 + 256;
+constexpr int kPairSmem = 1024 + kRing + kEpiWarps * (4096 + 128) + 256;  // staging, a chunk's bias, barriers
 constexpr int kGroupM = 8;  // tile rows swept together, for reuse of B's columns in L2
 
 struct Product {
@@ -305,18 +305,18 @@ __device__ __forceinline__ uint32_t part_piece(int r, int c) {
 // short product has to fetch first is half as long).
 template <typename T, typename F>
 __device__ __forceinline__ void finish_rows(F source, const uint4 (&res)[8], const Epilogue& e, uint8_t* stage,
-                                            int row0, int col0, int m, int n) {
+                                            const uint4* bias, int row0, int col0, int m, int n) {
   const int lane = threadIdx.x & 31;
   uint4* mine = reinterpret_cast<uint4*>(stage + lane * 128);
   auto take = [&](int h, bool last, float (&z)[32]) {
     source(h, last, z);
     if (e.bias) {
 #pragma unroll
-      for (int q = 0; q < 32; q += 8) {
+      for (int q = 0; q < 4; ++q) {
         float b[8];
-        load8(static_cast<const T*>(e.bias) + col0 + 32 * h + q, n - col0 - 32 * h - q, e.vec & 1, b);
+        unpack16<T>(bias[4 * h + q], b);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) z[q + i] += b[i];
+        for (int i = 0; i < 8; ++i) z[8 * q + i] += b[i];
       }
     }
   };
@@ -366,7 +366,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* staging = smem + kRing;
-  uint64_t* full = reinterpret_cast<uint64_t*>(staging + kEpiWarps * 4096);
+  uint8_t* biases = staging + kEpiWarps * 4096;
+  uint64_t* full = reinterpret_cast<uint64_t*>(biases + kEpiWarps * 128);
   uint64_t* empty = full + kMaxStages;
   uint64_t* tfull = empty + kMaxStages;
   uint64_t* tempty = tfull + 2;
@@ -515,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Lane quarter warp % 4; the quarter's two warps take alternate 64-column
     // chunks.
     const int ew = warp - 2, quarter = warp & 3, half = ew >> 2;
-    uint8_t* stage = staging + ew * 4096;
+    uint8_t *stage = staging + ew * 4096, *bias = biases + ew * 128;
     int n_tiles = 0;
     for (int t = pair; t < total; t += npairs, ++n_tiles) {
       const bool second = t >= first;
@@ -557,6 +558,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint4 res[8];
         if (e.res)
           read_rows(res, static_cast<const T*>(e.res), e.ldr, row0, col0, p.m, p.n, (e.vec & 2) != 0);
+        if (e.bias) {  // the chunk's 64 values, for every lane
+          const uint16_t* b = static_cast<const uint16_t*>(e.bias) + col0 + 2 * lane;
+          const int left = p.n - col0 - 2 * lane;
+          const uint32_t lo = left > 0 ? b[0] : 0, hi = left > 1 ? b[1] : 0;
+          __syncwarp();
+          reinterpret_cast<uint32_t*>(bias)[lane] = lo | (hi << 16);
+          __syncwarp();
+        }
         if (!waited) {
           live = warp_wait(&tfull[buf], use & 1, abort_word, flags);
           if (!live) break;
@@ -576,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(&tempty[buf], lead));
               }
             },
-            res, e, stage, row0, col0, p.m, p.n);
+            res, e, stage, reinterpret_cast<const uint4*>(bias), row0, col0, p.m, p.n);
       }
       if (!live) break;
       if (half * 64 >= cols) {  // nothing to take: still let the buffer go, after the tile is done
@@ -1096,18 +1105,23 @@ cudaError_t resident_clusters(Resident* out) {
 
 // The tiling of a product: the columns of a tile, and the pairs that share a
 // tile's reduction, whose estimated time in clocks is least.  Measured at
-// 2 GHz on 256-row tiles: a 64-element block of the reduction takes 0.30 us
-// at 256 and 192 columns and 0.27 us at 128 and 64 (a CTA's loads, not the
-// MMAs, which would take 2 BN clocks); joining a split tile's sums takes 4.5 us
-// at 256 columns and 3 us at 128.  2048 x 8192 -> 512: 40 us unsplit, 27 us by
-// two pairs, 18 us by four.  An MN-major B comes in whole blocks of 64 columns
-// for each CTA.
+// 2 GHz on 256-row tiles: a 64-element block of the reduction takes 0.263 us
+// at 256 columns (its MMAs 0.256), 0.21 at 192, 0.187 at 128 and 64 (a CTA's
+// loads); a round of short reductions 3 us at 256 columns and 1.66 at 128 (its
+// epilogue); joining a split tile's sums 5.2 us at 256 columns and 4 at 192.
+// 2560 x 8192 -> 512: 40 us by one pair a tile of 256, 29 by two, 33 and 25.6
+// at 192, 29 by one at 128; 512 x 4096 -> 4096: 23.5, 21.3, 20.7, 35.9, 18.4.
+// An MN-major B comes in whole blocks of 64 columns for each CTA.
 struct Tiling {
   int bn, split;
   long long cost;
 };
-// A round of a tile: its blocks of the reduction and its own epilogue.
-long long round_cost(int kb, int bn) { return static_cast<long long>(kb) * (bn > 128 ? 600 : 540) + 4 * bn; }
+// A round of tiles: their blocks of the reduction, or the epilogue of the
+// round before where that takes longer.
+long long round_cost(int kb, int bn) {
+  const int block = bn == 256 ? 530 : bn == 192 ? 430 : 375;
+  return std::max<long long>(static_cast<long long>(kb) * block, 2000 + 16 * bn);
+}
 long long tiles_of(int m, int n, int bn) { return static_cast<long long>((m + 255) / 256) * ((n + bn - 1) / bn); }
 
 Tiling tiling(const Product& p, const Resident& resident) {
@@ -1117,7 +1131,7 @@ Tiling tiling(const Product& p, const Resident& resident) {
       const int split = 1 << i;
       const long long rounds = (tiles_of(p.m, p.n, bn) + resident.tiles[i] - 1) / resident.tiles[i];
       const long long cost =
-          rounds * (round_cost((p.kb + split - 1) / split, bn) + (split > 1 ? 2500 + 25 * bn : 0)) + 4 * bn;
+          rounds * (round_cost((p.kb + split - 1) / split, bn) + (split > 1 ? 4000 + 25 * bn : 0)) + 16 * bn;
       if (t.cost < 0 || cost < t.cost) t = {bn, split, cost};
     }
   return t;
@@ -1144,7 +1158,7 @@ TwoTilings together(const Product& a, const Product& b, int pairs) {
       }
       if (best.cost < 0 || longest < best.cost) best = {{x, y}, longest};
     }
-  best.cost += 4 * 256;
+  best.cost += 16 * 256;
   return best;
 }
 
