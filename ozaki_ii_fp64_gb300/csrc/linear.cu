@@ -23,7 +23,7 @@ namespace {
 
 constexpr int kBlock = 64;               // elements of an operand block: 64 rows of 64 (128 bytes)
 constexpr int kBlockBytes = 64 * 128;
-constexpr int kEpiWarps = 8;
+constexpr int kEpiWarps = 16;
 constexpr int kThreads = 32 * (3 + kEpiWarps);
 
 // What happens to an accumulator on its way out.
@@ -131,69 +131,72 @@ __device__ __forceinline__ void activate_all(float (&z)[N], int act) {
   }
 }
 
-// A warp's 32 rows x 64 columns of 16-bit elements pass through its 4 KB of
-// shared memory (row r at byte 128 r, its 16-byte piece c at piece c ^ (r % 8):
-// no bank conflicts by rows or by pieces), so that a row moves as one 128-byte
-// run.  A lane's share on the way: piece lane % 8 of rows 4 i + lane / 8; or,
-// where rows do not start on 16-byte boundaries, elements 2 lane and
-// 2 lane + 1 of every row, moved by words, and between words where the row
-// starts on an odd element.
-__device__ __forceinline__ uint32_t* stage_word(uint8_t* stage, int r, int lane) {
-  return reinterpret_cast<uint32_t*>(stage + r * 128 + (((lane >> 2) ^ (r & 7)) << 4)) + (lane & 3);
+// A warp's 32 rows x 32 columns of 16-bit elements pass through its 2 KB of
+// shared memory (row r at byte 64 r, its 16-byte piece c at piece
+// c ^ (r / 2 % 4): no bank conflicts by rows or by pieces), so that a row moves
+// as one 64-byte run.  A lane's share on the way: piece lane % 4 of rows
+// 8 i + lane / 4; or, where rows do not start on 16-byte boundaries, word
+// lane % 16 of rows 2 i + lane / 16, between words where the row starts on an
+// odd element.
+__device__ __forceinline__ uint4* stage_piece(uint8_t* stage, int r, int c) {
+  return reinterpret_cast<uint4*>(stage + r * 64) + (c ^ (r >> 1 & 3));
+}
+__device__ __forceinline__ uint32_t* stage_word(uint8_t* stage, int r, int w) {
+  return reinterpret_cast<uint32_t*>(stage_piece(stage, r, w >> 2)) + (w & 3);
 }
 
 template <typename T>
-__device__ __forceinline__ void read_rows(uint4 (&v)[8], const T* in, long long ld, int row0, int col0, int m, int n,
+__device__ __forceinline__ void read_rows(uint4 (&v)[4], const T* in, long long ld, int row0, int col0, int m, int n,
                                           bool vec) {
   const int lane = threadIdx.x & 31;
-  if (vec && col0 + 64 <= n) {
+  if (vec && col0 + 32 <= n) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = row0 + 4 * i + (lane >> 3);
-      v[i] = r < m ? *reinterpret_cast<const uint4*>(in + r * ld + col0 + 8 * (lane & 7)) : make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < 4; ++i) {
+      const int r = row0 + 8 * i + (lane >> 2);
+      v[i] = r < m ? *reinterpret_cast<const uint4*>(in + r * ld + col0 + 8 * (lane & 3)) : make_uint4(0, 0, 0, 0);
     }
     return;
   }
   uint32_t* w = reinterpret_cast<uint32_t*>(v);
   const uint16_t* p = reinterpret_cast<const uint16_t*>(in) + row0 * ld + col0;
-  if (col0 > 0 && col0 + 64 <= n) {  // the element before the run is the row's, too
+  const int word = lane & 15;
+  if (col0 > 0 && col0 + 32 <= n) {  // the element before the run is the row's, too
     // All loads first: the words, and for row `lane` the last element, which a
-    // row that starts on an odd element has in a 33rd word.
-    const uint32_t last = row0 + lane < m ? p[lane * ld + 63] : 0;
+    // row that starts on an odd element has in a 17th word.
+    const uint32_t last = row0 + lane < m ? p[lane * ld + 31] : 0;
 #pragma unroll
-    for (int r = 0; r < 32; ++r) {
-      const uint16_t* q = p + r * ld;
-      w[r] = row0 + r < m ? *(reinterpret_cast<const uint32_t*>(reinterpret_cast<uintptr_t>(q) & ~uintptr_t(3)) + lane) : 0;
+    for (int i = 0; i < 16; ++i) {
+      const int r = 2 * i + (lane >> 4);
+      const uintptr_t q = reinterpret_cast<uintptr_t>(p + r * ld) & ~uintptr_t(3);
+      w[i] = row0 + r < m ? *(reinterpret_cast<const uint32_t*>(q) + word) : 0;
     }
 #pragma unroll
-    for (int r = 0; r < 32; ++r) {
-      const uint32_t next = __shfl_down_sync(0xFFFFFFFFu, w[r], 1), tail = __shfl_sync(0xFFFFFFFFu, last, r);
-      const bool odd = (reinterpret_cast<uintptr_t>(p + r * ld) & 2u) != 0;
-      if (odd) w[r] = __funnelshift_r(w[r], lane == 31 ? tail : next, 16);
+    for (int i = 0; i < 16; ++i) {
+      const int r = 2 * i + (lane >> 4);
+      const uint32_t next = __shfl_down_sync(0xFFFFFFFFu, w[i], 1), tail = __shfl_sync(0xFFFFFFFFu, last, r);
+      if (reinterpret_cast<uintptr_t>(p + r * ld) & 2u) w[i] = __funnelshift_r(w[i], word == 15 ? tail : next, 16);
     }
   } else {
 #pragma unroll
-    for (int r = 0; r < 32; ++r) {
-      const uint16_t* q = p + r * ld + 2 * lane;
-      const uint32_t a = row0 + r < m && col0 + 2 * lane < n ? q[0] : 0;
-      const uint32_t b = row0 + r < m && col0 + 2 * lane + 1 < n ? q[1] : 0;
-      w[r] = a | (b << 16);
+    for (int i = 0; i < 16; ++i) {
+      const int r = 2 * i + (lane >> 4);
+      const uint16_t* q = p + r * ld + 2 * word;
+      const uint32_t a = row0 + r < m && col0 + 2 * word < n ? q[0] : 0;
+      const uint32_t b = row0 + r < m && col0 + 2 * word + 1 < n ? q[1] : 0;
+      w[i] = a | (b << 16);
     }
   }
 }
 
-__device__ __forceinline__ void stage_rows(const uint4 (&v)[8], uint8_t* stage, int col0, int n, bool vec) {
+__device__ __forceinline__ void stage_rows(const uint4 (&v)[4], uint8_t* stage, int col0, int n, bool vec) {
   const int lane = threadIdx.x & 31;
-  if (vec && col0 + 64 <= n) {
+  if (vec && col0 + 32 <= n) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = 4 * i + (lane >> 3);
-      reinterpret_cast<uint4*>(stage + r * 128)[(lane & 7) ^ (r & 7)] = v[i];
-    }
+    for (int i = 0; i < 4; ++i) *stage_piece(stage, 8 * i + (lane >> 2), lane & 3) = v[i];
   } else {
     const uint32_t* w = reinterpret_cast<const uint32_t*>(v);
 #pragma unroll
-    for (int r = 0; r < 32; ++r) *stage_word(stage, r, lane) = w[r];
+    for (int i = 0; i < 16; ++i) *stage_word(stage, 2 * i + (lane >> 4), lane & 15) = w[i];
   }
 }
 
@@ -201,37 +204,38 @@ template <typename T>
 __device__ __forceinline__ void write_rows(uint8_t* stage, T* out, long long ldo, int row0, int col0, int m, int n,
                                            bool vec) {
   const int lane = threadIdx.x & 31;
-  if (vec && col0 + 64 <= n) {
+  if (vec && col0 + 32 <= n) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = 4 * i + (lane >> 3);
+    for (int i = 0; i < 4; ++i) {
+      const int r = 8 * i + (lane >> 2);
       if (row0 + r < m)
-        *reinterpret_cast<uint4*>(out + (row0 + r) * ldo + col0 + 8 * (lane & 7)) =
-            reinterpret_cast<const uint4*>(stage + r * 128)[(lane & 7) ^ (r & 7)];
+        *reinterpret_cast<uint4*>(out + (row0 + r) * ldo + col0 + 8 * (lane & 3)) = *stage_piece(stage, r, lane & 3);
     }
     return;
   }
   uint16_t* p = reinterpret_cast<uint16_t*>(out) + row0 * ldo + col0;
-  const bool whole = col0 + 64 <= n;
+  const bool whole = col0 + 32 <= n;
+  const int word = lane & 15;
 #pragma unroll 1
-  for (int r0 = 0; r0 < 32; r0 += 8) {
-    uint32_t a[8], b[8];
+  for (int i0 = 0; i0 < 16; i0 += 4) {
+    uint32_t a[4], b[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) a[i] = *stage_word(stage, r0 + i, lane);
+    for (int i = 0; i < 4; ++i) a[i] = *stage_word(stage, 2 * (i0 + i) + (lane >> 4), word);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) b[i] = __shfl_down_sync(0xFFFFFFFFu, a[i], 1);
+    for (int i = 0; i < 4; ++i) b[i] = __shfl_down_sync(0xFFFFFFFFu, a[i], 1);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      uint16_t* q = p + (r0 + i) * ldo;
-      const bool odd = (reinterpret_cast<uintptr_t>(q) & 2u) != 0, in_m = row0 + r0 + i < m;
-      if (whole) {  // from an odd start: words of elements 2 lane + 1 and 2 lane + 2, and the two ends
-        const uint32_t word = odd ? __funnelshift_r(a[i], b[i], 16) : a[i];
-        if (in_m && !(odd && lane == 31)) *reinterpret_cast<uint32_t*>(q + 2 * lane + (odd ? 1 : 0)) = word;
-        if (in_m && odd && lane == 31) q[63] = static_cast<uint16_t>(a[i] >> 16);
-        if (in_m && odd && lane == 0) q[0] = static_cast<uint16_t>(a[i]);
+    for (int i = 0; i < 4; ++i) {
+      const int r = 2 * (i0 + i) + (lane >> 4);
+      uint16_t* q = p + r * ldo;
+      const bool odd = (reinterpret_cast<uintptr_t>(q) & 2u) != 0, in_m = row0 + r < m;
+      if (whole) {  // from an odd start: words of elements 2 word + 1 and 2 word + 2, and the two ends
+        const uint32_t both = odd ? __funnelshift_r(a[i], b[i], 16) : a[i];
+        if (in_m && !(odd && word == 15)) *reinterpret_cast<uint32_t*>(q + 2 * word + (odd ? 1 : 0)) = both;
+        if (in_m && odd && word == 15) q[31] = static_cast<uint16_t>(a[i] >> 16);
+        if (in_m && odd && word == 0) q[0] = static_cast<uint16_t>(a[i]);
       } else {
-        if (in_m && col0 + 2 * lane < n) q[2 * lane] = static_cast<uint16_t>(a[i]);
-        if (in_m && col0 + 2 * lane + 1 < n) q[2 * lane + 1] = static_cast<uint16_t>(a[i] >> 16);
+        if (in_m && col0 + 2 * word < n) q[2 * word] = static_cast<uint16_t>(a[i]);
+        if (in_m && col0 + 2 * word + 1 < n) q[2 * word + 1] = static_cast<uint16_t>(a[i] >> 16);
       }
     }
   }
@@ -255,7 +259,7 @@ __device__ __forceinline__ void write_rows(uint8_t* stage, T* out, long long ldo
 // ---------------------------------------------------------------------------
 constexpr int kRing = 192 * 1024;  // stages of two blocks of A and one or two of B: 8 or 6
 constexpr int kMaxStages = 8;
-constexpr int kPairSmem = 1024 + kRing + kEpiWarps * (4096 + 128) + 256;  // staging, a chunk's bias, barriers
+constexpr int kPairSmem = 1024 + kRing + kEpiWarps * (2048 + 64) + 256;  // staging, a chunk's bias, barriers
 constexpr int kGroupM = 8;  // tile rows swept together, for reuse of B's columns in L2
 
 struct Product {
@@ -300,34 +304,30 @@ __device__ __forceinline__ uint32_t part_piece(int r, int c) {
   return static_cast<uint32_t>(r * 1024 + ((c ^ (r & 31)) << 4));
 }
 
-// One warp's 32 rows x 64 columns of accumulators through the epilogue: half
-// of the columns at a time, in a loop, from source(h, z) (the code that a
-// short product has to fetch first is half as long).
+// One warp's 32 rows x 32 columns of accumulators, a row a lane, from
+// source(last, z) through the epilogue; the source is asked for the last time
+// with last = true.
 template <typename T, typename F>
-__device__ __forceinline__ void finish_rows(F source, const uint4 (&res)[8], const Epilogue& e, uint8_t* stage,
+__device__ __forceinline__ void finish_rows(F source, const uint4 (&res)[4], const Epilogue& e, uint8_t* stage,
                                             const uint4* bias, int row0, int col0, int m, int n) {
   const int lane = threadIdx.x & 31;
-  uint4* mine = reinterpret_cast<uint4*>(stage + lane * 128);
-  auto take = [&](int h, bool last, float (&z)[32]) {
-    source(h, last, z);
+  float z[32];
+  auto take = [&](bool last) {
+    source(last, z);
     if (e.bias) {
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         float b[8];
-        unpack16<T>(bias[4 * h + q], b);
+        unpack16<T>(bias[q], b);
 #pragma unroll
         for (int i = 0; i < 8; ++i) z[8 * q + i] += b[i];
       }
     }
   };
   if (e.pre) {
-#pragma unroll 1
-    for (int h = 0; h < 2; ++h) {
-      float z[32];
-      take(h, false, z);
+    take(false);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) mine[(4 * h + c) ^ (lane & 7)] = pack16<T>(z + 8 * c);
-    }
+    for (int c = 0; c < 4; ++c) *stage_piece(stage, lane, c) = pack16<T>(z + 8 * c);
     __syncwarp();
     write_rows(stage, static_cast<T*>(e.pre), e.ldpre, row0, col0, m, n, (e.vec & 4) != 0);
     __syncwarp();
@@ -336,22 +336,18 @@ __device__ __forceinline__ void finish_rows(F source, const uint4 (&res)[8], con
     stage_rows(res, stage, col0, n, (e.vec & 2) != 0);
     __syncwarp();
   }
-#pragma unroll 1
-  for (int h = 0; h < 2; ++h) {
-    float z[32];
-    take(h, h == 1, z);
-    activate_all(z, e.act);
+  take(true);
+  activate_all(z, e.act);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      uint4* at = mine + ((4 * h + c) ^ (lane & 7));
-      if (e.res) {
-        float r[8];
-        unpack16<T>(*at, r);
+  for (int c = 0; c < 4; ++c) {
+    uint4* at = stage_piece(stage, lane, c);
+    if (e.res) {
+      float r[8];
+      unpack16<T>(*at, r);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) z[8 * c + i] += r[i];
-      }
-      *at = pack16<T>(z + 8 * c);
+      for (int i = 0; i < 8; ++i) z[8 * c + i] += r[i];
     }
+    *at = pack16<T>(z + 8 * c);
   }
   __syncwarp();
   write_rows(stage, static_cast<T*>(e.out), e.ldo, row0, col0, m, n, (e.vec & 8) != 0);
@@ -366,8 +362,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* staging = smem + kRing;
-  uint8_t* biases = staging + kEpiWarps * 4096;
-  uint64_t* full = reinterpret_cast<uint64_t*>(biases + kEpiWarps * 128);
+  uint8_t* biases = staging + kEpiWarps * 2048;
+  uint64_t* full = reinterpret_cast<uint64_t*>(biases + kEpiWarps * 64);
   uint64_t* empty = full + kMaxStages;
   uint64_t* tfull = empty + kMaxStages;
   uint64_t* tempty = tfull + 2;
@@ -513,10 +509,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else {
-    // Lane quarter warp % 4; the quarter's two warps take alternate 64-column
-    // chunks.
-    const int ew = warp - 2, quarter = warp & 3, half = ew >> 2;
-    uint8_t *stage = staging + ew * 4096, *bias = biases + ew * 128;
+    // Lane quarter warp % 4; the quarter's four warps take 32-column chunks in
+    // turn.  (Eight warps of 64-column chunks left each scheduler two warps to
+    // hide an epilogue's latencies with.)
+    const int ew = warp - 2, quarter = warp & 3, group = ew >> 2;
+    uint8_t *stage = staging + ew * 2048, *bias = biases + ew * 64;
     int n_tiles = 0;
     for (int t = pair; t < total; t += npairs, ++n_tiles) {
       const bool second = t >= first;
@@ -535,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!warp_wait(&tfull[buf], use & 1, abort_word, flags)) break;
         tc_fence_after();
         const int r = quarter * 32 + lane;
-        for (int c = half * 32; c < cols; c += 64) {
+        for (int c = group * 32; c < cols; c += 128) {
           uint32_t u[32];
           if (kb0 < kb1) {
             tmem_ld32(tcol + c, u);
@@ -553,17 +550,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       bool waited = false, live = true;
 #pragma unroll 1
-      for (int c = half * 64; c < cols; c += 128) {
+      for (int c = group * 32; c < cols; c += 128) {
         const int col0 = tn * p.bn + c;
-        uint4 res[8];
+        uint4 res[4];
         if (e.res)
           read_rows(res, static_cast<const T*>(e.res), e.ldr, row0, col0, p.m, p.n, (e.vec & 2) != 0);
-        if (e.bias) {  // the chunk's 64 values, for every lane
-          const uint16_t* b = static_cast<const uint16_t*>(e.bias) + col0 + 2 * lane;
-          const int left = p.n - col0 - 2 * lane;
-          const uint32_t lo = left > 0 ? b[0] : 0, hi = left > 1 ? b[1] : 0;
+        if (e.bias) {  // the chunk's 32 values, for every lane
+          const uint16_t b = col0 + lane < p.n ? static_cast<const uint16_t*>(e.bias)[col0 + lane] : 0;
           __syncwarp();
-          reinterpret_cast<uint32_t*>(bias)[lane] = lo | (hi << 16);
+          reinterpret_cast<uint16_t*>(bias)[lane] = b;
           __syncwarp();
         }
         if (!waited) {
@@ -573,9 +568,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           waited = true;
         }
         finish_rows<T>(
-            [&](int h, bool last, float(&z)[32]) {
+            [&](bool last, float(&z)[32]) {
               uint32_t u[32];
-              tmem_ld32(tcol + c + 32 * h, u);
+              tmem_ld32(tcol + c, u);
               tmem_wait_ld();
 #pragma unroll
               for (int i = 0; i < 32; ++i) z[i] = __uint_as_float(u[i]);
@@ -588,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             res, e, stage, reinterpret_cast<const uint4*>(bias), row0, col0, p.m, p.n);
       }
       if (!live) break;
-      if (half * 64 >= cols) {  // nothing to take: still let the buffer go, after the tile is done
+      if (group * 32 >= cols) {  // nothing to take: still let the buffer go, after the tile is done
         if (!warp_wait(&tfull[buf], use & 1, abort_word, flags)) break;
         if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(&tempty[buf], lead));
       }
@@ -600,22 +595,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     cluster_sync();  // every pair's sums are in its shared memory
     if (warp >= 2 && warp < 2 + kEpiWarps) {
-      // Sixteen rows a warp, a row's 64 columns to half a warp: shared memory
-      // of another CTA is read in contiguous runs, and so is global memory.
+      // Eight rows a warp, a row's 64 columns to half a warp: shared memory of
+      // another CTA is read in contiguous runs, and so is global memory.
       const Epilogue& e = p.e;
       int tm, tn;
       tile_of(pair, p, tm, tn);
-      const int row0 = (warp - 2) * 16 + (lane >> 4), cols = min(p.bn, p.n - tn * p.bn);
+      const int r0 = (warp - 2) * 8 + (lane >> 4), cols = min(p.bn, p.n - tn * p.bn);
       const long long grow0 = tm * 256 + rank * 128;
-      for (int c = (place >> 1) * 64; c < cols; c += 64 * p.split) {
+      for (int c = (place >> 1) * 64; c < cols; c += 64 * split) {
         const int piece = c / 4 + (lane & 15), col = tn * p.bn + c + (lane & 15) * 4, left = p.n - col;
         if (left <= 0) continue;
         float b[4] = {0.f, 0.f, 0.f, 0.f};
         if (e.bias) load4(static_cast<const T*>(e.bias) + col, left, e.vec & 1, b);
-#pragma unroll 1
-        for (int r0 = row0; r0 < row0 + 16; r0 += 8) {
+        {
           float z[4][4] = {};
-          for (int q = 0; q < p.split; q += 2) {
+          for (int q = 0; q < split; q += 2) {
             float4 v[2][4];  // all loads before the first sum
 #pragma unroll
             for (int k = 0; k < 2; ++k)
