@@ -249,8 +249,8 @@ __device__ __forceinline__ void write_rows(uint8_t* stage, T* out, long long ldo
 // serves twice the multiplications of a single-CTA tile.  Persistent: each
 // pair walks the tiles.  A thread of warp 0 issues the TMA loads of A, one of
 // warp 10 those of B, one of warp 1 the MMAs (4 of K = 16 per 64-element
-// stage), warps 2-9 take finished accumulators out of TMEM; two accumulators alternate, so the next tile's
-// MMAs run under this tile's epilogue.
+// stage), warps 2-9 take finished accumulators out of TMEM; two accumulators of 256 columns, or four of
+// 128, alternate, so the next tiles' MMAs run under this tile's epilogue.
 //
 // Few tiles with a long reduction: `split` (2 or 4) pairs of a cluster share a
 // tile, each with a part of the reduction.  Each CTA leaves its fp32 sums in
@@ -268,7 +268,9 @@ struct Product {
   int a_mn, b_mn;  // the operand's reduction runs down its rows
   int bn;          // columns of a tile
   int split;       // pairs that share a tile's reduction
+  int share;       // blocks of it for each
   int tiles_m, tiles_n;
+  uint32_t group_inverse, group_shift;  // of kGroupM tiles_n
   Epilogue e;
 };
 
@@ -278,14 +280,22 @@ struct Products {
   Product p[2];
   int count;
   int stage_bytes;
+  int bufs;  // accumulators in TMEM: 4 of 128 columns or 2 of 256
 };
 
 __device__ __forceinline__ void tile_of(int t, const Product& p, int& tm, int& tn) {
-  const int group = kGroupM * p.tiles_n;
-  const int first = t / group * kGroupM;
+  // t / (kGroupM tiles_n) by the reciprocal that the host rounded up: exact
+  // for the product's tiles.
+  const int turn = static_cast<int>(__umulhi(static_cast<uint32_t>(t), p.group_inverse) >> p.group_shift);
+  const int first = turn * kGroupM, rest = t - turn * kGroupM * p.tiles_n;
   const int gm = min(kGroupM, p.tiles_m - first);
-  tm = first + (t % group) % gm;
-  tn = (t % group) / gm;
+  if (gm == kGroupM) {
+    tn = rest / kGroupM;
+    tm = first + rest % kGroupM;
+  } else {
+    tn = rest / gm;
+    tm = first + rest % gm;
+  }
 }
 
 // 16 bytes of shared memory of a CTA of the cluster.
@@ -366,8 +376,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(biases + kEpiWarps * 64);
   uint64_t* empty = full + kMaxStages;
   uint64_t* tfull = empty + kMaxStages;
-  uint64_t* tempty = tfull + 2;
-  uint64_t* mma_done = tempty + 2;
+  uint64_t* tempty = tfull + 4;
+  uint64_t* mma_done = tempty + 4;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(mma_done + 1);
   volatile int* abort_word = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
@@ -381,11 +391,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int split = g.p[0].split;
   const int pair = blockIdx.x / (2 * split), npairs = split > 1 ? total : gridDim.x >> 1;
   const int stage_bytes = g.stage_bytes, stages = kRing / stage_bytes;
+  const int buf_shift = g.bufs == 4 ? 2 : 1, buf_columns = 512 >> buf_shift;
   // This pair's blocks of a product's reduction.
   auto part = [&](const Product& p, int& kb0, int& kb1) {
-    const int per = (p.kb + split - 1) / split;
-    kb0 = min((place >> 1) * per, p.kb);
-    kb1 = min(kb0 + per, p.kb);
+    kb0 = min((place >> 1) * p.share, p.kb);
+    kb1 = min(kb0 + p.share, p.kb);
   };
 
   if (warp == 0 && lane == 0) {
@@ -393,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&full[s], 1);   // armed by the first CTA with both CTAs' bytes
       mbar_init(&empty[s], 1);  // one commit from the pair's MMA issuer
     }
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < 4; ++b) {
       mbar_init(&tfull[b], 1);
       mbar_init(&tempty[b], 2 * kEpiWarps);
     }
@@ -475,10 +485,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t b_lo = smem_desc_sw128_lo(smem_u32(smem) + 2 * kBlockBytes, p.b_mn != 0);
         int kb0, kb1;
         part(p, kb0, kb1);
-        const int buf = n_tiles & 1, use = n_tiles >> 1;
+        const int buf = n_tiles & (g.bufs - 1), use = n_tiles >> buf_shift;
         if (use > 0 && !all_wait(&tempty[buf], (use - 1) & 1, abort_word, flags)) break;
         tc_fence_after();
-        const uint32_t d = tbase + static_cast<uint32_t>(buf * 256);
+        const uint32_t d = tbase + static_cast<uint32_t>(buf * buf_columns);
         for (int kb = kb0; kb < kb1; ++kb) {
           if (!all_wait(&full[s], phase, abort_word, flags)) {
             ok = false;
@@ -521,11 +531,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Epilogue& e = p.e;
       int tm, tn;
       tile_of(second ? t - first : t, p, tm, tn);
-      const int buf = n_tiles & 1, use = n_tiles >> 1;
+      const int buf = n_tiles & (g.bufs - 1), use = n_tiles >> buf_shift;
       const int row0 = tm * 256 + rank * 128 + quarter * 32;
       // Columns of the tile that this warp has to take: none past D's edge.
       const int cols = row0 < p.m ? min(p.bn, p.n - tn * p.bn) : 0;
-      const uint32_t tcol = tbase + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(buf * 256);
+      const uint32_t tcol = tbase + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(buf * buf_columns);
       if (split > 1) {  // leave the sums; the cluster joins them below
         int kb0, kb1;
         part(p, kb0, kb1);
@@ -1174,13 +1184,24 @@ cudaError_t launch_pairs(Ready* r, int count, int pairs, uint32_t* flags, cudaSt
   Products g;
   g.count = count;
   g.stage_bytes = 3 * kBlockBytes;
+  g.bufs = 4;
   int tiles = 0;
   for (int i = 0; i < count; ++i) {
     Product& p = r[i].p;
     p.tiles_m = (p.m + 255) / 256;
     p.tiles_n = (p.n + p.bn - 1) / p.bn;
+    p.share = (p.kb + p.split - 1) / p.split;
+    // ceil(2^(32 + shift) / d) with 2^shift >= d gives t / d for t < 2^31; with
+    // the shift one less the multiplier fits 32 bits, for t < 2^31 still.
+    const uint64_t d = static_cast<uint64_t>(kGroupM) * p.tiles_n;
+    p.group_shift = 0;
+    while ((2ull << p.group_shift) < d) ++p.group_shift;
+    p.group_inverse = static_cast<uint32_t>(((1ull << (32 + p.group_shift)) + d - 1) / d);
     tiles += p.tiles_m * p.tiles_n;
-    if (p.bn > 128) g.stage_bytes = 4 * kBlockBytes;
+    if (p.bn > 128) {
+      g.stage_bytes = 4 * kBlockBytes;
+      g.bufs = 2;
+    }
     if (!make_maps<T>(r[i], &m[2 * i], &m[2 * i + 1])) return cudaErrorInvalidValue;
     g.p[i] = p;
   }
@@ -1227,7 +1248,16 @@ cudaError_t launch_few(const Matrix& w, bool w_mn, const Matrix& x, FewProduct p
 Ready ready(int m, int n, int depth, const Matrix& a, bool a_mn, const Matrix& b, bool b_mn, Epilogue e) {
   e.vec = (e.bias && rows_aligned(e.bias, 0, 1) ? 1 : 0) | (e.res && rows_aligned(e.res, e.ldr, m) ? 2 : 0) |
           (e.pre && rows_aligned(e.pre, e.ldpre, m) ? 4 : 0) | (rows_aligned(e.out, e.ldo, m) ? 8 : 0);
-  return {{m, n, (depth + kBlock - 1) / kBlock, a_mn, b_mn, 256, 1, 0, 0, e}, a, b};
+  Product p = {};
+  p.m = m;
+  p.n = n;
+  p.kb = (depth + kBlock - 1) / kBlock;
+  p.a_mn = a_mn;
+  p.b_mn = b_mn;
+  p.bn = 256;
+  p.split = 1;
+  p.e = e;
+  return {p, a, b};
 }
 
 // Whether the kernel for few rows takes a product: up to 128 rows, and up to
