@@ -489,6 +489,7 @@ int ozemu_dgemm_host_mixed(int m, int n, int k, const double* A, int lda, const 
  * backward, on 16-bit (layer norm: also 32-bit) floating-point data.  The
  * source pages have no counterpart.
  *
+ *   - Sizes: up to 2^26 for the linear layer, 2^31 - 2^16 for layer norm.
  *   - Matrices are row-major with unit inner stride and a leading dimension
  *     of at least the row length; vectors are dense.  Every pointer needs its
  *     element type's natural alignment only; rows on 16-byte boundaries are
@@ -502,6 +503,10 @@ int ozemu_dgemm_host_mixed(int m, int n, int k, const double* A, int lda, const 
  *     calls above, these may overlap on different streams with workspaces of
  *     their own.  Too small a one -> OZEMU_ERR_SCRATCH_TOO_SMALL.
  *   - Outputs must not overlap inputs, except where a call says so.
+ *   - Calls may be captured in a CUDA graph (the first call on a device, which
+ *     allocates its status word, may not).  A call's kernels may start before
+ *     the kernel ahead of them on the stream has ended; they wait for it
+ *     before their first access to memory.
  *   - Infinities and NaN go through as the formulas take them, and set no
  *     flag.  A product's pipeline wait that times out sets the flag that
  *     ozemu_get_status reports. */

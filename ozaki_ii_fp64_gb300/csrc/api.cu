@@ -1483,11 +1483,24 @@ static int scratch_ok(const void* ws, size_t have, size_t need) {
   return (reinterpret_cast<uintptr_t>(ws) & 255u) == 0 ? OZEMU_OK : OZEMU_ERR_INVALID_ARG;
 }
 
+// Sizes of a linear layer, at most 2^26: the longest reduction then takes a
+// third of the time that a pipeline wait allows.
+constexpr int kMaxLinear = 1 << 26;
+static bool linear_sizes(int m, int n, int k) {
+  return m >= 0 && n >= 0 && k >= 0 && m <= kMaxLinear && n <= kMaxLinear && k <= kMaxLinear;
+}
+// Rows and columns of a layer norm, at most 2^31 - 2^16: a thread's index
+// stays an int past the last element.
+static bool norm_sizes(int rows, int cols) {
+  constexpr int most = INT32_MAX - 65535;
+  return rows >= 0 && cols >= 0 && rows <= most && cols <= most;
+}
+
 static bool product_type(int type) { return type == OZEMU_BF16 || type == OZEMU_F16; }
 static bool activation_ok(int a) { return a >= OZEMU_ACT_NONE && a <= OZEMU_ACT_SILU; }
 
 size_t ozemu_linear_bytes(int m, int n, int k, const void* X, int ldx, const void* W, int ldw) {
-  if (m <= 0 || n <= 0 || k <= 0 || ldx < k || ldw < k) return 0;
+  if (!linear_sizes(m, n, k) || m == 0 || n == 0 || k == 0 || ldx < k || ldw < k) return 0;
   LinearCall c = {};
   c.m = m;
   c.n = n;
@@ -1502,7 +1515,7 @@ size_t ozemu_linear_bytes(int m, int n, int k, const void* X, int ldx, const voi
 int ozemu_linear(int m, int n, int k, int type, const void* X, int ldx, const void* W, int ldw, const void* bias,
                  const void* R, int ldr, int activation, void* pre, int ldpre, void* Y, int ldy, void* workspace,
                  size_t workspace_bytes, cudaStream_t stream) {
-  if (m < 0 || n < 0 || k < 0 || !product_type(type) || !activation_ok(activation)) return OZEMU_ERR_INVALID_ARG;
+  if (!linear_sizes(m, n, k) || !product_type(type) || !activation_ok(activation)) return OZEMU_ERR_INVALID_ARG;
   if (!matrix_ok(X, m, k, ldx, type) || !matrix_ok(W, n, k, ldw, type) || !vector_ok(bias, type) ||
       !matrix_ok(R, m, n, ldr, type, true) || !matrix_ok(pre, m, n, ldpre, type, true) ||
       !matrix_ok(Y, m, n, ldy, type))
@@ -1520,7 +1533,8 @@ int ozemu_linear(int m, int n, int k, int type, const void* X, int ldx, const vo
 
 size_t ozemu_linear_backward_bytes(int m, int n, int k, const void* dY, int lddy, const void* X, int ldx,
                                    const void* W, int ldw, int activation) {
-  if (m <= 0 || n <= 0 || k < 0 || lddy < n || ldx < k || ldw < k || !activation_ok(activation)) return 0;
+  if (!linear_sizes(m, n, k) || m == 0 || n == 0 || lddy < n || ldx < k || ldw < k || !activation_ok(activation))
+    return 0;
   LinearGradCall c = {};
   c.m = m;
   c.n = n;
@@ -1539,7 +1553,7 @@ int ozemu_linear_backward(int m, int n, int k, int type, const void* dY, int ldd
                           const void* W, int ldw, int activation, const void* pre, int ldpre, void* dX, int lddx,
                           void* dW, int lddw, void* db, void* workspace, size_t workspace_bytes,
                           cudaStream_t stream) {
-  if (m < 0 || n < 0 || k < 0 || !product_type(type) || !activation_ok(activation)) return OZEMU_ERR_INVALID_ARG;
+  if (!linear_sizes(m, n, k) || !product_type(type) || !activation_ok(activation)) return OZEMU_ERR_INVALID_ARG;
   const bool slope = activation != OZEMU_ACT_NONE;
   if (!matrix_ok(dY, m, n, lddy, type) || !matrix_ok(X, m, k, ldx, type, !dW) ||
       !matrix_ok(W, n, k, ldw, type, !dX) || (slope && !matrix_ok(pre, m, n, ldpre, type)) ||
@@ -1563,7 +1577,7 @@ static bool norm_types(int type, int param_type) {
 
 int ozemu_layer_norm(int rows, int cols, int type, const void* X, int ldx, int param_type, const void* weight,
                      const void* bias, float eps, void* Y, int ldy, float* mean, float* rstd, cudaStream_t stream) {
-  if (rows < 0 || cols < 0 || !norm_types(type, param_type) || !(eps >= 0.0f)) return OZEMU_ERR_INVALID_ARG;
+  if (!norm_sizes(rows, cols) || !norm_types(type, param_type) || !(eps >= 0.0f)) return OZEMU_ERR_INVALID_ARG;
   if (!matrix_ok(X, rows, cols, ldx, type) || !matrix_ok(Y, rows, cols, ldy, type) ||
       !vector_ok(weight, param_type) || !vector_ok(bias, param_type) || !vector_ok(mean, OZEMU_F32) ||
       !vector_ok(rstd, OZEMU_F32))
@@ -1577,7 +1591,7 @@ int ozemu_layer_norm(int rows, int cols, int type, const void* X, int ldx, int p
 }
 
 size_t ozemu_layer_norm_backward_bytes(int rows, int cols) {
-  if (rows <= 0 || cols <= 0) return 0;
+  if (!norm_sizes(rows, cols) || rows == 0 || cols == 0) return 0;
   return layer_norm_backward_workspace(rows, cols);
 }
 
@@ -1585,7 +1599,7 @@ int ozemu_layer_norm_backward(int rows, int cols, int type, const void* dY, int 
                               int param_type, const void* weight, const float* mean, const float* rstd,
                               const void* dR, int lddr, void* dX, int lddx, void* dweight, void* dbias,
                               void* workspace, size_t workspace_bytes, cudaStream_t stream) {
-  if (rows < 0 || cols < 0 || !norm_types(type, param_type)) return OZEMU_ERR_INVALID_ARG;
+  if (!norm_sizes(rows, cols) || !norm_types(type, param_type)) return OZEMU_ERR_INVALID_ARG;
   if (!matrix_ok(dY, rows, cols, lddy, type) || !matrix_ok(X, rows, cols, ldx, type) ||
       !matrix_ok(dX, rows, cols, lddx, type) || !matrix_ok(dR, rows, cols, lddr, type, true) ||
       !vector_ok(weight, param_type) || !vector_ok(dweight, param_type) || !vector_ok(dbias, param_type) ||

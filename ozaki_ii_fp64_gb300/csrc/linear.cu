@@ -11,8 +11,11 @@
 // descriptors say which way the reduction runs, so no operand is transposed
 // in memory.
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 #include <cuda.h>
+#include <mutex>
+#include <utility>
 
 #include "kernels.h"
 #include "layer.cuh"
@@ -1076,10 +1079,12 @@ struct Resident {
 template <typename T>
 cudaError_t resident_clusters(Resident* out) {
   static Resident known[kMaxDev];
+  static std::mutex mu;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= kMaxDev) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> lock(mu);
   if (known[dev].tiles[0] == 0) {
     auto kern = product_pair_kernel<T>;
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem);
@@ -1222,7 +1227,7 @@ cudaError_t launch_few(const Matrix& w, bool w_mn, const Matrix& x, FewProduct p
   if (!make_map(&mw, w, Pair<T>::kBf16, w_mn ? kBlock : 2 * kBlock) || !make_map(&mx, x, Pair<T>::kBf16, NT))
     return cudaErrorInvalidValue;
   auto kern = product_few_kernel<T, NT>;
-  static bool ready[kMaxDev] = {false};
+  static std::atomic<bool> ready[kMaxDev];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;

@@ -97,6 +97,8 @@ def _norm_backward(oz, rows=4, cols=8, type=BF16, dY=FAKE, lddy=8, X=FAKE, ldx=8
 
 
 @pytest.mark.parametrize("call, bad", [
+    (_linear, dict(m=(1 << 26) + 1)), (_linear, dict(k=(1 << 26) + 1, ldx=1 << 27, ldw=1 << 27)),
+    (_norm, dict(rows=(1 << 31) - 1)), (_norm, dict(cols=(1 << 31) - 1, ldx=(1 << 31) - 1, ldy=(1 << 31) - 1)),
     (_linear, dict(m=-1)), (_linear, dict(n=-1)), (_linear, dict(k=-1)),
     (_linear, dict(type=F32)), (_linear, dict(type=3)), (_linear, dict(type=-1)),
     (_linear, dict(act=5)), (_linear, dict(act=-1)),
@@ -144,6 +146,7 @@ def test_workspace_queries_on_bad_arguments(oz):
     assert oz.ozemu_linear_backward_bytes(4, 4, 8, FAKE, 3, FAKE, 8, FAKE, 8, 2) == 0
     assert oz.ozemu_linear_backward_bytes(4, 4, 8, FAKE, 4, FAKE, 8, FAKE, 8, 7) == 0
     assert oz.ozemu_layer_norm_backward_bytes(-1, 8) == 0
+    assert oz.ozemu_linear_bytes((1 << 26) + 1, 4, 8, FAKE + 2, 8, FAKE, 8) == 0
 
 
 def test_binding_refuses_wrong_tensors(oz):
