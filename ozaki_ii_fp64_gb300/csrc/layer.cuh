@@ -173,29 +173,52 @@ __device__ __forceinline__ float activate(float z, int act) {
   }
 }
 
-// act'(z).  The factors that multiply an already vanished exponential take z
-// limited to +-64 (where it has vanished), so that a large z gives the limit
-// 0 or 1 and not 0 * inf.
-__device__ __forceinline__ float activation_slope(float z, int act) {
-  const float zc = fminf(fmaxf(z, -64.f), 64.f);
-  switch (act) {
-    case kActRelu:
-      return z > 0.f ? 1.f : 0.f;
-    case kActGelu: {
-      float e;
-      const float p = normal_cdf(z, e);
-      return fmaf(zc * 0.3989422804014327f, e, p);
-    }
-    case kActGeluTanh: {
-      const float s = __fdividef(1.f, 1.f + __expf(-2.f * kGeluC * z * fmaf(kGeluA * z, z, 1.f)));
-      return fmaf(zc * s * (1.f - s), 2.f * kGeluC * fmaf(3.f * kGeluA * zc, zc, 1.f), s);
-    }
-    case kActSilu: {
-      const float s = __fdividef(1.f, 1.f + __expf(-z));
-      return s * fmaf(zc, 1.f - s, 1.f);
-    }
-    default:
-      return 1.f;
+__device__ __forceinline__ float2 exp2_2(float2 v) {
+  float2 r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(v.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(v.y));
+  return r;
+}
+__device__ __forceinline__ float2 reciprocal2(float2 v) {
+  float2 r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(v.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(v.y));
+  return r;
+}
+
+// act'(z) of two values at once: a pass over the gradients is bound by the
+// instructions of this.  The factors that multiply an already vanished
+// exponential take z limited to +-64 (where it has vanished), so that a large
+// or infinite z gives the limit 0 or 1 and not 0 * inf; a NaN stays one through
+// the other factors.
+template <int kAct>
+__device__ __forceinline__ float2 activation_slope2(float2 z) {
+  const float2 one = both(1.f);
+  const float2 zc = make_float2(fminf(fmaxf(z.x, -64.f), 64.f), fminf(fmaxf(z.y, -64.f), 64.f));
+  if constexpr (kAct == kActRelu) {
+    return make_float2(z.x > 0.f ? 1.f : 0.f, z.y > 0.f ? 1.f : 0.f);
+  } else if constexpr (kAct == kActGelu) {  // Phi(z) + z phi(z), as in normal_cdf
+    const float2 a = make_float2(fabsf(z.x), fabsf(z.y));
+    const float2 t = reciprocal2(fma2(a, both(0.3275911f * 0.70710678118654752f), one));
+    float2 q = fma2(t, both(0.5f * 1.061405429f), both(0.5f * -1.453152027f));
+    q = fma2(t, q, both(0.5f * 1.421413741f));
+    q = fma2(t, q, both(0.5f * -0.284496736f));
+    q = fma2(t, q, both(0.5f * 0.254829592f));
+    const float2 e = exp2_2(mul2(mul2(z, z), both(-0.5f * 1.4426950408889634f)));
+    q = mul2(mul2(q, t), e);
+    const float2 p = make_float2(z.x < 0.f ? q.x : 1.f - q.x, z.y < 0.f ? q.y : 1.f - q.y);
+    return fma2(mul2(zc, both(0.3989422804014327f)), e, p);
+  } else if constexpr (kAct == kActGeluTanh) {  // s + z s (1 - s) 2 u'(z), s = 1 / (1 + e^(-2u))
+    const float2 zz = mul2(z, z);
+    const float2 u = mul2(mul2(z, both(-2.f * kGeluC * 1.4426950408889634f)), fma2(zz, both(kGeluA), one));
+    const float2 s = reciprocal2(add2(exp2_2(u), one));
+    const float2 du = fma2(mul2(zc, zc), both(6.f * kGeluC * kGeluA), both(2.f * kGeluC));
+    return fma2(mul2(mul2(zc, s), fma2(s, both(-1.f), one)), du, s);
+  } else if constexpr (kAct == kActSilu) {  // s (1 + z (1 - s)), s = 1 / (1 + e^(-z))
+    const float2 s = reciprocal2(add2(exp2_2(mul2(z, both(-1.4426950408889634f))), one));
+    return mul2(s, fma2(zc, fma2(s, both(-1.f), one), one));
+  } else {
+    return one;
   }
 }
 

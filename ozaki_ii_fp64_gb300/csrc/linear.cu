@@ -83,16 +83,17 @@ __device__ __forceinline__ void settle_after_abort() {
 // Eight consecutive elements p[0..7] of which `left` exist, as floats (0 past
 // the end); one 16-byte load where the address allows.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, int left, bool vec, float (&v)[8]) {
+__device__ __forceinline__ void load8(const T* p, int left, bool vec, float2 (&v)[4]) {
   if (vec && left >= 8) {
     unpack16<T>(__ldg(reinterpret_cast<const uint4*>(p)), v);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < left ? to_float(p[i]) : 0.f;
+    for (int i = 0; i < 4; ++i)
+      v[i] = make_float2(2 * i < left ? to_float(p[2 * i]) : 0.f, 2 * i + 1 < left ? to_float(p[2 * i + 1]) : 0.f);
   }
 }
 
-// The same for four, by plain loads (the memory may be the output's).
+// Four elements, by plain loads (the memory may be the output's).
 template <typename T>
 __device__ __forceinline__ void load4(const T* p, int left, bool vec, float (&v)[4]) {
   if (vec && left >= 4) {
@@ -957,21 +958,21 @@ __global__ void __launch_bounds__(256, 4) slope_kernel(const T* dy, long long ld
   chain_wait();
   const int tx = threadIdx.x % TX, ty = threadIdx.x / TX;
   const int col = blockIdx.x * kCols + tx * 8, left = n - col;
-  float s[8] = {};
+  float2 s[4] = {};
   const long long end = min(static_cast<long long>(m), (blockIdx.y + 1LL) * chunk);
   if (left > 0) {
 #pragma unroll 2
     for (long long i = static_cast<long long>(blockIdx.y) * chunk + ty; i < end; i += TY) {
-      float v[8];
+      float2 v[4];
       load8(dy + i * lddy + col, left, vec & 1, v);
       if constexpr (kAct != kActNone) {
-        float z[8];
+        float2 z[4];
         load8(pre + i * ldpre + col, left, vec & 2, z);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) v[q] *= activation_slope(z[q], kAct);
+        for (int q = 0; q < 4; ++q) v[q] = mul2(v[q], activation_slope2<kAct>(z[q]));
       }
 #pragma unroll
-      for (int q = 0; q < 8; ++q) s[q] += v[q];
+      for (int q = 0; q < 4; ++q) s[q] = add2(s[q], v[q]);
       if (dz) {  // rows of dz start on 16-byte boundaries and are padded to 8
         *reinterpret_cast<uint4*>(dz + i * lddz + col) = pack16<T>(v);
       }
@@ -979,7 +980,10 @@ __global__ void __launch_bounds__(256, 4) slope_kernel(const T* dy, long long ld
   }
   if (!part && !db) return;
 #pragma unroll
-  for (int q = 0; q < 8; ++q) red[ty][tx * 8 + q] = s[q];
+  for (int q = 0; q < 4; ++q) {
+    red[ty][tx * 8 + 2 * q] = s[q].x;
+    red[ty][tx * 8 + 2 * q + 1] = s[q].y;
+  }
   __syncthreads();
   const int j = blockIdx.x * kCols + threadIdx.x;
   if (threadIdx.x < kCols && j < n) {

@@ -160,6 +160,22 @@ def test_activations_of_large_arguments(oz):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("act", ACTS)
+def test_slopes_of_infinite_and_nan_arguments(oz, act, dtype):
+    # Saved sums that overflowed have the slope's limit; a NaN makes its column's sum NaN and no other.
+    big = [float("inf"), float("-inf"), 6e4, -6e4, 40.0, -40.0]
+    pre = torch.tensor([big + [float("nan"), 0.5]], dtype=dtype, device=DEV)
+    dy, x, w = torch.ones_like(pre), rnd(1, 4, dtype, 240), rnd(8, 4, dtype, 241)
+    _, _, db = oz.linear_backward(dy, x, w, pre, activation=act, x_grad=False, w_grad=False)
+    assert db[:2].tolist() == [1.0, 1.0 if act == "none" else 0.0]
+    s = slope64(pre[0, 2:6].double(), act)
+    assert float((db[2:6].double() - s).abs().max()) <= 2.0 ** -8 + 2.0 ** -17
+    if act not in ("none", "relu"):
+        assert bool(torch.isnan(db[6]))
+    assert bool(torch.isfinite(db[7]))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
 @pytest.mark.parametrize("shape", SHAPES, ids=str)
 def test_linear_backward_shapes(oz, shape, dtype):
     m, k, n = shape
