@@ -299,16 +299,17 @@ __device__ __forceinline__ uint32_t start_row(uint8_t* slot, const void* base, l
   }
 }
 
-// A thread's elements of the row in a slot; 0 past the row's end.
-template <typename T, int TPR, int EPT, int kMode>
+// A thread's elements of the row in a slot, NQ vectors from vector q0 on; 0
+// past the row's end.
+template <typename T, int TPR, int EPT, int kMode, int NQ = EPT / (16 / sizeof(T))>
 __device__ __forceinline__ void take_row(const uint8_t* slot, const void* base, long long ld, long long row, int rows,
-                                         int cols, int tid, float2 (&v)[EPT / (16 / sizeof(T))][8 / sizeof(T)]) {
+                                         int cols, int tid, float2 (&v)[NQ][8 / sizeof(T)], int q0 = 0) {
   using L = Row<T, TPR, EPT, kMode>;
   if constexpr (kMode != kAnyRow) {
 #pragma unroll
-    for (int q = 0; q < L::NV; ++q) {
-      if (kMode == kExactRow || L::column(tid, q, 0) < cols) {
-        unpack16<T>(*reinterpret_cast<const uint4*>(slot + (q * TPR + tid) * 16), v[q]);
+    for (int q = 0; q < NQ; ++q) {
+      if (kMode == kExactRow || L::column(tid, q0 + q, 0) < cols) {
+        unpack16<T>(*reinterpret_cast<const uint4*>(slot + ((q0 + q) * TPR + tid) * 16), v[q]);
       } else {
 #pragma unroll
         for (int i = 0; i < L::H; ++i) v[q][i] = make_float2(0.f, 0.f);
@@ -320,20 +321,20 @@ __device__ __forceinline__ void take_row(const uint8_t* slot, const void* base, 
     const RowCopy c = row_copy<T>(base, ld, row, rows, cols);
     const uint8_t* mine = slot + c.shift + tid * static_cast<int>(sizeof(T));
 #pragma unroll
-    for (int q = 0; q < L::NV; ++q)
+    for (int q = 0; q < NQ; ++q)
 #pragma unroll
       for (int i = 0; i < L::VEC; ++i) {
-        const int j = L::column(tid, q, i);
-        const float f = j < cols ? to_float(*reinterpret_cast<const T*>(mine + (q * L::VEC + i) * TPR * sizeof(T))) : 0.f;
+        const int j = L::column(tid, q0 + q, i);
+        const float f = j < cols ? to_float(*reinterpret_cast<const T*>(mine + ((q0 + q) * L::VEC + i) * TPR * sizeof(T))) : 0.f;
         (i & 1 ? v[q][i / 2].y : v[q][i / 2].x) = f;
       }
     if (row == 0 || row == rows - 1) {
       const T* whole = static_cast<const T*>(base) + row * ld;
 #pragma unroll
-      for (int q = 0; q < L::NV; ++q)
+      for (int q = 0; q < NQ; ++q)
 #pragma unroll
         for (int i = 0; i < L::VEC; ++i) {
-          const int j = L::column(tid, q, i), off = c.shift + j * static_cast<int>(sizeof(T));
+          const int j = L::column(tid, q0 + q, i), off = c.shift + j * static_cast<int>(sizeof(T));
           if (j < cols && (off < 0 || off + static_cast<int>(sizeof(T)) > static_cast<int>(c.bytes)))
             (i & 1 ? v[q][i / 2].y : v[q][i / 2].x) = to_float(whole[j]);
         }
@@ -529,6 +530,13 @@ __device__ __forceinline__ float2 row_sum2(float2 s, float2* red) {
 }
 
 // Rows through the ring: a slot holds x, dy and, where given, dr of one row.
+// Up to 8192 columns a thread keeps its 16 elements of x and dy from the sums
+// to dx; with 32 (and their 64 column sums) it takes them from the slot twice,
+// and the slot is free after dx.  16384 x 4096 bf16 with dr: 91.6 us, 0.87 of
+// the copy rate (two reads in three bytes, latency of 512 threads); 8192 x
+// 16384 bf16: 150 us where the two passes below took 413; with dr and fp32
+// weights, one slot, 292; 777 x 2051 f16, odd rows: 12.2 (5 rows an SM, each
+// its latency; element by element).
 template <typename T, typename W, int TPR, int EPT, int kMode>
 __global__ void __launch_bounds__(RingCfg<TPR, EPT, true>::kThreads, 1)
     norm_backward_ring_kernel(const NormGradCall c, float* part, int parts, int stages, float inv) {
@@ -547,6 +555,9 @@ __global__ void __launch_bounds__(RingCfg<TPR, EPT, true>::kThreads, 1)
   uint64_t* full = bars[group];
   float2(*red)[TPR < 128 ? 4 : TPR / 32] = red_all[group];
   const int step = gridDim.x * R::kGroups, first = group * gridDim.x + blockIdx.x;
+  constexpr bool kTwice = EPT > 16;
+  constexpr int NQ = kTwice ? 1 : L::NV;  // vectors held at a time
+  auto past = [&](int q) { return kMode != kExactRow && L::column(tid, q, 0) >= c.cols; };
   float2 sw[L::NV][L::H], sb[L::NV][L::H];
 #pragma unroll
   for (int q = 0; q < L::NV; ++q)
@@ -590,51 +601,85 @@ __global__ void __launch_bounds__(RingCfg<TPR, EPT, true>::kThreads, 1)
     }
     if (!ring_wait<TPR>(full, turn, slot, stages, issued, &abort_word, c.flags)) return;
     const uint8_t* in = slots + slot * slot_bytes;
-    float2 xh[L::NV][L::H], g[L::NV][L::H];
-    take_row<T, TPR, EPT, kMode>(in, c.x, c.ldx, row, c.rows, c.cols, tid, xh);
-    take_row<T, TPR, EPT, kMode>(in + bytes, c.dy, c.lddy, row, c.rows, c.cols, tid, g);
+    float2 xh[NQ][L::H], g[NQ][L::H], dr[NQ][L::H];
+    auto take = [&](int q0) {
+      take_row<T, TPR, EPT, kMode, NQ>(in, c.x, c.ldx, row, c.rows, c.cols, tid, xh, q0);
+      take_row<T, TPR, EPT, kMode, NQ>(in + bytes, c.dy, c.lddy, row, c.rows, c.cols, tid, g, q0);
+    };
+    auto normalise = [&](float2(&v)[L::H]) {
+#pragma unroll
+      for (int i = 0; i < L::H; ++i) v[i] = mul2(add2(v[i], both(-mean)), both(rstd));
+    };
+    auto weigh = [&](int q, float2(&v)[L::H]) {
+      if (!c.weight) return;
+      float2 w[L::H];
+      take_params<T, W, TPR, EPT, kMode>(weight, c.cols, tid, q, w);
+#pragma unroll
+      for (int i = 0; i < L::H; ++i) v[i] = mul2(v[i], w[i]);
+    };
     float2 s1 = make_float2(0.f, 0.f), s2 = s1;
 #pragma unroll
-    for (int q = 0; q < L::NV; ++q) {
-      if (kMode != kExactRow && L::column(tid, q, 0) >= c.cols) break;  // past the end dy is 0, and so are the sums
+    for (int q0 = 0; q0 < L::NV; q0 += NQ) {
+      take(q0);
 #pragma unroll
-      for (int i = 0; i < L::H; ++i) {
-        xh[q][i] = mul2(add2(xh[q][i], both(-mean)), both(rstd));
-        sw[q][i] = fma2(g[q][i], xh[q][i], sw[q][i]);
-        sb[q][i] = add2(sb[q][i], g[q][i]);
-      }
-      if (c.weight) {
-        float2 w[L::H];
-        take_params<T, W, TPR, EPT, kMode>(weight, c.cols, tid, q, w);
+      for (int q = 0; q < NQ; ++q) {
+        if (past(q0 + q)) break;  // dy is 0 there, and so are the sums
+        normalise(xh[q]);
 #pragma unroll
-        for (int i = 0; i < L::H; ++i) g[q][i] = mul2(g[q][i], w[i]);
-      }
+        for (int i = 0; i < L::H; ++i) {
+          sw[q0 + q][i] = fma2(g[q][i], xh[q][i], sw[q0 + q][i]);
+          sb[q0 + q][i] = add2(sb[q0 + q][i], g[q][i]);
+        }
+        weigh(q0 + q, g[q]);
 #pragma unroll
-      for (int i = 0; i < L::H; ++i) {
-        s1 = add2(s1, g[q][i]);
-        s2 = fma2(g[q][i], xh[q][i], s2);
+        for (int i = 0; i < L::H; ++i) {
+          s1 = add2(s1, g[q][i]);
+          s2 = fma2(g[q][i], xh[q][i], s2);
+        }
       }
     }
-    float2 dr[L::NV][L::H];
-    if (c.dr) take_row<T, TPR, EPT, kMode>(in + 2 * bytes, c.dr, c.lddr, row, c.rows, c.cols, tid, dr);
+    auto take_dr = [&](int q0) {
+      if (c.dr) take_row<T, TPR, EPT, kMode, NQ>(in + 2 * bytes, c.dr, c.lddr, row, c.rows, c.cols, tid, dr, q0);
+    };
+    auto release = [&] {
+      if (tid == 0) {
+        const long long later = row + static_cast<long long>(stages) * step;
+        if (later < c.rows) issue(later, slot);
+      }
+      if (++slot == stages) slot = 0;
+    };
+    if (!kTwice) take_dr(0);
     const float2 s = row_sum2<TPR>(make_float2(s1.x + s1.y, s2.x + s2.y), red[turn & 1]);
-    __syncwarp();
-    if (tid == 0) {
-      const long long later = row + static_cast<long long>(stages) * step;
-      if (later < c.rows) issue(later, slot);
+    if (!kTwice) {
+      __syncwarp();
+      release();
     }
-    if (++slot == stages) slot = 0;
     const float c1 = mean_of(s.x, n, inv), c2 = mean_of(s.y, n, inv);
     T* dx = static_cast<T*>(c.dx) + row * c.lddx;
 #pragma unroll
-    for (int q = 0; q < L::NV; ++q) {
-      if (kMode != kExactRow && L::column(tid, q, 0) >= c.cols) break;
-#pragma unroll
-      for (int i = 0; i < L::H; ++i) {
-        const float2 v = fma2(xh[q][i], both(-c2), add2(g[q][i], both(-c1)));
-        g[q][i] = c.dr ? fma2(v, both(rstd), dr[q][i]) : mul2(v, both(rstd));
+    for (int q0 = 0; q0 < L::NV; q0 += NQ) {
+      if (kTwice) {
+        take(q0);
+        take_dr(q0);
       }
-      put_row<T, TPR, EPT, kMode>(dx, c.cols, tid, q, g[q]);
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) {
+        if (past(q0 + q)) break;
+        if (kTwice) {
+          normalise(xh[q]);
+          weigh(q0 + q, g[q]);
+        }
+#pragma unroll
+        for (int i = 0; i < L::H; ++i) {
+          const float2 v = fma2(xh[q][i], both(-c2), add2(g[q][i], both(-c1)));
+          g[q][i] = c.dr ? fma2(v, both(rstd), dr[q][i]) : mul2(v, both(rstd));
+        }
+        put_row<T, TPR, EPT, kMode>(dx, c.cols, tid, q0 + q, g[q]);
+      }
+    }
+    if (kTwice) {
+      row_barrier<TPR>();
+      release();
     }
     mean = next_mean;
     rstd = next_rstd;
@@ -687,7 +732,8 @@ __global__ void __launch_bounds__(RingCfg<TPR, EPT, true>::kThreads, 1)
   }
 }
 
-// Rows of any length, in two passes: the row's mean(g) and mean(g xhat), a CTA
+// Rows too long for a slot (above 16384 columns; fp32 with dr above 13,000 or
+// so), and those below 64 bytes, in two passes: the row's mean(g) and mean(g xhat), a CTA
 // a row; then dx and the column sums, a CTA 256 columns of a chunk of rows.
 // The second reading of x and dy is the price of rows that no CTA can hold.
 template <typename T>
@@ -920,7 +966,7 @@ struct BackwardLaunch {
   template <typename T, typename W, int kMode>
   bool any() {
     return ring<T, W, 32, 8, kMode>() || ring<T, W, 128, 16, kMode>() || ring<T, W, 256, 16, kMode>() ||
-           ring<T, W, 512, 16, kMode>();
+           ring<T, W, 512, 16, kMode>() || ring<T, W, 512, 32, kMode>();
   }
   template <typename T>
   void two_passes(bool vec) {

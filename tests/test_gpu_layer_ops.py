@@ -280,6 +280,22 @@ def test_layer_norm_backward_shapes(oz, rows, cols, dtype, wdtype):
             assert worst(g, v, e) <= 1
 
 
+# Several rows to a CTA, each taken from its slot twice; in place, as the skip connection's gradient allows.
+@pytest.mark.parametrize("rows, cols, dtype, wdtype", [(500, 8200, BF16, BF16), (470, 9001, F16, F32), (330, 16384, BF16, F32),
+                                                       (320, 16383, BF16, BF16), (310, 10000, F32, F32)])
+def test_layer_norm_backward_of_many_long_rows(oz, rows, cols, dtype, wdtype):
+    x, w = hidden(rows, cols, dtype, 250), vec(cols, wdtype, 251)
+    dy, dr = rnd(rows, cols, dtype, 252), rnd(rows, cols, dtype, 253)
+    (_, mean, rstd), _ = norm64(x, w)
+    mean, rstd = mean.float(), rstd.float()
+    for extra in (None, dr):
+        want, bounds = norm_backward64(dy, x, mean, rstd, w, extra)
+        for out in (None, extra):
+            got = oz.layer_norm_backward(dy, x, mean, rstd, w, dresidual=extra, out=out)
+            for g, v, e in zip(got, want, bounds):
+                assert worst(g, v, e) <= 1
+
+
 @pytest.mark.parametrize("cols, pad, offset", [(64, 8, 0), (64, 3, 0), (61, 0, 5), (520, 8, 1), (1000, 0, 4),
                                                (4099, 5, 0)])
 @pytest.mark.parametrize("dtype", [BF16, F32])
