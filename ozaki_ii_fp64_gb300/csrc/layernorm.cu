@@ -121,7 +121,9 @@ __device__ __forceinline__ float mean_of(float s, float n, float inv) {
 
 constexpr int cta_threads(int tpr) { return tpr < 128 ? 128 : tpr; }
 
-// One row per TPR threads, NV vectors each.
+// One row per TPR threads, NV vectors each, straight to registers: for fewer
+// rows than the ring's groups, where a row's latency is the time (1 x 4096
+// bf16: 4.0 us a call, the launch and two sums).
 template <typename T, int VEC, int TPR, int NV>
 __global__ void __launch_bounds__(cta_threads(TPR)) norm_forward_kernel(const NormCall c, int vec) {
   __shared__ __align__(16) float red[2][32];
@@ -187,7 +189,9 @@ __global__ void __launch_bounds__(cta_threads(TPR)) norm_forward_kernel(const No
 // the row in registers, which the first sum's barrier says.  The parameters
 // lie in shared memory too, once for all groups: read through L1, what the
 // ring leaves of it did not hold them (16384 x 8192 bf16: 107 us, 84 % of the
-// stalls on those loads).
+// stalls on those loads).  Bound by HBM: 16384 x 8192 bf16 87 us, 6.15 TB/s,
+// 0.91 of the copy rate; 1021 x 5003 f32 in rows of no alignment 16 us, bound
+// by its element-by-element loads and stores.
 // ---------------------------------------------------------------------------
 template <int TPR, int EPT, bool kBackward>
 struct RingCfg {
@@ -467,7 +471,8 @@ __global__ void __launch_bounds__(RingCfg<TPR, EPT, false>::kThreads, 1)
   }
 }
 
-// Rows of any length, read three times (from L2 after the first).
+// Rows of more than 32,768 columns, or too long for two slots: read three times
+// (from L2 after the first).
 constexpr int kLong = 1024;
 template <typename T>
 __global__ void __launch_bounds__(kLong) norm_forward_long_kernel(const NormCall c) {
@@ -533,9 +538,9 @@ __device__ __forceinline__ float2 row_sum2(float2 s, float2* red) {
 // Up to 8192 columns a thread keeps its 16 elements of x and dy from the sums
 // to dx; with 32 (and their 64 column sums) it takes them from the slot twice,
 // and the slot is free after dx.  16384 x 4096 bf16 with dr: 91.6 us, 0.87 of
-// the copy rate (two reads in three bytes, latency of 512 threads); 8192 x
-// 16384 bf16: 150 us where the two passes below took 413; with dr and fp32
-// weights, one slot, 292; 777 x 2051 f16, odd rows: 12.2 (5 rows an SM, each
+// the copy rate (its 512 threads, all that the column sums leave registers for,
+// wait for shared memory); 8192 x 16384 bf16: 150 us where the two passes below
+// took 413; with dr and fp32 weights, room for one slot, 292; 777 x 2051 f16, odd rows: 12.2 (5 rows an SM, each
 // its latency; element by element).
 template <typename T, typename W, int TPR, int EPT, int kMode>
 __global__ void __launch_bounds__(RingCfg<TPR, EPT, true>::kThreads, 1)
