@@ -136,20 +136,18 @@ __device__ __forceinline__ uint4 pack16(const float* v) {
 constexpr float kGeluC = 0.7978845608028654f;  // sqrt(2 / pi)
 constexpr float kGeluA = 0.044715f;
 
-// The normal distribution function Phi(z) = 1/2 (1 + erf(z / sqrt 2)) and
-// e^(-z^2 / 2), by the rational approximation 7.1.26 of Abramowitz and
-// Stegun's Handbook: erfc(x) = (a1 t + ... + a5 t^5) e^(-x^2) with t =
-// 1 / (1 + p x), within 1.5e-7 for x >= 0.  One reciprocal and one exponential
-// serve Phi and its density; on the negative side the tail itself is formed,
-// without cancellation.
-__device__ __forceinline__ float normal_cdf(float z, float& density) {
+// The normal distribution function Phi(z) = 1/2 (1 + erf(z / sqrt 2)), by the
+// rational approximation 7.1.26 of Abramowitz and Stegun's Handbook: erfc(x) =
+// (a1 t + ... + a5 t^5) e^(-x^2) with t = 1 / (1 + p x), within 1.5e-7 for
+// x >= 0.  On the negative side the tail itself is formed, without
+// cancellation.
+__device__ __forceinline__ float normal_cdf(float z) {
   const float t = __fdividef(1.f, fmaf(0.3275911f * 0.70710678118654752f, fabsf(z), 1.f));
   float q = fmaf(t, 0.5f * 1.061405429f, 0.5f * -1.453152027f);
   q = fmaf(t, q, 0.5f * 1.421413741f);
   q = fmaf(t, q, 0.5f * -0.284496736f);
   q = fmaf(t, q, 0.5f * 0.254829592f);
-  density = __expf(-0.5f * z * z);
-  q *= t * density;
+  q *= t * __expf(-0.5f * z * z);
   return z < 0.f ? q : 1.f - q;
 }
 
@@ -158,12 +156,11 @@ __device__ __forceinline__ float normal_cdf(float z, float& density) {
 // exponential and quotient are within a few 2^-20 of the result here, against
 // the 2^-9 and 2^-12 that its 16-bit rounding takes.
 __device__ __forceinline__ float activate(float z, int act) {
-  float e;
   switch (act) {
     case kActRelu:
       return z < 0.f ? 0.f : z;
     case kActGelu:
-      return z * normal_cdf(z, e);
+      return z * normal_cdf(z);
     case kActGeluTanh:
       return __fdividef(z, 1.f + __expf(-2.f * kGeluC * z * fmaf(kGeluA * z, z, 1.f)));
     case kActSilu:
@@ -197,7 +194,7 @@ __device__ __forceinline__ float2 activation_slope2(float2 z) {
   const float2 zc = make_float2(fminf(fmaxf(z.x, -64.f), 64.f), fminf(fmaxf(z.y, -64.f), 64.f));
   if constexpr (kAct == kActRelu) {
     return make_float2(z.x > 0.f ? 1.f : 0.f, z.y > 0.f ? 1.f : 0.f);
-  } else if constexpr (kAct == kActGelu) {  // Phi(z) + z phi(z), as in normal_cdf
+  } else if constexpr (kAct == kActGelu) {  // Phi(z) + z phi(z); one exponential serves both
     const float2 a = make_float2(fabsf(z.x), fabsf(z.y));
     const float2 t = reciprocal2(fma2(a, both(0.3275911f * 0.70710678118654752f), one));
     float2 q = fma2(t, both(0.5f * 1.061405429f), both(0.5f * -1.453152027f));
