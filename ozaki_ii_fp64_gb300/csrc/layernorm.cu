@@ -12,6 +12,7 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "layer.cuh"
+#include "slot_wait.cuh"
 
 namespace ozemu {
 
@@ -84,12 +85,6 @@ __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   return v;
-}
-
-// Barrier of the TPR threads of a row, one of the CTA's groups of that many.
-template <int TPR>
-__device__ __forceinline__ void row_barrier() {
-  asm volatile("bar.sync %0, %1;" ::"r"(static_cast<int>(threadIdx.x) / TPR + 1), "n"(TPR) : "memory");
 }
 
 // Sum over the TPR threads of a row.  TPR = 32: one warp, no barrier.  Else
@@ -232,22 +227,6 @@ __device__ __forceinline__ void load_params16(const void* base, int j, float2* v
   if constexpr (sizeof(W) > sizeof(T)) unpack16<W>(p[1], v + 2);
 }
 
-// Waits for a slot.  False: give up (this thread leaves the kernel; the thread
-// that issues the group's copies first lets those in flight land).
-template <int TPR>
-__device__ __forceinline__ bool ring_wait(uint64_t* full, int turn, int slot, int stages, int issued,
-                                          volatile int* abort_word, uint32_t* flags) {
-  if (mbar_wait(&full[slot], (turn / stages) & 1, abort_word, flags)) return true;
-  if (threadIdx.x % TPR == 0) {
-    for (int i = turn; i < issued; ++i) {
-      const uint64_t t0 = globaltimer();
-      while (!mbar_try_wait(&full[i % stages], (i / stages) & 1) && globaltimer() - t0 < kWaitLimitNs) {
-      }
-    }
-  }
-  return false;
-}
-
 // The ring's rows: any start, 16-byte rows, and 16-byte rows of exactly TPR EPT
 // columns, which need no comparison for each vector (backward at 16384 x 4096
 // bf16: 100 -> 92 us; forward it made no difference and is not built).
@@ -382,7 +361,7 @@ __global__ void __launch_bounds__(RingCfg<TPR, EPT, false>::kThreads, 1)
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ __align__(16) float red_all[R::kGroups][2][TPR < 128 ? 4 : TPR / 32];
   __shared__ uint64_t bars[R::kGroups][kMaxStages];
-  __shared__ int abort_word;
+  __shared__ int gave_up[R::kGroups][2], abort_word;
   const int tid = threadIdx.x % TPR, group = threadIdx.x / TPR;
   const uint32_t bytes = slot_bytes_of<T, kMode>(c.cols);
   const float n = static_cast<float>(c.cols);
@@ -402,6 +381,7 @@ __global__ void __launch_bounds__(RingCfg<TPR, EPT, false>::kThreads, 1)
     ++issued;
   };
   if (threadIdx.x == 0) abort_word = 0;
+  if (tid < 2) gave_up[group][tid] = 0;
   chain_next();
   if (tid == 0) {
     for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
@@ -415,7 +395,7 @@ __global__ void __launch_bounds__(RingCfg<TPR, EPT, false>::kThreads, 1)
   __syncthreads();
   int slot = 0, turn = 0;
   for (long long row = first; row < c.rows; row += step, ++turn) {
-    if (!ring_wait<TPR>(full, turn, slot, stages, issued, &abort_word, c.flags)) return;
+    if (!slot_wait<TPR>(&full[slot], (turn / stages) & 1, &gave_up[group][turn & 1], &abort_word, c.flags)) break;
     float2 d[L::NV][L::H];
     take_row<T, TPR, EPT, kMode>(slots + slot * bytes, c.x, c.ldx, row, c.rows, c.cols, tid, d);
     float2 s = make_float2(0.f, 0.f);
@@ -424,6 +404,7 @@ __global__ void __launch_bounds__(RingCfg<TPR, EPT, false>::kThreads, 1)
 #pragma unroll
       for (int i = 0; i < L::H; ++i) s = add2(s, d[q][i]);
     const float mean = mean_of(row_sum<TPR>(s.x + s.y, red[0]), n, inv);
+    if (!group_goes_on<TPR>(&gave_up[group][turn & 1])) break;
     __syncwarp();
     if (tid == 0) {
       const long long later = row + static_cast<long long>(stages) * step;
@@ -469,6 +450,7 @@ __global__ void __launch_bounds__(RingCfg<TPR, EPT, false>::kThreads, 1)
       if (c.rstd) c.rstd[row] = rstd;
     }
   }
+  if (tid == 0) let_copies_land(full, turn, stages, issued);  // none, unless the group gave up
 }
 
 // Rows of more than 32,768 columns, or too long for two slots: read three times
@@ -550,7 +532,7 @@ __global__ void __launch_bounds__(RingCfg<TPR, EPT, true>::kThreads, 1)
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ __align__(16) float2 red_all[R::kGroups][2][TPR < 128 ? 4 : TPR / 32];
   __shared__ uint64_t bars[R::kGroups][kMaxStages];
-  __shared__ int abort_word;
+  __shared__ int gave_up[R::kGroups][2], abort_word;
   const int tid = threadIdx.x % TPR, group = threadIdx.x / TPR;
   const uint32_t bytes = slot_bytes_of<T, kMode>(c.cols), slot_bytes = bytes * (c.dr ? 3 : 2);
   const float n = static_cast<float>(c.cols);
@@ -582,6 +564,7 @@ __global__ void __launch_bounds__(RingCfg<TPR, EPT, true>::kThreads, 1)
     ++issued;
   };
   if (threadIdx.x == 0) abort_word = 0;
+  if (tid < 2) gave_up[group][tid] = 0;
   chain_next();
   if (tid == 0) {
     for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
@@ -604,7 +587,7 @@ __global__ void __launch_bounds__(RingCfg<TPR, EPT, true>::kThreads, 1)
       next_mean = c.mean[row + step];
       next_rstd = c.rstd[row + step];
     }
-    if (!ring_wait<TPR>(full, turn, slot, stages, issued, &abort_word, c.flags)) return;
+    if (!slot_wait<TPR>(&full[slot], (turn / stages) & 1, &gave_up[group][turn & 1], &abort_word, c.flags)) break;
     const uint8_t* in = slots + slot * slot_bytes;
     float2 xh[NQ][L::H], g[NQ][L::H], dr[NQ][L::H];
     auto take = [&](int q0) {
@@ -655,6 +638,7 @@ __global__ void __launch_bounds__(RingCfg<TPR, EPT, true>::kThreads, 1)
     };
     if (!kTwice) take_dr(0);
     const float2 s = row_sum2<TPR>(make_float2(s1.x + s1.y, s2.x + s2.y), red[turn & 1]);
+    if (!group_goes_on<TPR>(&gave_up[group][turn & 1])) break;
     if (!kTwice) {
       __syncwarp();
       release();
@@ -689,6 +673,7 @@ __global__ void __launch_bounds__(RingCfg<TPR, EPT, true>::kThreads, 1)
     mean = next_mean;
     rstd = next_rstd;
   }
+  if (tid == 0) let_copies_land(full, turn, stages, issued);  // none, unless the group gave up
 
   // This CTA's sums: part[0][cta][.] of dw, part[1][cta][.] of db.
   float* pw = part + static_cast<long long>(blockIdx.x) * c.cols;
