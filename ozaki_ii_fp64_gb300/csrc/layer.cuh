@@ -136,25 +136,39 @@ __device__ __forceinline__ uint4 pack16(const float* v) {
 constexpr float kGeluC = 0.7978845608028654f;  // sqrt(2 / pi)
 constexpr float kGeluA = 0.044715f;
 
-// The normal distribution function Phi(z) = 1/2 (1 + erf(z / sqrt 2)), by the
-// rational approximation 7.1.26 of Abramowitz and Stegun's Handbook: erfc(x) =
-// (a1 t + ... + a5 t^5) e^(-x^2) with t = 1 / (1 + p x), within 1.5e-7 for
-// x >= 0.  On the negative side the tail itself is formed, without
-// cancellation.
+// The normal distribution's tail Phi(-a) = e^(-a^2/2) t P(t), t = 1 / (1 + p a),
+// for a >= 0: the form of 7.1.26 of Abramowitz and Stegun's Handbook with two
+// more coefficients, fitted by linear programming so that the largest error
+// relative to Phi(-a) over 0 <= a <= 14.5 is least: 6.0e-7 (2^-20.6).  (Their
+// five coefficients keep the absolute error below 1.5e-7, which is 5e-4 of the
+// tail at a = 4 and 4e-3 at 6: more than the rounding to 16 bits.)  The fp32
+// evaluation adds some 1e-6, the exponential a^2 2^-24.  The two more steps cost
+// the pass over the slopes (8192 x 16384) 4 us of 161, the product 8192 x 4096 ->
+// 16384 2 of 573.
+constexpr float kTailP = 0.265f;
+__device__ __forceinline__ constexpr float tail_coefficient(int i) {
+  constexpr float c[7] = {0.105598755f,   0.107850529f, 0.0828776509f, 0.142668769f,
+                          -0.0666030422f, 0.195441261f, -0.0678342208f};
+  return c[i];
+}
+
+// The normal distribution function Phi(z) = 1/2 (1 + erf(z / sqrt 2)).  On the
+// negative side the tail itself is formed, without cancellation.
 __device__ __forceinline__ float normal_cdf(float z) {
-  const float t = __fdividef(1.f, fmaf(0.3275911f * 0.70710678118654752f, fabsf(z), 1.f));
-  float q = fmaf(t, 0.5f * 1.061405429f, 0.5f * -1.453152027f);
-  q = fmaf(t, q, 0.5f * 1.421413741f);
-  q = fmaf(t, q, 0.5f * -0.284496736f);
-  q = fmaf(t, q, 0.5f * 0.254829592f);
+  const float t = __fdividef(1.f, fmaf(kTailP, fabsf(z), 1.f));
+  float q = tail_coefficient(6);
+#pragma unroll
+  for (int i = 5; i >= 0; --i) q = fmaf(t, q, tail_coefficient(i));
   q *= t * __expf(-0.5f * z * z);
   return z < 0.f ? q : 1.f - q;
 }
 
 // act(z).  NaN passes through every activation (relu by its comparison).
-// gelu_tanh is written with 1/2 (1 + tanh u) = 1 / (1 + e^(-2u)).  The fast
-// exponential and quotient are within a few 2^-20 of the result here, against
-// the 2^-9 and 2^-12 that its 16-bit rounding takes.
+// gelu_tanh is written with 1/2 (1 + tanh u) = 1 / (1 + e^(-2u)).  Where the
+// exponential's argument is a, the fast exponential, the quotient and gelu's tail
+// are together within 2^-19 + (1 + |a|) 2^-22 of the result, relative to it,
+// against the 2^-9 and 2^-12 that its 16-bit rounding takes.  (A quotient by more
+// than 2^126 is 0: silu and gelu_tanh where they are below 2^-119.)
 __device__ __forceinline__ float activate(float z, int act) {
   switch (act) {
     case kActRelu:
@@ -196,11 +210,10 @@ __device__ __forceinline__ float2 activation_slope2(float2 z) {
     return make_float2(z.x > 0.f ? 1.f : 0.f, z.y > 0.f ? 1.f : 0.f);
   } else if constexpr (kAct == kActGelu) {  // Phi(z) + z phi(z); one exponential serves both
     const float2 a = make_float2(fabsf(z.x), fabsf(z.y));
-    const float2 t = reciprocal2(fma2(a, both(0.3275911f * 0.70710678118654752f), one));
-    float2 q = fma2(t, both(0.5f * 1.061405429f), both(0.5f * -1.453152027f));
-    q = fma2(t, q, both(0.5f * 1.421413741f));
-    q = fma2(t, q, both(0.5f * -0.284496736f));
-    q = fma2(t, q, both(0.5f * 0.254829592f));
+    const float2 t = reciprocal2(fma2(a, both(kTailP), one));
+    float2 q = both(tail_coefficient(6));
+#pragma unroll
+    for (int i = 5; i >= 0; --i) q = fma2(t, q, both(tail_coefficient(i)));
     const float2 e = exp2_2(mul2(mul2(z, z), both(-0.5f * 1.4426950408889634f)));
     q = mul2(mul2(q, t), e);
     const float2 p = make_float2(z.x < 0.f ? q.x : 1.f - q.x, z.y < 0.f ? q.y : 1.f - q.y);

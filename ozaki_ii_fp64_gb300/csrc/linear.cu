@@ -958,7 +958,7 @@ __global__ void __launch_bounds__(256) align_rows_kernel(const __grid_constant__
 // time; the partial sums of a column are joined in shared memory in a fixed
 // order.  TX = 4 for few rows (64 at a time, so that one or two turns read
 // them all), else 32.  Bound by HBM and the slopes' instructions: 8192 x 16384
-// bf16 gelu, 805 MB, 157 us (5.1 TB/s).
+// bf16 gelu, 805 MB, 161 us (5.0 TB/s).
 template <typename T, int kAct, int TX>
 __global__ void __launch_bounds__(256, 4) slope_kernel(const T* dy, long long lddy, const T* pre, long long ldpre,
                                                        T* dz, long long lddz, float* part, T* db, int m, int n,
