@@ -961,8 +961,9 @@ struct BackwardLaunch {
   template <typename T>
   void two_passes(bool vec) {
     float2* means = reinterpret_cast<float2*>(static_cast<float*>(c.ws) + 2LL * kMaxParts * c.cols);
-    launch_chained(norm_backward_means_kernel<T>, dim3(std::min(c.rows, 65536)), 512, 0, stream, 0, c, means, vec,
-                   aligned16(c.weight));
+    error = launch_chained(norm_backward_means_kernel<T>, dim3(std::min(c.rows, 65536)), 512, 0, stream, 0, c, means, vec,
+                           aligned16(c.weight));
+    if (error != cudaSuccess) return;
     const int across = (c.cols + 255) / 256;
     const int chunks = std::max(1, std::min({kMaxParts, 1216 / across, (c.rows + 7) / 8}));
     const int chunk = (c.rows + chunks - 1) / chunks;
@@ -1015,13 +1016,13 @@ cudaError_t launch_layer_norm_backward(const NormGradCall& c, cudaStream_t strea
   }
   if (c.dweight || c.dbias) {
     const dim3 grid((c.cols + 31) / 32, 2);
-    with_type(c.param_type, [&](auto w) {
+    return with_type(c.param_type, [&](auto w) {
       using W = decltype(w);
       return launch_chained(join_parts_kernel<W>, grid, 1024, 0, stream, 0, static_cast<const float*>(c.ws), l.used,
                             kMaxParts, c.cols, static_cast<W*>(c.dweight), static_cast<W*>(c.dbias));
     });
   }
-  return cudaGetLastError();
+  return cudaSuccess;
 }
 
 }  // namespace ozemu

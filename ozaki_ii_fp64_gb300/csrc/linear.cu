@@ -1048,7 +1048,7 @@ size_t aligned_copy_bytes(const Matrix& x) {
 
 // Makes those copies (where they are needed) of x and y at ws, in one launch,
 // and points x and y at them.
-void align_operands(Matrix* x, Matrix* y, uint8_t* ws, cudaStream_t stream) {
+cudaError_t align_operands(Matrix* x, Matrix* y, uint8_t* ws, cudaStream_t stream) {
   AlignPair both;
   int count = 0;
   long long most = 0;
@@ -1062,9 +1062,9 @@ void align_operands(Matrix* x, Matrix* y, uint8_t* ws, cudaStream_t stream) {
     m->ld = pad8(m->cols);
     ws += bytes;
   }
-  if (count == 0) return;
-  launch_chained(align_rows_kernel, dim3(static_cast<unsigned>(std::min<long long>((most + 7) / 8, 152 * 16)), 1, count),
-                 256, 0, stream, 0, both);
+  if (count == 0) return cudaSuccess;
+  return launch_chained(align_rows_kernel, dim3(static_cast<unsigned>(std::min<long long>((most + 7) / 8, 152 * 16)), 1, count),
+                        256, 0, stream, 0, both);
 }
 
 // Map of an operand read in blocks of `box` rows of 64 elements; what lies
@@ -1337,7 +1337,8 @@ cudaError_t run_products(Ready a, Ready b, uint32_t* flags, cudaStream_t stream)
 template <typename T>
 cudaError_t linear_t(const LinearCall& c, cudaStream_t stream) {
   Matrix x = {c.x, c.ldx, c.m, c.k}, w = {c.w, c.ldw, c.n, c.k};
-  align_operands(&x, &w, static_cast<uint8_t*>(c.ws), stream);
+  const cudaError_t s = align_operands(&x, &w, static_cast<uint8_t*>(c.ws), stream);
+  if (s != cudaSuccess) return s;
   const Epilogue e = {c.bias, c.res, c.ldr, c.pre, c.ldpre, c.y, c.ldy, c.act, 0};
   return run_product<T>(ready(c.m, c.n, c.k, x, false, w, false, e), c.flags, stream);
 }
@@ -1371,24 +1372,25 @@ BackwardPlan backward_plan(const LinearGradCall& c) {
 }
 
 template <typename T, int kAct>
-void run_slope(const LinearGradCall& c, const BackwardPlan& p, T* dz, float* part, cudaStream_t stream) {
+cudaError_t run_slope(const LinearGradCall& c, const BackwardPlan& p, T* dz, float* part, cudaStream_t stream) {
   const int vec = (rows_aligned(c.dy, c.lddy, c.m) ? 1 : 0) |
                   (kAct != kActNone && rows_aligned(c.pre, c.ldpre, c.m) ? 2 : 0);
   T* db = static_cast<T*>(c.db);
   const bool whole = p.chunks == 1;
   const int tx = c.m <= kFewSlopeRows ? 4 : 32;
-  launch_chained(tx == 4 ? slope_kernel<T, kAct, 4> : slope_kernel<T, kAct, 32>,
-                 dim3((c.n + 8 * tx - 1) / (8 * tx), p.chunks), 256, 0, stream, 0, static_cast<const T*>(c.dy), c.lddy,
-                 static_cast<const T*>(c.pre), c.ldpre, dz, pad8(c.n), db && !whole ? part : nullptr,
-                 whole ? db : nullptr, c.m, c.n, p.chunk, vec);
-  if (db && !whole)
-    launch_chained(join_parts_kernel<T>, dim3((c.n + 31) / 32), 1024, 0, stream, 0, part, p.chunks, p.chunks, c.n, db,
-                   nullptr);
+  const cudaError_t s = launch_chained(
+      tx == 4 ? slope_kernel<T, kAct, 4> : slope_kernel<T, kAct, 32>, dim3((c.n + 8 * tx - 1) / (8 * tx), p.chunks), 256,
+      0, stream, 0, static_cast<const T*>(c.dy), c.lddy, static_cast<const T*>(c.pre), c.ldpre, dz, pad8(c.n),
+      db && !whole ? part : nullptr, whole ? db : nullptr, c.m, c.n, p.chunk, vec);
+  if (s != cudaSuccess || !db || whole) return s;
+  return launch_chained(join_parts_kernel<T>, dim3((c.n + 31) / 32), 1024, 0, stream, 0, part, p.chunks, p.chunks, c.n,
+                        db, nullptr);
 }
 
 template <typename T>
 cudaError_t linear_backward_t(const LinearGradCall& c, cudaStream_t stream) {
   Matrix dz = {c.dy, c.lddy, c.m, c.n}, x = {c.x, c.ldx, c.m, c.k}, w = {c.w, c.ldw, c.n, c.k};
+  cudaError_t s = cudaSuccess;
   if (c.m > 0 && c.n > 0) {
     const BackwardPlan plan = backward_plan(c);
     uint8_t* ws = static_cast<uint8_t*>(c.ws);
@@ -1400,20 +1402,19 @@ cudaError_t linear_backward_t(const LinearGradCall& c, cudaStream_t stream) {
     float* part = reinterpret_cast<float*>(ws + plan.dz);
     if (own || c.db) {
       switch (c.act) {
-        case kActRelu: run_slope<T, kActRelu>(c, plan, own, part, stream); break;
-        case kActGelu: run_slope<T, kActGelu>(c, plan, own, part, stream); break;
-        case kActGeluTanh: run_slope<T, kActGeluTanh>(c, plan, own, part, stream); break;
-        case kActSilu: run_slope<T, kActSilu>(c, plan, own, part, stream); break;
-        default: run_slope<T, kActNone>(c, plan, own, part, stream); break;
+        case kActRelu: s = run_slope<T, kActRelu>(c, plan, own, part, stream); break;
+        case kActGelu: s = run_slope<T, kActGelu>(c, plan, own, part, stream); break;
+        case kActGeluTanh: s = run_slope<T, kActGeluTanh>(c, plan, own, part, stream); break;
+        case kActSilu: s = run_slope<T, kActSilu>(c, plan, own, part, stream); break;
+        default: s = run_slope<T, kActNone>(c, plan, own, part, stream); break;
       }
     }
     Matrix none = {nullptr, 0, 0, 0};
-    align_operands(c.dw ? &x : &none, c.dx ? &w : &none, ws + plan.dz + plan.part, stream);
+    if (s == cudaSuccess) s = align_operands(c.dw ? &x : &none, c.dx ? &w : &none, ws + plan.dz + plan.part, stream);
   } else if (c.db && c.n > 0) {
-    launch_chained(join_parts_kernel<T>, dim3((c.n + 31) / 32), 1024, 0, stream, 0, nullptr, 0, 0, c.n,
-                   static_cast<T*>(c.db), nullptr);
+    s = launch_chained(join_parts_kernel<T>, dim3((c.n + 31) / 32), 1024, 0, stream, 0, nullptr, 0, 0, c.n,
+                       static_cast<T*>(c.db), nullptr);
   }
-  const cudaError_t s = cudaGetLastError();
   if (s != cudaSuccess) return s;
   Epilogue to_dx = {nullptr, nullptr, 0, nullptr, 0, c.dx, c.lddx, kActNone, 0}, to_dw = to_dx;
   to_dw.out = c.dw;
