@@ -967,7 +967,7 @@ struct BackwardLaunch {
     const int across = (c.cols + 255) / 256;
     const int chunks = std::max(1, std::min({kMaxParts, 1216 / across, (c.rows + 7) / 8}));
     const int chunk = (c.rows + chunks - 1) / chunks;
-    used = (c.rows + chunk - 1) / chunk;
+    used = (c.rows - 1) / chunk + 1;  // rows + chunk may pass 2^31
     auto kern = vec ? norm_backward_columns_kernel<T, true> : norm_backward_columns_kernel<T, false>;
     error = launch_chained(kern, dim3(across, used), 256, 0, stream, 0, c, means, static_cast<float*>(c.ws), kMaxParts,
                            chunk);

@@ -51,3 +51,19 @@ def test_each_launch_failure_is_the_calls(launches, what, a, b, c, odd, count):
     for i, (status, tried) in enumerate(failures):
         assert status == NO_MEMORY
         assert tried == grids[:i + 1]  # nothing is launched on what was not made
+
+
+MOST = 2**31 - 2**16  # rows or columns of a norm
+
+
+@pytest.mark.parametrize("what, a, b, c", [
+    ("norm_backward", MOST, 3, 0), ("norm_backward", 2_140_000_000, 1, 0), ("norm_backward", 2_133_400_000, 7, 0),
+    ("norm_backward", MOST, 1000, 0), ("norm_backward", 9, MOST, 0), ("norm", MOST, 3, 0), ("norm", MOST, 1000, 0),
+    ("norm", 9, MOST, 0), ("linear", 1 << 26, 9, 16), ("linear", 9, 1 << 26, 16), ("linear", 300, 300, 1 << 26),
+    ("linear_backward", 1 << 26, 9, 16), ("linear_backward", 9, 1 << 26, 16), ("linear_backward", 300, 300, 1 << 26)])
+def test_grids_at_the_size_limits(launches, what, a, b, c):
+    # CUDA's limits; a grid that wrapped round is above them.
+    (status, grids), *_ = launches(what, a, b, c)
+    assert status == 0
+    for x, y, z in grids:
+        assert 0 < x < 2**31 and 0 < y < 2**16 and 0 < z < 2**16
