@@ -557,7 +557,8 @@ size_t ozemu_linear_backward_bytes(int m, int n, int k, const void* dY, int lddy
  * mean = sum(X)/cols, rstd = (sum (X - mean)^2 / cols + eps)^(-1/2).  weight
  * and bias have cols entries (NULL: 1 and 0), of param_type, which is type or
  * OZEMU_F32.  mean and rstd (rows fp32 values each) are written unless NULL.
- * eps >= 0.  Y (ldy) may be X itself (same leading dimension). */
+ * eps >= 0.  Y (ldy) may be X itself (same leading dimension).  cols = 0 gives
+ * mean = rstd = NaN (0 / 0); rows = 0 is a no-op. */
 int ozemu_layer_norm(int rows, int cols, int type, const void* X, int ldx, int param_type, const void* weight,
                      const void* bias, float eps, void* Y, int ldy, float* mean, float* rstd, cudaStream_t stream);
 

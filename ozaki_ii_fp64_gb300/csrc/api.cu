@@ -1582,7 +1582,15 @@ int ozemu_layer_norm(int rows, int cols, int type, const void* X, int ldx, int p
       !vector_ok(weight, param_type) || !vector_ok(bias, param_type) || !vector_ok(mean, OZEMU_F32) ||
       !vector_ok(rstd, OZEMU_F32))
     return OZEMU_ERR_INVALID_ARG;
-  if (rows == 0 || cols == 0) return OZEMU_OK;
+  if (rows == 0) return OZEMU_OK;
+  if (cols == 0) {  // 0 / 0: every bit of a float set is a NaN
+    for (float* stat : {mean, rstd})
+      if (stat) {
+        const int s = cuda_status(cudaMemsetAsync(stat, 0xFF, static_cast<size_t>(rows) * 4, stream));
+        if (s != OZEMU_OK) return s;
+      }
+    return OZEMU_OK;
+  }
   DeviceState* d = nullptr;
   const int s = device_state(&d);
   if (s != OZEMU_OK) return s;
