@@ -567,7 +567,7 @@ int ozemu_layer_norm(int rows, int cols, int type, const void* X, int ldx, int p
  *   dX = rstd (g - mean(g) - xhat mean(g xhat)) + dR,
  *   dweight = sum over rows of dY xhat,  dbias = sum over rows of dY.
  * dR (rows x cols, lddr; NULL: none) is the gradient that reaches X along a
- * skip connection; dX may be dR or dY itself (same leading dimension).
+ * skip connection; dX may be dR, dY or X itself (same leading dimension).
  * dweight and dbias have param_type; NULL: not computed.  rows = 0 zeroes
  * them. */
 int ozemu_layer_norm_backward(int rows, int cols, int type, const void* dY, int lddy, const void* X, int ldx,

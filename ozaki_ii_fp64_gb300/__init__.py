@@ -809,7 +809,7 @@ def linear(x, w, bias=None, residual=None, activation="none", save_pre=False, ou
     """act(x @ w.T + bias) + residual of bfloat16 or float16 cuda tensors: x m x k, w n x k, bias n, residual m x n.
 
     With save_pre also the pre-activation x @ w.T + bias, rounded, for linear_backward: (y, pre).  out may be
-    residual itself.  On a stream of its own (stream=), the caller orders the inputs' values (wait_stream)."""
+    residual itself, and overlaps no other argument (ValueError).  On a stream of its own (stream=), the caller orders the inputs' values (wait_stream)."""
     return (_native or _layer_calls()).linear(x, w, bias, residual, _activation(activation), save_pre, out, stream)
 
 
@@ -824,7 +824,8 @@ def linear_backward(dy, x, w, pre=None, activation="none", x_grad=True, w_grad=T
 def layer_norm(x, weight=None, bias=None, eps=1e-5, stats=False, out=None, stream=None):
     """Layer norm of the rows of a bfloat16, float16 or float32 cuda matrix; weight and bias in x's type or float32.
 
-    With stats also the fp32 row statistics that layer_norm_backward takes: (y, mean, rstd).  out may be x itself."""
+    With stats also the fp32 row statistics that layer_norm_backward takes: (y, mean, rstd).  out may be x itself, and
+    overlaps no other argument (ValueError)."""
     return (_native or _layer_calls()).layer_norm(x, weight, bias, eps, stats, out, stream)
 
 
@@ -833,6 +834,6 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, dresidual=None, weight_g
     """(dx, dweight, dbias) of layer_norm from its saved statistics (None for those not asked for).
 
     dresidual, the gradient that reaches x along a skip connection, is added to dx; out (dx's memory) may be
-    dresidual or dy itself.  dweight and dbias have weight's type (x's without a weight)."""
+    dresidual, dy or x itself, and overlaps no other argument (ValueError).  dweight and dbias have weight's type (x's without a weight)."""
     return (_native or _layer_calls()).layer_norm_backward(dy, x, mean, rstd, weight, dresidual, weight_grad,
                                                            bias_grad, out, stream)

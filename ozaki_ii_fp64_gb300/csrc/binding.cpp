@@ -12,6 +12,8 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
+#include <climits>
 #include <optional>
 #include <stdexcept>
 #include <string>
@@ -90,6 +92,58 @@ void* vector(const at::Tensor* t, int n, at::ScalarType type, const at::Tensor& 
                   " on " + like.device().str());
   return n > 0 ? t->data_ptr() : nullptr;
 }
+
+// Whether some row of `rows` rows of `width` bytes, `ld` bytes apart from `p`
+// on, shares a byte with one of the other matrix's.
+struct Area {
+  intptr_t p;
+  long long ld;
+  int rows;
+  long long width;
+};
+long long floor_div(long long a, long long b) { return a / b - (a % b < 0); }  // b > 0
+bool share(const Area& a, const Area& b) {
+  if (a.rows == 0 || b.rows == 0 || a.width == 0 || b.width == 0) return false;
+  if (a.p + (a.rows - 1) * a.ld + a.width <= b.p || b.p + (b.rows - 1) * b.ld + b.width <= a.p) return false;
+  // A row at distance d from one of a's meets it where -b.width < d < a.width.
+  // Of the distances d + t ld, t = first ... last, the first above -b.width:
+  auto meets = [&](long long d, long long ld, long long first, long long last) {
+    const long long t = std::max(first, floor_div(-b.width - d, ld) + 1);
+    return t <= last && d + t * ld < a.width;
+  };
+  if (a.ld == b.ld) return meets(b.p - a.p, a.ld, 1 - a.rows, b.rows - 1);
+  for (int i = 0; i < a.rows; ++i)  // matrices that lie within each other in rows of different lengths
+    if (meets(b.p - (a.p + i * a.ld), b.ld, 0, b.rows - 1)) return true;
+  return false;
+}
+
+// An output that the caller gives, against an input: they share nothing, or
+// are the same matrix where the call takes it so.
+class Output {
+ public:
+  Output(const at::Tensor* given, const Matrix& m, int rows, int cols, const at::Tensor& like)
+      : given_(given), at_(area(m, rows, cols, static_cast<int>(like.element_size()))) {}
+  void apart(const at::Tensor* input, const Matrix& m, int rows, int cols, const char* name, bool or_same = false) const {
+    if (!given_ || !input) return;
+    const Area in = area(m, rows, cols, static_cast<int>(input->element_size()));
+    if (or_same && in.p == at_.p && (in.ld == at_.ld || rows <= 1)) return;
+    if (share(at_, in)) throw Refused(std::string("out: overlaps ") + name);
+  }
+  void apart(const at::Tensor* input, void* p, int n, const char* name) const {
+    Matrix m;
+    m.p = p;
+    m.ld = n > 0 ? n : 1;
+    apart(input, m, 1, n, name);
+  }
+
+ private:
+  static Area area(const Matrix& m, int rows, int cols, int size) {
+    return {reinterpret_cast<intptr_t>(m.p), static_cast<long long>(m.ld) * size, m.p ? rows : 0,
+            static_cast<long long>(cols) * size};
+  }
+  const at::Tensor* given_;
+  Area at_;
+};
 
 // The stream of one call.  With a stream given, outputs and workspace are
 // taken on it and the allocator learns of the inputs' use there; ordering
@@ -213,6 +267,11 @@ PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t count) {
     const Matrix mx = matrix(&x, s.m, s.k, x, "x"), mw = matrix(&w, s.n, s.k, x, "w");
     const Matrix mr = matrix(res, s.m, s.n, x, "residual"), mo = matrix(given, s.m, s.n, x, "out");
     void* pb = vector(bias, s.n, x.scalar_type(), x, "bias");
+    const Output o(given, mo, s.m, s.n, x);
+    o.apart(&x, mx, s.m, s.k, "x");
+    o.apart(&w, mw, s.n, s.k, "w");
+    o.apart(bias, pb, s.n, "bias");
+    o.apart(res, mr, s.m, s.n, "residual", true);
     OnStream on(x, a[7], {&x, &w, bias, res, given});
     at::Tensor fresh, pre;
     Matrix my = mo, mp;
@@ -292,6 +351,10 @@ PyObject* layer_norm(PyObject*, PyObject* const* a, Py_ssize_t count) {
     sizes(x, "x", &rows, &cols);
     const Matrix mx = matrix(&x, rows, cols, x, "x"), mo = matrix(given, rows, cols, x, "out");
     void *pw = vector(weight, cols, pt, x, "weight"), *pb = vector(bias, cols, pt, x, "bias");
+    const Output o(given, mo, rows, cols, x);
+    o.apart(&x, mx, rows, cols, "x", true);
+    o.apart(weight, pw, cols, "weight");
+    o.apart(bias, pb, cols, "bias");
     OnStream on(x, a[6], {&x, weight, bias, given});
     at::Tensor fresh, mean, rstd;
     Matrix my = mo;
@@ -327,6 +390,13 @@ PyObject* layer_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t count) {
     const Matrix mr = matrix(dr, rows, cols, x, "dresidual"), mo = matrix(given, rows, cols, x, "out");
     void* pw = vector(weight, cols, pt, x, "weight");
     void *pm = vector(&mean, rows, at::kFloat, x, "mean"), *ps = vector(&rstd, rows, at::kFloat, x, "rstd");
+    const Output o(given, mo, rows, cols, x);
+    o.apart(&dy, md, rows, cols, "dy", true);
+    o.apart(&x, mx, rows, cols, "x", true);
+    o.apart(dr, mr, rows, cols, "dresidual", true);
+    o.apart(weight, pw, cols, "weight");
+    o.apart(&mean, pm, rows, "mean");
+    o.apart(&rstd, ps, rows, "rstd");
     OnStream on(x, a[9], {&dy, &x, &mean, &rstd, weight, dr, given});
     at::Tensor fresh, dw, db;
     Matrix mdx = mo;

@@ -1,4 +1,4 @@
-"""Edges of the layer operators' calls: what empty rows give."""
+"""Edges of the layer operators' calls: empty rows, outputs in the place of inputs."""
 
 import pytest
 
@@ -30,3 +30,33 @@ def test_statistics_of_rows_without_columns(oz, rows):
         assert y.shape == (rows, 0)
         assert bool(torch.isnan(mean).all()) and bool(torch.isnan(rstd).all())
     assert oz.get_status() == oz.OZEMU_OK
+
+
+@pytest.mark.parametrize("rows, cols", [(5, 7), (700, 520), (3000, 1001), (1600, 4096), (500, 8200), (320, 16383), (100, 20001),
+                                        (60, 24000)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_norm_gradient_in_the_place_of_x(oz, rows, cols, dtype):
+    gen = torch.Generator(device=DEV).manual_seed(3)
+    x, dy, dr = (torch.randn(rows, cols, generator=gen, device=DEV).to(dtype) for _ in range(3))
+    w = torch.randn(cols, generator=gen, device=DEV)
+    _, mean, rstd = oz.layer_norm(x, w, stats=True)
+    for extra in (None, dr):
+        want = oz.layer_norm_backward(dy, x, mean, rstd, w, dresidual=extra)
+        place = x.clone()
+        got = oz.layer_norm_backward(dy, place, mean, rstd, w, dresidual=extra, out=place)
+        assert got[0] is place
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+    assert oz.get_status() == oz.OZEMU_OK
+
+
+def test_overlapping_output_is_refused(oz):
+    x, w = torch.randn(64, 64, device=DEV).to(BF16), torch.randn(64, 64, device=DEV).to(BF16)
+    before = x.clone()
+    for call in (lambda: oz.linear(x, w, out=x), lambda: oz.linear(x, w, out=w), lambda: oz.layer_norm(x[1:], out=x[:-1])):
+        with pytest.raises(ValueError, match="overlaps"):
+            call()
+    assert torch.equal(x, before)
+    wide = torch.randn(64, 192, device=DEV).to(BF16)  # columns of one matrix share nothing
+    y = oz.linear(wide[:, :64], w, residual=wide[:, 64:128], out=wide[:, 128:])
+    assert torch.equal(y, oz.linear(wide[:, :64].clone(), w, residual=wide[:, 64:128].clone()))
