@@ -775,6 +775,10 @@ def crt_f64_mixed(m, n, r, residues, shifts_a, shifts_b, out=None, stream=None):
 
 
 # ------------------------------------- layer operators: linear, layer norm
+#
+# None of these calls records a graph for automatic gradients: a result never requires one, and an input that does is
+# answered with a UserWarning unless gradients are switched off (torch.no_grad()).  The gradients are the _backward
+# calls'.
 
 ACTIVATIONS = {"none": OZEMU_ACT_NONE, "relu": OZEMU_ACT_RELU, "gelu": OZEMU_ACT_GELU,
                "gelu_tanh": OZEMU_ACT_GELU_TANH, "silu": OZEMU_ACT_SILU}
@@ -809,7 +813,8 @@ def linear(x, w, bias=None, residual=None, activation="none", save_pre=False, ou
     """act(x @ w.T + bias) + residual of bfloat16 or float16 cuda tensors: x m x k, w n x k, bias n, residual m x n.
 
     With save_pre also the pre-activation x @ w.T + bias, rounded, for linear_backward: (y, pre).  out may be
-    residual itself, and overlaps no other argument (ValueError).  On a stream of its own (stream=), the caller orders the inputs' values (wait_stream)."""
+    residual itself, and overlaps no other argument (ValueError).  On a stream of its own (stream=), the caller orders the inputs' values (wait_stream).  No graph
+    is recorded for automatic gradients: linear_backward computes them."""
     return (_native or _layer_calls()).linear(x, w, bias, residual, _activation(activation), save_pre, out, stream)
 
 
@@ -825,7 +830,8 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, stats=False, out=None, strea
     """Layer norm of the rows of a bfloat16, float16 or float32 cuda matrix; weight and bias in x's type or float32.
 
     With stats also the fp32 row statistics that layer_norm_backward takes: (y, mean, rstd).  out may be x itself, and
-    overlaps no other argument (ValueError)."""
+    overlaps no other argument (ValueError).  No graph is recorded for automatic gradients: layer_norm_backward computes
+    them."""
     return (_native or _layer_calls()).layer_norm(x, weight, bias, eps, stats, out, stream)
 
 

@@ -7,6 +7,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -179,6 +180,20 @@ class OnStream {
   std::optional<c10::cuda::CUDAStreamGuard> guard_;
 };
 
+// The calls record no graph: what requires a gradient would miss it without a
+// word, so they say it (as a Python warning; an error where those are errors).
+void no_graph(const char* call, const char* instead, std::initializer_list<const at::Tensor*> inputs) {
+  if (!c10::GradMode::is_enabled()) return;
+  for (const at::Tensor* t : inputs)
+    if (t && t->requires_grad()) {
+      const std::string text = std::string(call) +
+                               ": an input requires a gradient, but this call records no graph for automatic "
+                               "gradients; " + instead;
+      if (PyErr_WarnEx(PyExc_UserWarning, text.c_str(), 2) < 0) throw Raised();
+      return;
+    }
+}
+
 // A workspace of `bytes` on the current stream, 256-byte aligned.
 struct Scratch {
   Scratch(const at::Tensor& like, size_t n) : bytes(n) {
@@ -273,6 +288,7 @@ PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t count) {
     o.apart(bias, pb, s.n, "bias");
     o.apart(res, mr, s.m, s.n, "residual", true);
     OnStream on(x, a[7], {&x, &w, bias, res, given});
+    no_graph("linear", "linear_backward computes them (torch.no_grad() says that none are wanted)", {&x, &w, bias, res});
     at::Tensor fresh, pre;
     Matrix my = mo, mp;
     if (!given) {
@@ -312,6 +328,7 @@ PyObject* linear_backward(PyObject*, PyObject* const* a, Py_ssize_t count) {
     const Matrix md = matrix(&dy, s.m, s.n, x, "dy"), mx = matrix(&x, s.m, s.k, x, "x");
     const Matrix mw = matrix(&w, s.n, s.k, x, "w"), mp = matrix(pre, s.m, s.n, x, "pre");
     OnStream on(x, a[8], {&dy, &x, &w, pre});
+    no_graph("linear_backward", "torch.no_grad() says that none are wanted", {&dy, &x, &w, pre});
     at::Tensor dx, dw, db;
     if (truth(a[5])) dx = at::empty({s.m, s.k}, x.options());
     if (truth(a[6])) dw = at::empty({s.n, s.k}, x.options());
@@ -356,6 +373,8 @@ PyObject* layer_norm(PyObject*, PyObject* const* a, Py_ssize_t count) {
     o.apart(weight, pw, cols, "weight");
     o.apart(bias, pb, cols, "bias");
     OnStream on(x, a[6], {&x, weight, bias, given});
+    no_graph("layer_norm", "layer_norm_backward computes them (torch.no_grad() says that none are wanted)",
+             {&x, weight, bias});
     at::Tensor fresh, mean, rstd;
     Matrix my = mo;
     if (!given) {
@@ -398,6 +417,7 @@ PyObject* layer_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t count) {
     o.apart(&mean, pm, rows, "mean");
     o.apart(&rstd, ps, rows, "rstd");
     OnStream on(x, a[9], {&dy, &x, &mean, &rstd, weight, dr, given});
+    no_graph("layer_norm_backward", "torch.no_grad() says that none are wanted", {&dy, &x, weight, dr});
     at::Tensor fresh, dw, db;
     Matrix mdx = mo;
     if (!given) {

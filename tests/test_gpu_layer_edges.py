@@ -1,5 +1,7 @@
 """Edges of the layer operators' calls: empty rows, outputs in the place of inputs."""
 
+import warnings
+
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -60,3 +62,27 @@ def test_overlapping_output_is_refused(oz):
     wide = torch.randn(64, 192, device=DEV).to(BF16)  # columns of one matrix share nothing
     y = oz.linear(wide[:, :64], w, residual=wide[:, 64:128], out=wide[:, 128:])
     assert torch.equal(y, oz.linear(wide[:, :64].clone(), w, residual=wide[:, 64:128].clone()))
+
+
+def test_inputs_that_require_gradients_are_answered_with_a_warning(oz):
+    x, w = torch.randn(4, 64, device=DEV).to(BF16), torch.nn.Parameter(torch.randn(32, 64, device=DEV).to(BF16))
+    gain = torch.nn.Parameter(torch.ones(64, device=DEV))
+    dy, mean, rstd = torch.ones(4, 32, dtype=BF16, device=DEV), torch.zeros(4, device=DEV), torch.ones(4, device=DEV)
+    calls = {"linear": lambda: oz.linear(x, w), "linear_backward": lambda: oz.linear_backward(dy, x, w)[0],
+             "layer_norm": lambda: oz.layer_norm(x, gain),
+             "layer_norm_backward": lambda: oz.layer_norm_backward(x, x, mean, rstd, gain)[0]}
+    for name, call in calls.items():
+        with pytest.warns(UserWarning, match="^%s: an input requires a gradient" % name):
+            loud = call()
+        assert not loud.requires_grad
+        with warnings.catch_warnings():
+            warnings.simplefilter("error")
+            with pytest.raises(UserWarning):
+                call()
+            with torch.no_grad():
+                assert torch.equal(call(), loud)
+    with warnings.catch_warnings():  # and none where nothing requires one
+        warnings.simplefilter("error")
+        oz.linear(x, w.detach())
+        oz.layer_norm(x, gain.detach())
+    assert oz.get_status() == oz.OZEMU_OK
