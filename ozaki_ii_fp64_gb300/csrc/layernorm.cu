@@ -897,10 +897,17 @@ struct ForwardLaunch {
   cudaError_t error = cudaSuccess;
 
   // Launches the ring for rows of at most TPR * EPT columns, if there are
-  // enough rows to go round.
+  // enough rows to go round.  Fewer rows go to wider groups, of which fewer
+  // fit, but not to groups of which a row fills an eighth or less (a sixteenth
+  // where it goes element by element): norm_forward_kernel is quicker there,
+  // by its narrower groups and its lack of a start.  us, the wider ring and it,
+  // bf16 unless named: 300 x 256 4.2, 2.2; 2000 x 256 5.9, 3.2; 456 x 1024 f32
+  // 5.5, 3.0; 456 x 2048 5.5, 4.0; 950 x 63 5.9, 2.6.  Above those shares the
+  // ring is: 700 x 2048 5.1, 6.8; 2000 x 1024 f32 7.6, 9.0; 300 x 2047 6.6, 8.4.
   template <typename T, typename W, int TPR, int EPT, int kMode>
   bool fits() {
     if (c.cols > TPR * EPT) return false;
+    if (TPR > 32 && c.cols * (kMode == kAnyRow ? 16 : 8) <= TPR * EPT) return false;
     using R = RingCfg<TPR, EPT, false>;
     const int bytes = static_cast<int>(slot_bytes_of<T, kMode>(c.cols));
     const int params = param_bytes<W>(c.cols) * ((c.weight ? 1 : 0) + (c.bias ? 1 : 0));

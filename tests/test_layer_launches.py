@@ -67,3 +67,13 @@ def test_grids_at_the_size_limits(launches, what, a, b, c):
     assert status == 0
     for x, y, z in grids:
         assert 0 < x < 2**31 and 0 < y < 2**16 and 0 < z < 2**16
+
+
+@pytest.mark.parametrize("rows, cols, odd, first", [
+    # Too few rows for the ring's narrow groups: the kernel that keeps a row in registers, not wide groups left idle.
+    (300, 256, 0, 75), (912, 64, 0, 228), (3000, 512, 0, 750), (300, 2048, 0, 300), (1000, 63, 1, 250),
+    # The ring, one CTA an SM: enough rows for the narrow groups, or rows that fill a share of wide ones.
+    (5000, 256, 0, 152), (1000, 1024, 0, 152), (480, 2048, 0, 152), (300, 4096, 0, 152), (300, 2047, 1, 152)])
+def test_forward_norm_variant(launches, rows, cols, odd, first):
+    (status, grids), *_ = launches("norm", rows, cols, 0, odd)
+    assert status == 0 and grids == [(first, 1, 1)]
