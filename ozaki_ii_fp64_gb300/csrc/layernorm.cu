@@ -522,7 +522,7 @@ __device__ __forceinline__ float2 row_sum2(float2 s, float2* red) {
 // and the slot is free after dx.  16384 x 4096 bf16 with dr: 91.6 us, 0.87 of
 // the copy rate (its 512 threads, all that the column sums leave registers for,
 // wait for shared memory); 8192 x 16384 bf16: 150 us where the two passes below
-// took 413; with dr and fp32 weights, room for one slot, 292; 777 x 2051 f16, odd rows: 12.2 (5 rows an SM, each
+// took 413; with dr and fp32 weights, room for one slot, 292; 777 x 2051 f16, odd rows: 12.8 (5 rows an SM, each
 // its latency; element by element).
 template <typename T, typename W, int TPR, int EPT, int kMode>
 __global__ void __launch_bounds__(RingCfg<TPR, EPT, true>::kThreads, 1)
@@ -629,16 +629,19 @@ __global__ void __launch_bounds__(RingCfg<TPR, EPT, true>::kThreads, 1)
     auto take_dr = [&](int q0) {
       if (c.dr) take_row<T, TPR, EPT, kMode, NQ>(in + 2 * bytes, c.dr, c.lddr, row, c.rows, c.cols, tid, dr, q0);
     };
+    if (!kTwice) take_dr(0);
+    const float2 s = row_sum2<TPR>(make_float2(s1.x + s1.y, s2.x + s2.y), red[turn & 1]);
+    // A group that gives up still writes this row, of whatever its slot holds
+    // (the status tells), and leaves at its end: a way out from here took the
+    // rows of any start 76 bytes of spilled registers (777 x 2051 f16 13.4 us, 12.8 without).
+    const bool on = group_goes_on<TPR>(&gave_up[group][turn & 1]);
     auto release = [&] {
-      if (tid == 0) {
+      if (tid == 0 && on) {
         const long long later = row + static_cast<long long>(stages) * step;
         if (later < c.rows) issue(later, slot);
       }
       if (++slot == stages) slot = 0;
     };
-    if (!kTwice) take_dr(0);
-    const float2 s = row_sum2<TPR>(make_float2(s1.x + s1.y, s2.x + s2.y), red[turn & 1]);
-    if (!group_goes_on<TPR>(&gave_up[group][turn & 1])) break;
     if (!kTwice) {
       __syncwarp();
       release();
@@ -670,6 +673,7 @@ __global__ void __launch_bounds__(RingCfg<TPR, EPT, true>::kThreads, 1)
       row_barrier<TPR>();
       release();
     }
+    if (!on) break;
     mean = next_mean;
     rstd = next_rstd;
   }
