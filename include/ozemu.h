@@ -542,8 +542,10 @@ size_t ozemu_linear_bytes(int m, int n, int k, const void* X, int ldx, const voi
  *   dX = dZ W (m x k, lddx),  dW = dZ^T X (n x k, lddw),  db = sum_i dZ_i (n);
  * each of dX, dW, db may be NULL: not computed.  The gradient of R is dY.
  * dZ is rounded to the type for the two products (the tensor cores take
- * 16-bit operands); db sums it unrounded.  m = 0 zeroes dW and db, n = 0
- * zeroes dX. */
+ * 16-bit operands): with an activation other than none and relu one rounding
+ * more than dX and dW have from an unrounded dZ, a factor sqrt(2) of their error,
+ * and in f16 an infinity beyond 65504.  db sums it unrounded.  m = 0 zeroes dW
+ * and db, n = 0 zeroes dX. */
 int ozemu_linear_backward(int m, int n, int k, int type, const void* dY, int lddy, const void* X, int ldx,
                           const void* W, int ldw, int activation, const void* pre, int ldpre, void* dX, int lddx,
                           void* dW, int lddw, void* db, void* workspace, size_t workspace_bytes,

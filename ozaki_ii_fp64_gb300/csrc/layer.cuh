@@ -143,7 +143,7 @@ constexpr float kGeluA = 0.044715f;
 // five coefficients keep the absolute error below 1.5e-7, which is 5e-4 of the
 // tail at a = 4 and 4e-3 at 6: more than the rounding to 16 bits.)  The fp32
 // evaluation adds some 1e-6, the exponential a^2 2^-24.  The two more steps cost
-// the pass over the slopes (8192 x 16384) 4 us of 161, the product 8192 x 4096 ->
+// the pass over the slopes (8192 x 16384) 4 us of 159, the product 8192 x 4096 ->
 // 16384 2 of 573.
 constexpr float kTailP = 0.265f;
 __device__ __forceinline__ constexpr float tail_coefficient(int i) {

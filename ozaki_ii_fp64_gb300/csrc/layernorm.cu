@@ -184,8 +184,8 @@ __global__ void __launch_bounds__(cta_threads(TPR)) norm_forward_kernel(const No
 // the row in registers, which the first sum's barrier says.  The parameters
 // lie in shared memory too, once for all groups: read through L1, what the
 // ring leaves of it did not hold them (16384 x 8192 bf16: 107 us, 84 % of the
-// stalls on those loads).  Bound by HBM: 16384 x 8192 bf16 87 us, 6.15 TB/s,
-// 0.91 of the copy rate; 1021 x 5003 f32 in rows of no alignment 16 us, bound
+// stalls on those loads).  Bound by HBM: 16384 x 8192 bf16 88 us, 6.1 TB/s,
+// 0.90 of the copy rate; 1021 x 5003 f32 in rows of no alignment 15.5 us, bound
 // by its element-by-element loads and stores.
 // ---------------------------------------------------------------------------
 template <int TPR, int EPT, bool kBackward>
@@ -519,7 +519,7 @@ __device__ __forceinline__ float2 row_sum2(float2 s, float2* red) {
 // Rows through the ring: a slot holds x, dy and, where given, dr of one row.
 // Up to 8192 columns a thread keeps its 16 elements of x and dy from the sums
 // to dx; with 32 (and their 64 column sums) it takes them from the slot twice,
-// and the slot is free after dx.  16384 x 4096 bf16 with dr: 91.6 us, 0.87 of
+// and the slot is free after dx.  16384 x 4096 bf16 with dr: 92.1 us, 0.86 of
 // the copy rate (its 512 threads, all that the column sums leave registers for,
 // wait for shared memory); 8192 x 16384 bf16: 150 us where the two passes below
 // took 413; with dr and fp32 weights, room for one slot, 292; 777 x 2051 f16, odd rows: 12.8 (5 rows an SM, each
