@@ -482,7 +482,8 @@ int ozemu_dgemm_host_mixed(int m, int n, int k, const double* A, int lda, const 
                            int ldb, double* C, int ldc, int r, cudaStream_t stream);
 
 /* ------------------------------------------------------------------------ */
-/* Layer operators: linear layer and layer norm                             */
+/* Layer operators: linear layers (plain, gated, of 4 bits), layer norm,     */
+/* gradient clipping                                                        */
 /* ------------------------------------------------------------------------ */
 
 /* The operators of a transformer layer round a matrix product, forward and
@@ -554,6 +555,84 @@ int ozemu_linear_backward(int m, int n, int k, int type, const void* dY, int ldd
 /* Workspace bytes of that call; 0 on bad arguments.  host. */
 size_t ozemu_linear_backward_bytes(int m, int n, int k, const void* dY, int lddy, const void* X, int ldx,
                                    const void* W, int ldw, int activation);
+
+/* The gated linear layer: H = act(G) U with [G U] = X W^T + bias.  W holds two
+ * layers' rows, 2n x k (ldw): rows 0..n-1 are the gate's, rows n..2n-1 the up
+ * projection's; bias has 2n entries in that order (NULL: none).  X is m x k
+ * (ldx), H m x n (ldh).  pre (m x 2n, ldpre) receives [G U] rounded to the
+ * type, as the backward pass wants it (NULL: not written); H is formed from the
+ * unrounded values.  type: OZEMU_BF16 or OZEMU_F16, of every operand.  n up to
+ * 2^25.  k = 0 gives [G U] = bias; m or n = 0 is a no-op. */
+int ozemu_gated_linear(int m, int n, int k, int type, const void* X, int ldx, const void* W, int ldw, const void* bias,
+                       int activation, void* pre, int ldpre, void* H, int ldh, void* workspace, size_t workspace_bytes,
+                       cudaStream_t stream);
+
+/* Workspace bytes of that call; 0 on bad arguments.  host. */
+size_t ozemu_gated_linear_bytes(int m, int n, int k, const void* X, int ldx, const void* W, int ldw);
+
+/* Gradients of ozemu_gated_linear: with dZ = [dH U act'(G)  dH act(G)] of pre's
+ * G and U,
+ *   dX = dZ W (m x k, lddx),  dW = dZ^T X (2n x k, lddw),  db = sum_i dZ_i (2n);
+ * each of dX, dW, db may be NULL: not computed.  dZ is rounded to the type for
+ * the two products, as in ozemu_linear_backward; db sums it unrounded.  m = 0
+ * zeroes dW and db, n = 0 zeroes dX. */
+int ozemu_gated_linear_backward(int m, int n, int k, int type, const void* dH, int lddh, const void* X, int ldx,
+                                const void* W, int ldw, int activation, const void* pre, int ldpre, void* dX, int lddx,
+                                void* dW, int lddw, void* db, void* workspace, size_t workspace_bytes,
+                                cudaStream_t stream);
+
+/* Workspace bytes of that call; 0 on bad arguments.  host. */
+size_t ozemu_gated_linear_backward_bytes(int m, int n, int k, const void* X, int ldx, const void* W, int ldw);
+
+/* Microscaled 4-bit matrices (MXFP4): each 32 consecutive columns of a row share
+ * a scale s = 2^max(floor(log2 max|x|) - 2, -127), and an element is s times 0,
+ * 0.5, 1, 1.5, 2, 3, 4 or 6 and a sign: x / s rounded to the nearest of these (of
+ * two as near, the one with the even code), beyond 6 to 6.  A block with an
+ * infinity or a NaN is NaN throughout; one of zeros is zeros.  A matrix of rows
+ * x k (each up to 2^26) is two arrays on 16-byte boundaries:
+ *   codes   uint8 [rows][ceil(k/32)*16]: element j of a row in byte j/2, the low
+ *           half for even j, as e2m1 (sign, two bits of exponent, one of
+ *           significand); 0 past column k;
+ *   scales  uint8 [ceil(rows/128)][ceil(k/256)][1024]: within a tile of 128 rows
+ *           and 256 columns, the byte 127 + log2 s (255: NaN) of row r and
+ *           columns 32b..32b+31 at (b/4)*512 + (r%32)*16 + (r/32)*4 + b%4; 127
+ *           where the row or the columns lie past the matrix. */
+size_t ozemu_mx_code_bytes(int rows, int k);  /* host; 0 on bad arguments */
+size_t ozemu_mx_scale_bytes(int rows, int k); /* host; 0 on bad arguments */
+
+/* The rows of X (rows x k, ldx; any ozemu_type) to codes and scales. */
+int ozemu_mx_quantize(int rows, int k, int type, const void* X, int ldx, uint8_t* codes, uint8_t* scales,
+                      cudaStream_t stream);
+
+/* The values of codes and scales, rounded once to Y's type (ldy).  Those of a
+ * matrix quantised from that type are represented exactly. */
+int ozemu_mx_dequantize(int rows, int k, int type, const uint8_t* codes, const uint8_t* scales, void* Y, int ldy,
+                        cudaStream_t stream);
+
+/* Y = act(X W^T + bias) + R of two such matrices, X of m x k and W of n x k:
+ * ozemu_linear on the values that they stand for, the products exact and their
+ * sums fp32.  type (OZEMU_BF16 or OZEMU_F16) is that of bias, R and Y; Y may be R
+ * itself.  k = 0 gives X W^T = 0. */
+int ozemu_mx_linear(int m, int n, int k, int type, const uint8_t* x_codes, const uint8_t* x_scales,
+                    const uint8_t* w_codes, const uint8_t* w_scales, const void* bias, const void* R, int ldr,
+                    int activation, void* Y, int ldy, cudaStream_t stream);
+
+/* Gradients clipped by their global norm: with N the square root of the sum of
+ * all elements' squares, over all tensors,
+ *   outs[i] = grads[i] min(1, max_norm / (N + eps)),  *norm = N (NULL: not wanted).
+ * grads, sizes, types and outs are HOST arrays of `count` entries, read before
+ * the call returns: device pointers, numbers of elements (dense; up to 2^40)
+ * and ozemu_types, which may differ.  outs[i] may be grads[i] itself, and
+ * overlaps nothing else.  max_norm and eps >= 0, not both 0.  Squares are formed
+ * in fp32: a norm with an element beyond 1.8e19 is infinite, elements below 1e-23
+ * do not count.  A NaN or an infinity goes through as the formula takes it.
+ * Any device workspace of the bytes below, 256-byte aligned. */
+int ozemu_clip_grad_norm(int count, const void* const* grads, const long long* sizes, const int* types,
+                         void* const* outs, float max_norm, float eps, float* norm, void* workspace,
+                         size_t workspace_bytes, cudaStream_t stream);
+
+/* Workspace bytes of that call; 0 for a negative count.  host. */
+size_t ozemu_clip_grad_norm_bytes(int count);
 
 /* Y = (X - mean) rstd weight + bias for each row of X (rows x cols, ldx):
  * mean = sum(X)/cols, rstd = (sum (X - mean)^2 / cols + eps)^(-1/2).  weight

@@ -4,7 +4,8 @@ A thin ctypes layer over libozemu.so (``include/ozemu.h``).  The functions
 named ``ozemu_*`` mirror the C ABI one to one (ints for device pointers and
 streams); the short-named helpers (``dgemm``, ``igemm_s8``, ``split_rows_f64``
 ...) only marshal torch CUDA tensors into those calls.  Those of the layer
-operators (``linear``, ``layer_norm`` and their ``_backward``) do so natively
+operators (``linear``, ``gated_linear``, ``layer_norm`` and their ``_backward``,
+``mx_linear``, ``clip_grad_norm`` ...) do so natively
 (``csrc/binding.cpp``): their calls for one token are a few microseconds.  Every step of the
 computation runs in the library's CUDA kernels; there is no fallback: if the
 library cannot be built or loaded, importing the binding's functions raises.
@@ -119,6 +120,18 @@ _SIGNATURES = {
     "ozemu_layer_norm_backward": (_I, [_I, _I, _I, _P, _I, _P, _I, _I, _P, _P, _P, _P, _I, _P, _I, _P, _P, _P, _S,
                                        _P]),
     "ozemu_layer_norm_backward_bytes": (_S, [_I, _I]),
+    "ozemu_gated_linear": (_I, [_I, _I, _I, _I, _P, _I, _P, _I, _P, _I, _P, _I, _P, _I, _P, _S, _P]),
+    "ozemu_gated_linear_bytes": (_S, [_I, _I, _I, _P, _I, _P, _I]),
+    "ozemu_gated_linear_backward": (_I, [_I, _I, _I, _I, _P, _I, _P, _I, _P, _I, _I, _P, _I, _P, _I, _P, _I, _P, _P, _S,
+                                         _P]),
+    "ozemu_gated_linear_backward_bytes": (_S, [_I, _I, _I, _P, _I, _P, _I]),
+    "ozemu_mx_code_bytes": (_S, [_I, _I]),
+    "ozemu_mx_scale_bytes": (_S, [_I, _I]),
+    "ozemu_mx_quantize": (_I, [_I, _I, _I, _P, _I, _P, _P, _P]),
+    "ozemu_mx_dequantize": (_I, [_I, _I, _I, _P, _P, _P, _I, _P]),
+    "ozemu_mx_linear": (_I, [_I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _I, _I, _P, _I, _P]),
+    "ozemu_clip_grad_norm": (_I, [_I, _P, _P, _P, _P, _F, _F, _P, _P, _S, _P]),
+    "ozemu_clip_grad_norm_bytes": (_S, [_I]),
 }
 
 
@@ -419,6 +432,56 @@ def ozemu_layer_norm_backward(rows, cols, type, dY, lddy, X, ldx, param_type, we
 
 def ozemu_layer_norm_backward_bytes(rows, cols):
     return _call("ozemu_layer_norm_backward_bytes", rows, cols)
+
+
+def ozemu_gated_linear(m, n, k, type, X, ldx, W, ldw, bias, activation, pre, ldpre, H, ldh, workspace, workspace_bytes,
+                       stream):
+    return _call("ozemu_gated_linear", m, n, k, type, X, ldx, W, ldw, bias, activation, pre, ldpre, H, ldh, workspace,
+                 workspace_bytes, stream)
+
+
+def ozemu_gated_linear_bytes(m, n, k, X, ldx, W, ldw):
+    return _call("ozemu_gated_linear_bytes", m, n, k, X, ldx, W, ldw)
+
+
+def ozemu_gated_linear_backward(m, n, k, type, dH, lddh, X, ldx, W, ldw, activation, pre, ldpre, dX, lddx, dW, lddw, db,
+                                workspace, workspace_bytes, stream):
+    return _call("ozemu_gated_linear_backward", m, n, k, type, dH, lddh, X, ldx, W, ldw, activation, pre, ldpre, dX, lddx,
+                 dW, lddw, db, workspace, workspace_bytes, stream)
+
+
+def ozemu_gated_linear_backward_bytes(m, n, k, X, ldx, W, ldw):
+    return _call("ozemu_gated_linear_backward_bytes", m, n, k, X, ldx, W, ldw)
+
+
+def ozemu_mx_code_bytes(rows, k):
+    return _call("ozemu_mx_code_bytes", rows, k)
+
+
+def ozemu_mx_scale_bytes(rows, k):
+    return _call("ozemu_mx_scale_bytes", rows, k)
+
+
+def ozemu_mx_quantize(rows, k, type, X, ldx, codes, scales, stream):
+    return _call("ozemu_mx_quantize", rows, k, type, X, ldx, codes, scales, stream)
+
+
+def ozemu_mx_dequantize(rows, k, type, codes, scales, Y, ldy, stream):
+    return _call("ozemu_mx_dequantize", rows, k, type, codes, scales, Y, ldy, stream)
+
+
+def ozemu_mx_linear(m, n, k, type, x_codes, x_scales, w_codes, w_scales, bias, R, ldr, activation, Y, ldy, stream):
+    return _call("ozemu_mx_linear", m, n, k, type, x_codes, x_scales, w_codes, w_scales, bias, R, ldr, activation, Y, ldy,
+                 stream)
+
+
+def ozemu_clip_grad_norm(count, grads, sizes, types, outs, max_norm, eps, norm, workspace, workspace_bytes, stream):
+    return _call("ozemu_clip_grad_norm", count, grads, sizes, types, outs, max_norm, eps, norm, workspace,
+                 workspace_bytes, stream)
+
+
+def ozemu_clip_grad_norm_bytes(count):
+    return _call("ozemu_clip_grad_norm_bytes", count)
 
 
 # ------------------------------------------------------- torch marshalling
@@ -774,7 +837,7 @@ def crt_f64_mixed(m, n, r, residues, shifts_a, shifts_b, out=None, stream=None):
     return C
 
 
-# ------------------------------------- layer operators: linear, layer norm
+# ------------------- layer operators: linear layers, layer norm, clipping
 #
 # None of these calls records a graph for automatic gradients: a result never requires one, and an input that does is
 # answered with a UserWarning unless gradients are switched off (torch.no_grad()).  The gradients are the _backward
@@ -843,3 +906,106 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, dresidual=None, weight_g
     dresidual, dy or x itself, and overlaps no other argument (ValueError).  dweight and dbias have weight's type (x's without a weight)."""
     return (_native or _layer_calls()).layer_norm_backward(dy, x, mean, rstd, weight, dresidual, weight_grad,
                                                            bias_grad, out, stream)
+
+
+def gated_linear(x, w, bias=None, activation="silu", save_pre=False, out=None, stream=None):
+    """act(gate) * up of bfloat16 or float16 cuda tensors, with [gate up] = x @ w.T + bias: x m x k, w 2n x k (the n rows
+    of the gate, then the n of the up projection), bias 2n; m x n.
+
+    With save_pre also [gate up], m x 2n, rounded, for gated_linear_backward: (h, pre).  out overlaps no argument
+    (ValueError).  No graph is recorded for automatic gradients: gated_linear_backward computes them."""
+    return (_native or _layer_calls()).gated_linear(x, w, bias, _activation(activation), save_pre, out, stream)
+
+
+def gated_linear_backward(dh, x, w, pre, activation="silu", x_grad=True, w_grad=True, bias_grad=True, stream=None):
+    """(dx, dw, db) of gated_linear for the gradient dh of its output and its saved pre-activations (None for those not
+    asked for); dw and db hold the gate's rows, then the up projection's, as w and bias do."""
+    return (_native or _layer_calls()).gated_linear_backward(dh, x, w, pre, _activation(activation), x_grad, w_grad,
+                                                             bias_grad, stream)
+
+
+class MXMatrix:
+    """A rows x cols matrix of 4-bit floats (e2m1) with a power of two for each 32 columns of a row, as mx_quantize makes
+    it: `codes` (uint8, rows x bytes of a row) and `scales` (uint8, tiles of 128 rows x 256 columns), in the layout that
+    the C header gives."""
+
+    __slots__ = ("codes", "scales", "rows", "cols")
+
+    def __init__(self, codes, scales, rows, cols):
+        self.codes, self.scales, self.rows, self.cols = codes, scales, rows, cols
+
+    @property
+    def shape(self):
+        return (self.rows, self.cols)
+
+    def __repr__(self):
+        return "MXMatrix(%d x %d)" % (self.rows, self.cols)
+
+
+def _mx(q, name):
+    if not isinstance(q, MXMatrix):
+        raise ValueError("%s: expected an MXMatrix" % name)
+    return q
+
+
+def _float_type(dtype, names):
+    torch = _torch()
+    code = {torch.bfloat16: OZEMU_BF16, torch.float16: OZEMU_F16, torch.float32: OZEMU_F32}.get(dtype)
+    if code is None or code not in names:
+        raise ValueError("dtype: expected one of %s" % ", ".join(
+            n for c, n in ((OZEMU_BF16, "bfloat16"), (OZEMU_F16, "float16"), (OZEMU_F32, "float32")) if c in names))
+    return code
+
+
+def mx_quantize(x, out=None, stream=None):
+    """The MXMatrix of a bfloat16, float16 or float32 cuda matrix: for each 32 columns of a row the scale
+    2^(floor(log2 of the largest magnitude) - 2), and each element's nearest of 0, 0.5, 1, 1.5, 2, 3, 4 and 6 times it
+    (the even code of two as near, 6 beyond).  A block with an infinity or a NaN is NaN throughout.
+
+    out: an MXMatrix of x's size whose memory takes the result; it overlaps x in nothing (ValueError)."""
+    native = _native or _layer_calls()
+    if out is None:
+        codes, scales = native.mx_quantize(x, None, None, stream)
+        return MXMatrix(codes, scales, x.shape[0], x.shape[1])
+    if _mx(out, "out").shape != tuple(x.shape):
+        raise ValueError("out: expected an MXMatrix of x's size")
+    native.mx_quantize(x, out.codes, out.scales, stream)
+    return out
+
+
+def mx_dequantize(q, dtype=None, out=None, stream=None):
+    """The values of an MXMatrix as a cuda matrix of dtype (default: out's, or bfloat16): exact, but for values that the
+    type does not have."""
+    _mx(q, "q")
+    if dtype is None:
+        dtype = _torch().bfloat16 if out is None else out.dtype
+    return (_native or _layer_calls()).mx_dequantize(
+        q.codes, q.scales, q.rows, q.cols, _float_type(dtype, (OZEMU_BF16, OZEMU_F16, OZEMU_F32)), out, stream)
+
+
+def mx_linear(x, w, bias=None, residual=None, activation="none", dtype=None, out=None, stream=None):
+    """act(x @ w.T + bias) + residual of two MXMatrix: x m x k, w n x k; bias n, residual and the result m x n of dtype,
+    bfloat16 or float16 (default: that of out, residual or bias, else bfloat16).
+
+    The products of the 4-bit values are exact, their sums fp32.  out may be residual itself, and overlaps no other
+    argument (ValueError).  No graph is recorded for automatic gradients."""
+    _mx(x, "x")
+    _mx(w, "w")
+    if x.cols != w.cols:
+        raise ValueError("inner dimensions differ")
+    if dtype is None:
+        like = next((t for t in (out, residual, bias) if t is not None), None)
+        dtype = _torch().bfloat16 if like is None else like.dtype
+    return (_native or _layer_calls()).mx_linear(
+        x.codes, x.scales, x.rows, w.codes, w.scales, w.rows, x.cols, bias, residual, _activation(activation),
+        _float_type(dtype, (OZEMU_BF16, OZEMU_F16)), out, stream)
+
+
+def clip_grad_norm(grads, max_norm, eps=1e-6, out=None, stream=None):
+    """(norm, clipped): the norm of all elements of a sequence of dense bfloat16, float16 or float32 cuda tensors of any
+    shapes (a 0-dimensional float32 tensor), and each of them times min(1, max_norm / (norm + eps)).
+
+    out: as many tensors of the same sizes, types and strides that take the result; each may be its gradient itself
+    (out=grads clips in place), and overlaps no other (ValueError).  A norm of infinity gives zeros (NaN where the
+    gradients are infinite), one of NaN gives NaN."""
+    return (_native or _layer_calls()).clip_grad_norm(grads, max_norm, eps, out, stream)

@@ -1571,6 +1571,143 @@ int ozemu_linear_backward(int m, int n, int k, int type, const void* dY, int ldd
   return cuda_status(launch_linear_backward(c, stream));
 }
 
+// Sizes of a gated layer: its weights have 2 n rows.
+static bool gated_sizes(int m, int n, int k) { return linear_sizes(m, n, k) && n <= kMaxLinear / 2; }
+
+size_t ozemu_gated_linear_bytes(int m, int n, int k, const void* X, int ldx, const void* W, int ldw) {
+  if (!gated_sizes(m, n, k) || m == 0 || n == 0 || k == 0 || ldx < k || ldw < k) return 0;
+  LinearCall c = {};
+  c.m = m;
+  c.n = n;
+  c.k = k;
+  c.x = X;
+  c.ldx = ldx;
+  c.w = W;
+  c.ldw = ldw;
+  return gated_linear_workspace(c);
+}
+
+int ozemu_gated_linear(int m, int n, int k, int type, const void* X, int ldx, const void* W, int ldw, const void* bias,
+                       int activation, void* pre, int ldpre, void* H, int ldh, void* workspace, size_t workspace_bytes,
+                       cudaStream_t stream) {
+  if (!gated_sizes(m, n, k) || !product_type(type) || !activation_ok(activation)) return OZEMU_ERR_INVALID_ARG;
+  if (!matrix_ok(X, m, k, ldx, type) || !matrix_ok(W, 2 * n, k, ldw, type) || !vector_ok(bias, type) ||
+      !matrix_ok(pre, m, 2 * n, ldpre, type, true) || !matrix_ok(H, m, n, ldh, type))
+    return OZEMU_ERR_INVALID_ARG;
+  if (m == 0 || n == 0) return OZEMU_OK;
+  LinearCall c = {m, n, k, type, X, ldx, W, ldw, bias, nullptr, n, activation, pre, ldpre, H, ldh, workspace, nullptr};
+  int s = scratch_ok(workspace, workspace_bytes, k > 0 ? gated_linear_workspace(c) : 0);
+  if (s != OZEMU_OK) return s;
+  DeviceState* d = nullptr;
+  s = device_state(&d);
+  if (s != OZEMU_OK) return s;
+  c.flags = d->flags;
+  return cuda_status(launch_gated_linear(c, stream));
+}
+
+size_t ozemu_gated_linear_backward_bytes(int m, int n, int k, const void* X, int ldx, const void* W, int ldw) {
+  if (!gated_sizes(m, n, k) || m == 0 || n == 0 || ldx < k || ldw < k) return 0;
+  LinearGradCall c = {};
+  c.m = m;
+  c.n = n;
+  c.k = k;
+  c.x = X;
+  c.ldx = ldx;
+  c.w = W;
+  c.ldw = ldw;
+  return gated_linear_backward_workspace(c);
+}
+
+int ozemu_gated_linear_backward(int m, int n, int k, int type, const void* dH, int lddh, const void* X, int ldx,
+                                const void* W, int ldw, int activation, const void* pre, int ldpre, void* dX, int lddx,
+                                void* dW, int lddw, void* db, void* workspace, size_t workspace_bytes,
+                                cudaStream_t stream) {
+  if (!gated_sizes(m, n, k) || !product_type(type) || !activation_ok(activation)) return OZEMU_ERR_INVALID_ARG;
+  if (!matrix_ok(dH, m, n, lddh, type) || !matrix_ok(X, m, k, ldx, type, !dW) ||
+      !matrix_ok(W, 2 * n, k, ldw, type, !dX) || !matrix_ok(pre, m, 2 * n, ldpre, type) ||
+      !matrix_ok(dX, m, k, lddx, type, true) || !matrix_ok(dW, 2 * n, k, lddw, type, true) || !vector_ok(db, type))
+    return OZEMU_ERR_INVALID_ARG;
+  LinearGradCall c = {m, n, k, type, dH, lddh, X, ldx, W, ldw, activation, pre, ldpre, dX, lddx, dW, lddw, db,
+                      workspace, nullptr};
+  int s = scratch_ok(workspace, workspace_bytes, m > 0 && n > 0 ? gated_linear_backward_workspace(c) : 0);
+  if (s != OZEMU_OK) return s;
+  if ((m == 0 && n == 0) || (k == 0 && n == 0) || (!dX && !dW && !db)) return OZEMU_OK;
+  DeviceState* d = nullptr;
+  s = device_state(&d);
+  if (s != OZEMU_OK) return s;
+  c.flags = d->flags;
+  return cuda_status(launch_gated_linear_backward(c, stream));
+}
+
+// Rows and columns of a microscaled matrix, at most 2^26.
+static bool mx_sizes(int rows, int k) { return rows >= 0 && k >= 0 && rows <= kMaxLinear && k <= kMaxLinear; }
+static bool float_type(int type) { return type >= OZEMU_BF16 && type <= OZEMU_F32; }
+static bool mx_ok(const void* codes, const void* scales, int rows, int k) {
+  if (rows == 0 || k == 0) return true;
+  return codes && scales && ((reinterpret_cast<uintptr_t>(codes) | reinterpret_cast<uintptr_t>(scales)) & 15u) == 0;
+}
+
+size_t ozemu_mx_code_bytes(int rows, int k) { return mx_sizes(rows, k) ? mx_code_bytes(rows, k) : 0; }
+size_t ozemu_mx_scale_bytes(int rows, int k) { return mx_sizes(rows, k) ? mx_scale_bytes(rows, k) : 0; }
+
+int ozemu_mx_quantize(int rows, int k, int type, const void* X, int ldx, uint8_t* codes, uint8_t* scales,
+                      cudaStream_t stream) {
+  if (!mx_sizes(rows, k) || !float_type(type) || !matrix_ok(X, rows, k, ldx, type) || !mx_ok(codes, scales, rows, k))
+    return OZEMU_ERR_INVALID_ARG;
+  if (rows == 0 || k == 0) return OZEMU_OK;
+  return cuda_status(launch_mx_quantize({rows, k, type, X, ldx, codes, scales}, stream));
+}
+
+int ozemu_mx_dequantize(int rows, int k, int type, const uint8_t* codes, const uint8_t* scales, void* Y, int ldy,
+                        cudaStream_t stream) {
+  if (!mx_sizes(rows, k) || !float_type(type) || !matrix_ok(Y, rows, k, ldy, type) || !mx_ok(codes, scales, rows, k))
+    return OZEMU_ERR_INVALID_ARG;
+  if (rows == 0 || k == 0) return OZEMU_OK;
+  return cuda_status(launch_mx_dequantize({rows, k, type, codes, scales, Y, ldy}, stream));
+}
+
+int ozemu_mx_linear(int m, int n, int k, int type, const uint8_t* x_codes, const uint8_t* x_scales,
+                    const uint8_t* w_codes, const uint8_t* w_scales, const void* bias, const void* R, int ldr,
+                    int activation, void* Y, int ldy, cudaStream_t stream) {
+  if (!linear_sizes(m, n, k) || !product_type(type) || !activation_ok(activation)) return OZEMU_ERR_INVALID_ARG;
+  if (!mx_ok(x_codes, x_scales, m, k) || !mx_ok(w_codes, w_scales, n, k) || !vector_ok(bias, type) ||
+      !matrix_ok(R, m, n, ldr, type, true) || !matrix_ok(Y, m, n, ldy, type))
+    return OZEMU_ERR_INVALID_ARG;
+  if (m == 0 || n == 0) return OZEMU_OK;
+  DeviceState* d = nullptr;
+  const int s = device_state(&d);
+  if (s != OZEMU_OK) return s;
+  if (k == 0)  // an empty reduction: the plain layer's
+    return cuda_status(launch_linear({m, n, 0, type, nullptr, 1, nullptr, 1, bias, R, ldr, activation, nullptr, n, Y,
+                                      ldy, nullptr, d->flags},
+                                     stream));
+  return cuda_status(launch_mx_linear({m, n, k, type, x_codes, x_scales, w_codes, w_scales, bias, R, ldr, activation, Y,
+                                       ldy, d->flags},
+                                      stream));
+}
+
+// Elements of one gradient, at most 2^40.
+constexpr long long kMaxGradient = 1LL << 40;
+size_t ozemu_clip_grad_norm_bytes(int count) { return count < 0 ? 0 : clip_workspace(count); }
+
+int ozemu_clip_grad_norm(int count, const void* const* grads, const long long* sizes, const int* types,
+                         void* const* outs, float max_norm, float eps, float* norm, void* workspace,
+                         size_t workspace_bytes, cudaStream_t stream) {
+  if (count < 0 || (count > 0 && (!grads || !sizes || !types || !outs)) || !(max_norm >= 0.f) || !(eps >= 0.f) ||
+      !(max_norm > 0.f || eps > 0.f) || !vector_ok(norm, OZEMU_F32))
+    return OZEMU_ERR_INVALID_ARG;
+  for (int i = 0; i < count; ++i) {
+    if (sizes[i] < 0 || sizes[i] > kMaxGradient || !float_type(types[i])) return OZEMU_ERR_INVALID_ARG;
+    if (sizes[i] > 0 &&
+        (!grads[i] || !outs[i] || !type_aligned(grads[i], types[i]) || !type_aligned(outs[i], types[i])))
+      return OZEMU_ERR_INVALID_ARG;
+  }
+  const int s = scratch_ok(workspace, workspace_bytes, clip_workspace(count));
+  if (s != OZEMU_OK) return s;
+  return cuda_status(
+      launch_clip_grad_norm({count, grads, sizes, types, outs, max_norm, eps, norm, workspace}, stream));
+}
+
 static bool norm_types(int type, int param_type) {
   return type >= OZEMU_BF16 && type <= OZEMU_F32 && (param_type == type || param_type == OZEMU_F32);
 }

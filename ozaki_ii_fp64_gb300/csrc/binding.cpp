@@ -7,6 +7,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <ATen/ops/empty_like.h>
 #include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
@@ -18,6 +19,7 @@
 #include <optional>
 #include <stdexcept>
 #include <string>
+#include <vector>
 
 #include "ozemu.h"
 
@@ -130,6 +132,12 @@ class Output {
     if (or_same && in.p == at_.p && (in.ld == at_.ld || rows <= 1)) return;
     if (share(at_, in)) throw Refused(std::string("out: overlaps ") + name);
   }
+  // Against an array of bytes.
+  void apart(const at::Tensor& bytes, const char* name) const {
+    const long long n = bytes.numel();
+    if (given_ && share(at_, {reinterpret_cast<intptr_t>(bytes.data_ptr()), n, n > 0 ? 1 : 0, n}))
+      throw Refused(std::string("out: overlaps ") + name);
+  }
   void apart(const at::Tensor* input, void* p, int n, const char* name) const {
     Matrix m;
     m.p = p;
@@ -151,7 +159,7 @@ class Output {
 // their values is the caller's.
 class OnStream {
  public:
-  OnStream(const at::Tensor& like, PyObject* stream, std::initializer_list<const at::Tensor*> inputs) {
+  OnStream(const at::Tensor& like, PyObject* stream, const std::vector<const at::Tensor*>& inputs) {
     if (!like.is_cuda()) throw Refused("expected CUDA tensors");
     if (like.device().index() != c10::cuda::current_device()) throw Refused("expected tensors on the current device");
     if (stream == Py_None) {
@@ -182,7 +190,7 @@ class OnStream {
 
 // The calls record no graph: what requires a gradient would miss it without a
 // word, so they say it (as a Python warning; an error where those are errors).
-void no_graph(const char* call, const char* instead, std::initializer_list<const at::Tensor*> inputs) {
+void no_graph(const char* call, const char* instead, const std::vector<const at::Tensor*>& inputs) {
   if (!c10::GradMode::is_enabled()) return;
   for (const at::Tensor* t : inputs)
     if (t && t->requires_grad()) {
@@ -268,6 +276,14 @@ LinearSizes linear_sizes(const at::Tensor& x, const at::Tensor& w, PyObject* act
     throw Refused(std::string("expected bfloat16 or float16, got ") + c10::toString(x.scalar_type()));
   sizes(x, "x", &s.m, &s.k);
   sizes(w, "w", &s.n, &k2);
+  return s;
+}
+
+// The same for a gated layer, whose w has two rows for an output.
+LinearSizes gated_sizes(const at::Tensor& x, const at::Tensor& w, PyObject* act) {
+  LinearSizes s = linear_sizes(x, w, act);
+  if (s.n % 2 != 0) throw Refused("w: expected an even number of rows, the gate's and as many of the up projection");
+  s.n /= 2;
   return s;
 }
 
@@ -436,6 +452,329 @@ PyObject* layer_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t count) {
   });
 }
 
+// gated_linear(x, w, bias, activation, save_pre, out, stream)
+PyObject* gated_linear(PyObject*, PyObject* const* a, Py_ssize_t count) {
+  return guarded(count, 7, [&]() -> PyObject* {
+    const at::Tensor &x = tensor(a[0], "x"), &w = tensor(a[1], "w");
+    const at::Tensor *bias = tensor_or_none(a[2], "bias"), *given = tensor_or_none(a[5], "out");
+    const LinearSizes s = gated_sizes(x, w, a[3]);
+    const bool save = truth(a[4]);
+    const Matrix mx = matrix(&x, s.m, s.k, x, "x"), mw = matrix(&w, 2 * s.n, s.k, x, "w");
+    const Matrix mo = matrix(given, s.m, s.n, x, "out");
+    void* pb = vector(bias, 2 * s.n, x.scalar_type(), x, "bias");
+    const Output o(given, mo, s.m, s.n, x);
+    o.apart(&x, mx, s.m, s.k, "x");
+    o.apart(&w, mw, 2 * s.n, s.k, "w");
+    o.apart(bias, pb, 2 * s.n, "bias");
+    OnStream on(x, a[6], {&x, &w, bias, given});
+    no_graph("gated_linear", "gated_linear_backward computes them (torch.no_grad() says that none are wanted)",
+             {&x, &w, bias});
+    at::Tensor fresh, pre;
+    Matrix mh = mo, mp;
+    if (!given) {
+      fresh = at::empty({s.m, s.n}, x.options());
+      mh = matrix(&fresh, s.m, s.n, x, "out");
+    }
+    mp.ld = s.n > 0 ? 2 * s.n : 1;
+    if (save) {
+      pre = at::empty({s.m, 2 * s.n}, x.options());
+      mp = matrix(&pre, s.m, 2 * s.n, x, "pre");
+    }
+    const Scratch ws(x, ozemu_gated_linear_bytes(s.m, s.n, s.k, mx.p, mx.ld, mw.p, mw.ld));
+    check(ozemu_gated_linear(s.m, s.n, s.k, s.type, mx.p, mx.ld, mw.p, mw.ld, pb, s.act, mp.p, mp.ld, mh.p, mh.ld, ws.p,
+                             ws.bytes, on.handle),
+          "ozemu_gated_linear");
+    PyObject* h = given ? Py_NewRef(a[5]) : THPVariable_Wrap(fresh);
+    if (!save || !h) return h;
+    PyObject* z = THPVariable_Wrap(pre);
+    PyObject* r = z ? PyTuple_Pack(2, h, z) : nullptr;
+    Py_DECREF(h);
+    Py_XDECREF(z);
+    return r;
+  });
+}
+
+// gated_linear_backward(dh, x, w, pre, activation, x_grad, w_grad, bias_grad, stream)
+PyObject* gated_linear_backward(PyObject*, PyObject* const* a, Py_ssize_t count) {
+  return guarded(count, 9, [&]() -> PyObject* {
+    const at::Tensor &dh = tensor(a[0], "dh"), &x = tensor(a[1], "x"), &w = tensor(a[2], "w"), &pre = tensor(a[3], "pre");
+    const LinearSizes s = gated_sizes(x, w, a[4]);
+    const Matrix md = matrix(&dh, s.m, s.n, x, "dh"), mx = matrix(&x, s.m, s.k, x, "x");
+    const Matrix mw = matrix(&w, 2 * s.n, s.k, x, "w"), mp = matrix(&pre, s.m, 2 * s.n, x, "pre");
+    OnStream on(x, a[8], {&dh, &x, &w, &pre});
+    no_graph("gated_linear_backward", "torch.no_grad() says that none are wanted", {&dh, &x, &w, &pre});
+    at::Tensor dx, dw, db;
+    if (truth(a[5])) dx = at::empty({s.m, s.k}, x.options());
+    if (truth(a[6])) dw = at::empty({2 * s.n, s.k}, x.options());
+    if (truth(a[7])) db = at::empty({2 * s.n}, x.options());
+    const int ld = s.k > 0 ? s.k : 1;
+    const Scratch ws(x, ozemu_gated_linear_backward_bytes(s.m, s.n, s.k, mx.p, mx.ld, mw.p, mw.ld));
+    check(ozemu_gated_linear_backward(s.m, s.n, s.k, s.type, md.p, md.ld, mx.p, mx.ld, mw.p, mw.ld, s.act, mp.p, mp.ld,
+                                      dx.defined() ? dx.data_ptr() : nullptr, ld, dw.defined() ? dw.data_ptr() : nullptr,
+                                      ld, db.defined() ? db.data_ptr() : nullptr, ws.p, ws.bytes, on.handle),
+          "ozemu_gated_linear_backward");
+    return triple(dx, dw, db);
+  });
+}
+
+// One of the two arrays of a microscaled matrix.
+uint8_t* mx_array(const at::Tensor& t, size_t bytes, const at::Tensor& like, const char* name) {
+  if (t.scalar_type() != at::kByte || t.device() != like.device() || !t.is_contiguous() ||
+      static_cast<size_t>(t.numel()) != bytes)
+    throw Refused(std::string(name) + ": expected " + std::to_string(bytes) + " contiguous bytes on " +
+                  like.device().str());
+  if ((reinterpret_cast<uintptr_t>(t.data_ptr()) & 15u) != 0) throw Refused(std::string(name) + ": not on a 16-byte boundary");
+  return static_cast<uint8_t*>(t.data_ptr());
+}
+
+int integer(PyObject* o) {
+  const long long n = PyLong_AsLongLong(o);
+  if (n == -1 && PyErr_Occurred()) throw Raised();
+  if (n < 0 || n > INT_MAX) throw Refused("sizes: out of range");
+  return static_cast<int>(n);
+}
+
+at::ScalarType scalar_type(int code) {
+  return code == OZEMU_F32 ? at::kFloat : code == OZEMU_F16 ? at::kHalf : at::kBFloat16;
+}
+
+// mx_quantize(x, codes, scales, stream): (codes, scales), fresh ones for None
+PyObject* mx_quantize(PyObject*, PyObject* const* a, Py_ssize_t count) {
+  return guarded(count, 4, [&]() -> PyObject* {
+    const at::Tensor& x = tensor(a[0], "x");
+    const at::Tensor *codes = tensor_or_none(a[1], "codes"), *scales = tensor_or_none(a[2], "scales");
+    int rows, k;
+    sizes(x, "x", &rows, &k);
+    if (type_code(x.scalar_type()) < 0)
+      throw Refused(std::string("expected bfloat16, float16 or float32, got ") + c10::toString(x.scalar_type()));
+    const Matrix mx = matrix(&x, rows, k, x, "x");
+    const size_t cb = ozemu_mx_code_bytes(rows, k), sb = ozemu_mx_scale_bytes(rows, k);
+    uint8_t *pc = codes ? mx_array(*codes, cb, x, "codes") : nullptr, *ps = scales ? mx_array(*scales, sb, x, "scales") : nullptr;
+    const long long size = x.element_size();
+    const Area in = {reinterpret_cast<intptr_t>(mx.p), mx.ld * size, mx.p ? rows : 0, k * size};
+    const Area ac = {reinterpret_cast<intptr_t>(pc), static_cast<long long>(cb), pc ? 1 : 0, static_cast<long long>(cb)};
+    const Area as = {reinterpret_cast<intptr_t>(ps), static_cast<long long>(sb), ps ? 1 : 0, static_cast<long long>(sb)};
+    if (share(ac, in) || share(as, in)) throw Refused("out: overlaps x");
+    if (share(ac, as)) throw Refused("out: codes and scales overlap");
+    OnStream on(x, a[3], {&x, codes, scales});
+    no_graph("mx_quantize", "torch.no_grad() says that none are wanted", {&x});
+    at::Tensor fresh_codes, fresh_scales;
+    if (!codes) {
+      fresh_codes = at::empty({rows, static_cast<int64_t>(rows > 0 ? cb / rows : 0)}, x.options().dtype(at::kByte));
+      pc = mx_array(fresh_codes, cb, x, "codes");
+    }
+    if (!scales) {
+      fresh_scales = at::empty({(rows + 127) / 128, (k + 255LL) / 256, 1024}, x.options().dtype(at::kByte));
+      ps = mx_array(fresh_scales, sb, x, "scales");
+    }
+    check(ozemu_mx_quantize(rows, k, type_code(x.scalar_type()), mx.p, mx.ld, pc, ps, on.handle), "ozemu_mx_quantize");
+    PyObject *oc = a[1] == Py_None ? THPVariable_Wrap(fresh_codes) : Py_NewRef(a[1]);
+    PyObject *os = a[2] == Py_None ? THPVariable_Wrap(fresh_scales) : Py_NewRef(a[2]);
+    PyObject* r = oc && os ? PyTuple_Pack(2, oc, os) : nullptr;
+    Py_XDECREF(oc);
+    Py_XDECREF(os);
+    return r;
+  });
+}
+
+// mx_dequantize(codes, scales, rows, k, type, out, stream)
+PyObject* mx_dequantize(PyObject*, PyObject* const* a, Py_ssize_t count) {
+  return guarded(count, 7, [&]() -> PyObject* {
+    const at::Tensor &codes = tensor(a[0], "codes"), &scales = tensor(a[1], "scales");
+    const int rows = integer(a[2]), k = integer(a[3]), type = integer(a[4]);
+    const at::Tensor* given = tensor_or_none(a[5], "out");
+    const uint8_t *pc = mx_array(codes, ozemu_mx_code_bytes(rows, k), codes, "codes");
+    const uint8_t* ps = mx_array(scales, ozemu_mx_scale_bytes(rows, k), codes, "scales");
+    const at::TensorOptions options = codes.options().dtype(scalar_type(type));
+    Matrix my;
+    if (given) {
+      if (given->scalar_type() != scalar_type(type) || given->device() != codes.device())
+        throw Refused(std::string("out: expected a matrix of ") + c10::toString(scalar_type(type)) + " on " +
+                      codes.device().str());
+      my = matrix(given, rows, k, *given, "out");
+      const Output o(given, my, rows, k, *given);
+      o.apart(codes, "q");
+      o.apart(scales, "q");
+    }
+    OnStream on(codes, a[6], {&codes, &scales, given});
+    at::Tensor fresh;
+    if (!given) {
+      fresh = at::empty({rows, k}, options);
+      my = matrix(&fresh, rows, k, fresh, "out");
+    }
+    check(ozemu_mx_dequantize(rows, k, type, pc, ps, my.p, my.ld, on.handle), "ozemu_mx_dequantize");
+    return given ? Py_NewRef(a[5]) : THPVariable_Wrap(fresh);
+  });
+}
+
+// mx_linear(x_codes, x_scales, m, w_codes, w_scales, n, k, bias, residual, activation, type, out, stream)
+PyObject* mx_linear(PyObject*, PyObject* const* a, Py_ssize_t count) {
+  return guarded(count, 13, [&]() -> PyObject* {
+    const at::Tensor &xc = tensor(a[0], "x"), &xs = tensor(a[1], "x"), &wc = tensor(a[3], "w"), &ws = tensor(a[4], "w");
+    const int m = integer(a[2]), n = integer(a[5]), k = integer(a[6]), act = integer(a[9]), type = integer(a[10]);
+    const at::Tensor *bias = tensor_or_none(a[7], "bias"), *res = tensor_or_none(a[8], "residual");
+    const at::Tensor* given = tensor_or_none(a[11], "out");
+    const uint8_t *pxc = mx_array(xc, ozemu_mx_code_bytes(m, k), xc, "x"), *pxs = mx_array(xs, ozemu_mx_scale_bytes(m, k), xc, "x");
+    const uint8_t *pwc = mx_array(wc, ozemu_mx_code_bytes(n, k), xc, "w"), *pws = mx_array(ws, ozemu_mx_scale_bytes(n, k), xc, "w");
+    const at::ScalarType t = scalar_type(type);
+    // The matrices of the call's type, against one of that type.
+    const at::Tensor* like = given ? given : res ? res : bias;
+    if (like && (like->scalar_type() != t || like->device() != xc.device()))
+      throw Refused(std::string(given ? "out" : res ? "residual" : "bias") + ": expected " + c10::toString(t) + " on " +
+                    xc.device().str());
+    Matrix mr, my;
+    void* pb = nullptr;
+    mr.ld = my.ld = n > 0 ? n : 1;
+    if (like) {
+      mr = matrix(res, m, n, *like, "residual");
+      my = matrix(given, m, n, *like, "out");
+      pb = vector(bias, n, t, *like, "bias");
+      const Output o(given, my, m, n, *like);
+      o.apart(bias, pb, n, "bias");
+      o.apart(res, mr, m, n, "residual", true);
+      o.apart(xc, "x");
+      o.apart(xs, "x");
+      o.apart(wc, "w");
+      o.apart(ws, "w");
+    }
+    OnStream on(xc, a[12], {&xc, &xs, &wc, &ws, bias, res, given});
+    no_graph("mx_linear", "torch.no_grad() says that none are wanted", {bias, res});
+    at::Tensor fresh;
+    if (!given) {
+      fresh = at::empty({m, n}, xc.options().dtype(t));
+      my = matrix(&fresh, m, n, fresh, "out");
+    }
+    check(ozemu_mx_linear(m, n, k, type, pxc, pxs, pwc, pws, pb, mr.p, mr.ld, act, my.p, my.ld, on.handle),
+          "ozemu_mx_linear");
+    return given ? Py_NewRef(a[11]) : THPVariable_Wrap(fresh);
+  });
+}
+
+// The tensors of a sequence, which `keep` holds a reference to.
+struct Sequence {
+  Sequence(PyObject* o, const char* name) : keep(PySequence_Fast(o, name)) {
+    if (!keep) throw Raised();
+    for (Py_ssize_t i = 0; i < PySequence_Fast_GET_SIZE(keep); ++i) {
+      PyObject* item = PySequence_Fast_GET_ITEM(keep, i);
+      if (!THPVariable_Check(item)) {
+        Py_DECREF(keep);
+        throw Refused(std::string(name) + ": expected a sequence of tensors");
+      }
+      t.push_back(&THPVariable_Unpack(item));
+    }
+  }
+  ~Sequence() { Py_DECREF(keep); }
+  Sequence(const Sequence&) = delete;
+  PyObject* keep;
+  std::vector<const at::Tensor*> t;
+};
+
+struct Bytes {
+  uintptr_t begin, end;
+  size_t which;
+};
+bool before(const Bytes& a, const Bytes& b) { return a.begin < b.begin; }
+
+// clip_grad_norm(grads, max_norm, eps, out, stream)
+PyObject* clip_grad_norm(PyObject*, PyObject* const* a, Py_ssize_t count) {
+  return guarded(count, 5, [&]() -> PyObject* {
+    const Sequence grads(a[0], "grads: expected a sequence of tensors");
+    const size_t n = grads.t.size();
+    if (n == 0) throw Refused("grads: expected at least one tensor");
+    if (n > static_cast<size_t>(INT_MAX)) throw Refused("grads: too many tensors");
+    const double max_norm = PyFloat_AsDouble(a[1]);
+    if (max_norm == -1.0 && PyErr_Occurred()) throw Raised();
+    const double eps = PyFloat_AsDouble(a[2]);
+    if (eps == -1.0 && PyErr_Occurred()) throw Raised();
+    std::optional<Sequence> given;
+    if (a[3] != Py_None) {
+      given.emplace(a[3], "out: expected a sequence of tensors");
+      if (given->t.size() != n) throw Refused("out: expected as many tensors as grads");
+    }
+    const at::Tensor& first = *grads.t[0];
+    for (const at::Tensor* t : grads.t) {
+      if (type_code(t->scalar_type()) < 0)
+        throw Refused(std::string("grads: expected bfloat16, float16 or float32, got ") + c10::toString(t->scalar_type()));
+      if (t->device() != first.device()) throw Refused("grads: expected tensors of one device");
+      if (t->layout() != at::kStrided || !t->is_non_overlapping_and_dense())
+        throw Refused("grads: expected dense tensors");
+    }
+    std::vector<const at::Tensor*> all = grads.t;
+    if (given) all.insert(all.end(), given->t.begin(), given->t.end());
+    std::vector<const void*> in(n);
+    std::vector<void*> outs(n);
+    std::vector<long long> sizes(n);
+    std::vector<int> types(n);
+    std::vector<Bytes> written;
+    for (size_t i = 0; i < n; ++i) {
+      const at::Tensor& g = *grads.t[i];
+      in[i] = g.numel() > 0 ? g.data_ptr() : nullptr;
+      sizes[i] = g.numel();
+      types[i] = type_code(g.scalar_type());
+      if (!given) continue;
+      const at::Tensor& o = *given->t[i];
+      if (o.scalar_type() != g.scalar_type() || o.device() != g.device() || o.layout() != at::kStrided ||
+          o.sizes() != g.sizes())
+        throw Refused("out: expected tensors of the gradients' sizes, types and device");
+      if (g.numel() == 0) continue;
+      for (int64_t d = 0; d < g.dim(); ++d)
+        if (g.size(d) > 1 && o.stride(d) != g.stride(d)) throw Refused("out: expected tensors of the gradients' strides");
+      outs[i] = o.data_ptr();
+      const uintptr_t p = reinterpret_cast<uintptr_t>(outs[i]);
+      written.push_back({p, p + g.nbytes(), i});
+    }
+    // Outputs share nothing with each other, nor with a gradient but their own.
+    std::sort(written.begin(), written.end(), before);
+    for (size_t i = 1; i < written.size(); ++i)
+      if (written[i].begin < written[i - 1].end) throw Refused("out: overlaps another output");
+    if (given)
+      for (size_t i = 0; i < n; ++i) {
+        if (sizes[i] == 0) continue;
+        const uintptr_t p = reinterpret_cast<uintptr_t>(in[i]);
+        const uintptr_t end = p + grads.t[i]->nbytes();
+        // The last output that begins before this gradient's end, and those before it that reach into it.
+        auto at = std::lower_bound(written.begin(), written.end(), Bytes{end, 0, 0}, before);
+        while (at != written.begin()) {
+          --at;
+          if (at->end <= p) break;
+          if (!(at->which == i && at->begin == p)) throw Refused("out: overlaps a gradient that is not its own");
+        }
+      }
+    OnStream on(first, a[4], all);
+    no_graph("clip_grad_norm", "torch.no_grad() says that none are wanted", grads.t);
+    std::vector<at::Tensor> fresh;
+    if (!given) {
+      fresh.reserve(n);
+      for (size_t i = 0; i < n; ++i) {
+        fresh.push_back(at::empty_like(*grads.t[i]));
+        outs[i] = sizes[i] > 0 ? fresh[i].data_ptr() : nullptr;
+      }
+    }
+    const at::Tensor norm = at::empty({}, first.options().dtype(at::kFloat));
+    const int total = static_cast<int>(n);
+    const Scratch ws(first, ozemu_clip_grad_norm_bytes(total));
+    check(ozemu_clip_grad_norm(total, in.data(), sizes.data(), types.data(), outs.data(), static_cast<float>(max_norm),
+                               static_cast<float>(eps), norm.data_ptr<float>(), ws.p, ws.bytes, on.handle),
+          "ozemu_clip_grad_norm");
+    PyObject* list = PyList_New(static_cast<Py_ssize_t>(n));
+    if (!list) throw Raised();
+    for (size_t i = 0; i < n; ++i) {
+      PyObject* o = given ? Py_NewRef(PySequence_Fast_GET_ITEM(given->keep, static_cast<Py_ssize_t>(i)))
+                          : THPVariable_Wrap(fresh[i]);
+      if (!o) {
+        Py_DECREF(list);
+        throw Raised();
+      }
+      PyList_SET_ITEM(list, static_cast<Py_ssize_t>(i), o);
+    }
+    PyObject* length = THPVariable_Wrap(norm);
+    PyObject* r = length ? PyTuple_Pack(2, length, list) : nullptr;
+    Py_XDECREF(length);
+    Py_DECREF(list);
+    return r;
+  });
+}
+
 // setup(OzemuError)
 PyObject* setup(PyObject*, PyObject* error) {
   Py_INCREF(error);
@@ -451,6 +790,15 @@ PyMethodDef g_methods[] = {
     {"layer_norm", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(layer_norm)), METH_FASTCALL, nullptr},
     {"layer_norm_backward", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(layer_norm_backward)),
      METH_FASTCALL, nullptr},
+    {"gated_linear", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(gated_linear)), METH_FASTCALL, nullptr},
+    {"gated_linear_backward", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(gated_linear_backward)),
+     METH_FASTCALL, nullptr},
+    {"mx_quantize", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(mx_quantize)), METH_FASTCALL, nullptr},
+    {"mx_dequantize", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(mx_dequantize)), METH_FASTCALL,
+     nullptr},
+    {"mx_linear", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(mx_linear)), METH_FASTCALL, nullptr},
+    {"clip_grad_norm", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(clip_grad_norm)), METH_FASTCALL,
+     nullptr},
     {"setup", setup, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 

@@ -178,6 +178,64 @@ struct LinearGradCall {
 size_t linear_backward_workspace(const LinearGradCall& call);
 cudaError_t launch_linear_backward(const LinearGradCall& call, cudaStream_t stream);
 
+// Gated linear layer (linear.cu): w is 2 n x k, pre m x 2 n, bias and db have
+// 2 n entries; no residual.
+size_t gated_linear_workspace(const LinearCall& call);
+cudaError_t launch_gated_linear(const LinearCall& call, cudaStream_t stream);
+size_t gated_linear_backward_workspace(const LinearGradCall& call);
+cudaError_t launch_gated_linear_backward(const LinearGradCall& call, cudaStream_t stream);
+
+// Microscaled 4-bit matrices (mx.cu); the product's rows by columns by depth is
+// m x n x k, k > 0.
+size_t mx_code_bytes(int rows, int k);
+size_t mx_scale_bytes(int rows, int k);
+struct MxQuantCall {
+  int rows, k, type;
+  const void* x;
+  long long ldx;
+  uint8_t* codes;
+  uint8_t* scales;
+};
+cudaError_t launch_mx_quantize(const MxQuantCall& call, cudaStream_t stream);
+struct MxDequantCall {
+  int rows, k, type;
+  const uint8_t* codes;
+  const uint8_t* scales;
+  void* y;
+  long long ldy;
+};
+cudaError_t launch_mx_dequantize(const MxDequantCall& call, cudaStream_t stream);
+struct MxLinearCall {
+  int m, n, k, type;
+  const uint8_t* xcodes;
+  const uint8_t* xscales;
+  const uint8_t* wcodes;
+  const uint8_t* wscales;
+  const void* bias;
+  const void* res;
+  long long ldr;
+  int act;
+  void* y;
+  long long ldy;
+  uint32_t* flags;
+};
+cudaError_t launch_mx_linear(const MxLinearCall& call, cudaStream_t stream);
+
+// Clipping by the global norm (clip.cu): `count` tensors, host arrays; ws holds
+// clip_workspace(count) bytes.
+struct ClipCall {
+  int count;
+  const void* const* grads;
+  const long long* sizes;
+  const int* types;
+  void* const* outs;
+  float max_norm, eps;
+  float* norm;
+  void* ws;
+};
+size_t clip_workspace(int count);
+cudaError_t launch_clip_grad_norm(const ClipCall& call, cudaStream_t stream);
+
 // Launches a kernel that begins with chain_wait (common.cuh).  cluster: CTAs
 // of a cluster, 0 where the kernel itself says.
 template <typename... K, typename... A>

@@ -197,17 +197,18 @@ __device__ __forceinline__ float2 reciprocal2(float2 v) {
   return r;
 }
 
-// act'(z) of two values at once: a pass over the gradients is bound by the
-// instructions of this.  The factors that multiply an already vanished
-// exponential take z limited to +-64 (where it has vanished), so that a large
-// or infinite z gives the limit 0 or 1 and not 0 * inf; a NaN stays one through
-// the other factors.
+// act(z) and act'(z) of two values at once: a pass over the gradients is bound by
+// the instructions of this.  The slope's factors that multiply an already
+// vanished exponential take z limited to +-64 (where it has vanished), so that a
+// large or infinite z gives the limit 0 or 1 and not 0 * inf; a NaN stays one
+// through the other factors.  What the caller does not use, the compiler drops.
 template <int kAct>
-__device__ __forceinline__ float2 activation_slope2(float2 z) {
+__device__ __forceinline__ void activation_and_slope2(float2 z, float2& act, float2& slope) {
   const float2 one = both(1.f);
   const float2 zc = make_float2(fminf(fmaxf(z.x, -64.f), 64.f), fminf(fmaxf(z.y, -64.f), 64.f));
   if constexpr (kAct == kActRelu) {
-    return make_float2(z.x > 0.f ? 1.f : 0.f, z.y > 0.f ? 1.f : 0.f);
+    act = make_float2(z.x < 0.f ? 0.f : z.x, z.y < 0.f ? 0.f : z.y);
+    slope = make_float2(z.x > 0.f ? 1.f : 0.f, z.y > 0.f ? 1.f : 0.f);
   } else if constexpr (kAct == kActGelu) {  // Phi(z) + z phi(z); one exponential serves both
     const float2 a = make_float2(fabsf(z.x), fabsf(z.y));
     const float2 t = reciprocal2(fma2(a, both(kTailP), one));
@@ -217,19 +218,29 @@ __device__ __forceinline__ float2 activation_slope2(float2 z) {
     const float2 e = exp2_2(mul2(mul2(z, z), both(-0.5f * 1.4426950408889634f)));
     q = mul2(mul2(q, t), e);
     const float2 p = make_float2(z.x < 0.f ? q.x : 1.f - q.x, z.y < 0.f ? q.y : 1.f - q.y);
-    return fma2(mul2(zc, both(0.3989422804014327f)), e, p);
+    act = mul2(z, p);
+    slope = fma2(mul2(zc, both(0.3989422804014327f)), e, p);
   } else if constexpr (kAct == kActGeluTanh) {  // s + z s (1 - s) 2 u'(z), s = 1 / (1 + e^(-2u))
     const float2 zz = mul2(z, z);
     const float2 u = mul2(mul2(z, both(-2.f * kGeluC * 1.4426950408889634f)), fma2(zz, both(kGeluA), one));
     const float2 s = reciprocal2(add2(exp2_2(u), one));
     const float2 du = fma2(mul2(zc, zc), both(6.f * kGeluC * kGeluA), both(2.f * kGeluC));
-    return fma2(mul2(mul2(zc, s), fma2(s, both(-1.f), one)), du, s);
+    act = mul2(z, s);
+    slope = fma2(mul2(mul2(zc, s), fma2(s, both(-1.f), one)), du, s);
   } else if constexpr (kAct == kActSilu) {  // s (1 + z (1 - s)), s = 1 / (1 + e^(-z))
     const float2 s = reciprocal2(add2(exp2_2(mul2(z, both(-1.4426950408889634f))), one));
-    return mul2(s, fma2(zc, fma2(s, both(-1.f), one), one));
+    act = mul2(z, s);
+    slope = mul2(s, fma2(zc, fma2(s, both(-1.f), one), one));
   } else {
-    return one;
+    act = z;
+    slope = one;
   }
+}
+template <int kAct>
+__device__ __forceinline__ float2 activation_slope2(float2 z) {
+  float2 act, slope;
+  activation_and_slope2<kAct>(z, act, slope);
+  return slope;
 }
 
 // out[s][j] = sum over the `used` parts of part[s][.][j], s = blockIdx.y: 32

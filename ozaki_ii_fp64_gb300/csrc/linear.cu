@@ -3,6 +3,11 @@
 //   z = x w^T + b,  y = act(z) + r
 //   dz = dy act'(pre),  dx = dz w,  dw = dz^T x,  db = sum over rows of dz
 //
+// and its gated form, whose w holds the rows of two layers, gate and up:
+//
+//   [g u] = x w^T + b,  h = act(g) u
+//   dz = [dh u act'(g)  dh act(g)],  dx, dw, db as above
+//
 // Each product D(i, j) = sum_p A(i, p) B(j, p) runs on bf16 or f16 operands
 // with fp32 accumulators in TMEM.  The operands of the three products are the
 // same three matrices, read with the reduction along a row (K-major: x and w
@@ -29,7 +34,7 @@
 #include <utility>
 
 #include "kernels.h"
-#include "layer.cuh"
+#include "product.cuh"
 
 namespace ozemu {
 
@@ -37,59 +42,7 @@ namespace {
 
 constexpr int kBlock = 64;               // elements of an operand block: 64 rows of 64 (128 bytes)
 constexpr int kBlockBytes = 64 * 128;
-constexpr int kEpiWarps = 16;
 constexpr int kThreads = 32 * (3 + kEpiWarps);
-
-// What happens to an accumulator on its way out.
-struct Epilogue {
-  const void* bias;
-  const void* res;
-  long long ldr;
-  void* pre;
-  long long ldpre;
-  void* out;
-  long long ldo;
-  int act;
-  int vec;  // bits: 1 bias, 2 res, 4 pre, 8 out rows start on 16-byte boundaries
-};
-
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_word,
-                                          uint32_t* flags) {
-  int ok = 0;
-  if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, abort_word, flags) ? 1 : 0;
-  return __shfl_sync(0xFFFFFFFFu, ok, 0) != 0;
-}
-
-// The loops that issue loads and MMAs are run by a whole warp, so that their
-// addresses and descriptors stay in uniform registers, which these
-// instructions take; one elected lane, always the same, issues.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t one;
-  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(one));
-  return one != 0;
-}
-__device__ __forceinline__ bool all_wait(uint64_t* bar, uint32_t parity, volatile int* abort_word, uint32_t* flags) {
-  const bool ok = mbar_wait(bar, parity, abort_word, flags);
-  return __all_sync(0xFFFFFFFFu, ok);
-}
-
-// Bounded wait that ignores the abort word (used while draining).
-__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, uint32_t* flags) {
-  const uint64_t t0 = globaltimer();
-  while (!mbar_try_wait(bar, parity)) {
-    if (globaltimer() - t0 > kWaitLimitNs) {
-      atomicOr(flags, kFlagTimeout);
-      return;
-    }
-  }
-}
-
-// After an abort, gives copies already issued time to land.
-__device__ __forceinline__ void settle_after_abort() {
-  const uint64_t t0 = globaltimer();
-  while (globaltimer() - t0 < 50000ull) {
-  }
-}
 
 // Eight consecutive elements p[0..7] of which `left` exist, as floats (0 past
 // the end); one 16-byte load where the address allows.
@@ -101,158 +54,6 @@ __device__ __forceinline__ void load8(const T* p, int left, bool vec, float2 (&v
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       v[i] = make_float2(2 * i < left ? to_float(p[2 * i]) : 0.f, 2 * i + 1 < left ? to_float(p[2 * i + 1]) : 0.f);
-  }
-}
-
-// Four elements, by plain loads (the memory may be the output's).
-template <typename T>
-__device__ __forceinline__ void load4(const T* p, int left, bool vec, float (&v)[4]) {
-  if (vec && left >= 4) {
-    const uint2 u = *reinterpret_cast<const uint2*>(p);
-    const float2 a = Pair<T>::unpack(u.x), b = Pair<T>::unpack(u.y);
-    v[0] = a.x;
-    v[1] = a.y;
-    v[2] = b.x;
-    v[3] = b.y;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = i < left ? to_float(p[i]) : 0.f;
-  }
-}
-template <typename T>
-__device__ __forceinline__ void store4(T* p, const float (&v)[4], int left, bool vec) {
-  if (vec && left >= 4) {
-    *reinterpret_cast<uint2*>(p) = make_uint2(Pair<T>::pack(v[0], v[1]), Pair<T>::pack(v[2], v[3]));
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < left) p[i] = from_float<T>(v[i]);
-  }
-}
-
-template <int kAct, int N>
-__device__ __forceinline__ void activate_each(float (&z)[N]) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) z[i] = activate(z[i], kAct);
-}
-template <int N>
-__device__ __forceinline__ void activate_all(float (&z)[N], int act) {
-  switch (act) {
-    case kActRelu: activate_each<kActRelu>(z); break;
-    case kActGelu: activate_each<kActGelu>(z); break;
-    case kActGeluTanh: activate_each<kActGeluTanh>(z); break;
-    case kActSilu: activate_each<kActSilu>(z); break;
-    default: break;
-  }
-}
-
-// A warp's 32 rows x 32 columns of 16-bit elements pass through its 2 KB of
-// shared memory (row r at byte 64 r, its 16-byte piece c at piece
-// c ^ (r / 2 % 4): no bank conflicts by rows or by pieces), so that a row moves
-// as one 64-byte run.  A lane's share on the way: piece lane % 4 of rows
-// 8 i + lane / 4; or, where rows do not start on 16-byte boundaries, word
-// lane % 16 of rows 2 i + lane / 16, between words where the row starts on an
-// odd element.
-__device__ __forceinline__ uint4* stage_piece(uint8_t* stage, int r, int c) {
-  return reinterpret_cast<uint4*>(stage + r * 64) + (c ^ (r >> 1 & 3));
-}
-__device__ __forceinline__ uint32_t* stage_word(uint8_t* stage, int r, int w) {
-  return reinterpret_cast<uint32_t*>(stage_piece(stage, r, w >> 2)) + (w & 3);
-}
-
-template <typename T>
-__device__ __forceinline__ void read_rows(uint4 (&v)[4], const T* in, long long ld, int row0, int col0, int m, int n,
-                                          bool vec) {
-  const int lane = threadIdx.x & 31;
-  if (vec && col0 + 32 <= n) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = row0 + 8 * i + (lane >> 2);
-      v[i] = r < m ? *reinterpret_cast<const uint4*>(in + r * ld + col0 + 8 * (lane & 3)) : make_uint4(0, 0, 0, 0);
-    }
-    return;
-  }
-  uint32_t* w = reinterpret_cast<uint32_t*>(v);
-  const uint16_t* p = reinterpret_cast<const uint16_t*>(in) + row0 * ld + col0;
-  const int word = lane & 15;
-  if (col0 > 0 && col0 + 32 <= n) {  // the element before the run is the row's, too
-    // All loads first: the words, and for row `lane` the last element, which a
-    // row that starts on an odd element has in a 17th word.
-    const uint32_t last = row0 + lane < m ? p[lane * ld + 31] : 0;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int r = 2 * i + (lane >> 4);
-      const uintptr_t q = reinterpret_cast<uintptr_t>(p + r * ld) & ~uintptr_t(3);
-      w[i] = row0 + r < m ? *(reinterpret_cast<const uint32_t*>(q) + word) : 0;
-    }
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int r = 2 * i + (lane >> 4);
-      const uint32_t next = __shfl_down_sync(0xFFFFFFFFu, w[i], 1), tail = __shfl_sync(0xFFFFFFFFu, last, r);
-      if (reinterpret_cast<uintptr_t>(p + r * ld) & 2u) w[i] = __funnelshift_r(w[i], word == 15 ? tail : next, 16);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int r = 2 * i + (lane >> 4);
-      const uint16_t* q = p + r * ld + 2 * word;
-      const uint32_t a = row0 + r < m && col0 + 2 * word < n ? q[0] : 0;
-      const uint32_t b = row0 + r < m && col0 + 2 * word + 1 < n ? q[1] : 0;
-      w[i] = a | (b << 16);
-    }
-  }
-}
-
-__device__ __forceinline__ void stage_rows(const uint4 (&v)[4], uint8_t* stage, int col0, int n, bool vec) {
-  const int lane = threadIdx.x & 31;
-  if (vec && col0 + 32 <= n) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) *stage_piece(stage, 8 * i + (lane >> 2), lane & 3) = v[i];
-  } else {
-    const uint32_t* w = reinterpret_cast<const uint32_t*>(v);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) *stage_word(stage, 2 * i + (lane >> 4), lane & 15) = w[i];
-  }
-}
-
-template <typename T>
-__device__ __forceinline__ void write_rows(uint8_t* stage, T* out, long long ldo, int row0, int col0, int m, int n,
-                                           bool vec) {
-  const int lane = threadIdx.x & 31;
-  if (vec && col0 + 32 <= n) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = 8 * i + (lane >> 2);
-      if (row0 + r < m)
-        *reinterpret_cast<uint4*>(out + (row0 + r) * ldo + col0 + 8 * (lane & 3)) = *stage_piece(stage, r, lane & 3);
-    }
-    return;
-  }
-  uint16_t* p = reinterpret_cast<uint16_t*>(out) + row0 * ldo + col0;
-  const bool whole = col0 + 32 <= n;
-  const int word = lane & 15;
-#pragma unroll 1
-  for (int i0 = 0; i0 < 16; i0 += 4) {
-    uint32_t a[4], b[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) a[i] = *stage_word(stage, 2 * (i0 + i) + (lane >> 4), word);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) b[i] = __shfl_down_sync(0xFFFFFFFFu, a[i], 1);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = 2 * (i0 + i) + (lane >> 4);
-      uint16_t* q = p + r * ldo;
-      const bool odd = (reinterpret_cast<uintptr_t>(q) & 2u) != 0, in_m = row0 + r < m;
-      if (whole) {  // from an odd start: words of elements 2 word + 1 and 2 word + 2, and the two ends
-        const uint32_t both = odd ? __funnelshift_r(a[i], b[i], 16) : a[i];
-        if (in_m && !(odd && word == 15)) *reinterpret_cast<uint32_t*>(q + 2 * word + (odd ? 1 : 0)) = both;
-        if (in_m && odd && word == 15) q[31] = static_cast<uint16_t>(a[i] >> 16);
-        if (in_m && odd && word == 0) q[0] = static_cast<uint16_t>(a[i]);
-      } else {
-        if (in_m && col0 + 2 * word < n) q[2 * word] = static_cast<uint16_t>(a[i]);
-        if (in_m && col0 + 2 * word + 1 < n) q[2 * word + 1] = static_cast<uint16_t>(a[i] >> 16);
-      }
-    }
   }
 }
 
@@ -281,8 +82,6 @@ __device__ __forceinline__ void write_rows(uint8_t* stage, T* out, long long ldo
 constexpr int kRing = 192 * 1024;  // stages of two blocks of A and one or two of B: 8 or 6
 constexpr int kMaxStages = 8;
 constexpr int kPairSmem = 1024 + kRing + kEpiWarps * (2048 + 64) + 256;  // staging, a chunk's bias, barriers
-constexpr int kGroupM = 8;  // tile rows swept together, for reuse of B's columns in L2
-
 struct Product {
   int m, n;        // rows and columns of D
   int kb;          // 64-element blocks of the reduction
@@ -290,8 +89,7 @@ struct Product {
   int bn;          // columns of a tile
   int split;       // pairs that share a tile's reduction
   int share;       // blocks of it for each
-  int tiles_m, tiles_n;
-  uint32_t group_inverse, group_shift;  // of kGroupM tiles_n
+  Raster tiles;
   Epilogue e;
 };
 
@@ -304,30 +102,6 @@ struct Products {
   int bufs;  // accumulators in TMEM: 4 of 128 columns or 2 of 256
 };
 
-__device__ __forceinline__ void tile_of(int t, const Product& p, int& tm, int& tn) {
-  // t / (kGroupM tiles_n) by the reciprocal that the host rounded up: exact
-  // for the product's tiles.
-  const int turn = static_cast<int>(__umulhi(static_cast<uint32_t>(t), p.group_inverse) >> p.group_shift);
-  const int first = turn * kGroupM, rest = t - turn * kGroupM * p.tiles_n;
-  const int gm = min(kGroupM, p.tiles_m - first);
-  if (gm == kGroupM) {
-    tn = rest / kGroupM;
-    tm = first + rest % kGroupM;
-  } else {
-    tn = rest / gm;
-    tm = first + rest % gm;
-  }
-}
-
-// 16 bytes of shared memory of a CTA of the cluster.
-__device__ __forceinline__ float4 load_cluster16(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr));
-  return v;
-}
-
 // The sums that a pair of a split tile leaves: 128 rows of up to 256 fp32, the
 // 16-byte piece c of row r at piece c ^ (r % 32), so that a warp's rows meet
 // in no bank.
@@ -335,57 +109,52 @@ __device__ __forceinline__ uint32_t part_piece(int r, int c) {
   return static_cast<uint32_t>(r * 1024 + ((c ^ (r & 31)) << 4));
 }
 
-// One warp's 32 rows x 32 columns of accumulators, a row a lane, from
-// source(last, z) through the epilogue; the source is asked for the last time
-// with last = true.
-template <typename T, typename F>
-__device__ __forceinline__ void finish_rows(F source, const uint4 (&res)[4], const Epilogue& e, uint8_t* stage,
-                                            const uint4* bias, int row0, int col0, int m, int n) {
+// The same for a gated tile: z the gate's accumulators, u the up projection's.
+template <typename T>
+__device__ __forceinline__ void finish_gated(float (&z)[32], float (&u)[32], const Epilogue& e, uint8_t* stage,
+                                             uint8_t* bias, int row0, int col0, int m, int n) {
   const int lane = threadIdx.x & 31;
-  float z[32];
-  auto take = [&](bool last) {
-    source(last, z);
-    if (e.bias) {
+  // One half's bias and rounded pre-activation.
+  auto half = [&](float (&v)[32], int at) {
+    if (e.bias) {  // the chunk's 32 values, for every lane
+      const uint16_t b = col0 + lane < n ? static_cast<const uint16_t*>(e.bias)[at + col0 + lane] : 0;
+      __syncwarp();
+      reinterpret_cast<uint16_t*>(bias)[lane] = b;
+      __syncwarp();
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        float b[8];
-        unpack16<T>(bias[q], b);
+        float f[8];
+        unpack16<T>(reinterpret_cast<const uint4*>(bias)[q], f);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) z[8 * q + i] += b[i];
+        for (int i = 0; i < 8; ++i) v[8 * q + i] += f[i];
       }
     }
-  };
-  if (e.pre) {
-    take(false);
+    if (e.pre) {
 #pragma unroll
-    for (int c = 0; c < 4; ++c) *stage_piece(stage, lane, c) = pack16<T>(z + 8 * c);
-    __syncwarp();
-    write_rows(stage, static_cast<T*>(e.pre), e.ldpre, row0, col0, m, n, (e.vec & 4) != 0);
-    __syncwarp();
-  }
-  if (e.res) {
-    stage_rows(res, stage, col0, n, (e.vec & 2) != 0);
-    __syncwarp();
-  }
-  take(true);
+      for (int c = 0; c < 4; ++c) *stage_piece(stage, lane, c) = pack16<T>(v + 8 * c);
+      __syncwarp();
+      write_rows(stage, static_cast<T*>(e.pre) + at, e.ldpre, row0, col0, m, n, (e.vec & (at ? 32 : 4)) != 0);
+      __syncwarp();
+    }
+  };
+  half(z, 0);
+  half(u, n);
   activate_all(z, e.act);
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    uint4* at = stage_piece(stage, lane, c);
-    if (e.res) {
-      float r[8];
-      unpack16<T>(*at, r);
+  for (int i = 0; i < 32; ++i) z[i] *= u[i];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) z[8 * c + i] += r[i];
-    }
-    *at = pack16<T>(z + 8 * c);
-  }
+  for (int c = 0; c < 4; ++c) *stage_piece(stage, lane, c) = pack16<T>(z + 8 * c);
   __syncwarp();
   write_rows(stage, static_cast<T*>(e.out), e.ldo, row0, col0, m, n, (e.vec & 8) != 0);
   __syncwarp();
 }
 
-template <typename T>
+// kGated: B holds the rows of two layers, gate (n of them) and up (n more), and
+// D is m x n.  One CTA of a pair stages a tile's gate rows, the other as many
+// up rows, so the accumulators of an output's two halves lie BN / 2 columns
+// apart in the same TMEM lane and meet in one thread's registers: the gate and
+// up products are never written unless they are kept for the backward pass.
+template <typename T, bool kGated>
 __global__ void __launch_bounds__(kThreads, 1)
     product_pair_kernel(const __grid_constant__ CUtensorMap ma0, const __grid_constant__ CUtensorMap mb0,
                         const __grid_constant__ CUtensorMap ma1, const __grid_constant__ CUtensorMap mb1,
@@ -405,8 +174,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int place = static_cast<int>(cluster_rank()), rank = place & 1, lead = place & ~1;
   const uint16_t both_ctas = static_cast<uint16_t>(0x3 << lead);
-  const int first = g.p[0].tiles_m * g.p[0].tiles_n;  // tiles of the first product
-  const int total = first + (g.count > 1 ? g.p[1].tiles_m * g.p[1].tiles_n : 0);
+  const int first = g.p[0].tiles.count();  // tiles of the first product
+  const int total = first + (g.count > 1 ? g.p[1].tiles.count() : 0);
   // A pair walks the tiles, or takes its part of one tile's reduction (of one
   // product).
   const int split = g.p[0].split;
@@ -459,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Product& p = g.p[second];
       const CUtensorMap* map = loads_a ? (second ? &ma1 : &ma0) : (second ? &mb1 : &mb0);
       int tm, tn, kb0, kb1;
-      tile_of(second ? t - first : t, p, tm, tn);
+      tile_of(second ? t - first : t, p.tiles, tm, tn);
       part(p, kb0, kb1);
       // B's BN / 2 rows of this CTA come in whole blocks (a part block's last
       // rows are loaded and not used).
@@ -468,7 +237,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool arms = loads_a && rank == 0;  // for both CTAs and operands
       const bool down = loads_a ? p.a_mn != 0 : p.b_mn != 0;
       const bool two = down && (loads_a || b_blocks == 2);
-      const int at = loads_a ? tm * 256 + rank * 128 : tn * p.bn + rank * (p.bn / 2);
+      const int at = loads_a  ? tm * 256 + rank * 128
+                     : kGated ? tn * (p.bn / 2) + rank * p.n
+                              : tn * p.bn + rank * (p.bn / 2);
       const uint32_t to = loads_a ? 0 : 2 * kBlockBytes;
       for (int k = kb0 * kBlock; k < kb1 * kBlock; k += kBlock) {
         if (!all_wait(&empty[s], phase, abort_word, flags)) {
@@ -551,11 +322,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Product& p = g.p[second];
       const Epilogue& e = p.e;
       int tm, tn;
-      tile_of(second ? t - first : t, p, tm, tn);
+      tile_of(second ? t - first : t, p.tiles, tm, tn);
       const int buf = n_tiles & (g.bufs - 1), use = n_tiles >> buf_shift;
       const int row0 = tm * 256 + rank * 128 + quarter * 32;
       // Columns of the tile that this warp has to take: none past D's edge.
-      const int cols = row0 < p.m ? min(p.bn, p.n - tn * p.bn) : 0;
+      const int width = kGated ? p.bn / 2 : p.bn;  // of the tile in D
+      const int cols = row0 < p.m ? min(width, p.n - tn * width) : 0;
       const uint32_t tcol = tbase + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(buf * buf_columns);
       if (split > 1) {  // leave the sums; the cluster joins them below
         int kb0, kb1;
@@ -563,7 +335,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!warp_wait(&tfull[buf], use & 1, abort_word, flags)) break;
         tc_fence_after();
         const int r = quarter * 32 + lane;
-        for (int c = group * 32; c < cols; c += 128) {
+        const int sums = kGated && cols > 0 ? p.bn : cols;
+        for (int c = group * 32; c < sums; c += 128) {
           uint32_t u[32];
           if (kb0 < kb1) {
             tmem_ld32(tcol + c, u);
@@ -582,7 +355,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool waited = false, live = true;
 #pragma unroll 1
       for (int c = group * 32; c < cols; c += 128) {
-        const int col0 = tn * p.bn + c;
+        const int col0 = tn * width + c;
+        if constexpr (kGated) {
+          live = warp_wait(&tfull[buf], use & 1, abort_word, flags);  // c < 128: a warp's only chunk
+          if (!live) break;
+          tc_fence_after();
+          uint32_t a[32], b[32];
+          tmem_ld32(tcol + c, a);
+          tmem_ld32(tcol + width + c, b);
+          tmem_wait_ld();
+          float z[32], u[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            z[i] = __uint_as_float(a[i]);
+            u[i] = __uint_as_float(b[i]);
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(&tempty[buf], lead));
+          finish_gated<T>(z, u, e, stage, bias, row0, col0, p.m, p.n);
+          continue;
+        }
         uint4 res[4];
         if (e.res)
           read_rows(res, static_cast<const T*>(e.res), e.ldr, row0, col0, p.m, p.n, (e.vec & 2) != 0);
@@ -630,16 +423,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       // another CTA is read in contiguous runs, and so is global memory.
       const Epilogue& e = p.e;
       int tm, tn;
-      tile_of(pair, p, tm, tn);
-      const int r0 = (warp - 2) * 8 + (lane >> 4), cols = min(p.bn, p.n - tn * p.bn);
+      tile_of(pair, p.tiles, tm, tn);
+      const int width = kGated ? p.bn / 2 : p.bn;
+      const int r0 = (warp - 2) * 8 + (lane >> 4), cols = min(width, p.n - tn * width);
       const long long grow0 = tm * 256 + rank * 128;
       for (int c = (place >> 1) * 64; c < cols; c += 64 * split) {
-        const int piece = c / 4 + (lane & 15), col = tn * p.bn + c + (lane & 15) * 4, left = p.n - col;
+        const int piece = c / 4 + (lane & 15), col = tn * width + c + (lane & 15) * 4, left = p.n - col;
         if (left <= 0) continue;
         float b[4] = {0.f, 0.f, 0.f, 0.f};
         if (e.bias) load4(static_cast<const T*>(e.bias) + col, left, e.vec & 1, b);
-        {
-          float z[4][4] = {};
+        // The pairs' sums of a piece of four rows, in order.
+        auto joined = [&](int piece, float(&z)[4][4]) {
           for (int q = 0; q < split; q += 2) {
             float4 v[2][4];  // all loads before the first sum
 #pragma unroll
@@ -657,6 +451,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                 z[i][3] += v[k][i].w;
               }
           }
+        };
+        float z[4][4] = {};
+        joined(piece, z);
+        if constexpr (kGated) {
+          float u[4][4] = {}, bu[4] = {0.f, 0.f, 0.f, 0.f};
+          joined(piece + width / 4, u);
+          if (e.bias) load4(static_cast<const T*>(e.bias) + p.n + col, left, (e.vec & 16) != 0, bu);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const long long row = grow0 + r0 + 2 * i;
+            if (row >= p.m) continue;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              z[i][k] += b[k];
+              u[i][k] += bu[k];
+            }
+            if (e.pre) {
+              store4(static_cast<T*>(e.pre) + row * e.ldpre + col, z[i], left, (e.vec & 4) != 0);
+              store4(static_cast<T*>(e.pre) + row * e.ldpre + p.n + col, u[i], left, (e.vec & 32) != 0);
+            }
+            activate_all(z[i], e.act);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) z[i][k] *= u[i][k];
+            store4(static_cast<T*>(e.out) + row * e.ldo + col, z[i], left, (e.vec & 8) != 0);
+          }
+        } else {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const long long row = grow0 + r0 + 2 * i;
@@ -718,7 +538,9 @@ struct FewProduct {
   Epilogue e;
 };
 
-template <typename T, int NT>
+// kGated: the MMA's 128 rows are 64 gate rows of the wide operand and the 64 up
+// rows that belong to the same outputs, so a CTA's sums hold both halves.
+template <typename T, int NT, bool kGated>
 __global__ void __launch_bounds__(kFewThreads, 2)
     product_few_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap mx,
                        const __grid_constant__ FewProduct p, uint32_t* flags) {
@@ -733,7 +555,8 @@ __global__ void __launch_bounds__(kFewThreads, 2)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_rank());
-  const int j0 = blockIdx.x / p.split * 128, i0 = blockIdx.y * NT;
+  constexpr int kCols = kGated ? 64 : 128;  // of D
+  const int j0 = blockIdx.x / p.split * kCols, i0 = blockIdx.y * NT;
   const int per = (p.kb + p.split - 1) / p.split;
   const int kb0 = min(rank * per, p.kb), kb1 = min(kb0 + per, p.kb);
 
@@ -772,7 +595,10 @@ __global__ void __launch_bounds__(kFewThreads, 2)
       const int k0 = kb * kBlock;
       if (elect_one()) {
         mbar_arrive_expect_tx_relaxed(&full[s], C::kStage);
-        if (p.w_mn) {
+        if (kGated) {
+          tma_load_2d(st, &mw, &full[s], k0, j0);
+          tma_load_2d(st + kBlockBytes, &mw, &full[s], k0, p.n + j0);
+        } else if (p.w_mn) {
           tma_load_2d(st, &mw, &full[s], j0, k0);
           tma_load_2d(st + kBlockBytes, &mw, &full[s], j0 + kBlock, k0);
         } else {
@@ -841,45 +667,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   __syncthreads();
   cluster_sync();
 
-  // This CTA's share of the columns: 128 / split of them, every token, four
-  // columns of a token at a time.
-  const Epilogue& e = p.e;
-  const int width = 32 / p.split, rows = min(NT, p.m - i0);
-  for (int at = threadIdx.x; at < rows * width; at += kFewThreads) {
-    const int i = at / width, jj = (rank * width + at % width) * 4, j = j0 + jj, left = p.n - j;
-    if (left <= 0) continue;
-    const float* mine = reinterpret_cast<const float*>(smem) + i * 128 + jj;
-    float z[4] = {};
-    for (int s0 = 0; s0 < p.split; s0 += 8) {
-      float4 u[8];  // all loads before the first sum
-#pragma unroll
-      for (int s = 0; s < 8; ++s)
-        if (s0 + s < p.split) u[s] = load_cluster16(mapa_shared(mine, s0 + s));
-#pragma unroll
-      for (int s = 0; s < 8; ++s)
-        if (s0 + s < p.split) {
-          z[0] += u[s].x;
-          z[1] += u[s].y;
-          z[2] += u[s].z;
-          z[3] += u[s].w;
-        }
-    }
-    const long long row = i0 + i;
-    float v[4];
-    if (e.bias) {
-      load4(static_cast<const T*>(e.bias) + j, left, e.vec & 1, v);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) z[q] += v[q];
-    }
-    if (e.pre) store4(static_cast<T*>(e.pre) + row * e.ldpre + j, z, left, (e.vec & 4) != 0);
-    activate_all(z, e.act);
-    if (e.res) {
-      load4(static_cast<const T*>(e.res) + row * e.ldr + j, left, (e.vec & 2) != 0, v);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) z[q] += v[q];
-    }
-    store4(static_cast<T*>(e.out) + row * e.ldo + j, z, left, (e.vec & 8) != 0);
-  }
+  join_few<T, kCols>(smem, p.e, p.split, rank, j0, i0, min(NT, p.m - i0), p.n, kFewThreads);
   cluster_sync();  // peers have read this CTA's sums
   if (warp == 1) {
     tc_fence_after();
@@ -906,6 +694,27 @@ __global__ void __launch_bounds__(256) empty_product_kernel(const Product p) {
     float y = activate(z, e.act);
     if (e.res) y += to_float(static_cast<const T*>(e.res)[row * e.ldr + col]);
     static_cast<T*>(e.out)[row * e.ldo + col] = from_float<T>(y);
+  }
+}
+
+// The same of a gated layer: out = act(bias of the gate) bias of up.
+template <typename T>
+__global__ void __launch_bounds__(256) empty_gated_kernel(const Product p) {
+  chain_next();
+  chain_wait();
+  const Epilogue& e = p.e;
+  const long long all = static_cast<long long>(p.m) * p.n;
+  for (long long i = blockIdx.x * 256LL + threadIdx.x; i < all; i += gridDim.x * 256LL) {
+    const long long row = i / p.n;
+    const int col = static_cast<int>(i % p.n);
+    const T* b = static_cast<const T*>(e.bias);
+    const float z = b ? to_float(b[col]) : 0.f, u = b ? to_float(b[p.n + col]) : 0.f;
+    if (e.pre) {
+      T* pre = static_cast<T*>(e.pre) + row * e.ldpre + col;
+      pre[0] = from_float<T>(z);
+      pre[p.n] = from_float<T>(u);
+    }
+    static_cast<T*>(e.out)[row * e.ldo + col] = from_float<T>(activate(z, e.act) * u);
   }
 }
 
@@ -1019,24 +828,83 @@ __global__ void __launch_bounds__(256, 4) slope_kernel(const T* dy, long long ld
   }
 }
 
-// ------------------------------------------------------------------- host
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static const EncodeTiledFn fn = [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) !=
-            cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      p = nullptr;
-    return reinterpret_cast<EncodeTiledFn>(p);
-  }();
-  return fn;
+// Stores eight consecutive elements of which `left` exist.
+template <typename T>
+__device__ __forceinline__ void store8(T* p, int left, bool vec, const float2 (&v)[4]) {
+  if (vec && left >= 8) {
+    *reinterpret_cast<uint4*>(p) = pack16<T>(v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (2 * i < left) p[2 * i] = from_float<T>(v[i].x);
+      if (2 * i + 1 < left) p[2 * i + 1] = from_float<T>(v[i].y);
+    }
+  }
 }
+
+// dz = [dh u act'(g)  dh act(g)] of the gated layer, rounded (where dz is given;
+// rows of 2 n elements, lddz apart), and its column sums per chunk of rows as
+// slope_kernel forms them: to part ([chunk][2 n]) or db.  vec: bits 1 dh, 2 g,
+// 4 u start on 16-byte boundaries, 8 so does dz's second half.  Bound by HBM:
+// three matrices read and two written.
+template <typename T, int kAct, int TX>
+__global__ void __launch_bounds__(256, 3) gated_slope_kernel(const T* dh, long long lddh, const T* pre, long long ldpre,
+                                                             T* dz, long long lddz, float* part, T* db, int m, int n,
+                                                             int chunk, int vec) {
+  constexpr int TY = 256 / TX, kCols = 8 * TX;
+  __shared__ float red[TY][kCols + 8];
+  chain_next();
+  chain_wait();
+  const int tx = threadIdx.x % TX, ty = threadIdx.x / TX;
+  const int col = blockIdx.x * kCols + tx * 8, left = n - col;
+  float2 sums[2][4] = {};
+  const long long end = min(static_cast<long long>(m), (blockIdx.y + 1LL) * chunk);
+  if (left > 0) {
+#pragma unroll 2
+    for (long long i = static_cast<long long>(blockIdx.y) * chunk + ty; i < end; i += TY) {
+      float2 d[4], g[4], u[4];
+      load8(dh + i * lddh + col, left, vec & 1, d);
+      load8(pre + i * ldpre + col, left, vec & 2, g);
+      load8(pre + i * ldpre + n + col, left, vec & 4, u);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float2 a, slope;
+        activation_and_slope2<kAct>(g[q], a, slope);
+        u[q] = mul2(mul2(d[q], u[q]), slope);
+        d[q] = mul2(d[q], a);
+        sums[0][q] = add2(sums[0][q], u[q]);
+        sums[1][q] = add2(sums[1][q], d[q]);
+      }
+      if (dz) {
+        store8(dz + i * lddz + col, left, true, u);  // rows start on 16-byte boundaries
+        store8(dz + i * lddz + n + col, left, vec & 8, d);
+      }
+    }
+  }
+  if (!part && !db) return;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      red[ty][tx * 8 + 2 * q] = sums[h][q].x;
+      red[ty][tx * 8 + 2 * q + 1] = sums[h][q].y;
+    }
+    __syncthreads();
+    const int j = blockIdx.x * kCols + threadIdx.x;
+    if (threadIdx.x < kCols && j < n) {
+      float sum = 0.f;
+#pragma unroll 8
+      for (int y = 0; y < TY; ++y) sum += red[y][threadIdx.x];
+      if (db)  // one chunk: the sum is whole
+        db[static_cast<long long>(h) * n + j] = from_float<T>(sum);
+      else
+        part[(2LL * blockIdx.y + h) * n + j] = sum;
+    }
+  }
+}
+
+// ------------------------------------------------------------------- host
 
 struct Matrix {
   const void* p;
@@ -1044,11 +912,6 @@ struct Matrix {
   int rows, cols;
 };
 
-int pad8(int x) { return (x + 7) & ~7; }
-
-bool rows_aligned(const void* p, long long ld, int rows) {
-  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (rows <= 1 || (ld & 7) == 0);
-}
 bool rows_aligned(const Matrix& x) { return rows_aligned(x.p, x.ld, x.rows); }
 
 // Bytes of a copy of x with rows on 16-byte boundaries; 0 where x's are.
@@ -1093,8 +956,6 @@ bool make_map(CUtensorMap* map, const Matrix& x, bool bf16, int box) {
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-constexpr int kMaxDev = 64;
-
 // Tiles that can be worked on at once by clusters of one, two or four CTA
 // pairs (a persistent grid must not exceed the first; the GPCs leave some SMs
 // out of the larger clusters: 76, 36 and 15 on this GPU); sets the kernel's
@@ -1102,7 +963,7 @@ constexpr int kMaxDev = 64;
 struct Resident {
   int tiles[3] = {0, 0, 0};
 };
-template <typename T>
+template <typename T, bool kGated>
 cudaError_t resident_clusters(Resident* out) {
   static Resident known[kMaxDev];
   static std::mutex mu;
@@ -1112,7 +973,7 @@ cudaError_t resident_clusters(Resident* out) {
   if (dev < 0 || dev >= kMaxDev) return cudaErrorInvalidDevice;
   std::lock_guard<std::mutex> lock(mu);
   if (known[dev].tiles[0] == 0) {
-    auto kern = product_pair_kernel<T>;
+    auto kern = product_pair_kernel<T, kGated>;
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem);
     if (e != cudaSuccess) return e;
     Resident r;
@@ -1157,14 +1018,17 @@ long long round_cost(int kb, int bn) {
   const int block = bn == 256 ? 530 : bn == 192 ? 430 : 375;
   return std::max<long long>(static_cast<long long>(kb) * block, 2000 + 16 * bn);
 }
-long long tiles_of(int m, int n, int bn) { return static_cast<long long>((m + 255) / 256) * ((n + bn - 1) / bn); }
+long long tiles_of(int m, long long n, int bn) { return static_cast<long long>((m + 255) / 256) * ((n + bn - 1) / bn); }
 
-Tiling tiling(const Product& p, const Resident& resident) {
+// A gated product's tiles have n / (bn / 2) columns, of 256 or 128: whole
+// 64-column chunks of each half.
+Tiling tiling(const Product& p, const Resident& resident, bool gated = false) {
   Tiling t = {256, 1, -1};
-  for (int bn = 256; bn >= 64; bn -= p.b_mn ? 128 : 64)
+  for (int bn = 256; bn >= (gated ? 128 : 64); bn -= p.b_mn || gated ? 128 : 64)
     for (int i = 0; i < 3 && (64 << i) <= bn && resident.tiles[i] > 0; ++i) {
       const int split = 1 << i;
-      const long long rounds = (tiles_of(p.m, p.n, bn) + resident.tiles[i] - 1) / resident.tiles[i];
+      const long long rounds =
+          (tiles_of(p.m, gated ? 2LL * p.n : p.n, bn) + resident.tiles[i] - 1) / resident.tiles[i];
       const long long cost =
           rounds * (round_cost((p.kb + split - 1) / split, bn) + (split > 1 ? 4000 + 25 * bn : 0)) + 16 * bn;
       if (t.cost < 0 || cost < t.cost) t = {bn, split, cost};
@@ -1209,7 +1073,7 @@ bool make_maps(const Ready& r, CUtensorMap* ma, CUtensorMap* mb) {
   return make_map(ma, r.a, Pair<T>::kBf16, r.p.a_mn ? kBlock : 2 * kBlock) &&
          make_map(mb, r.b, Pair<T>::kBf16, r.p.b_mn || r.p.bn <= 128 ? kBlock : 2 * kBlock);
 }
-template <typename T>
+template <typename T, bool kGated>
 cudaError_t launch_pairs(Ready* r, int count, int pairs, uint32_t* flags, cudaStream_t stream) {
   CUtensorMap m[4];
   Products g;
@@ -1219,16 +1083,10 @@ cudaError_t launch_pairs(Ready* r, int count, int pairs, uint32_t* flags, cudaSt
   int tiles = 0;
   for (int i = 0; i < count; ++i) {
     Product& p = r[i].p;
-    p.tiles_m = (p.m + 255) / 256;
-    p.tiles_n = (p.n + p.bn - 1) / p.bn;
+    const int width = kGated ? p.bn / 2 : p.bn;
+    p.tiles = raster((p.m + 255) / 256, (p.n + width - 1) / width);
     p.share = (p.kb + p.split - 1) / p.split;
-    // ceil(2^(32 + shift) / d) with 2^shift >= d gives t / d for t < 2^31; with
-    // the shift one less the multiplier fits 32 bits, for t < 2^31 still.
-    const uint64_t d = static_cast<uint64_t>(kGroupM) * p.tiles_n;
-    p.group_shift = 0;
-    while ((2ull << p.group_shift) < d) ++p.group_shift;
-    p.group_inverse = static_cast<uint32_t>(((1ull << (32 + p.group_shift)) + d - 1) / d);
-    tiles += p.tiles_m * p.tiles_n;
+    tiles += p.tiles.count();
     if (p.bn > 128) {
       g.stage_bytes = 4 * kBlockBytes;
       g.bufs = 2;
@@ -1242,17 +1100,17 @@ cudaError_t launch_pairs(Ready* r, int count, int pairs, uint32_t* flags, cudaSt
     m[3] = m[1];
   }
   const int split = g.p[0].split;
-  return launch_chained(product_pair_kernel<T>, dim3(2 * (split > 1 ? tiles * split : std::min(tiles, pairs))), kThreads,
+  return launch_chained(product_pair_kernel<T, kGated>, dim3(2 * (split > 1 ? tiles * split : std::min(tiles, pairs))), kThreads,
                         kPairSmem, stream, 2 * split, m[0], m[1], m[2], m[3], g, flags);
 }
 
-template <typename T, int NT>
+template <typename T, int NT, bool kGated>
 cudaError_t launch_few(const Matrix& w, bool w_mn, const Matrix& x, FewProduct p, uint32_t* flags,
                        cudaStream_t stream) {
   CUtensorMap mw, mx;
-  if (!make_map(&mw, w, Pair<T>::kBf16, w_mn ? kBlock : 2 * kBlock) || !make_map(&mx, x, Pair<T>::kBf16, NT))
+  if (!make_map(&mw, w, Pair<T>::kBf16, w_mn || kGated ? kBlock : 2 * kBlock) || !make_map(&mx, x, Pair<T>::kBf16, NT))
     return cudaErrorInvalidValue;
-  auto kern = product_few_kernel<T, NT>;
+  auto kern = product_few_kernel<T, NT, kGated>;
   static std::atomic<bool> ready[kMaxDev];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1264,7 +1122,7 @@ cudaError_t launch_few(const Matrix& w, bool w_mn, const Matrix& x, FewProduct p
     if (e != cudaSuccess) return e;
     ready[dev] = true;
   }
-  const int across = (p.n + 127) / 128, down = (p.m + NT - 1) / NT;
+  const int across = kGated ? (p.n + 63) / 64 : (p.n + 127) / 128, down = (p.m + NT - 1) / NT;
   p.w_mn = w_mn;
   // Two CTAs on each SM, and at least four blocks of the reduction for each.
   p.split = 1;
@@ -1277,7 +1135,11 @@ cudaError_t launch_few(const Matrix& w, bool w_mn, const Matrix& x, FewProduct p
 // The product D = A B^T over `depth`, with the epilogue e.  a: m x depth (or
 // depth x m where a_mn), b likewise; rows on 16-byte boundaries.
 Ready ready(int m, int n, int depth, const Matrix& a, bool a_mn, const Matrix& b, bool b_mn, Epilogue e) {
-  e.vec = (e.bias && rows_aligned(e.bias, 0, 1) ? 1 : 0) | (e.res && rows_aligned(e.res, e.ldr, m) ? 2 : 0) |
+  // A gated product's second halves start n elements on.
+  const bool half = (n & 7) == 0;
+  e.vec = (half && e.bias && rows_aligned(e.bias, 0, 1) ? 16 : 0) |
+          (half && e.pre && rows_aligned(e.pre, e.ldpre, m) ? 32 : 0) |
+          (e.bias && rows_aligned(e.bias, 0, 1) ? 1 : 0) | (e.res && rows_aligned(e.res, e.ldr, m) ? 2 : 0) |
           (e.pre && rows_aligned(e.pre, e.ldpre, m) ? 4 : 0) | (rows_aligned(e.out, e.ldo, m) ? 8 : 0);
   Product p = {};
   p.m = m;
@@ -1295,33 +1157,34 @@ Ready ready(int m, int n, int depth, const Matrix& a, bool a_mn, const Matrix& b
 // 76 tiles of 128 x 128 with a reduction worth sharing.  128 rows of 4096 ->
 // 4096 take it 15.5 us (pairs 18), 256 rows of 8192 -> 1024 15.7 (19.5); but
 // 256 rows of 4096 -> 16384 41.7 (30).
-bool few_rows(const Product& p) {
-  const long long squares = static_cast<long long>((p.m + 127) / 128) * ((p.n + 127) / 128);
+bool few_rows(const Product& p, bool gated = false) {
+  const long long squares =
+      static_cast<long long>((p.m + 127) / 128) * (gated ? (p.n + 63) / 64 : (p.n + 127) / 128);
   return !p.a_mn && (p.m <= 128 || (squares <= 76 && p.kb >= 32));
 }
 
-template <typename T>
+template <typename T, bool kGated = false>
 cudaError_t run_product(Ready r, uint32_t* flags, cudaStream_t stream) {
   Product& p = r.p;
   if (p.kb == 0) {
     const long long all = static_cast<long long>(p.m) * p.n;
-    return launch_chained(empty_product_kernel<T>,
+    return launch_chained(kGated ? empty_gated_kernel<T> : empty_product_kernel<T>,
                           dim3(static_cast<unsigned>(std::min<long long>((all + 255) / 256, 4096))), 256, 0, stream, 0, p);
   }
-  if (few_rows(p)) {
+  if (few_rows(p, kGated)) {
     const FewProduct f = {p.m, p.n, p.kb, 0, 1, p.e};
-    return p.m <= 16   ? launch_few<T, 16>(r.b, p.b_mn, r.a, f, flags, stream)
-           : p.m <= 32 ? launch_few<T, 32>(r.b, p.b_mn, r.a, f, flags, stream)
-           : p.m <= 64 ? launch_few<T, 64>(r.b, p.b_mn, r.a, f, flags, stream)
-                       : launch_few<T, 128>(r.b, p.b_mn, r.a, f, flags, stream);
+    return p.m <= 16   ? launch_few<T, 16, kGated>(r.b, p.b_mn, r.a, f, flags, stream)
+           : p.m <= 32 ? launch_few<T, 32, kGated>(r.b, p.b_mn, r.a, f, flags, stream)
+           : p.m <= 64 ? launch_few<T, 64, kGated>(r.b, p.b_mn, r.a, f, flags, stream)
+                       : launch_few<T, 128, kGated>(r.b, p.b_mn, r.a, f, flags, stream);
   }
   Resident resident;
-  const cudaError_t s = resident_clusters<T>(&resident);
+  const cudaError_t s = resident_clusters<T, kGated>(&resident);
   if (s != cudaSuccess) return s;
-  const Tiling t = tiling(p, resident);
+  const Tiling t = tiling(p, resident, kGated);
   p.bn = t.bn;
   p.split = t.split;
-  return launch_pairs<T>(&r, 1, resident.tiles[0], flags, stream);
+  return launch_pairs<T, kGated>(&r, 1, resident.tiles[0], flags, stream);
 }
 
 // Two products, in one launch where that is quicker: their tiles together fill
@@ -1330,7 +1193,7 @@ template <typename T>
 cudaError_t run_products(Ready a, Ready b, uint32_t* flags, cudaStream_t stream) {
   if (a.p.kb > 0 && b.p.kb > 0 && !few_rows(a.p) && !few_rows(b.p)) {
     Resident resident;
-    const cudaError_t s = resident_clusters<T>(&resident);
+    const cudaError_t s = resident_clusters<T, false>(&resident);
     if (s != cudaSuccess) return s;
     if (a.p.kb < b.p.kb) std::swap(a, b);  // the longer tiles first
     const TwoTilings t = together(a.p, b.p, resident.tiles[0]);
@@ -1338,7 +1201,7 @@ cudaError_t run_products(Ready a, Ready b, uint32_t* flags, cudaStream_t stream)
       a.p.bn = t.bn[0];
       b.p.bn = t.bn[1];
       Ready both[2] = {a, b};
-      return launch_pairs<T>(both, 2, resident.tiles[0], flags, stream);
+      return launch_pairs<T, false>(both, 2, resident.tiles[0], flags, stream);
     }
   }
   const cudaError_t s = run_product<T>(a, flags, stream);
@@ -1398,6 +1261,21 @@ cudaError_t run_slope(const LinearGradCall& c, const BackwardPlan& p, T* dz, flo
                         db, nullptr);
 }
 
+// dx = dz w and dw = dz^T x, with dz of n columns.
+template <typename T>
+cudaError_t grad_products(const LinearGradCall& c, int n, const Matrix& dz, const Matrix& x, const Matrix& w,
+                          cudaStream_t stream) {
+  Epilogue to_dx = {nullptr, nullptr, 0, nullptr, 0, c.dx, c.lddx, kActNone, 0}, to_dw = to_dx;
+  to_dw.out = c.dw;
+  to_dw.ldo = c.lddw;
+  const bool want_dx = c.dx && c.m > 0 && c.k > 0, want_dw = c.dw && n > 0 && c.k > 0;
+  const Ready dx = ready(c.m, c.k, n, dz, false, w, true, to_dx), dw = ready(n, c.k, c.m, dz, true, x, true, to_dw);
+  if (want_dx && want_dw) return run_products<T>(dx, dw, c.flags, stream);
+  if (want_dx) return run_product<T>(dx, c.flags, stream);
+  if (want_dw) return run_product<T>(dw, c.flags, stream);
+  return cudaSuccess;
+}
+
 template <typename T>
 cudaError_t linear_backward_t(const LinearGradCall& c, cudaStream_t stream) {
   Matrix dz = {c.dy, c.lddy, c.m, c.n}, x = {c.x, c.ldx, c.m, c.k}, w = {c.w, c.ldw, c.n, c.k};
@@ -1426,16 +1304,77 @@ cudaError_t linear_backward_t(const LinearGradCall& c, cudaStream_t stream) {
     s = launch_chained(join_parts_kernel<T>, dim3((c.n + 31) / 32), 1024, 0, stream, 0, nullptr, 0, 0, c.n,
                        static_cast<T*>(c.db), nullptr);
   }
+  return s == cudaSuccess ? grad_products<T>(c, c.n, dz, x, w, stream) : s;
+}
+
+// ------------------------------------------------------- the gated layer's
+
+template <typename T>
+cudaError_t gated_t(const LinearCall& c, cudaStream_t stream) {
+  Matrix x = {c.x, c.ldx, c.m, c.k}, w = {c.w, c.ldw, 2 * c.n, c.k};
+  const cudaError_t s = align_operands(&x, &w, static_cast<uint8_t*>(c.ws), stream);
   if (s != cudaSuccess) return s;
-  Epilogue to_dx = {nullptr, nullptr, 0, nullptr, 0, c.dx, c.lddx, kActNone, 0}, to_dw = to_dx;
-  to_dw.out = c.dw;
-  to_dw.ldo = c.lddw;
-  const bool want_dx = c.dx && c.m > 0 && c.k > 0, want_dw = c.dw && c.n > 0 && c.k > 0;
-  const Ready dx = ready(c.m, c.k, c.n, dz, false, w, true, to_dx), dw = ready(c.n, c.k, c.m, dz, true, x, true, to_dw);
-  if (want_dx && want_dw) return run_products<T>(dx, dw, c.flags, stream);
-  if (want_dx) return run_product<T>(dx, c.flags, stream);
-  if (want_dw) return run_product<T>(dw, c.flags, stream);
-  return cudaSuccess;
+  const Epilogue e = {c.bias, nullptr, 0, c.pre, c.ldpre, c.y, c.ldy, c.act, 0};
+  return run_product<T, true>(ready(c.m, c.n, c.k, x, false, w, false, e), c.flags, stream);
+}
+
+struct GatedPlan {
+  int chunk, chunks;
+  size_t dz, part, x, w;
+};
+GatedPlan gated_plan(const LinearGradCall& c) {
+  GatedPlan p;
+  const size_t up = 255;
+  p.dz = (static_cast<size_t>(c.m) * pad8(2 * c.n) * 2 + up) & ~up;
+  p.chunk = slope_chunk(c.m, c.n);
+  p.chunks = (c.m + p.chunk - 1) / p.chunk;
+  p.part = p.chunks > 1 ? (static_cast<size_t>(p.chunks) * 2 * c.n * 4 + up) & ~up : 0;
+  p.x = aligned_copy_bytes({c.x, c.ldx, c.m, c.k});
+  p.w = aligned_copy_bytes({c.w, c.ldw, 2 * c.n, c.k});
+  return p;
+}
+
+template <typename T, int kAct>
+cudaError_t run_gated_slope(const LinearGradCall& c, const GatedPlan& p, T* dz, float* part, cudaStream_t stream) {
+  const bool half = (c.n & 7) == 0, pre = rows_aligned(c.pre, c.ldpre, c.m);
+  const int vec = (rows_aligned(c.dy, c.lddy, c.m) ? 1 : 0) | (pre ? 2 : 0) | (pre && half ? 4 : 0) | (half ? 8 : 0);
+  T* db = static_cast<T*>(c.db);
+  const bool whole = p.chunks == 1;
+  const int tx = c.m <= kFewSlopeRows ? 4 : 32;
+  const cudaError_t s = launch_chained(
+      tx == 4 ? gated_slope_kernel<T, kAct, 4> : gated_slope_kernel<T, kAct, 32>,
+      dim3((c.n + 8 * tx - 1) / (8 * tx), p.chunks), 256, 0, stream, 0, static_cast<const T*>(c.dy), c.lddy,
+      static_cast<const T*>(c.pre), c.ldpre, dz, pad8(2 * c.n), db && !whole ? part : nullptr, whole ? db : nullptr, c.m,
+      c.n, p.chunk, vec);
+  if (s != cudaSuccess || !db || whole) return s;
+  return launch_chained(join_parts_kernel<T>, dim3((2 * c.n + 31) / 32), 1024, 0, stream, 0, part, p.chunks, p.chunks,
+                        2 * c.n, db, nullptr);
+}
+
+template <typename T>
+cudaError_t gated_backward_t(const LinearGradCall& c, cudaStream_t stream) {
+  Matrix dz = {nullptr, pad8(2 * c.n), c.m, 2 * c.n}, x = {c.x, c.ldx, c.m, c.k}, w = {c.w, c.ldw, 2 * c.n, c.k};
+  cudaError_t s = cudaSuccess;
+  if (c.m > 0 && c.n > 0) {
+    const GatedPlan plan = gated_plan(c);
+    uint8_t* ws = static_cast<uint8_t*>(c.ws);
+    T* own = c.dx || c.dw ? reinterpret_cast<T*>(ws) : nullptr;
+    dz.p = own;
+    float* part = reinterpret_cast<float*>(ws + plan.dz);
+    switch (c.act) {
+      case kActRelu: s = run_gated_slope<T, kActRelu>(c, plan, own, part, stream); break;
+      case kActGelu: s = run_gated_slope<T, kActGelu>(c, plan, own, part, stream); break;
+      case kActGeluTanh: s = run_gated_slope<T, kActGeluTanh>(c, plan, own, part, stream); break;
+      case kActSilu: s = run_gated_slope<T, kActSilu>(c, plan, own, part, stream); break;
+      default: s = run_gated_slope<T, kActNone>(c, plan, own, part, stream); break;
+    }
+    Matrix none = {nullptr, 0, 0, 0};
+    if (s == cudaSuccess) s = align_operands(c.dw ? &x : &none, c.dx ? &w : &none, ws + plan.dz + plan.part, stream);
+  } else if (c.db && c.n > 0) {
+    s = launch_chained(join_parts_kernel<T>, dim3((2 * c.n + 31) / 32), 1024, 0, stream, 0, nullptr, 0, 0, 2 * c.n,
+                       static_cast<T*>(c.db), nullptr);
+  }
+  return s == cudaSuccess ? grad_products<T>(c, 2 * c.n, dz, x, w, stream) : s;
 }
 
 }  // namespace
@@ -1455,6 +1394,23 @@ size_t linear_backward_workspace(const LinearGradCall& c) {
 
 cudaError_t launch_linear_backward(const LinearGradCall& c, cudaStream_t stream) {
   return c.type == kF16 ? linear_backward_t<__half>(c, stream) : linear_backward_t<__nv_bfloat16>(c, stream);
+}
+
+size_t gated_linear_workspace(const LinearCall& c) {
+  return aligned_copy_bytes({c.x, c.ldx, c.m, c.k}) + aligned_copy_bytes({c.w, c.ldw, 2 * c.n, c.k});
+}
+
+cudaError_t launch_gated_linear(const LinearCall& c, cudaStream_t stream) {
+  return c.type == kF16 ? gated_t<__half>(c, stream) : gated_t<__nv_bfloat16>(c, stream);
+}
+
+size_t gated_linear_backward_workspace(const LinearGradCall& c) {
+  const GatedPlan p = gated_plan(c);
+  return p.dz + p.part + p.x + p.w;
+}
+
+cudaError_t launch_gated_linear_backward(const LinearGradCall& c, cudaStream_t stream) {
+  return c.type == kF16 ? gated_backward_t<__half>(c, stream) : gated_backward_t<__nv_bfloat16>(c, stream);
 }
 
 }  // namespace ozemu

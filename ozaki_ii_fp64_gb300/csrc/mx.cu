@@ -1,0 +1,761 @@
+// Microscaled 4-bit matrices (MXFP4) and their product.
+//
+//   s = 2^max(floor(log2 max|x|) - 2, -127) over 32 consecutive columns,
+//   q = x / s rounded to e2m1 (half to even, 6 beyond),  x ~ s q
+//   y = act(x w^T + b) + r  of two such matrices
+//
+// Every step of the quantisation is exact but the one rounding: s is a power of
+// two, so x / s is, and the conversion instruction rounds it.  The product runs
+// on tcgen05 kind::mxf4, whose operands are the codes and whose scales are the
+// bytes as they lie in memory, with fp32 accumulators in TMEM.
+//
+// A matrix of `rows` x k:
+//   codes   [rows][ceil(k / 32) * 16] bytes, element j of a row in byte j / 2,
+//           the low half for even j; 0 past column k
+//   scales  [ceil(rows / 128)][ceil(k / 256)][1024] bytes: of 128 rows and 256
+//           columns, the exponent byte (127 + log2 s) of row r and columns
+//           32 b .. 32 b + 31 at (b / 4) 512 + (r % 32) 16 + (r / 32) 4 + b % 4;
+//           127 past the last row or column.  512 bytes are what one tcgen05.cp
+//           brings to TMEM as the MMA reads them (32 lanes of 16 bytes), so a
+//           stage's scales are one contiguous copy.
+#include <algorithm>
+#include <atomic>
+#include <cstdint>
+#include <cuda.h>
+#include <mutex>
+
+#include "kernels.h"
+#include "product.cuh"
+
+namespace ozemu {
+
+namespace {
+
+constexpr int kTileRows = 128, kTileCols = 256;  // of a 1024-byte tile of scales
+
+// Eight elements of which `left` exist as floats, 0 past them.
+template <typename T>
+__device__ __forceinline__ void load_eight(const T* p, int left, bool vec, float2 (&v)[4]) {
+  if (vec && left >= 8) {
+    if constexpr (sizeof(T) == 4) {
+      const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+      v[0] = make_float2(a.x, a.y);
+      v[1] = make_float2(a.z, a.w);
+      v[2] = make_float2(b.x, b.y);
+      v[3] = make_float2(b.z, b.w);
+    } else {
+      unpack16<T>(__ldg(reinterpret_cast<const uint4*>(p)), v);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      v[i] = make_float2(2 * i < left ? to_float(p[2 * i]) : 0.f, 2 * i + 1 < left ? to_float(p[2 * i + 1]) : 0.f);
+  }
+}
+
+// Eight values already divided by their scale to eight codes, the first lowest.
+__device__ __forceinline__ uint32_t to_codes(const float2 (&v)[4]) {
+  uint32_t r;
+  asm("{\n .reg .b8 a, b, c, d;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n"
+      " mov.b32 %0, {a, b, c, d};\n}"
+      : "=r"(r)
+      : "f"(v[0].x), "f"(v[0].y), "f"(v[1].x), "f"(v[1].y), "f"(v[2].x), "f"(v[2].y), "f"(v[3].x), "f"(v[3].y));
+  return r;
+}
+
+// The values of eight codes.
+__device__ __forceinline__ void from_codes(uint32_t w, float2 (&v)[4]) {
+  uint32_t h[4];
+  asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %4;\n"
+      " cvt.rn.f16x2.e2m1x2 %0, a;\n cvt.rn.f16x2.e2m1x2 %1, b;\n"
+      " cvt.rn.f16x2.e2m1x2 %2, c;\n cvt.rn.f16x2.e2m1x2 %3, d;\n}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = Pair<__half>::unpack(h[i]);
+}
+
+// Place of the scale of a tile's row r and 32-column block b.
+__device__ __forceinline__ int scale_at(int r, int b) { return (b >> 2) * 512 + (r & 31) * 16 + (r >> 5) * 4 + (b & 3); }
+
+// One CTA to a tile of scales: 128 rows of 256 columns.  A warp takes a row, a
+// lane eight columns of it, four lanes a block; four rows of a warp are in
+// flight.  A block with an infinity or a NaN takes the scale NaN (255).
+template <typename T>
+__global__ void __launch_bounds__(256) mx_quantize_kernel(const T* x, long long ldx, int rows, int k, uint8_t* codes,
+                                                          uint8_t* scales, int ktiles, int vec) {
+  __shared__ uint4 tile[64];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x < 64) tile[threadIdx.x] = make_uint4(0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+  chain_next();
+  chain_wait();
+  __syncthreads();
+  const int rb = blockIdx.x / ktiles, kt = blockIdx.x % ktiles;
+  const int r0 = rb * kTileRows, here = min(kTileRows, rows - r0);
+  const int col = kt * kTileCols + lane * 8, left = k - col;
+  const long long row_bytes = (k + 31LL) / 32 * 16;
+  const bool stored = col < (k + 31) / 32 * 32;
+#pragma unroll 1
+  for (int i0 = warp; i0 < here; i0 += 32) {
+    float2 v[4][4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      load_eight(x + (r0 + i0 + 8LL * q) * ldx + col, i0 + 8 * q < here ? left : 0, vec, v[q]);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int r = i0 + 8 * q;
+      uint32_t most = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        most = max(most, max(__float_as_uint(v[q][i].x) & 0x7FFFFFFFu, __float_as_uint(v[q][i].y) & 0x7FFFFFFFu));
+      most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
+      most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
+      const int e = static_cast<int>(most >> 23), byte = e == 255 ? 255 : max(e - 2, 0);
+      const float2 inverse = both(__uint_as_float(static_cast<uint32_t>(254 - byte) << 23));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[q][i] = mul2(v[q][i], inverse);
+      const uint32_t w = byte == 255 ? 0 : to_codes(v[q]);
+      if (r < here && stored) {
+        *reinterpret_cast<uint32_t*>(codes + (r0 + r) * row_bytes + col / 2) = w;
+        if ((lane & 3) == 0) reinterpret_cast<uint8_t*>(tile)[scale_at(r, lane >> 2)] = static_cast<uint8_t>(byte);
+      }
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x < 64) reinterpret_cast<uint4*>(scales + blockIdx.x * 1024LL)[threadIdx.x] = tile[threadIdx.x];
+}
+
+// The values that codes and scales stand for: the same tiles and lanes.
+template <typename T>
+__global__ void __launch_bounds__(256) mx_dequantize_kernel(const uint8_t* codes, const uint8_t* scales, int ktiles, T* y,
+                                                            long long ldy, int rows, int k, int vec) {
+  chain_next();
+  chain_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rb = blockIdx.x / ktiles, kt = blockIdx.x % ktiles;
+  const int r0 = rb * kTileRows, here = min(kTileRows, rows - r0);
+  const int col = kt * kTileCols + lane * 8, left = k - col;
+  if (left <= 0) return;
+  const long long row_bytes = (k + 31LL) / 32 * 16;
+  const uint8_t* tile = scales + blockIdx.x * 1024LL;
+#pragma unroll 4
+  for (int r = warp; r < here; r += 8) {
+    const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(codes + (r0 + r) * row_bytes + col / 2));
+    const uint32_t byte = __ldg(tile + scale_at(r, lane >> 2));
+    const float s = __uint_as_float(byte == 255 ? 0x7FC00000u : byte == 0 ? 0x00400000u : byte << 23);
+    float2 v[4];
+    from_codes(w, v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = mul2(v[i], both(s));
+    T* p = y + static_cast<long long>(r0 + r) * ldy + col;
+    if (vec && left >= 8) {
+      if constexpr (sizeof(T) == 4) {
+        reinterpret_cast<uint4*>(p)[0] = pack16<T>(v);
+        reinterpret_cast<uint4*>(p)[1] = pack16<T>(v + 2);
+      } else {
+        *reinterpret_cast<uint4*>(p) = pack16<T>(v);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (2 * i < left) p[2 * i] = from_float<T>(v[i].x);
+        if (2 * i + 1 < left) p[2 * i + 1] = from_float<T>(v[i].y);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Large products: 256 x BN tiles on CTA pairs, BN = 256 or 128.
+//
+// As the pair kernel of linear.cu: each CTA of a cluster of two stages its 128
+// rows of A and BN / 2 rows of B, 256 of the reduction (128 bytes) a stage,
+// with the scales of its rows of A and of all the tile's rows of B; a warp loads
+// A, one B, one brings the scales to TMEM and issues the MMAs (4 of K = 64 a
+// stage), and sixteen take finished accumulators out.  Scales take 24 columns a
+// stage, two stages in turn.  That leaves 448 columns for accumulators: two of
+// 256 that share 64, the end of one and the start of the other.  The epilogue
+// takes the half with the shared columns first, and the next tile's MMAs start
+// once that half is in registers.
+// ---------------------------------------------------------------------------
+constexpr int kMxThreads = 32 * (3 + kEpiWarps);
+constexpr int kCodes = 128 * 128;                        // bytes of 128 rows of 256 codes
+constexpr int kMxStage = 2 * kCodes + 3 * 1024;          // A, B, scales of A's 128 rows and of B's 256
+constexpr int kMxStages = 5;
+constexpr int kMxSmem = 1024 + kMxStages * kMxStage + kEpiWarps * (2048 + 64) + 256;
+constexpr uint32_t kScaleColumns = 448, kScaleTurn = 32;
+constexpr uint32_t kSecondAccumulator = 192;  // of two of 256 columns
+
+struct MxProduct {
+  int m, n, kt;  // kt: 256-element stages of the reduction
+  int bn;
+  Raster tiles;
+  Epilogue e;
+};
+
+template <int kGroup>
+__device__ __forceinline__ void mma_mx(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
+                                       uint32_t accumulate) {
+  if constexpr (kGroup == 2)
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+        : "memory");
+}
+
+// 512 bytes of scales (32 lanes of 16 bytes, no swizzle) to four columns of
+// TMEM, the same for each of its four lane quarters.
+template <int kGroup>
+__device__ __forceinline__ void copy_scales(uint32_t columns, uint32_t saddr) {
+  const uint64_t desc = ((saddr & 0x3FFFFu) >> 4) | (1u << 16) | (static_cast<uint64_t>((128u >> 4) | (1u << 14)) << 32);
+  if constexpr (kGroup == 2)
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(columns), "l"(desc) : "memory");
+  else
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(columns), "l"(desc) : "memory");
+}
+
+// Instruction descriptor: e2m1 operands, K-major, exponent-byte scales, of which
+// a 32-bit word of TMEM holds four for a row: this MMA takes those of byte
+// 2 half and the next.
+__device__ __forceinline__ uint32_t idesc_mx(int m, int n, int half) {
+  return (static_cast<uint32_t>(2 * half) << 4)    // B's scales
+         | (1u << 7)                               // A format: e2m1
+         | (1u << 10)                              // B format: e2m1
+         | (static_cast<uint32_t>(n >> 3) << 17)   // N / 8
+         | (1u << 23)                              // scale type: exponent byte
+         | (static_cast<uint32_t>(m >> 7) << 27)   // M / 128
+         | (static_cast<uint32_t>(2 * half) << 29);  // A's scales
+}
+
+// The copies and MMAs of one stage: codes at a and b, scales of A's 128 rows and
+// of B's (b_tiles tiles of 128 rows) to 8 + 8 b_tiles columns of TMEM.
+template <int kGroup>
+__device__ __forceinline__ void stage_mmas(uint32_t d, uint32_t a, uint32_t b, uint32_t scales_a, uint32_t scales_b,
+                                           int b_tiles, uint32_t columns, int m, int n, bool first) {
+  const uint32_t sa = columns, sb = columns + 8, b_step = 4 * b_tiles;
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    copy_scales<kGroup>(sa + 4 * q, scales_a + 512 * q);
+    copy_scales<kGroup>(sb + b_step * q, scales_b + 512 * q);
+    if (b_tiles > 1) copy_scales<kGroup>(sb + b_step * q + 4, scales_b + 1024 + 512 * q);
+  }
+  const uint32_t a_lo = smem_desc_sw128_lo(a, false), b_lo = smem_desc_sw128_lo(b, false);
+#pragma unroll
+  for (int ks = 0; ks < 4; ++ks)
+    mma_mx<kGroup>(d, smem_desc_sw128(a_lo + 2 * ks), smem_desc_sw128(b_lo + 2 * ks), idesc_mx(m, n, ks & 1),
+                   sa + 4 * (ks >> 1), sb + b_step * (ks >> 1), first && ks == 0 ? 0u : 1u);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kMxThreads, 1)
+    mx_pair_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
+                   const __grid_constant__ CUtensorMap msa, const __grid_constant__ CUtensorMap msb,
+                   const __grid_constant__ MxProduct p, uint32_t* flags) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* staging = smem + kMxStages * kMxStage;
+  uint8_t* biases = staging + kEpiWarps * 2048;
+  uint64_t* full = reinterpret_cast<uint64_t*>(biases + kEpiWarps * 64);
+  uint64_t* empty = full + kMxStages;
+  uint64_t* tfull = empty + kMxStages;
+  uint64_t* taken = tfull + 2;
+  uint64_t* mma_done = taken + 2;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(mma_done + 1);
+  volatile int* abort_word = reinterpret_cast<volatile int*>(tmem_holder + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_rank());
+  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1, total = p.tiles.count();
+  const bool wide = p.bn == 256;
+  const uint32_t second = wide ? kSecondAccumulator : 128;
+
+  if (warp == 0 && lane == 0) {
+    for (int s = 0; s < kMxStages; ++s) {
+      mbar_init(&full[s], 1);   // armed by the first CTA with both CTAs' bytes
+      mbar_init(&empty[s], 1);  // one commit from the pair's MMA issuer
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&tfull[b], 1);
+      mbar_init(&taken[b], 2 * kEpiWarps);
+    }
+    mbar_init(mma_done, 1);
+    *abort_word = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&ma);
+    tma_prefetch_desc(&mb);
+    tma_prefetch_desc(&msa);
+    tma_prefetch_desc(&msb);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_holder, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tbase = *tmem_holder;
+  chain_next();
+  chain_wait();
+
+  if (warp == 0 || warp == 2 + kEpiWarps) {
+    const bool loads_a = warp == 0;
+    const uint32_t bar0 = mapa_shared(&full[0], 0);
+    const uint32_t bytes = 2 * (kCodes + p.bn / 2 * 128 + 1024 + p.bn / 128 * 1024);  // of both CTAs
+    int s = 0;
+    uint32_t phase = 1;
+    bool ok = true;
+    for (int t = pair; t < total && ok; t += npairs) {
+      int tm, tn;
+      tile_of(t, p.tiles, tm, tn);
+      const int at = loads_a ? tm * 256 + rank * 128 : tn * p.bn + rank * (p.bn / 2);
+      const int block = loads_a ? tm * 2 + rank : tn * p.bn / 128;  // of 128 rows, the scales'
+      for (int kt = 0; kt < p.kt; ++kt) {
+        if (!all_wait(&empty[s], phase, abort_word, flags)) {
+          ok = false;
+          break;
+        }
+        uint8_t* st = smem + s * kMxStage;
+        const uint32_t bar = bar0 + s * 8;
+        if (elect_one()) {
+          if (loads_a) {
+            if (rank == 0) mbar_arrive_expect_tx_relaxed(&full[s], bytes);
+            tma_load_2d_pair(st, &ma, bar, kt * 128, at);
+            tma_load_2d_pair(st + 2 * kCodes, &msa, bar, kt * 256, block);
+          } else {
+            tma_load_2d_pair(st + kCodes, &mb, bar, kt * 128, at);
+            tma_load_2d_pair(st + 2 * kCodes + 1024, &msb, bar, kt * 256, block);
+            if (wide) tma_load_2d_pair(st + 2 * kCodes + 2048, &msb, bar, kt * 256, block + 1);
+          }
+        }
+        __syncwarp();
+        if (++s == kMxStages) {
+          s = 0;
+          phase ^= 1;
+        }
+      }
+    }
+    if (!ok) settle_after_abort();
+    __syncwarp();
+  } else if (warp == 1) {
+    if (rank == 0) {
+      int s = 0, n_tiles = 0, turn = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int t = pair; t < total && ok; t += npairs, ++n_tiles) {
+        const int buf = n_tiles & 1;
+        // Its columns are free: of two wide accumulators, once the tile before
+        // has left the shared ones, else once the tile before that has.
+        const int before = n_tiles - (wide ? 1 : 2);
+        if (before >= 0 && !all_wait(&taken[before & 1], (before >> 1) & 1, abort_word, flags)) break;
+        tc_fence_after();
+        const uint32_t d = tbase + (buf ? second : 0);
+        for (int kt = 0; kt < p.kt; ++kt, turn ^= 1) {
+          if (!all_wait(&full[s], phase, abort_word, flags)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t st = smem_u32(smem) + s * kMxStage;
+          if (elect_one()) {
+            stage_mmas<2>(d, st, st + kCodes, st + 2 * kCodes, st + 2 * kCodes + 1024, p.bn / 128,
+                          tbase + kScaleColumns + turn * kScaleTurn, 256, p.bn, kt == 0);
+            tc_commit_pair_multicast(&empty[s], 0x3);
+          }
+          __syncwarp();
+          if (++s == kMxStages) {
+            s = 0;
+            phase ^= 1;
+          }
+        }
+        if (ok && elect_one()) tc_commit_pair_multicast(&tfull[buf], 0x3);
+        __syncwarp();
+      }
+      if (elect_one()) {
+        tc_commit_pair_multicast(mma_done, 0x1);
+        drain_wait(mma_done, 0, flags);
+        if (!ok) settle_after_abort();
+      }
+    }
+    __syncwarp();
+  } else {
+    const int ew = warp - 2, quarter = warp & 3, group = ew >> 2;
+    uint8_t *stage = staging + ew * 2048, *bias = biases + ew * 64;
+    const Epilogue& e = p.e;
+    int n_tiles = 0;
+    bool live = true;
+    for (int t = pair; t < total && live; t += npairs, ++n_tiles) {
+      int tm, tn;
+      tile_of(t, p.tiles, tm, tn);
+      const int buf = n_tiles & 1, use = n_tiles >> 1;
+      const int row0 = tm * 256 + rank * 128 + quarter * 32;
+      const int cols = row0 < p.m ? min(p.bn, p.n - tn * p.bn) : 0;
+      const uint32_t tcol = tbase + (static_cast<uint32_t>(quarter * 32) << 16) + (buf ? second : 0);
+      // The half with the shared columns (the upper one of the first
+      // accumulator), then the other; what is left of this is nothing to take.
+      const int first = wide && !buf ? 128 : 0;
+      bool waited = false;
+#pragma unroll 1
+      for (int h = 0; h < p.bn; h += 128) {
+        const int c = (first ^ h) + group * 32;
+        const int col0 = tn * p.bn + c;
+        uint4 res[4];
+        if (c < cols) {
+          if (e.res)
+            read_rows(res, static_cast<const T*>(e.res), e.ldr, row0, col0, p.m, p.n, (e.vec & 2) != 0);
+          if (e.bias) {  // the chunk's 32 values, for every lane
+            const uint16_t b = col0 + lane < p.n ? static_cast<const uint16_t*>(e.bias)[col0 + lane] : 0;
+            __syncwarp();
+            reinterpret_cast<uint16_t*>(bias)[lane] = b;
+            __syncwarp();
+          }
+        }
+        if (!waited) {
+          live = warp_wait(&tfull[buf], use & 1, abort_word, flags);
+          if (!live) break;
+          tc_fence_after();
+          waited = true;
+        }
+        uint32_t u[32];
+        if (c < cols) {
+          tmem_ld32(tcol + c, u);
+          tmem_wait_ld();
+        }
+        if (h == 0) {  // (BN = 128: the whole tile)
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(&taken[buf], 0));
+        }
+        if (c < cols)
+          finish_rows<T>(
+              [&](bool, float(&z)[32]) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) z[i] = __uint_as_float(u[i]);
+              },
+              res, e, stage, reinterpret_cast<const uint4*>(bias), row0, col0, p.m, p.n);
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // the pair's MMAs, commits and remote signals are all done
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tbase, 512);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Few rows (tokens being decoded): the weights are all the traffic.
+//
+// As the kernel for few rows of linear.cu: the weights take the MMA's 128 rows,
+// the tokens its N = NT columns, a cluster of up to 16 CTAs shares the
+// reduction of 128 columns of D, and joins its fp32 sums in rank order.
+// ---------------------------------------------------------------------------
+template <int NT>
+struct MxFewCfg {
+  static constexpr int kStage = kCodes + NT * 128 + 2048;
+  static constexpr int kStages = 108 * 1024 / kStage;
+  static constexpr int kSmem = 1024 + kStages * kStage + 256;
+  static constexpr int kScales = NT < 32 ? 32 : NT;        // columns of TMEM: NT sums, then 16 of scales a stage,
+  static constexpr int kTmemCols = kScales < 64 ? 64 : 2 * NT;  // two stages in turn; a power of two
+  static_assert(kScales + 32 <= kTmemCols, "");
+  static_assert(NT * 512 <= kStages * kStage, "the partial sums take the ring's memory");
+  static_assert(kStage % 1024 == 0, "tiles on the swizzle's boundaries");
+};
+constexpr int kMxFewThreads = 192;
+
+struct MxFewProduct {
+  int m, n, kt, split;
+  Epilogue e;
+};
+
+template <typename T, int NT>
+__global__ void __launch_bounds__(kMxFewThreads, 2)
+    mx_few_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap mx,
+                  const __grid_constant__ CUtensorMap msw, const __grid_constant__ CUtensorMap msx,
+                  const __grid_constant__ MxFewProduct p, uint32_t* flags) {
+  using C = MxFewCfg<NT>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kStages * C::kStage);
+  uint64_t* empty = full + C::kStages;
+  uint64_t* tfull = empty + C::kStages;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(tfull + 1);
+  volatile int* abort_word = reinterpret_cast<volatile int*>(tmem_holder + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_rank());
+  const int block = blockIdx.x / p.split, j0 = block * 128, i0 = blockIdx.y * NT;
+  const int per = (p.kt + p.split - 1) / p.split;
+  const int kt0 = min(rank * per, p.kt), kt1 = min(kt0 + per, p.kt);
+
+  if (warp == 0 && lane == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(tfull, 1);
+    *abort_word = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&mw);
+    tma_prefetch_desc(&mx);
+    tma_prefetch_desc(&msw);
+    tma_prefetch_desc(&msx);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_holder, C::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = *tmem_holder;
+  chain_next();
+  chain_wait();
+
+  if (warp == 0) {
+    int s = 0;
+    uint32_t phase = 1;
+    bool ok = true;
+    for (int kt = kt0; kt < kt1; ++kt) {
+      if (!all_wait(&empty[s], phase, abort_word, flags)) {
+        ok = false;
+        break;
+      }
+      uint8_t* st = smem + s * C::kStage;
+      if (elect_one()) {
+        mbar_arrive_expect_tx_relaxed(&full[s], C::kStage);
+        tma_load_2d(st, &mw, &full[s], kt * 128, j0);
+        tma_load_2d(st + kCodes, &mx, &full[s], kt * 128, i0);
+        tma_load_2d(st + kCodes + NT * 128, &msw, &full[s], kt * 256, block);
+        tma_load_2d(st + kCodes + NT * 128 + 1024, &msx, &full[s], kt * 256, i0 / 128);
+      }
+      __syncwarp();
+      if (++s == C::kStages) {
+        s = 0;
+        phase ^= 1;
+      }
+    }
+    if (!ok) settle_after_abort();
+    __syncwarp();
+  } else if (warp == 1) {
+    int s = 0, turn = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int kt = kt0; kt < kt1; ++kt, turn ^= 1) {
+      if (!all_wait(&full[s], phase, abort_word, flags)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t st = smem_u32(smem) + s * C::kStage;
+      if (elect_one()) {
+        stage_mmas<1>(tbase, st, st + kCodes, st + kCodes + NT * 128, st + kCodes + NT * 128 + 1024, 1,
+                      tbase + C::kScales + turn * 16, 128, NT, kt == kt0);
+        tc_commit(&empty[s]);
+      }
+      __syncwarp();
+      if (++s == C::kStages) {
+        s = 0;
+        phase ^= 1;
+      }
+    }
+    if (elect_one()) {
+      tc_commit(tfull);  // also when giving up: the MMAs issued are waited for below
+      if (!ok) settle_after_abort();
+    }
+    __syncwarp();
+  } else {
+    const int quarter = warp & 3;
+    float* part = reinterpret_cast<float*>(smem);
+    if (kt0 == kt1) {
+      for (int i = 0; i < NT; ++i) part[i * 128 + quarter * 32 + lane] = 0.f;
+    } else if (warp_wait(tfull, 0, abort_word, flags)) {
+      tc_fence_after();
+#pragma unroll
+      for (int i = 0; i < NT; i += 16) {
+        uint32_t v[16];
+        tmem_ld16(tbase + (static_cast<uint32_t>(quarter * 32) << 16) + i, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int q = 0; q < 16; ++q) part[(i + q) * 128 + quarter * 32 + lane] = __uint_as_float(v[q]);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  join_few<T, 128>(smem, p.e, p.split, rank, j0, i0, min(NT, p.m - i0), p.n, kMxFewThreads);
+  cluster_sync();  // peers have read this CTA's sums
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tbase, C::kTmemCols);
+  }
+}
+
+// ------------------------------------------------------------------- host
+
+long long row_bytes(int k) { return (k + 31LL) / 32 * 16; }
+int k_tiles(int k) { return static_cast<int>((k + 255LL) / 256); }
+
+bool code_map(CUtensorMap* map, const void* codes, int rows, int k, int box) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(row_bytes(k)), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(row_bytes(k))};
+  const cuuint32_t shape[2] = {128, static_cast<cuuint32_t>(box)}, ones[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(codes), dims, strides, shape, ones,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// Tiles of scales, 256 words each (past the last one: zeros, which stand for
+// 2^-127 and meet codes of 0 only).
+bool scale_map(CUtensorMap* map, const void* scales, int rows, int k) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(k_tiles(k)) * 256, static_cast<cuuint64_t>((rows + 127) / 128)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(k_tiles(k)) * 1024};
+  const cuuint32_t shape[2] = {256, 1}, ones[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(scales), dims, strides, shape, ones,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T>
+cudaError_t quantize_t(const MxQuantCall& c, cudaStream_t stream) {
+  const long long tiles = static_cast<long long>((c.rows + 127) / 128) * k_tiles(c.k);
+  if (tiles > INT32_MAX) return cudaErrorInvalidConfiguration;
+  const int vec = rows_aligned(c.x, c.ldx * static_cast<long long>(sizeof(T)) / 2, c.rows);
+  return launch_chained(mx_quantize_kernel<T>, dim3(static_cast<unsigned>(tiles)), 256, 0, stream, 0,
+                        static_cast<const T*>(c.x), c.ldx, c.rows, c.k, c.codes, c.scales, k_tiles(c.k), vec);
+}
+
+template <typename T>
+cudaError_t dequantize_t(const MxDequantCall& c, cudaStream_t stream) {
+  const long long tiles = static_cast<long long>((c.rows + 127) / 128) * k_tiles(c.k);
+  if (tiles > INT32_MAX) return cudaErrorInvalidConfiguration;
+  const int vec = rows_aligned(c.y, c.ldy * static_cast<long long>(sizeof(T)) / 2, c.rows);
+  return launch_chained(mx_dequantize_kernel<T>, dim3(static_cast<unsigned>(tiles)), 256, 0, stream, 0, c.codes, c.scales,
+                        k_tiles(c.k), static_cast<T*>(c.y), c.ldy, c.rows, c.k, vec);
+}
+
+// CTA pairs that are resident at once (a persistent grid must not exceed
+// them); sets the kernel's shared-memory size on the way.
+template <typename T>
+cudaError_t resident_pairs(int* out) {
+  static int known[kMaxDev];
+  static std::mutex mu;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDev) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> lock(mu);
+  if (known[dev] == 0) {
+    auto kern = mx_pair_kernel<T>;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMxSmem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2, 1, 1);
+    cfg.blockDim = dim3(kMxThreads, 1, 1);
+    cfg.dynamicSmemBytes = kMxSmem;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 2;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
+    if (e != cudaSuccess) return e;
+    if (n < 1) return cudaErrorInvalidConfiguration;
+    known[dev] = n;
+  }
+  *out = known[dev];
+  return cudaSuccess;
+}
+
+template <typename T, int NT>
+cudaError_t launch_mx_few(const MxLinearCall& c, const Epilogue& e, cudaStream_t stream) {
+  CUtensorMap mw, mx, msw, msx;
+  if (!code_map(&mw, c.wcodes, c.n, c.k, 128) || !code_map(&mx, c.xcodes, c.m, c.k, NT) ||
+      !scale_map(&msw, c.wscales, c.n, c.k) || !scale_map(&msx, c.xscales, c.m, c.k))
+    return cudaErrorInvalidValue;
+  auto kern = mx_few_kernel<T, NT>;
+  static std::atomic<bool> ready[kMaxDev];
+  int dev = 0;
+  cudaError_t s = cudaGetDevice(&dev);
+  if (s != cudaSuccess) return s;
+  if (dev < 0 || dev >= kMaxDev) return cudaErrorInvalidDevice;
+  if (!ready[dev]) {
+    s = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, MxFewCfg<NT>::kSmem);
+    if (s == cudaSuccess) s = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (s != cudaSuccess) return s;
+    ready[dev] = true;
+  }
+  const int across = (c.n + 127) / 128, down = (c.m + NT - 1) / NT;
+  MxFewProduct p = {c.m, c.n, k_tiles(c.k), 1, e};
+  // Two CTAs on each SM, and at least two stages of the reduction for each.
+  while (p.split < (NT > 32 ? 8 : 16) && 2LL * p.split * across * down <= 304 && p.kt >= 4 * p.split) p.split *= 2;
+  return launch_chained(kern, dim3(across * p.split, down, 1), kMxFewThreads, MxFewCfg<NT>::kSmem, stream, p.split, mw,
+                        mx, msw, msx, p, c.flags);
+}
+
+template <typename T>
+cudaError_t mx_linear_t(const MxLinearCall& c, cudaStream_t stream) {
+  Epilogue e = {c.bias, c.res, c.ldr, nullptr, 0, c.y, c.ldy, c.act, 0};
+  e.vec = (e.bias && rows_aligned(e.bias, 0, 1) ? 1 : 0) | (e.res && rows_aligned(e.res, e.ldr, c.m) ? 2 : 0) |
+          (rows_aligned(e.out, e.ldo, c.m) ? 8 : 0);
+  const long long squares = static_cast<long long>((c.m + 127) / 128) * ((c.n + 127) / 128);
+  if (c.m <= 16) return launch_mx_few<T, 16>(c, e, stream);
+  if (c.m <= 32) return launch_mx_few<T, 32>(c, e, stream);
+  if (c.m <= 64) return launch_mx_few<T, 64>(c, e, stream);
+  if (c.m <= 128 || squares <= 76) return launch_mx_few<T, 128>(c, e, stream);
+  int pairs = 0;
+  const cudaError_t s = resident_pairs<T>(&pairs);
+  if (s != cudaSuccess) return s;
+  MxProduct p = {c.m, c.n, k_tiles(c.k), 256, {}, e};
+  auto tiles = [&](int bn) { return static_cast<long long>((c.m + 255) / 256) * ((c.n + bn - 1) / bn); };
+  if (tiles(128) <= pairs) p.bn = 128;
+  p.tiles = raster((c.m + 255) / 256, (c.n + p.bn - 1) / p.bn);
+  CUtensorMap ma, mb, msa, msb;
+  if (!code_map(&ma, c.xcodes, c.m, c.k, 128) || !code_map(&mb, c.wcodes, c.n, c.k, p.bn / 2) ||
+      !scale_map(&msa, c.xscales, c.m, c.k) || !scale_map(&msb, c.wscales, c.n, c.k))
+    return cudaErrorInvalidValue;
+  return launch_chained(mx_pair_kernel<T>, dim3(2 * static_cast<unsigned>(std::min<long long>(tiles(p.bn), pairs))),
+                        kMxThreads, kMxSmem, stream, 2, ma, mb, msa, msb, p, c.flags);
+}
+
+}  // namespace
+
+size_t mx_code_bytes(int rows, int k) { return static_cast<size_t>(rows) * row_bytes(k); }
+size_t mx_scale_bytes(int rows, int k) { return static_cast<size_t>((rows + 127) / 128) * k_tiles(k) * 1024; }
+
+cudaError_t launch_mx_quantize(const MxQuantCall& c, cudaStream_t stream) {
+  return c.type == kF32   ? quantize_t<float>(c, stream)
+         : c.type == kF16 ? quantize_t<__half>(c, stream)
+                          : quantize_t<__nv_bfloat16>(c, stream);
+}
+
+cudaError_t launch_mx_dequantize(const MxDequantCall& c, cudaStream_t stream) {
+  return c.type == kF32   ? dequantize_t<float>(c, stream)
+         : c.type == kF16 ? dequantize_t<__half>(c, stream)
+                          : dequantize_t<__nv_bfloat16>(c, stream);
+}
+
+cudaError_t launch_mx_linear(const MxLinearCall& c, cudaStream_t stream) {
+  return c.type == kF16 ? mx_linear_t<__half>(c, stream) : mx_linear_t<__nv_bfloat16>(c, stream);
+}
+
+}  // namespace ozemu

@@ -1,0 +1,411 @@
+// What the products on the tensor cores share (linear.cu, mx.cu): waits of
+// whole warps, the way of accumulators through the epilogue into rows of any
+// alignment, the order of tiles, and the host's helpers.
+#pragma once
+
+#include <cstdint>
+#include <cuda.h>
+
+#include "layer.cuh"
+
+namespace ozemu {
+
+namespace {
+
+constexpr int kEpiWarps = 16;
+
+// What happens to an accumulator on its way out.
+struct Epilogue {
+  const void* bias;
+  const void* res;
+  long long ldr;
+  void* pre;
+  long long ldpre;
+  void* out;
+  long long ldo;
+  int act;
+  int vec;  // bits: 1 bias, 2 res, 4 pre, 8 out rows start on 16-byte boundaries; gated, 16 and 32: bias's, pre's second half
+};
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_word,
+                                          uint32_t* flags) {
+  int ok = 0;
+  if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, abort_word, flags) ? 1 : 0;
+  return __shfl_sync(0xFFFFFFFFu, ok, 0) != 0;
+}
+
+// The loops that issue loads and MMAs are run by a whole warp, so that their
+// addresses and descriptors stay in uniform registers, which these
+// instructions take; one elected lane, always the same, issues.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(one));
+  return one != 0;
+}
+__device__ __forceinline__ bool all_wait(uint64_t* bar, uint32_t parity, volatile int* abort_word, uint32_t* flags) {
+  const bool ok = mbar_wait(bar, parity, abort_word, flags);
+  return __all_sync(0xFFFFFFFFu, ok);
+}
+
+// Bounded wait that ignores the abort word (used while draining).
+__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, uint32_t* flags) {
+  const uint64_t t0 = globaltimer();
+  while (!mbar_try_wait(bar, parity)) {
+    if (globaltimer() - t0 > kWaitLimitNs) {
+      atomicOr(flags, kFlagTimeout);
+      return;
+    }
+  }
+}
+
+// After an abort, gives copies already issued time to land.
+__device__ __forceinline__ void settle_after_abort() {
+  const uint64_t t0 = globaltimer();
+  while (globaltimer() - t0 < 50000ull) {
+  }
+}
+
+// Four elements, by plain loads (the memory may be the output's).
+template <typename T>
+__device__ __forceinline__ void load4(const T* p, int left, bool vec, float (&v)[4]) {
+  if (vec && left >= 4) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    const float2 a = Pair<T>::unpack(u.x), b = Pair<T>::unpack(u.y);
+    v[0] = a.x;
+    v[1] = a.y;
+    v[2] = b.x;
+    v[3] = b.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = i < left ? to_float(p[i]) : 0.f;
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store4(T* p, const float (&v)[4], int left, bool vec) {
+  if (vec && left >= 4) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(Pair<T>::pack(v[0], v[1]), Pair<T>::pack(v[2], v[3]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < left) p[i] = from_float<T>(v[i]);
+  }
+}
+
+template <int kAct, int N>
+__device__ __forceinline__ void activate_each(float (&z)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) z[i] = activate(z[i], kAct);
+}
+template <int N>
+__device__ __forceinline__ void activate_all(float (&z)[N], int act) {
+  switch (act) {
+    case kActRelu: activate_each<kActRelu>(z); break;
+    case kActGelu: activate_each<kActGelu>(z); break;
+    case kActGeluTanh: activate_each<kActGeluTanh>(z); break;
+    case kActSilu: activate_each<kActSilu>(z); break;
+    default: break;
+  }
+}
+
+// A warp's 32 rows x 32 columns of 16-bit elements pass through its 2 KB of
+// shared memory (row r at byte 64 r, its 16-byte piece c at piece
+// c ^ (r / 2 % 4): no bank conflicts by rows or by pieces), so that a row moves
+// as one 64-byte run.  A lane's share on the way: piece lane % 4 of rows
+// 8 i + lane / 4; or, where rows do not start on 16-byte boundaries, word
+// lane % 16 of rows 2 i + lane / 16, between words where the row starts on an
+// odd element.
+__device__ __forceinline__ uint4* stage_piece(uint8_t* stage, int r, int c) {
+  return reinterpret_cast<uint4*>(stage + r * 64) + (c ^ (r >> 1 & 3));
+}
+__device__ __forceinline__ uint32_t* stage_word(uint8_t* stage, int r, int w) {
+  return reinterpret_cast<uint32_t*>(stage_piece(stage, r, w >> 2)) + (w & 3);
+}
+
+template <typename T>
+__device__ __forceinline__ void read_rows(uint4 (&v)[4], const T* in, long long ld, int row0, int col0, int m, int n,
+                                          bool vec) {
+  const int lane = threadIdx.x & 31;
+  if (vec && col0 + 32 <= n) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = row0 + 8 * i + (lane >> 2);
+      v[i] = r < m ? *reinterpret_cast<const uint4*>(in + r * ld + col0 + 8 * (lane & 3)) : make_uint4(0, 0, 0, 0);
+    }
+    return;
+  }
+  uint32_t* w = reinterpret_cast<uint32_t*>(v);
+  const uint16_t* p = reinterpret_cast<const uint16_t*>(in) + row0 * ld + col0;
+  const int word = lane & 15;
+  if (col0 > 0 && col0 + 32 <= n) {  // the element before the run is the row's, too
+    // All loads first: the words, and for row `lane` the last element, which a
+    // row that starts on an odd element has in a 17th word.
+    const uint32_t last = row0 + lane < m ? p[lane * ld + 31] : 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int r = 2 * i + (lane >> 4);
+      const uintptr_t q = reinterpret_cast<uintptr_t>(p + r * ld) & ~uintptr_t(3);
+      w[i] = row0 + r < m ? *(reinterpret_cast<const uint32_t*>(q) + word) : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int r = 2 * i + (lane >> 4);
+      const uint32_t next = __shfl_down_sync(0xFFFFFFFFu, w[i], 1), tail = __shfl_sync(0xFFFFFFFFu, last, r);
+      if (reinterpret_cast<uintptr_t>(p + r * ld) & 2u) w[i] = __funnelshift_r(w[i], word == 15 ? tail : next, 16);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int r = 2 * i + (lane >> 4);
+      const uint16_t* q = p + r * ld + 2 * word;
+      const uint32_t a = row0 + r < m && col0 + 2 * word < n ? q[0] : 0;
+      const uint32_t b = row0 + r < m && col0 + 2 * word + 1 < n ? q[1] : 0;
+      w[i] = a | (b << 16);
+    }
+  }
+}
+
+__device__ __forceinline__ void stage_rows(const uint4 (&v)[4], uint8_t* stage, int col0, int n, bool vec) {
+  const int lane = threadIdx.x & 31;
+  if (vec && col0 + 32 <= n) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) *stage_piece(stage, 8 * i + (lane >> 2), lane & 3) = v[i];
+  } else {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(v);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) *stage_word(stage, 2 * i + (lane >> 4), lane & 15) = w[i];
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void write_rows(uint8_t* stage, T* out, long long ldo, int row0, int col0, int m, int n,
+                                           bool vec) {
+  const int lane = threadIdx.x & 31;
+  if (vec && col0 + 32 <= n) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 8 * i + (lane >> 2);
+      if (row0 + r < m)
+        *reinterpret_cast<uint4*>(out + (row0 + r) * ldo + col0 + 8 * (lane & 3)) = *stage_piece(stage, r, lane & 3);
+    }
+    return;
+  }
+  uint16_t* p = reinterpret_cast<uint16_t*>(out) + row0 * ldo + col0;
+  const bool whole = col0 + 32 <= n;
+  const int word = lane & 15;
+#pragma unroll 1
+  for (int i0 = 0; i0 < 16; i0 += 4) {
+    uint32_t a[4], b[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a[i] = *stage_word(stage, 2 * (i0 + i) + (lane >> 4), word);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) b[i] = __shfl_down_sync(0xFFFFFFFFu, a[i], 1);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 2 * (i0 + i) + (lane >> 4);
+      uint16_t* q = p + r * ldo;
+      const bool odd = (reinterpret_cast<uintptr_t>(q) & 2u) != 0, in_m = row0 + r < m;
+      if (whole) {  // from an odd start: words of elements 2 word + 1 and 2 word + 2, and the two ends
+        const uint32_t both = odd ? __funnelshift_r(a[i], b[i], 16) : a[i];
+        if (in_m && !(odd && word == 15)) *reinterpret_cast<uint32_t*>(q + 2 * word + (odd ? 1 : 0)) = both;
+        if (in_m && odd && word == 15) q[31] = static_cast<uint16_t>(a[i] >> 16);
+        if (in_m && odd && word == 0) q[0] = static_cast<uint16_t>(a[i]);
+      } else {
+        if (in_m && col0 + 2 * word < n) q[2 * word] = static_cast<uint16_t>(a[i]);
+        if (in_m && col0 + 2 * word + 1 < n) q[2 * word + 1] = static_cast<uint16_t>(a[i] >> 16);
+      }
+    }
+  }
+}
+
+constexpr int kGroupM = 8;  // tile rows swept together, for reuse of B's columns in L2
+
+// A grid of tiles and the reciprocal that gives a tile's turn.
+struct Raster {
+  int m, n;
+  uint32_t group_inverse, group_shift;  // of kGroupM n
+  __host__ __device__ int count() const { return m * n; }
+};
+inline Raster raster(int m, int n) {
+  // ceil(2^(32 + shift) / d) with 2^shift >= d gives t / d for t < 2^31; with
+  // the shift one less the multiplier fits 32 bits, for t < 2^31 still.
+  Raster r = {m, n, 0, 0};
+  const uint64_t d = static_cast<uint64_t>(kGroupM) * n;
+  while ((2ull << r.group_shift) < d) ++r.group_shift;
+  r.group_inverse = static_cast<uint32_t>(((1ull << (32 + r.group_shift)) + d - 1) / d);
+  return r;
+}
+
+__device__ __forceinline__ void tile_of(int t, const Raster& p, int& tm, int& tn) {
+  // t / (kGroupM n) by the reciprocal that the host rounded up: exact
+  // for the product's tiles.
+  const int turn = static_cast<int>(__umulhi(static_cast<uint32_t>(t), p.group_inverse) >> p.group_shift);
+  const int first = turn * kGroupM, rest = t - turn * kGroupM * p.n;
+  const int gm = min(kGroupM, p.m - first);
+  if (gm == kGroupM) {
+    tn = rest / kGroupM;
+    tm = first + rest % kGroupM;
+  } else {
+    tn = rest / gm;
+    tm = first + rest % gm;
+  }
+}
+
+// 16 bytes of shared memory of a CTA of the cluster.
+__device__ __forceinline__ float4 load_cluster16(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr));
+  return v;
+}
+
+// One warp's 32 rows x 32 columns of accumulators, a row a lane, from
+// source(last, z) through the epilogue; the source is asked for the last time
+// with last = true.
+template <typename T, typename F>
+__device__ __forceinline__ void finish_rows(F source, const uint4 (&res)[4], const Epilogue& e, uint8_t* stage,
+                                            const uint4* bias, int row0, int col0, int m, int n) {
+  const int lane = threadIdx.x & 31;
+  float z[32];
+  auto take = [&](bool last) {
+    source(last, z);
+    if (e.bias) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float b[8];
+        unpack16<T>(bias[q], b);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z[8 * q + i] += b[i];
+      }
+    }
+  };
+  if (e.pre) {
+    take(false);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) *stage_piece(stage, lane, c) = pack16<T>(z + 8 * c);
+    __syncwarp();
+    write_rows(stage, static_cast<T*>(e.pre), e.ldpre, row0, col0, m, n, (e.vec & 4) != 0);
+    __syncwarp();
+  }
+  if (e.res) {
+    stage_rows(res, stage, col0, n, (e.vec & 2) != 0);
+    __syncwarp();
+  }
+  take(true);
+  activate_all(z, e.act);
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    uint4* at = stage_piece(stage, lane, c);
+    if (e.res) {
+      float r[8];
+      unpack16<T>(*at, r);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) z[8 * c + i] += r[i];
+    }
+    *at = pack16<T>(z + 8 * c);
+  }
+  __syncwarp();
+  write_rows(stage, static_cast<T*>(e.out), e.ldo, row0, col0, m, n, (e.vec & 8) != 0);
+  __syncwarp();
+}
+
+// The join of a kernel for few rows: a cluster's CTAs hold the fp32 sums of 128
+// rows of the wide operand and each token, [token][128], in shared memory; this
+// CTA takes its share of the columns, kCols / split of them, every token, four
+// columns of a token at a time.  kCols = 64: a gated layer's, the gate in the
+// first 64 sums and up in the others.
+template <typename T, int kCols>
+__device__ __forceinline__ void join_few(const uint8_t* smem, const Epilogue& e, int split, int rank, int j0, int i0,
+                                         int rows, int n, int threads) {
+  const int width = kCols / 4 / split;
+  for (int at = threadIdx.x; at < rows * width; at += threads) {
+    const int i = at / width, jj = (rank * width + at % width) * 4, j = j0 + jj, left = n - j;
+    if (left <= 0) continue;
+    const float* mine = reinterpret_cast<const float*>(smem) + i * 128 + jj;
+    auto joined = [&](const float* at, float(&z)[4]) {
+      for (int s0 = 0; s0 < split; s0 += 8) {
+        float4 u[8];  // all loads before the first sum
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+          if (s0 + s < split) u[s] = load_cluster16(mapa_shared(at, s0 + s));
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+          if (s0 + s < split) {
+            z[0] += u[s].x;
+            z[1] += u[s].y;
+            z[2] += u[s].z;
+            z[3] += u[s].w;
+          }
+      }
+    };
+    float z[4] = {};
+    joined(mine, z);
+    const long long row = i0 + i;
+    float v[4];
+    if constexpr (kCols == 64) {
+      float u[4] = {};
+      joined(mine + 64, u);
+      if (e.bias) {
+        load4(static_cast<const T*>(e.bias) + j, left, e.vec & 1, v);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) z[q] += v[q];
+        load4(static_cast<const T*>(e.bias) + n + j, left, (e.vec & 16) != 0, v);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) u[q] += v[q];
+      }
+      if (e.pre) {
+        store4(static_cast<T*>(e.pre) + row * e.ldpre + j, z, left, (e.vec & 4) != 0);
+        store4(static_cast<T*>(e.pre) + row * e.ldpre + n + j, u, left, (e.vec & 32) != 0);
+      }
+      activate_all(z, e.act);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) z[q] *= u[q];
+      store4(static_cast<T*>(e.out) + row * e.ldo + j, z, left, (e.vec & 8) != 0);
+      continue;
+    }
+    if (e.bias) {
+      load4(static_cast<const T*>(e.bias) + j, left, e.vec & 1, v);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) z[q] += v[q];
+    }
+    if (e.pre) store4(static_cast<T*>(e.pre) + row * e.ldpre + j, z, left, (e.vec & 4) != 0);
+    activate_all(z, e.act);
+    if (e.res) {
+      load4(static_cast<const T*>(e.res) + row * e.ldr + j, left, (e.vec & 2) != 0, v);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) z[q] += v[q];
+    }
+    store4(static_cast<T*>(e.out) + row * e.ldo + j, z, left, (e.vec & 8) != 0);
+  }
+}
+
+// ------------------------------------------------------------------- host
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static const EncodeTiledFn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) !=
+            cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeTiledFn>(p);
+  }();
+  return fn;
+}
+
+int pad8(int x) { return (x + 7) & ~7; }
+
+bool rows_aligned(const void* p, long long ld, int rows) {
+  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (rows <= 1 || (ld & 7) == 0);
+}
+
+constexpr int kMaxDev = 64;
+
+}  // namespace
+
+}  // namespace ozemu
