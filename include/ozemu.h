@@ -623,16 +623,16 @@ int ozemu_mx_linear(int m, int n, int k, int type, const uint8_t* x_codes, const
  * grads, sizes, types and outs are HOST arrays of `count` entries, read before
  * the call returns: device pointers, numbers of elements (dense; up to 2^40)
  * and ozemu_types, which may differ.  outs[i] may be grads[i] itself, and
- * overlaps nothing else.  max_norm and eps >= 0, not both 0.  Squares are formed
- * in fp32: a norm with an element beyond 1.8e19 is infinite, elements below 1e-23
- * do not count.  A NaN or an infinity goes through as the formula takes it.
- * Any device workspace of the bytes below, 256-byte aligned. */
+ * overlaps nothing else.  max_norm and eps >= 0, not both 0.  Squares and sums
+ * of 2048 of them are fp32: gradients beyond 4e17 may give an infinite norm,
+ * elements below 1e-23 do not count.  A NaN or an infinity goes through as the formula takes it. */
 int ozemu_clip_grad_norm(int count, const void* const* grads, const long long* sizes, const int* types,
                          void* const* outs, float max_norm, float eps, float* norm, void* workspace,
                          size_t workspace_bytes, cudaStream_t stream);
 
-/* Workspace bytes of that call; 0 for a negative count.  host. */
-size_t ozemu_clip_grad_norm_bytes(int count);
+/* Workspace bytes of that call (of the pointers only the alignment is looked
+ * at); 0 on bad arguments.  host. */
+size_t ozemu_clip_grad_norm_bytes(int count, const void* const* grads, const long long* sizes, const int* types);
 
 /* Y = (X - mean) rstd weight + bias for each row of X (rows x cols, ldx):
  * mean = sum(X)/cols, rstd = (sum (X - mean)^2 / cols + eps)^(-1/2).  weight

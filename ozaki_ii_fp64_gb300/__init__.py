@@ -131,7 +131,7 @@ _SIGNATURES = {
     "ozemu_mx_dequantize": (_I, [_I, _I, _I, _P, _P, _P, _I, _P]),
     "ozemu_mx_linear": (_I, [_I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _I, _I, _P, _I, _P]),
     "ozemu_clip_grad_norm": (_I, [_I, _P, _P, _P, _P, _F, _F, _P, _P, _S, _P]),
-    "ozemu_clip_grad_norm_bytes": (_S, [_I]),
+    "ozemu_clip_grad_norm_bytes": (_S, [_I, _P, _P, _P]),
 }
 
 
@@ -480,8 +480,8 @@ def ozemu_clip_grad_norm(count, grads, sizes, types, outs, max_norm, eps, norm, 
                  workspace_bytes, stream)
 
 
-def ozemu_clip_grad_norm_bytes(count):
-    return _call("ozemu_clip_grad_norm_bytes", count)
+def ozemu_clip_grad_norm_bytes(count, grads, sizes, types):
+    return _call("ozemu_clip_grad_norm_bytes", count, grads, sizes, types)
 
 
 # ------------------------------------------------------- torch marshalling
@@ -926,17 +926,33 @@ def gated_linear_backward(dh, x, w, pre, activation="silu", x_grad=True, w_grad=
 
 class MXMatrix:
     """A rows x cols matrix of 4-bit floats (e2m1) with a power of two for each 32 columns of a row, as mx_quantize makes
-    it: `codes` (uint8, rows x bytes of a row) and `scales` (uint8, tiles of 128 rows x 256 columns), in the layout that
-    the C header gives."""
+    it.  `codes` (uint8, rows x bytes of a row) and `scales` (uint8, tiles of 128 rows x 256 columns x 1024), in the
+    layout that the C header gives, are views of `data`, one uint8 vector; MXMatrix.empty makes one to fill in."""
 
-    __slots__ = ("codes", "scales", "rows", "cols")
+    __slots__ = ("data", "rows", "cols")
 
-    def __init__(self, codes, scales, rows, cols):
-        self.codes, self.scales, self.rows, self.cols = codes, scales, rows, cols
+    def __init__(self, data, rows, cols):
+        self.data, self.rows, self.cols = data, rows, cols
+
+    @staticmethod
+    def empty(rows, cols, device="cuda"):
+        at = (ozemu_mx_code_bytes(rows, cols) + 255) // 256 * 256
+        return MXMatrix(_torch().empty(at + ozemu_mx_scale_bytes(rows, cols), dtype=_torch().uint8, device=device), rows,
+                        cols)
 
     @property
     def shape(self):
         return (self.rows, self.cols)
+
+    @property
+    def codes(self):
+        row = (self.cols + 31) // 32 * 16
+        return self.data[:self.rows * row].view(self.rows, row)
+
+    @property
+    def scales(self):
+        at = (ozemu_mx_code_bytes(self.rows, self.cols) + 255) // 256 * 256
+        return self.data[at:].view((self.rows + 127) // 128, (self.cols + 255) // 256, 1024)
 
     def __repr__(self):
         return "MXMatrix(%d x %d)" % (self.rows, self.cols)
@@ -948,12 +964,17 @@ def _mx(q, name):
     return q
 
 
-def _float_type(dtype, names):
-    torch = _torch()
-    code = {torch.bfloat16: OZEMU_BF16, torch.float16: OZEMU_F16, torch.float32: OZEMU_F32}.get(dtype)
-    if code is None or code not in names:
-        raise ValueError("dtype: expected one of %s" % ", ".join(
-            n for c, n in ((OZEMU_BF16, "bfloat16"), (OZEMU_F16, "float16"), (OZEMU_F32, "float32")) if c in names))
+_float_types = {}
+
+
+def _float_type(dtype, codes):
+    code = _float_types.get(dtype)
+    if code is None and not _float_types:
+        torch = _torch()
+        _float_types.update({torch.bfloat16: OZEMU_BF16, torch.float16: OZEMU_F16, torch.float32: OZEMU_F32})
+        code = _float_types.get(dtype)
+    if code not in codes:
+        raise ValueError("dtype: expected one of %s" % ", ".join(str(t) for t, c in _float_types.items() if c in codes))
     return code
 
 
@@ -965,11 +986,10 @@ def mx_quantize(x, out=None, stream=None):
     out: an MXMatrix of x's size whose memory takes the result; it overlaps x in nothing (ValueError)."""
     native = _native or _layer_calls()
     if out is None:
-        codes, scales = native.mx_quantize(x, None, None, stream)
-        return MXMatrix(codes, scales, x.shape[0], x.shape[1])
+        return MXMatrix(native.mx_quantize(x, None, stream), *x.shape)
     if _mx(out, "out").shape != tuple(x.shape):
         raise ValueError("out: expected an MXMatrix of x's size")
-    native.mx_quantize(x, out.codes, out.scales, stream)
+    native.mx_quantize(x, out.data, stream)
     return out
 
 
@@ -980,7 +1000,7 @@ def mx_dequantize(q, dtype=None, out=None, stream=None):
     if dtype is None:
         dtype = _torch().bfloat16 if out is None else out.dtype
     return (_native or _layer_calls()).mx_dequantize(
-        q.codes, q.scales, q.rows, q.cols, _float_type(dtype, (OZEMU_BF16, OZEMU_F16, OZEMU_F32)), out, stream)
+        q.data, q.rows, q.cols, _float_type(dtype, (OZEMU_BF16, OZEMU_F16, OZEMU_F32)), out, stream)
 
 
 def mx_linear(x, w, bias=None, residual=None, activation="none", dtype=None, out=None, stream=None):
@@ -997,7 +1017,7 @@ def mx_linear(x, w, bias=None, residual=None, activation="none", dtype=None, out
         like = next((t for t in (out, residual, bias) if t is not None), None)
         dtype = _torch().bfloat16 if like is None else like.dtype
     return (_native or _layer_calls()).mx_linear(
-        x.codes, x.scales, x.rows, w.codes, w.scales, w.rows, x.cols, bias, residual, _activation(activation),
+        x.data, x.rows, w.data, w.rows, x.cols, bias, residual, _activation(activation),
         _float_type(dtype, (OZEMU_BF16, OZEMU_F16)), out, stream)
 
 

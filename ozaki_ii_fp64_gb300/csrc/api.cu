@@ -1688,24 +1688,32 @@ int ozemu_mx_linear(int m, int n, int k, int type, const uint8_t* x_codes, const
 
 // Elements of one gradient, at most 2^40.
 constexpr long long kMaxGradient = 1LL << 40;
-size_t ozemu_clip_grad_norm_bytes(int count) { return count < 0 ? 0 : clip_workspace(count); }
+static bool gradients_ok(int count, const void* const* grads, const long long* sizes, const int* types) {
+  if (count < 0 || (count > 0 && (!grads || !sizes || !types))) return false;
+  for (int i = 0; i < count; ++i)
+    if (sizes[i] < 0 || sizes[i] > kMaxGradient || !float_type(types[i]) ||
+        (sizes[i] > 0 && (!grads[i] || !type_aligned(grads[i], types[i]))))
+      return false;
+  return true;
+}
+
+size_t ozemu_clip_grad_norm_bytes(int count, const void* const* grads, const long long* sizes, const int* types) {
+  if (!gradients_ok(count, grads, sizes, types)) return 0;
+  return clip_workspace({count, grads, sizes, types, nullptr, 0.f, 0.f, nullptr, nullptr});
+}
 
 int ozemu_clip_grad_norm(int count, const void* const* grads, const long long* sizes, const int* types,
                          void* const* outs, float max_norm, float eps, float* norm, void* workspace,
                          size_t workspace_bytes, cudaStream_t stream) {
-  if (count < 0 || (count > 0 && (!grads || !sizes || !types || !outs)) || !(max_norm >= 0.f) || !(eps >= 0.f) ||
+  if (!gradients_ok(count, grads, sizes, types) || (count > 0 && !outs) || !(max_norm >= 0.f) || !(eps >= 0.f) ||
       !(max_norm > 0.f || eps > 0.f) || !vector_ok(norm, OZEMU_F32))
     return OZEMU_ERR_INVALID_ARG;
-  for (int i = 0; i < count; ++i) {
-    if (sizes[i] < 0 || sizes[i] > kMaxGradient || !float_type(types[i])) return OZEMU_ERR_INVALID_ARG;
-    if (sizes[i] > 0 &&
-        (!grads[i] || !outs[i] || !type_aligned(grads[i], types[i]) || !type_aligned(outs[i], types[i])))
-      return OZEMU_ERR_INVALID_ARG;
-  }
-  const int s = scratch_ok(workspace, workspace_bytes, clip_workspace(count));
+  for (int i = 0; i < count; ++i)
+    if (sizes[i] > 0 && (!outs[i] || !type_aligned(outs[i], types[i]))) return OZEMU_ERR_INVALID_ARG;
+  const ClipCall c = {count, grads, sizes, types, outs, max_norm, eps, norm, workspace};
+  const int s = scratch_ok(workspace, workspace_bytes, clip_workspace(c));
   if (s != OZEMU_OK) return s;
-  return cuda_status(
-      launch_clip_grad_norm({count, grads, sizes, types, outs, max_norm, eps, norm, workspace}, stream));
+  return cuda_status(launch_clip_grad_norm(c, stream));
 }
 
 static bool norm_types(int type, int param_type) {

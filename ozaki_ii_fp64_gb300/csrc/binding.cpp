@@ -517,15 +517,27 @@ PyObject* gated_linear_backward(PyObject*, PyObject* const* a, Py_ssize_t count)
   });
 }
 
-// One of the two arrays of a microscaled matrix.
-uint8_t* mx_array(const at::Tensor& t, size_t bytes, const at::Tensor& like, const char* name) {
-  if (t.scalar_type() != at::kByte || t.device() != like.device() || !t.is_contiguous() ||
-      static_cast<size_t>(t.numel()) != bytes)
-    throw Refused(std::string(name) + ": expected " + std::to_string(bytes) + " contiguous bytes on " +
-                  like.device().str());
-  if ((reinterpret_cast<uintptr_t>(t.data_ptr()) & 15u) != 0) throw Refused(std::string(name) + ": not on a 16-byte boundary");
-  return static_cast<uint8_t*>(t.data_ptr());
-}
+// A microscaled matrix in one array: the codes, then the scales from the next
+// 256-byte boundary on.
+struct MxData {
+  MxData(int rows, int k) : rows(rows), k(k), codes(ozemu_mx_code_bytes(rows, k)) {
+    at = (codes + 255) & ~static_cast<size_t>(255);
+    bytes = static_cast<int64_t>(at + ozemu_mx_scale_bytes(rows, k));
+  }
+  void in(const at::Tensor& t, const at::Tensor& like, const char* name) {
+    if (t.scalar_type() != at::kByte || t.device() != like.device() || t.dim() != 1 || t.size(0) != bytes ||
+        (bytes > 1 && t.stride(0) != 1))
+      throw Refused(std::string(name) + ": expected a dense vector of " + std::to_string(bytes) + " Byte on " +
+                    like.device().str());
+    p = static_cast<uint8_t*>(t.data_ptr());
+    if ((reinterpret_cast<uintptr_t>(p) & 15u) != 0) throw Refused(std::string(name) + ": not on a 16-byte boundary");
+  }
+  uint8_t* scales() const { return p + at; }
+  int rows, k;
+  size_t codes, at;
+  int64_t bytes;
+  uint8_t* p = nullptr;
+};
 
 int integer(PyObject* o) {
   const long long n = PyLong_AsLongLong(o);
@@ -538,90 +550,82 @@ at::ScalarType scalar_type(int code) {
   return code == OZEMU_F32 ? at::kFloat : code == OZEMU_F16 ? at::kHalf : at::kBFloat16;
 }
 
-// mx_quantize(x, codes, scales, stream): (codes, scales), fresh ones for None
+// mx_quantize(x, out, stream): the matrix's array, a fresh one for None
 PyObject* mx_quantize(PyObject*, PyObject* const* a, Py_ssize_t count) {
-  return guarded(count, 4, [&]() -> PyObject* {
+  return guarded(count, 3, [&]() -> PyObject* {
     const at::Tensor& x = tensor(a[0], "x");
-    const at::Tensor *codes = tensor_or_none(a[1], "codes"), *scales = tensor_or_none(a[2], "scales");
+    const at::Tensor* given = tensor_or_none(a[1], "out");
     int rows, k;
     sizes(x, "x", &rows, &k);
     if (type_code(x.scalar_type()) < 0)
       throw Refused(std::string("expected bfloat16, float16 or float32, got ") + c10::toString(x.scalar_type()));
     const Matrix mx = matrix(&x, rows, k, x, "x");
-    const size_t cb = ozemu_mx_code_bytes(rows, k), sb = ozemu_mx_scale_bytes(rows, k);
-    uint8_t *pc = codes ? mx_array(*codes, cb, x, "codes") : nullptr, *ps = scales ? mx_array(*scales, sb, x, "scales") : nullptr;
-    const long long size = x.element_size();
-    const Area in = {reinterpret_cast<intptr_t>(mx.p), mx.ld * size, mx.p ? rows : 0, k * size};
-    const Area ac = {reinterpret_cast<intptr_t>(pc), static_cast<long long>(cb), pc ? 1 : 0, static_cast<long long>(cb)};
-    const Area as = {reinterpret_cast<intptr_t>(ps), static_cast<long long>(sb), ps ? 1 : 0, static_cast<long long>(sb)};
-    if (share(ac, in) || share(as, in)) throw Refused("out: overlaps x");
-    if (share(ac, as)) throw Refused("out: codes and scales overlap");
-    OnStream on(x, a[3], {&x, codes, scales});
+    MxData q(rows, k);
+    if (given) {
+      q.in(*given, x, "out");
+      const long long size = x.element_size();
+      if (share({reinterpret_cast<intptr_t>(q.p), q.bytes, q.bytes > 0 ? 1 : 0, q.bytes},
+                {reinterpret_cast<intptr_t>(mx.p), mx.ld * size, mx.p ? rows : 0, k * size}))
+        throw Refused("out: overlaps x");
+    }
+    OnStream on(x, a[2], {&x, given});
     no_graph("mx_quantize", "torch.no_grad() says that none are wanted", {&x});
-    at::Tensor fresh_codes, fresh_scales;
-    if (!codes) {
-      fresh_codes = at::empty({rows, static_cast<int64_t>(rows > 0 ? cb / rows : 0)}, x.options().dtype(at::kByte));
-      pc = mx_array(fresh_codes, cb, x, "codes");
+    at::Tensor fresh;
+    if (!given) {
+      fresh = at::empty({q.bytes}, x.options().dtype(at::kByte));
+      q.in(fresh, x, "out");
     }
-    if (!scales) {
-      fresh_scales = at::empty({(rows + 127) / 128, (k + 255LL) / 256, 1024}, x.options().dtype(at::kByte));
-      ps = mx_array(fresh_scales, sb, x, "scales");
-    }
-    check(ozemu_mx_quantize(rows, k, type_code(x.scalar_type()), mx.p, mx.ld, pc, ps, on.handle), "ozemu_mx_quantize");
-    PyObject *oc = a[1] == Py_None ? THPVariable_Wrap(fresh_codes) : Py_NewRef(a[1]);
-    PyObject *os = a[2] == Py_None ? THPVariable_Wrap(fresh_scales) : Py_NewRef(a[2]);
-    PyObject* r = oc && os ? PyTuple_Pack(2, oc, os) : nullptr;
-    Py_XDECREF(oc);
-    Py_XDECREF(os);
-    return r;
+    check(ozemu_mx_quantize(rows, k, type_code(x.scalar_type()), mx.p, mx.ld, q.p, q.scales(), on.handle),
+          "ozemu_mx_quantize");
+    return given ? Py_NewRef(a[1]) : THPVariable_Wrap(fresh);
   });
 }
 
-// mx_dequantize(codes, scales, rows, k, type, out, stream)
+// mx_dequantize(data, rows, k, type, out, stream)
 PyObject* mx_dequantize(PyObject*, PyObject* const* a, Py_ssize_t count) {
-  return guarded(count, 7, [&]() -> PyObject* {
-    const at::Tensor &codes = tensor(a[0], "codes"), &scales = tensor(a[1], "scales");
-    const int rows = integer(a[2]), k = integer(a[3]), type = integer(a[4]);
-    const at::Tensor* given = tensor_or_none(a[5], "out");
-    const uint8_t *pc = mx_array(codes, ozemu_mx_code_bytes(rows, k), codes, "codes");
-    const uint8_t* ps = mx_array(scales, ozemu_mx_scale_bytes(rows, k), codes, "scales");
-    const at::TensorOptions options = codes.options().dtype(scalar_type(type));
+  return guarded(count, 6, [&]() -> PyObject* {
+    const at::Tensor& data = tensor(a[0], "q");
+    const int rows = integer(a[1]), k = integer(a[2]), type = integer(a[3]);
+    const at::Tensor* given = tensor_or_none(a[4], "out");
+    MxData q(rows, k);
+    q.in(data, data, "q");
+    const at::TensorOptions options = data.options().dtype(scalar_type(type));
     Matrix my;
     if (given) {
-      if (given->scalar_type() != scalar_type(type) || given->device() != codes.device())
+      if (given->scalar_type() != scalar_type(type) || given->device() != data.device())
         throw Refused(std::string("out: expected a matrix of ") + c10::toString(scalar_type(type)) + " on " +
-                      codes.device().str());
+                      data.device().str());
       my = matrix(given, rows, k, *given, "out");
       const Output o(given, my, rows, k, *given);
-      o.apart(codes, "q");
-      o.apart(scales, "q");
+      o.apart(data, "q");
     }
-    OnStream on(codes, a[6], {&codes, &scales, given});
+    OnStream on(data, a[5], {&data, given});
     at::Tensor fresh;
     if (!given) {
       fresh = at::empty({rows, k}, options);
       my = matrix(&fresh, rows, k, fresh, "out");
     }
-    check(ozemu_mx_dequantize(rows, k, type, pc, ps, my.p, my.ld, on.handle), "ozemu_mx_dequantize");
-    return given ? Py_NewRef(a[5]) : THPVariable_Wrap(fresh);
+    check(ozemu_mx_dequantize(rows, k, type, q.p, q.scales(), my.p, my.ld, on.handle), "ozemu_mx_dequantize");
+    return given ? Py_NewRef(a[4]) : THPVariable_Wrap(fresh);
   });
 }
 
-// mx_linear(x_codes, x_scales, m, w_codes, w_scales, n, k, bias, residual, activation, type, out, stream)
+// mx_linear(x, m, w, n, k, bias, residual, activation, type, out, stream)
 PyObject* mx_linear(PyObject*, PyObject* const* a, Py_ssize_t count) {
-  return guarded(count, 13, [&]() -> PyObject* {
-    const at::Tensor &xc = tensor(a[0], "x"), &xs = tensor(a[1], "x"), &wc = tensor(a[3], "w"), &ws = tensor(a[4], "w");
-    const int m = integer(a[2]), n = integer(a[5]), k = integer(a[6]), act = integer(a[9]), type = integer(a[10]);
-    const at::Tensor *bias = tensor_or_none(a[7], "bias"), *res = tensor_or_none(a[8], "residual");
-    const at::Tensor* given = tensor_or_none(a[11], "out");
-    const uint8_t *pxc = mx_array(xc, ozemu_mx_code_bytes(m, k), xc, "x"), *pxs = mx_array(xs, ozemu_mx_scale_bytes(m, k), xc, "x");
-    const uint8_t *pwc = mx_array(wc, ozemu_mx_code_bytes(n, k), xc, "w"), *pws = mx_array(ws, ozemu_mx_scale_bytes(n, k), xc, "w");
+  return guarded(count, 11, [&]() -> PyObject* {
+    const at::Tensor &dx = tensor(a[0], "x"), &dw = tensor(a[2], "w");
+    const int m = integer(a[1]), n = integer(a[3]), k = integer(a[4]), act = integer(a[7]), type = integer(a[8]);
+    const at::Tensor *bias = tensor_or_none(a[5], "bias"), *res = tensor_or_none(a[6], "residual");
+    const at::Tensor* given = tensor_or_none(a[9], "out");
+    MxData x(m, k), w(n, k);
+    x.in(dx, dx, "x");
+    w.in(dw, dx, "w");
     const at::ScalarType t = scalar_type(type);
     // The matrices of the call's type, against one of that type.
     const at::Tensor* like = given ? given : res ? res : bias;
-    if (like && (like->scalar_type() != t || like->device() != xc.device()))
+    if (like && (like->scalar_type() != t || like->device() != dx.device()))
       throw Refused(std::string(given ? "out" : res ? "residual" : "bias") + ": expected " + c10::toString(t) + " on " +
-                    xc.device().str());
+                    dx.device().str());
     Matrix mr, my;
     void* pb = nullptr;
     mr.ld = my.ld = n > 0 ? n : 1;
@@ -632,21 +636,19 @@ PyObject* mx_linear(PyObject*, PyObject* const* a, Py_ssize_t count) {
       const Output o(given, my, m, n, *like);
       o.apart(bias, pb, n, "bias");
       o.apart(res, mr, m, n, "residual", true);
-      o.apart(xc, "x");
-      o.apart(xs, "x");
-      o.apart(wc, "w");
-      o.apart(ws, "w");
+      o.apart(dx, "x");
+      o.apart(dw, "w");
     }
-    OnStream on(xc, a[12], {&xc, &xs, &wc, &ws, bias, res, given});
+    OnStream on(dx, a[10], {&dx, &dw, bias, res, given});
     no_graph("mx_linear", "torch.no_grad() says that none are wanted", {bias, res});
     at::Tensor fresh;
     if (!given) {
-      fresh = at::empty({m, n}, xc.options().dtype(t));
+      fresh = at::empty({m, n}, dx.options().dtype(t));
       my = matrix(&fresh, m, n, fresh, "out");
     }
-    check(ozemu_mx_linear(m, n, k, type, pxc, pxs, pwc, pws, pb, mr.p, mr.ld, act, my.p, my.ld, on.handle),
+    check(ozemu_mx_linear(m, n, k, type, x.p, x.scales(), w.p, w.scales(), pb, mr.p, mr.ld, act, my.p, my.ld, on.handle),
           "ozemu_mx_linear");
-    return given ? Py_NewRef(a[11]) : THPVariable_Wrap(fresh);
+    return given ? Py_NewRef(a[9]) : THPVariable_Wrap(fresh);
   });
 }
 
@@ -752,7 +754,7 @@ PyObject* clip_grad_norm(PyObject*, PyObject* const* a, Py_ssize_t count) {
     }
     const at::Tensor norm = at::empty({}, first.options().dtype(at::kFloat));
     const int total = static_cast<int>(n);
-    const Scratch ws(first, ozemu_clip_grad_norm_bytes(total));
+    const Scratch ws(first, ozemu_clip_grad_norm_bytes(total, in.data(), sizes.data(), types.data()));
     check(ozemu_clip_grad_norm(total, in.data(), sizes.data(), types.data(), outs.data(), static_cast<float>(max_norm),
                                static_cast<float>(eps), norm.data_ptr<float>(), ws.p, ws.bytes, on.handle),
           "ozemu_clip_grad_norm");

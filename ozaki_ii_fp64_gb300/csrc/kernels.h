@@ -221,8 +221,7 @@ struct MxLinearCall {
 };
 cudaError_t launch_mx_linear(const MxLinearCall& call, cudaStream_t stream);
 
-// Clipping by the global norm (clip.cu): `count` tensors, host arrays; ws holds
-// clip_workspace(count) bytes.
+// Clipping by the global norm (clip.cu): `count` tensors, host arrays.
 struct ClipCall {
   int count;
   const void* const* grads;
@@ -233,7 +232,7 @@ struct ClipCall {
   float* norm;
   void* ws;
 };
-size_t clip_workspace(int count);
+size_t clip_workspace(const ClipCall& call);
 cudaError_t launch_clip_grad_norm(const ClipCall& call, cudaStream_t stream);
 
 // Launches a kernel that begins with chain_wait (common.cuh).  cluster: CTAs

@@ -111,11 +111,11 @@ __device__ __forceinline__ uint32_t part_piece(int r, int c) {
 
 // The same for a gated tile: z the gate's accumulators, u the up projection's.
 template <typename T>
-__device__ __forceinline__ void finish_gated(float (&z)[32], float (&u)[32], const Epilogue& e, uint8_t* stage,
+__device__ __forceinline__ void finish_gated(float2 (&z)[16], float2 (&u)[16], const Epilogue& e, uint8_t* stage,
                                              uint8_t* bias, int row0, int col0, int m, int n) {
   const int lane = threadIdx.x & 31;
   // One half's bias and rounded pre-activation.
-  auto half = [&](float (&v)[32], int at) {
+  auto half = [&](float2 (&v)[16], int at) {
     if (e.bias) {  // the chunk's 32 values, for every lane
       const uint16_t b = col0 + lane < n ? static_cast<const uint16_t*>(e.bias)[at + col0 + lane] : 0;
       __syncwarp();
@@ -123,15 +123,15 @@ __device__ __forceinline__ void finish_gated(float (&z)[32], float (&u)[32], con
       __syncwarp();
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        float f[8];
+        float2 f[4];
         unpack16<T>(reinterpret_cast<const uint4*>(bias)[q], f);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[8 * q + i] += f[i];
+        for (int i = 0; i < 4; ++i) v[4 * q + i] = add2(v[4 * q + i], f[i]);
       }
     }
     if (e.pre) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) *stage_piece(stage, lane, c) = pack16<T>(v + 8 * c);
+      for (int c = 0; c < 4; ++c) *stage_piece(stage, lane, c) = pack16<T>(v + 4 * c);
       __syncwarp();
       write_rows(stage, static_cast<T*>(e.pre) + at, e.ldpre, row0, col0, m, n, (e.vec & (at ? 32 : 4)) != 0);
       __syncwarp();
@@ -141,9 +141,9 @@ __device__ __forceinline__ void finish_gated(float (&z)[32], float (&u)[32], con
   half(u, n);
   activate_all(z, e.act);
 #pragma unroll
-  for (int i = 0; i < 32; ++i) z[i] *= u[i];
+  for (int i = 0; i < 16; ++i) z[i] = mul2(z[i], u[i]);
 #pragma unroll
-  for (int c = 0; c < 4; ++c) *stage_piece(stage, lane, c) = pack16<T>(z + 8 * c);
+  for (int c = 0; c < 4; ++c) *stage_piece(stage, lane, c) = pack16<T>(z + 4 * c);
   __syncwarp();
   write_rows(stage, static_cast<T*>(e.out), e.ldo, row0, col0, m, n, (e.vec & 8) != 0);
   __syncwarp();
@@ -364,11 +364,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld32(tcol + c, a);
           tmem_ld32(tcol + width + c, b);
           tmem_wait_ld();
-          float z[32], u[32];
+          float2 z[16], u[16];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            z[i] = __uint_as_float(a[i]);
-            u[i] = __uint_as_float(b[i]);
+          for (int i = 0; i < 16; ++i) {
+            z[i] = make_float2(__uint_as_float(a[2 * i]), __uint_as_float(a[2 * i + 1]));
+            u[i] = make_float2(__uint_as_float(b[2 * i]), __uint_as_float(b[2 * i + 1]));
           }
           tc_fence_before();
           __syncwarp();
@@ -828,17 +828,72 @@ __global__ void __launch_bounds__(256, 4) slope_kernel(const T* dy, long long ld
   }
 }
 
-// Stores eight consecutive elements of which `left` exist.
-template <typename T>
-__device__ __forceinline__ void store8(T* p, int left, bool vec, const float2 (&v)[4]) {
-  if (vec && left >= 8) {
-    *reinterpret_cast<uint4*>(p) = pack16<T>(v);
-  } else {
+// The 16 bytes that lie `off` bytes (even, under 16) into lo and hi together.
+__device__ __forceinline__ uint4 shifted16(const uint4& lo, const uint4& hi, uint32_t off) {
+  uint32_t u[5];
+  switch (off >> 2) {
+    case 0: u[0] = lo.x, u[1] = lo.y, u[2] = lo.z, u[3] = lo.w, u[4] = hi.x; break;
+    case 1: u[0] = lo.y, u[1] = lo.z, u[2] = lo.w, u[3] = hi.x, u[4] = hi.y; break;
+    case 2: u[0] = lo.z, u[1] = lo.w, u[2] = hi.x, u[3] = hi.y, u[4] = hi.z; break;
+    default: u[0] = lo.w, u[1] = hi.x, u[2] = hi.y, u[3] = hi.z, u[4] = hi.w; break;
+  }
+  if (off & 2) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (2 * i < left) p[2 * i] = from_float<T>(v[i].x);
-      if (2 * i + 1 < left) p[2 * i + 1] = from_float<T>(v[i].y);
+    for (int i = 0; i < 4; ++i) u[i] = __funnelshift_r(u[i], u[i + 1], 16);
+  }
+  return make_uint4(u[0], u[1], u[2], u[3]);
+}
+
+// Eight consecutive elements of a matrix whose rows start anywhere, of which
+// `left` exist (0 past the end): from the two aligned vectors that they lie in,
+// where those are the matrix's own memory, begin to end.
+template <typename T>
+__device__ __forceinline__ void load8_anywhere(const T* p, int left, bool vec, uintptr_t begin, uintptr_t end,
+                                               float2 (&v)[4]) {
+  const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 15u);
+  const uintptr_t from = reinterpret_cast<uintptr_t>(p) - off;
+  if (!vec && left >= 8 && from >= begin && from + 32 <= end) {
+    const uint4* at = reinterpret_cast<const uint4*>(from);
+    unpack16<T>(shifted16(__ldg(at), __ldg(at + 1), off), v);
+  } else {
+    load8(p, left, vec, v);
+  }
+}
+
+// Stores eight consecutive elements of which `left` exist.  A warp whose lanes'
+// elements follow each other (kRow) stores vectors from the first boundary on,
+// made of a lane's elements and the next one's, where p is on none; all of its
+// lanes call this.
+template <typename T, bool kRow>
+__device__ __forceinline__ void store8(T* p, int left, bool vec, const float2 (&v)[4]) {
+  const uint4 mine = pack16<T>(v);
+  if (vec) {
+    if (left >= 8) {
+      *reinterpret_cast<uint4*>(p) = mine;
+      return;
     }
+  } else if constexpr (kRow) {
+    const int lane = threadIdx.x & 31;
+    const uint32_t off = 16 - static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 15u);  // to the boundary
+    uint4 next;
+    next.x = __shfl_down_sync(0xFFFFFFFFu, mine.x, 1);
+    next.y = __shfl_down_sync(0xFFFFFFFFu, mine.y, 1);
+    next.z = __shfl_down_sync(0xFFFFFFFFu, mine.z, 1);
+    next.w = __shfl_down_sync(0xFFFFFFFFu, mine.w, 1);
+    const int head = static_cast<int>(off) / 2;
+    const bool joins = lane < 31 && left >= 16;
+    if (joins) *reinterpret_cast<uint4*>(p + head) = shifted16(mine, next, off);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {  // a head that the lane before does not take, a tail that does not join
+      const float f = i & 1 ? v[i / 2].y : v[i / 2].x;
+      if (i < left && (i < head ? lane == 0 || left < 8 : !joins)) p[i] = from_float<T>(f);
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (2 * i < left) p[2 * i] = from_float<T>(v[i].x);
+    if (2 * i + 1 < left) p[2 * i + 1] = from_float<T>(v[i].y);
   }
 }
 
@@ -859,26 +914,27 @@ __global__ void __launch_bounds__(256, 3) gated_slope_kernel(const T* dh, long l
   const int col = blockIdx.x * kCols + tx * 8, left = n - col;
   float2 sums[2][4] = {};
   const long long end = min(static_cast<long long>(m), (blockIdx.y + 1LL) * chunk);
-  if (left > 0) {
+  // Rows of no alignment: which memory a vector may be read from.
+  const uintptr_t dh0 = reinterpret_cast<uintptr_t>(dh), dh1 = reinterpret_cast<uintptr_t>(dh + (m - 1) * lddh + n);
+  const uintptr_t pre0 = reinterpret_cast<uintptr_t>(pre), pre1 = reinterpret_cast<uintptr_t>(pre + (m - 1) * ldpre + 2 * n);
 #pragma unroll 2
-    for (long long i = static_cast<long long>(blockIdx.y) * chunk + ty; i < end; i += TY) {
-      float2 d[4], g[4], u[4];
-      load8(dh + i * lddh + col, left, vec & 1, d);
-      load8(pre + i * ldpre + col, left, vec & 2, g);
-      load8(pre + i * ldpre + n + col, left, vec & 4, u);
+  for (long long i = static_cast<long long>(blockIdx.y) * chunk + ty; i < end; i += TY) {
+    float2 d[4], g[4], u[4];
+    load8_anywhere(dh + i * lddh + col, left, vec & 1, dh0, dh1, d);
+    load8_anywhere(pre + i * ldpre + col, left, vec & 2, pre0, pre1, g);
+    load8_anywhere(pre + i * ldpre + n + col, left, vec & 4, pre0, pre1, u);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        float2 a, slope;
-        activation_and_slope2<kAct>(g[q], a, slope);
-        u[q] = mul2(mul2(d[q], u[q]), slope);
-        d[q] = mul2(d[q], a);
-        sums[0][q] = add2(sums[0][q], u[q]);
-        sums[1][q] = add2(sums[1][q], d[q]);
-      }
-      if (dz) {
-        store8(dz + i * lddz + col, left, true, u);  // rows start on 16-byte boundaries
-        store8(dz + i * lddz + n + col, left, vec & 8, d);
-      }
+    for (int q = 0; q < 4; ++q) {
+      float2 a, slope;
+      activation_and_slope2<kAct>(g[q], a, slope);
+      u[q] = mul2(mul2(d[q], u[q]), slope);
+      d[q] = mul2(d[q], a);
+      sums[0][q] = add2(sums[0][q], u[q]);
+      sums[1][q] = add2(sums[1][q], d[q]);
+    }
+    if (dz) {
+      store8<T, TX == 32>(dz + i * lddz + col, left, true, u);  // rows start on 16-byte boundaries
+      store8<T, TX == 32>(dz + i * lddz + n + col, left, vec & 8, d);
     }
   }
   if (!part && !db) return;
@@ -1220,11 +1276,11 @@ cudaError_t linear_t(const LinearCall& c, cudaStream_t stream) {
 // Row chunks of the slope pass: one where that is quick, else enough CTAs to
 // fill the GPU.
 constexpr int kFewSlopeRows = 256;
-int slope_chunk(int m, int n) {
+int slope_chunk(int m, int n, int ctas, int least) {
   if (m <= kFewSlopeRows) return kFewSlopeRows;
   const int across = (n + 255) / 256;
-  const int chunks = std::max(1, std::min(256, 608 / across));
-  return std::max(32, ((m + chunks - 1) / chunks + 7) / 8 * 8);
+  const int chunks = std::max(1, std::min(256, ctas / across));
+  return std::max(least, ((m + chunks - 1) / chunks + 7) / 8 * 8);
 }
 
 struct BackwardPlan {
@@ -1237,7 +1293,7 @@ BackwardPlan backward_plan(const LinearGradCall& c) {
   p.own_dz = c.act != kActNone || !rows_aligned(c.dy, c.lddy, c.m);
   const size_t up = 255;
   p.dz = p.own_dz ? (static_cast<size_t>(c.m) * pad8(c.n) * 2 + up) & ~up : 0;
-  p.chunk = slope_chunk(c.m, c.n);
+  p.chunk = slope_chunk(c.m, c.n, 152 * 4, 32);
   p.chunks = (c.m + p.chunk - 1) / p.chunk;
   p.part = p.chunks > 1 ? (static_cast<size_t>(p.chunks) * c.n * 4 + up) & ~up : 0;
   p.x = aligned_copy_bytes({c.x, c.ldx, c.m, c.k});
@@ -1326,7 +1382,7 @@ GatedPlan gated_plan(const LinearGradCall& c) {
   GatedPlan p;
   const size_t up = 255;
   p.dz = (static_cast<size_t>(c.m) * pad8(2 * c.n) * 2 + up) & ~up;
-  p.chunk = slope_chunk(c.m, c.n);
+  p.chunk = slope_chunk(c.m, c.n, 152 * 3, 16);
   p.chunks = (c.m + p.chunk - 1) / p.chunk;
   p.part = p.chunks > 1 ? (static_cast<size_t>(p.chunks) * 2 * c.n * 4 + up) & ~up : 0;
   p.x = aligned_copy_bytes({c.x, c.ldx, c.m, c.k});

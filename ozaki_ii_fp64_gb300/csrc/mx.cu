@@ -33,25 +33,16 @@ namespace {
 
 constexpr int kTileRows = 128, kTileCols = 256;  // of a 1024-byte tile of scales
 
-// Eight elements of which `left` exist as floats, 0 past them.
+// Eight consecutive elements of a row, raw: one or two 16-byte vectors.
 template <typename T>
-__device__ __forceinline__ void load_eight(const T* p, int left, bool vec, float2 (&v)[4]) {
-  if (vec && left >= 8) {
-    if constexpr (sizeof(T) == 4) {
-      const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-      v[0] = make_float2(a.x, a.y);
-      v[1] = make_float2(a.z, a.w);
-      v[2] = make_float2(b.x, b.y);
-      v[3] = make_float2(b.z, b.w);
-    } else {
-      unpack16<T>(__ldg(reinterpret_cast<const uint4*>(p)), v);
-    }
-  } else {
+struct Eight {
+  static constexpr int kVectors = sizeof(T) / 2;
+  uint4 u[kVectors];
+  __device__ __forceinline__ void unpack(float2 (&v)[4]) const {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      v[i] = make_float2(2 * i < left ? to_float(p[2 * i]) : 0.f, 2 * i + 1 < left ? to_float(p[2 * i + 1]) : 0.f);
+    for (int i = 0; i < kVectors; ++i) unpack16<T>(u[i], v + 4 / kVectors * i);
   }
-}
+};
 
 // Eight values already divided by their scale to eight codes, the first lowest.
 __device__ __forceinline__ uint32_t to_codes(const float2 (&v)[4]) {
@@ -80,89 +71,191 @@ __device__ __forceinline__ void from_codes(uint32_t w, float2 (&v)[4]) {
 // Place of the scale of a tile's row r and 32-column block b.
 __device__ __forceinline__ int scale_at(int r, int b) { return (b >> 2) * 512 + (r & 31) * 16 + (r >> 5) * 4 + (b & 3); }
 
-// One CTA to a tile of scales: 128 rows of 256 columns.  A warp takes a row, a
-// lane eight columns of it, four lanes a block; four rows of a warp are in
-// flight.  A block with an infinity or a NaN takes the scale NaN (255).
-template <typename T>
-__global__ void __launch_bounds__(256) mx_quantize_kernel(const T* x, long long ldx, int rows, int k, uint8_t* codes,
-                                                          uint8_t* scales, int ktiles, int vec) {
+// A CTA's tile, or quarter of one.
+struct TilePart {
+  int tile, kt, quarter;
+  int r0, rows;  // the first row, and how many exist
+  __device__ __forceinline__ TilePart(int ktiles, int quarters, int all) {
+    tile = quarters ? blockIdx.x >> 2 : blockIdx.x;
+    quarter = quarters ? blockIdx.x & 3 : 0;
+    kt = tile % ktiles;
+    r0 = tile / ktiles * kTileRows + quarter * 32;
+    rows = min(quarters ? 32 : kTileRows, all - r0);
+  }
+};
+
+// One CTA to a tile of scales, 128 rows of 256 columns, or, where those are few
+// (1021 x 5003 fp32 has 160 of them: 12.8 us, by quarters 5.6), to a quarter of
+// one, the 32 rows of one byte column of its words.  A warp takes a row, a
+// lane eight columns of it, four lanes a block; the next rows of a warp (64
+// bytes a lane) are on their way while it works on as many.  kVec: rows start on 16-byte boundaries;
+// else their elements come one by one, a warp's side by side, and pass through
+// shared memory to the lanes that take eight.  A block with an infinity or a NaN
+// takes the scale NaN (255).
+template <typename T, bool kVec>
+__global__ void __launch_bounds__(256, 4) mx_quantize_kernel(const T* x, long long ldx, int rows, int k, uint8_t* codes,
+                                                             uint8_t* scales, int ktiles, int quarters) {
+  constexpr int kRows = 4 / Eight<T>::kVectors;  // of a warp at a time
   __shared__ uint4 tile[64];
+  __shared__ uint4 through[kVec ? 1 : 8 * 128];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x < 64) tile[threadIdx.x] = make_uint4(0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
   chain_next();
   chain_wait();
   __syncthreads();
-  const int rb = blockIdx.x / ktiles, kt = blockIdx.x % ktiles;
-  const int r0 = rb * kTileRows, here = min(kTileRows, rows - r0);
+  const TilePart part(ktiles, quarters, rows);
+  const int kt = part.kt, r0 = part.r0, here = part.rows;
   const int col = kt * kTileCols + lane * 8, left = k - col;
   const long long row_bytes = (k + 31LL) / 32 * 16;
   const bool stored = col < (k + 31) / 32 * 32;
-#pragma unroll 1
-  for (int i0 = warp; i0 < here; i0 += 32) {
-    float2 v[4][4];
+  const T* from = x + static_cast<long long>(r0) * ldx;
+
+  auto load = [&](Eight<T>(&e)[kRows], int i0) {
+    if constexpr (kVec) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-      load_eight(x + (r0 + i0 + 8LL * q) * ldx + col, i0 + 8 * q < here ? left : 0, vec, v[q]);
+      for (int q = 0; q < kRows; ++q) {
+        const int r = i0 + 8 * q;
+        const T* p = from + r * ldx + col;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int r = i0 + 8 * q;
-      uint32_t most = 0;
+        for (int i = 0; i < Eight<T>::kVectors; ++i) {
+          const int exist = left - i * static_cast<int>(16 / sizeof(T));
+          e[q].u[i] = make_uint4(0, 0, 0, 0);
+          if (r < here && exist >= static_cast<int>(16 / sizeof(T))) {
+            e[q].u[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+          } else if (r < here && exist > 0) {
+            T* at = reinterpret_cast<T*>(&e[q].u[i]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        most = max(most, max(__float_as_uint(v[q][i].x) & 0x7FFFFFFFu, __float_as_uint(v[q][i].y) & 0x7FFFFFFFu));
-      most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
-      most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
-      const int e = static_cast<int>(most >> 23), byte = e == 255 ? 255 : max(e - 2, 0);
-      const float2 inverse = both(__uint_as_float(static_cast<uint32_t>(254 - byte) << 23));
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[q][i] = mul2(v[q][i], inverse);
-      const uint32_t w = byte == 255 ? 0 : to_codes(v[q]);
-      if (r < here && stored) {
-        *reinterpret_cast<uint32_t*>(codes + (r0 + r) * row_bytes + col / 2) = w;
-        if ((lane & 3) == 0) reinterpret_cast<uint8_t*>(tile)[scale_at(r, lane >> 2)] = static_cast<uint8_t>(byte);
+            for (int c = 0; c < static_cast<int>(16 / sizeof(T)); ++c)
+              if (c < exist) at[c] = p[i * (16 / sizeof(T)) + c];
+          }
+        }
       }
+    } else {
+      T one[kRows][8];
+#pragma unroll
+      for (int q = 0; q < kRows; ++q)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = i0 + 8 * q, c = kt * kTileCols + 32 * i + lane;
+          one[q][i] = r < here && c < k ? from[r * ldx + c] : from_float<T>(0.f);
+        }
+      uint4* mine = through + warp * 128;
+      __syncwarp();
+#pragma unroll
+      for (int q = 0; q < kRows; ++q)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) reinterpret_cast<T*>(mine + q * 32 * Eight<T>::kVectors)[32 * i + lane] = one[q][i];
+      __syncwarp();
+#pragma unroll
+      for (int q = 0; q < kRows; ++q)
+#pragma unroll
+        for (int i = 0; i < Eight<T>::kVectors; ++i) e[q].u[i] = mine[(q * 32 + lane) * Eight<T>::kVectors + i];
     }
+  };
+  auto finish = [&](const Eight<T>& e, int r) {
+    float2 v[4];
+    e.unpack(v);
+    uint32_t most = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      most = max(most, max(__float_as_uint(v[i].x) & 0x7FFFFFFFu, __float_as_uint(v[i].y) & 0x7FFFFFFFu));
+    most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
+    most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
+    const int exponent = static_cast<int>(most >> 23), byte = exponent == 255 ? 255 : max(exponent - 2, 0);
+    const float2 inverse = both(__uint_as_float(static_cast<uint32_t>(254 - byte) << 23));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = mul2(v[i], inverse);
+    const uint32_t w = byte == 255 ? 0 : to_codes(v);
+    if (r < here && stored) {
+      *reinterpret_cast<uint32_t*>(codes + (r0 + r) * row_bytes + col / 2) = w;
+      if ((lane & 3) == 0) reinterpret_cast<uint8_t*>(tile)[scale_at(r, lane >> 2)] = static_cast<uint8_t>(byte);
+    }
+  };
+
+  Eight<T> next[kRows];
+  load(next, warp);
+#pragma unroll 1
+  for (int i0 = warp; i0 < here; i0 += 8 * kRows) {
+    Eight<T> now[kRows];
+#pragma unroll
+    for (int q = 0; q < kRows; ++q) now[q] = next[q];
+    if (i0 + 8 * kRows < here) load(next, i0 + 8 * kRows);
+#pragma unroll
+    for (int q = 0; q < kRows; ++q) finish(now[q], i0 + 8 * q);
   }
   __syncthreads();
-  if (threadIdx.x < 64) reinterpret_cast<uint4*>(scales + blockIdx.x * 1024LL)[threadIdx.x] = tile[threadIdx.x];
+  if (threadIdx.x >= 64) return;
+  uint4* to = reinterpret_cast<uint4*>(scales + part.tile * 1024LL) + threadIdx.x;
+  if (quarters)  // rows r of the quarter stood where a whole tile's first 32 rows do
+    reinterpret_cast<uint32_t*>(to)[part.quarter] = tile[threadIdx.x].x;
+  else
+    *to = tile[threadIdx.x];
 }
 
-// The values that codes and scales stand for: the same tiles and lanes.
-template <typename T>
-__global__ void __launch_bounds__(256) mx_dequantize_kernel(const uint8_t* codes, const uint8_t* scales, int ktiles, T* y,
-                                                            long long ldy, int rows, int k, int vec) {
+// The values that codes and scales stand for: the same tiles and lanes, and
+// through shared memory where rows start on no 16-byte boundaries.
+template <typename T, bool kVec>
+__global__ void __launch_bounds__(256) mx_dequantize_kernel(const uint8_t* codes, const uint8_t* scales, int ktiles,
+                                                            int quarters, T* y, long long ldy, int rows, int k) {
+  __shared__ uint4 through[kVec ? 1 : 8 * 4 * 32 * Eight<T>::kVectors];
   chain_next();
   chain_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rb = blockIdx.x / ktiles, kt = blockIdx.x % ktiles;
-  const int r0 = rb * kTileRows, here = min(kTileRows, rows - r0);
+  const TilePart part(ktiles, quarters, rows);
+  const int kt = part.kt, r0 = part.r0, here = part.rows;
   const int col = kt * kTileCols + lane * 8, left = k - col;
-  if (left <= 0) return;
   const long long row_bytes = (k + 31LL) / 32 * 16;
-  const uint8_t* tile = scales + blockIdx.x * 1024LL;
-#pragma unroll 4
-  for (int r = warp; r < here; r += 8) {
-    const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(codes + (r0 + r) * row_bytes + col / 2));
-    const uint32_t byte = __ldg(tile + scale_at(r, lane >> 2));
-    const float s = __uint_as_float(byte == 255 ? 0x7FC00000u : byte == 0 ? 0x00400000u : byte << 23);
-    float2 v[4];
-    from_codes(w, v);
+  const uint8_t* tile = scales + part.tile * 1024LL + part.quarter * 4;  // (a quarter's rows count from 0)
+#pragma unroll 1
+  for (int i0 = warp; i0 < here; i0 += 32) {
+    uint32_t w[4], byte[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = mul2(v[i], both(s));
-    T* p = y + static_cast<long long>(r0 + r) * ldy + col;
-    if (vec && left >= 8) {
-      if constexpr (sizeof(T) == 4) {
-        reinterpret_cast<uint4*>(p)[0] = pack16<T>(v);
-        reinterpret_cast<uint4*>(p)[1] = pack16<T>(v + 2);
-      } else {
-        *reinterpret_cast<uint4*>(p) = pack16<T>(v);
+    for (int q = 0; q < 4; ++q) {
+      const int r = i0 + 8 * q;
+      w[q] = byte[q] = 0;
+      if (r < here && left > 0) {
+        w[q] = __ldg(reinterpret_cast<const uint32_t*>(codes + (r0 + r) * row_bytes + col / 2));
+        byte[q] = __ldg(tile + scale_at(r, lane >> 2));
       }
-    } else {
+    }
+    uint4* mine = through + warp * 4 * 32 * Eight<T>::kVectors;
+    if constexpr (!kVec) __syncwarp();
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (2 * i < left) p[2 * i] = from_float<T>(v[i].x);
-        if (2 * i + 1 < left) p[2 * i + 1] = from_float<T>(v[i].y);
+    for (int q = 0; q < 4; ++q) {
+      const int r = i0 + 8 * q;
+      const float s = __uint_as_float(byte[q] == 255 ? 0x7FC00000u : byte[q] == 0 ? 0x00400000u : byte[q] << 23);
+      float2 v[4];
+      from_codes(w[q], v);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = mul2(v[i], both(s));
+      T* p = y + static_cast<long long>(r0 + r) * ldy + col;
+#pragma unroll
+      for (int i = 0; i < Eight<T>::kVectors; ++i) {
+        const uint4 u = pack16<T>(v + 4 / Eight<T>::kVectors * i);
+        const int exist = left - i * static_cast<int>(16 / sizeof(T));
+        if constexpr (!kVec) {
+          mine[(q * 32 + lane) * Eight<T>::kVectors + i] = u;
+        } else if (r < here && exist >= static_cast<int>(16 / sizeof(T))) {
+          reinterpret_cast<uint4*>(p)[i] = u;
+        } else if (r < here && exist > 0) {
+          const T* at = reinterpret_cast<const T*>(&u);
+#pragma unroll
+          for (int c = 0; c < static_cast<int>(16 / sizeof(T)); ++c)
+            if (c < exist) p[i * (16 / sizeof(T)) + c] = at[c];
+        }
       }
+    }
+    if constexpr (!kVec) {
+      __syncwarp();
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = i0 + 8 * q, c = kt * kTileCols + 32 * i + lane;
+          if (r < here && c < k)
+            y[static_cast<long long>(r0 + r) * ldy + c] =
+                reinterpret_cast<const T*>(mine + q * 32 * Eight<T>::kVectors)[32 * i + lane];
+        }
     }
   }
 }
@@ -253,6 +346,56 @@ __device__ __forceinline__ void stage_mmas(uint32_t d, uint32_t a, uint32_t b, u
   for (int ks = 0; ks < 4; ++ks)
     mma_mx<kGroup>(d, smem_desc_sw128(a_lo + 2 * ks), smem_desc_sw128(b_lo + 2 * ks), idesc_mx(m, n, ks & 1),
                    sa + 4 * (ks >> 1), sb + b_step * (ks >> 1), first && ks == 0 ? 0u : 1u);
+}
+
+// 32 bytes of global memory.
+__device__ __forceinline__ void load32(const void* p, uint32_t (&v)[8]) {
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+               : "l"(p)
+               : "memory");
+}
+// Without a place in L1, which nothing reads it from again: 8192 x 4096 -> 16384
+// takes 171 us, with one 180.
+__device__ __forceinline__ void store32(void* p, const uint32_t (&v)[8]) {
+  asm volatile("st.global.L1::no_allocate.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+// A warp's 32 rows x 32 columns of accumulators, a row a lane, where rows start
+// on 32-byte boundaries: straight from registers in 32-byte pieces.  (The MMAs
+// and the copies that feed them take all of shared memory's bandwidth, 67 KB in
+// the 512 clocks of a stage; passing the outputs through it cost them a sixth.)
+template <typename T>
+__device__ __forceinline__ void finish_direct(const uint32_t (&u)[32], const Epilogue& e, const uint4* bias,
+                                              long long row, int col0, int m) {
+  if (row >= m) return;
+  float2 z[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) z[i] = make_float2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
+  if (e.bias) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      float2 b[4];
+      unpack16<T>(bias[q], b);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) z[4 * q + i] = add2(z[4 * q + i], b[i]);
+    }
+  }
+  activate_all(z, e.act);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t w[8];
+    if (e.res) {
+      load32(static_cast<const T*>(e.res) + row * e.ldr + col0 + 16 * h, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) z[8 * h + i] = add2(z[8 * h + i], Pair<T>::unpack(w[i]));
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = Pair<T>::pack(z[8 * h + i].x, z[8 * h + i].y);
+    store32(static_cast<T*>(e.out) + row * e.ldo + col0 + 16 * h, w);
+  }
 }
 
 template <typename T>
@@ -408,9 +551,10 @@ __global__ void __launch_bounds__(kMxThreads, 1)
       for (int h = 0; h < p.bn; h += 128) {
         const int c = (first ^ h) + group * 32;
         const int col0 = tn * p.bn + c;
+        const bool direct = (e.vec & 16) != 0 && c + 32 <= cols;
         uint4 res[4];
         if (c < cols) {
-          if (e.res)
+          if (e.res && !direct)
             read_rows(res, static_cast<const T*>(e.res), e.ldr, row0, col0, p.m, p.n, (e.vec & 2) != 0);
           if (e.bias) {  // the chunk's 32 values, for every lane
             const uint16_t b = col0 + lane < p.n ? static_cast<const uint16_t*>(e.bias)[col0 + lane] : 0;
@@ -435,7 +579,9 @@ __global__ void __launch_bounds__(kMxThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(&taken[buf], 0));
         }
-        if (c < cols)
+        if (direct)
+          finish_direct<T>(u, e, reinterpret_cast<const uint4*>(bias), row0 + lane, col0, p.m);
+        else if (c < cols)
           finish_rows<T>(
               [&](bool, float(&z)[32]) {
 #pragma unroll
@@ -477,13 +623,13 @@ constexpr int kMxFewThreads = 192;
 
 struct MxFewProduct {
   int m, n, kt, split;
+  const uint8_t *wscales, *xscales;
   Epilogue e;
 };
 
 template <typename T, int NT>
 __global__ void __launch_bounds__(kMxFewThreads, 2)
     mx_few_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap mx,
-                  const __grid_constant__ CUtensorMap msw, const __grid_constant__ CUtensorMap msx,
                   const __grid_constant__ MxFewProduct p, uint32_t* flags) {
   using C = MxFewCfg<NT>;
   extern __shared__ uint8_t smem_raw[];
@@ -510,8 +656,6 @@ __global__ void __launch_bounds__(kMxFewThreads, 2)
     fence_mbar_init();
     tma_prefetch_desc(&mw);
     tma_prefetch_desc(&mx);
-    tma_prefetch_desc(&msw);
-    tma_prefetch_desc(&msx);
   }
   if (warp == 1) {
     tmem_alloc(tmem_holder, C::kTmemCols);
@@ -538,8 +682,9 @@ __global__ void __launch_bounds__(kMxFewThreads, 2)
         mbar_arrive_expect_tx_relaxed(&full[s], C::kStage);
         tma_load_2d(st, &mw, &full[s], kt * 128, j0);
         tma_load_2d(st + kCodes, &mx, &full[s], kt * 128, i0);
-        tma_load_2d(st + kCodes + NT * 128, &msw, &full[s], kt * 256, block);
-        tma_load_2d(st + kCodes + NT * 128 + 1024, &msx, &full[s], kt * 256, i0 / 128);
+        bulk_load(st + kCodes + NT * 128, p.wscales + (static_cast<long long>(block) * p.kt + kt) * 1024, 1024, &full[s]);
+        bulk_load(st + kCodes + NT * 128 + 1024, p.xscales + (static_cast<long long>(i0 / 128) * p.kt + kt) * 1024, 1024,
+                  &full[s]);
       }
       __syncwarp();
       if (++s == C::kStages) {
@@ -632,22 +777,34 @@ bool scale_map(CUtensorMap* map, const void* scales, int rows, int k) {
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// CTAs of a pass over a matrix: its tiles, or their quarters where those do not
+// give every SM four.
+long long tile_ctas(int rows, int k, int* quarters) {
+  const long long tiles = static_cast<long long>((rows + 127) / 128) * k_tiles(k);
+  *quarters = tiles < 152 * 4;
+  return *quarters ? 4 * tiles : tiles;
+}
+
 template <typename T>
 cudaError_t quantize_t(const MxQuantCall& c, cudaStream_t stream) {
-  const long long tiles = static_cast<long long>((c.rows + 127) / 128) * k_tiles(c.k);
-  if (tiles > INT32_MAX) return cudaErrorInvalidConfiguration;
-  const int vec = rows_aligned(c.x, c.ldx * static_cast<long long>(sizeof(T)) / 2, c.rows);
-  return launch_chained(mx_quantize_kernel<T>, dim3(static_cast<unsigned>(tiles)), 256, 0, stream, 0,
-                        static_cast<const T*>(c.x), c.ldx, c.rows, c.k, c.codes, c.scales, k_tiles(c.k), vec);
+  int quarters;
+  const long long ctas = tile_ctas(c.rows, c.k, &quarters);
+  if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
+  const bool vec = rows_aligned(c.x, c.ldx * static_cast<long long>(sizeof(T)) / 2, c.rows);
+  return launch_chained(vec ? mx_quantize_kernel<T, true> : mx_quantize_kernel<T, false>,
+                        dim3(static_cast<unsigned>(ctas)), 256, 0, stream, 0, static_cast<const T*>(c.x), c.ldx, c.rows,
+                        c.k, c.codes, c.scales, k_tiles(c.k), quarters);
 }
 
 template <typename T>
 cudaError_t dequantize_t(const MxDequantCall& c, cudaStream_t stream) {
-  const long long tiles = static_cast<long long>((c.rows + 127) / 128) * k_tiles(c.k);
-  if (tiles > INT32_MAX) return cudaErrorInvalidConfiguration;
-  const int vec = rows_aligned(c.y, c.ldy * static_cast<long long>(sizeof(T)) / 2, c.rows);
-  return launch_chained(mx_dequantize_kernel<T>, dim3(static_cast<unsigned>(tiles)), 256, 0, stream, 0, c.codes, c.scales,
-                        k_tiles(c.k), static_cast<T*>(c.y), c.ldy, c.rows, c.k, vec);
+  int quarters;
+  const long long ctas = tile_ctas(c.rows, c.k, &quarters);
+  if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
+  const bool vec = rows_aligned(c.y, c.ldy * static_cast<long long>(sizeof(T)) / 2, c.rows);
+  return launch_chained(vec ? mx_dequantize_kernel<T, true> : mx_dequantize_kernel<T, false>,
+                        dim3(static_cast<unsigned>(ctas)), 256, 0, stream, 0, c.codes, c.scales, k_tiles(c.k),
+                        quarters, static_cast<T*>(c.y), c.ldy, c.rows, c.k);
 }
 
 // CTA pairs that are resident at once (a persistent grid must not exceed
@@ -688,10 +845,8 @@ cudaError_t resident_pairs(int* out) {
 
 template <typename T, int NT>
 cudaError_t launch_mx_few(const MxLinearCall& c, const Epilogue& e, cudaStream_t stream) {
-  CUtensorMap mw, mx, msw, msx;
-  if (!code_map(&mw, c.wcodes, c.n, c.k, 128) || !code_map(&mx, c.xcodes, c.m, c.k, NT) ||
-      !scale_map(&msw, c.wscales, c.n, c.k) || !scale_map(&msx, c.xscales, c.m, c.k))
-    return cudaErrorInvalidValue;
+  CUtensorMap mw, mx;
+  if (!code_map(&mw, c.wcodes, c.n, c.k, 128) || !code_map(&mx, c.xcodes, c.m, c.k, NT)) return cudaErrorInvalidValue;
   auto kern = mx_few_kernel<T, NT>;
   static std::atomic<bool> ready[kMaxDev];
   int dev = 0;
@@ -705,11 +860,11 @@ cudaError_t launch_mx_few(const MxLinearCall& c, const Epilogue& e, cudaStream_t
     ready[dev] = true;
   }
   const int across = (c.n + 127) / 128, down = (c.m + NT - 1) / NT;
-  MxFewProduct p = {c.m, c.n, k_tiles(c.k), 1, e};
+  MxFewProduct p = {c.m, c.n, k_tiles(c.k), 1, c.wscales, c.xscales, e};
   // Two CTAs on each SM, and at least two stages of the reduction for each.
   while (p.split < (NT > 32 ? 8 : 16) && 2LL * p.split * across * down <= 304 && p.kt >= 4 * p.split) p.split *= 2;
   return launch_chained(kern, dim3(across * p.split, down, 1), kMxFewThreads, MxFewCfg<NT>::kSmem, stream, p.split, mw,
-                        mx, msw, msx, p, c.flags);
+                        mx, p, c.flags);
 }
 
 template <typename T>
@@ -717,6 +872,11 @@ cudaError_t mx_linear_t(const MxLinearCall& c, cudaStream_t stream) {
   Epilogue e = {c.bias, c.res, c.ldr, nullptr, 0, c.y, c.ldy, c.act, 0};
   e.vec = (e.bias && rows_aligned(e.bias, 0, 1) ? 1 : 0) | (e.res && rows_aligned(e.res, e.ldr, c.m) ? 2 : 0) |
           (rows_aligned(e.out, e.ldo, c.m) ? 8 : 0);
+  // Rows of the output and the residual on 32-byte boundaries.
+  const auto wide = [&](const void* p, long long ld) {
+    return (reinterpret_cast<uintptr_t>(p) & 31u) == 0 && (c.m <= 1 || (ld & 15) == 0);
+  };
+  if (wide(e.out, e.ldo) && (!e.res || wide(e.res, e.ldr))) e.vec |= 16;
   const long long squares = static_cast<long long>((c.m + 127) / 128) * ((c.n + 127) / 128);
   if (c.m <= 16) return launch_mx_few<T, 16>(c, e, stream);
   if (c.m <= 32) return launch_mx_few<T, 32>(c, e, stream);

@@ -107,6 +107,27 @@ __device__ __forceinline__ void activate_all(float (&z)[N], int act) {
   }
 }
 
+// The same of pairs of values, by packed arithmetic.
+template <int kAct, int N>
+__device__ __forceinline__ void activate_pairs(float2 (&z)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    float2 a, slope;
+    activation_and_slope2<kAct>(z[i], a, slope);
+    z[i] = a;
+  }
+}
+template <int N>
+__device__ __forceinline__ void activate_all(float2 (&z)[N], int act) {
+  switch (act) {
+    case kActRelu: activate_pairs<kActRelu>(z); break;
+    case kActGelu: activate_pairs<kActGelu>(z); break;
+    case kActGeluTanh: activate_pairs<kActGeluTanh>(z); break;
+    case kActSilu: activate_pairs<kActSilu>(z); break;
+    default: break;
+  }
+}
+
 // A warp's 32 rows x 32 columns of 16-bit elements pass through its 2 KB of
 // shared memory (row r at byte 64 r, its 16-byte piece c at piece
 // c ^ (r / 2 % 4): no bank conflicts by rows or by pieces), so that a row moves

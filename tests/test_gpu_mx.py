@@ -115,10 +115,12 @@ def test_quantize_of_held_values_keeps_them(oz):
 def test_quantize_into_memory_that_is_there(oz):
     x = rnd(40, 100, BF16, 9)
     q = oz.mx_quantize(rnd(40, 100, BF16, 10))
-    codes = q.codes
-    assert oz.mx_quantize(x, out=q) is q and q.codes is codes
+    data = q.data
+    assert oz.mx_quantize(x, out=q) is q and q.data is data
     fresh = oz.mx_quantize(x)
     assert torch.equal(q.codes, fresh.codes) and torch.equal(q.scales, fresh.scales)
+    empty = oz.mx_quantize(x, out=oz.MXMatrix.empty(40, 100))
+    assert torch.equal(empty.codes, fresh.codes) and torch.equal(empty.scales, fresh.scales)
     y = rnd(40, 100, F32, 11, pad=3)
     before = y._base.clone()
     assert oz.mx_dequantize(q, out=y) is y
