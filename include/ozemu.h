@@ -611,11 +611,12 @@ int ozemu_mx_dequantize(int rows, int k, int type, const uint8_t* codes, const u
 
 /* Y = act(X W^T + bias) + R of two such matrices, X of m x k and W of n x k:
  * ozemu_linear on the values that they stand for, the products exact and their
- * sums fp32.  type (OZEMU_BF16 or OZEMU_F16) is that of bias, R and Y; Y may be R
- * itself.  k = 0 gives X W^T = 0. */
+ * sums fp32.  With R_multiplies (not 0) Y = act(X W^T + bias) R: with R the up
+ * projection, the gated layer of 4-bit weights.  type (OZEMU_BF16 or OZEMU_F16)
+ * is that of bias, R and Y; Y may be R itself.  k = 0 gives X W^T = 0. */
 int ozemu_mx_linear(int m, int n, int k, int type, const uint8_t* x_codes, const uint8_t* x_scales,
                     const uint8_t* w_codes, const uint8_t* w_scales, const void* bias, const void* R, int ldr,
-                    int activation, void* Y, int ldy, cudaStream_t stream);
+                    int R_multiplies, int activation, void* Y, int ldy, cudaStream_t stream);
 
 /* Gradients clipped by their global norm: with N the square root of the sum of
  * all elements' squares, over all tensors,

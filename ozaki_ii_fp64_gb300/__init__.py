@@ -129,7 +129,7 @@ _SIGNATURES = {
     "ozemu_mx_scale_bytes": (_S, [_I, _I]),
     "ozemu_mx_quantize": (_I, [_I, _I, _I, _P, _I, _P, _P, _P]),
     "ozemu_mx_dequantize": (_I, [_I, _I, _I, _P, _P, _P, _I, _P]),
-    "ozemu_mx_linear": (_I, [_I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _I, _I, _P, _I, _P]),
+    "ozemu_mx_linear": (_I, [_I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _I, _I, _I, _P, _I, _P]),
     "ozemu_clip_grad_norm": (_I, [_I, _P, _P, _P, _P, _F, _F, _P, _P, _S, _P]),
     "ozemu_clip_grad_norm_bytes": (_S, [_I, _P, _P, _P]),
 }
@@ -470,9 +470,10 @@ def ozemu_mx_dequantize(rows, k, type, codes, scales, Y, ldy, stream):
     return _call("ozemu_mx_dequantize", rows, k, type, codes, scales, Y, ldy, stream)
 
 
-def ozemu_mx_linear(m, n, k, type, x_codes, x_scales, w_codes, w_scales, bias, R, ldr, activation, Y, ldy, stream):
-    return _call("ozemu_mx_linear", m, n, k, type, x_codes, x_scales, w_codes, w_scales, bias, R, ldr, activation, Y, ldy,
-                 stream)
+def ozemu_mx_linear(m, n, k, type, x_codes, x_scales, w_codes, w_scales, bias, R, ldr, R_multiplies, activation, Y, ldy,
+                    stream):
+    return _call("ozemu_mx_linear", m, n, k, type, x_codes, x_scales, w_codes, w_scales, bias, R, ldr, R_multiplies,
+                 activation, Y, ldy, stream)
 
 
 def ozemu_clip_grad_norm(count, grads, sizes, types, outs, max_norm, eps, norm, workspace, workspace_bytes, stream):
@@ -1003,21 +1004,26 @@ def mx_dequantize(q, dtype=None, out=None, stream=None):
         q.data, q.rows, q.cols, _float_type(dtype, (OZEMU_BF16, OZEMU_F16, OZEMU_F32)), out, stream)
 
 
-def mx_linear(x, w, bias=None, residual=None, activation="none", dtype=None, out=None, stream=None):
+def mx_linear(x, w, bias=None, residual=None, activation="none", dtype=None, times=None, out=None, stream=None):
     """act(x @ w.T + bias) + residual of two MXMatrix: x m x k, w n x k; bias n, residual and the result m x n of dtype,
-    bfloat16 or float16 (default: that of out, residual or bias, else bfloat16).
+    bfloat16 or float16 (default: that of out, residual, times or bias, else bfloat16).  times (m x n, instead of a
+    residual) multiplies act(x @ w.T + bias): a gated layer is mx_linear(x, gate, activation="silu",
+    times=mx_linear(x, up)).
 
-    The products of the 4-bit values are exact, their sums fp32.  out may be residual itself, and overlaps no other
-    argument (ValueError).  No graph is recorded for automatic gradients."""
+    The products of the 4-bit values are exact, their sums fp32.  out may be residual or times itself, and overlaps no
+    other argument (ValueError).  No graph is recorded for automatic gradients."""
     _mx(x, "x")
     _mx(w, "w")
     if x.cols != w.cols:
         raise ValueError("inner dimensions differ")
+    if times is not None and residual is not None:
+        raise ValueError("times: expected no residual beside it")
+    factor = times is not None
     if dtype is None:
-        like = next((t for t in (out, residual, bias) if t is not None), None)
+        like = next((t for t in (out, residual, times, bias) if t is not None), None)
         dtype = _torch().bfloat16 if like is None else like.dtype
     return (_native or _layer_calls()).mx_linear(
-        x.data, x.rows, w.data, w.rows, x.cols, bias, residual, _activation(activation),
+        x.data, x.rows, w.data, w.rows, x.cols, bias, times if factor else residual, factor, _activation(activation),
         _float_type(dtype, (OZEMU_BF16, OZEMU_F16)), out, stream)
 
 

@@ -1668,7 +1668,7 @@ int ozemu_mx_dequantize(int rows, int k, int type, const uint8_t* codes, const u
 
 int ozemu_mx_linear(int m, int n, int k, int type, const uint8_t* x_codes, const uint8_t* x_scales,
                     const uint8_t* w_codes, const uint8_t* w_scales, const void* bias, const void* R, int ldr,
-                    int activation, void* Y, int ldy, cudaStream_t stream) {
+                    int R_multiplies, int activation, void* Y, int ldy, cudaStream_t stream) {
   if (!linear_sizes(m, n, k) || !product_type(type) || !activation_ok(activation)) return OZEMU_ERR_INVALID_ARG;
   if (!mx_ok(x_codes, x_scales, m, k) || !mx_ok(w_codes, w_scales, n, k) || !vector_ok(bias, type) ||
       !matrix_ok(R, m, n, ldr, type, true) || !matrix_ok(Y, m, n, ldy, type))
@@ -1677,12 +1677,8 @@ int ozemu_mx_linear(int m, int n, int k, int type, const uint8_t* x_codes, const
   DeviceState* d = nullptr;
   const int s = device_state(&d);
   if (s != OZEMU_OK) return s;
-  if (k == 0)  // an empty reduction: the plain layer's
-    return cuda_status(launch_linear({m, n, 0, type, nullptr, 1, nullptr, 1, bias, R, ldr, activation, nullptr, n, Y,
-                                      ldy, nullptr, d->flags},
-                                     stream));
-  return cuda_status(launch_mx_linear({m, n, k, type, x_codes, x_scales, w_codes, w_scales, bias, R, ldr, activation, Y,
-                                       ldy, d->flags},
+  return cuda_status(launch_mx_linear({m, n, k, type, x_codes, x_scales, w_codes, w_scales, bias, R, ldr,
+                                       R_multiplies != 0, activation, Y, ldy, d->flags},
                                       stream));
 }
 

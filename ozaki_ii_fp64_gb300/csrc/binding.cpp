@@ -610,13 +610,15 @@ PyObject* mx_dequantize(PyObject*, PyObject* const* a, Py_ssize_t count) {
   });
 }
 
-// mx_linear(x, m, w, n, k, bias, residual, activation, type, out, stream)
+// mx_linear(x, m, w, n, k, bias, residual or factor, whether it is a factor, activation, type, out, stream)
 PyObject* mx_linear(PyObject*, PyObject* const* a, Py_ssize_t count) {
-  return guarded(count, 11, [&]() -> PyObject* {
+  return guarded(count, 12, [&]() -> PyObject* {
     const at::Tensor &dx = tensor(a[0], "x"), &dw = tensor(a[2], "w");
-    const int m = integer(a[1]), n = integer(a[3]), k = integer(a[4]), act = integer(a[7]), type = integer(a[8]);
-    const at::Tensor *bias = tensor_or_none(a[5], "bias"), *res = tensor_or_none(a[6], "residual");
-    const at::Tensor* given = tensor_or_none(a[9], "out");
+    const int m = integer(a[1]), n = integer(a[3]), k = integer(a[4]), act = integer(a[8]), type = integer(a[9]);
+    const bool times = truth(a[7]);
+    const char* name = times ? "times" : "residual";
+    const at::Tensor *bias = tensor_or_none(a[5], "bias"), *res = tensor_or_none(a[6], name);
+    const at::Tensor* given = tensor_or_none(a[10], "out");
     MxData x(m, k), w(n, k);
     x.in(dx, dx, "x");
     w.in(dw, dx, "w");
@@ -624,31 +626,31 @@ PyObject* mx_linear(PyObject*, PyObject* const* a, Py_ssize_t count) {
     // The matrices of the call's type, against one of that type.
     const at::Tensor* like = given ? given : res ? res : bias;
     if (like && (like->scalar_type() != t || like->device() != dx.device()))
-      throw Refused(std::string(given ? "out" : res ? "residual" : "bias") + ": expected " + c10::toString(t) + " on " +
+      throw Refused(std::string(given ? "out" : res ? name : "bias") + ": expected " + c10::toString(t) + " on " +
                     dx.device().str());
     Matrix mr, my;
     void* pb = nullptr;
     mr.ld = my.ld = n > 0 ? n : 1;
     if (like) {
-      mr = matrix(res, m, n, *like, "residual");
+      mr = matrix(res, m, n, *like, name);
       my = matrix(given, m, n, *like, "out");
       pb = vector(bias, n, t, *like, "bias");
       const Output o(given, my, m, n, *like);
       o.apart(bias, pb, n, "bias");
-      o.apart(res, mr, m, n, "residual", true);
+      o.apart(res, mr, m, n, name, true);
       o.apart(dx, "x");
       o.apart(dw, "w");
     }
-    OnStream on(dx, a[10], {&dx, &dw, bias, res, given});
+    OnStream on(dx, a[11], {&dx, &dw, bias, res, given});
     no_graph("mx_linear", "torch.no_grad() says that none are wanted", {bias, res});
     at::Tensor fresh;
     if (!given) {
       fresh = at::empty({m, n}, dx.options().dtype(t));
       my = matrix(&fresh, m, n, fresh, "out");
     }
-    check(ozemu_mx_linear(m, n, k, type, x.p, x.scales(), w.p, w.scales(), pb, mr.p, mr.ld, act, my.p, my.ld, on.handle),
+    check(ozemu_mx_linear(m, n, k, type, x.p, x.scales(), w.p, w.scales(), pb, mr.p, mr.ld, times, act, my.p, my.ld, on.handle),
           "ozemu_mx_linear");
-    return given ? Py_NewRef(a[9]) : THPVariable_Wrap(fresh);
+    return given ? Py_NewRef(a[10]) : THPVariable_Wrap(fresh);
   });
 }
 

@@ -186,7 +186,7 @@ size_t gated_linear_backward_workspace(const LinearGradCall& call);
 cudaError_t launch_gated_linear_backward(const LinearGradCall& call, cudaStream_t stream);
 
 // Microscaled 4-bit matrices (mx.cu); the product's rows by columns by depth is
-// m x n x k, k > 0.
+// m x n x k.  times: res multiplies instead of being added.
 size_t mx_code_bytes(int rows, int k);
 size_t mx_scale_bytes(int rows, int k);
 struct MxQuantCall {
@@ -214,6 +214,7 @@ struct MxLinearCall {
   const void* bias;
   const void* res;
   long long ldr;
+  bool times;
   int act;
   void* y;
   long long ldy;

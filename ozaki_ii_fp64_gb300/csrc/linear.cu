@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           waited = true;
         }
-        finish_rows<T>(
+        finish_rows<T, false>(
             [&](bool last, float(&z)[32]) {
               uint32_t u[32];
               tmem_ld32(tcol + c, u);
@@ -667,7 +667,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   __syncthreads();
   cluster_sync();
 
-  join_few<T, kCols>(smem, p.e, p.split, rank, j0, i0, min(NT, p.m - i0), p.n, kFewThreads);
+  join_few<T, kCols, false>(smem, p.e, p.split, rank, j0, i0, min(NT, p.m - i0), p.n, kFewThreads);
   cluster_sync();  // peers have read this CTA's sums
   if (warp == 1) {
     tc_fence_after();
@@ -900,9 +900,11 @@ __device__ __forceinline__ void store8(T* p, int left, bool vec, const float2 (&
 // dz = [dh u act'(g)  dh act(g)] of the gated layer, rounded (where dz is given;
 // rows of 2 n elements, lddz apart), and its column sums per chunk of rows as
 // slope_kernel forms them: to part ([chunk][2 n]) or db.  vec: bits 1 dh, 2 g,
-// 4 u start on 16-byte boundaries, 8 so does dz's second half.  Bound by HBM:
-// three matrices read and two written.
-template <typename T, int kAct, int TX>
+// 4 u start on 16-byte boundaries, 8 so does dz's second half; kVec: all do, and
+// the vectors of a thread's next row are on their way while it works on one.
+// Bound by HBM, three matrices read and two written: 8192 x 8192 bf16 silu 102 us,
+// 6.6 TB/s (two rows ahead: 122, three: 140, in spilled registers).
+template <typename T, int kAct, int TX, bool kVec>
 __global__ void __launch_bounds__(256, 3) gated_slope_kernel(const T* dh, long long lddh, const T* pre, long long ldpre,
                                                              T* dz, long long lddz, float* part, T* db, int m, int n,
                                                              int chunk, int vec) {
@@ -914,15 +916,8 @@ __global__ void __launch_bounds__(256, 3) gated_slope_kernel(const T* dh, long l
   const int col = blockIdx.x * kCols + tx * 8, left = n - col;
   float2 sums[2][4] = {};
   const long long end = min(static_cast<long long>(m), (blockIdx.y + 1LL) * chunk);
-  // Rows of no alignment: which memory a vector may be read from.
-  const uintptr_t dh0 = reinterpret_cast<uintptr_t>(dh), dh1 = reinterpret_cast<uintptr_t>(dh + (m - 1) * lddh + n);
-  const uintptr_t pre0 = reinterpret_cast<uintptr_t>(pre), pre1 = reinterpret_cast<uintptr_t>(pre + (m - 1) * ldpre + 2 * n);
-#pragma unroll 2
-  for (long long i = static_cast<long long>(blockIdx.y) * chunk + ty; i < end; i += TY) {
-    float2 d[4], g[4], u[4];
-    load8_anywhere(dh + i * lddh + col, left, vec & 1, dh0, dh1, d);
-    load8_anywhere(pre + i * ldpre + col, left, vec & 2, pre0, pre1, g);
-    load8_anywhere(pre + i * ldpre + n + col, left, vec & 4, pre0, pre1, u);
+  const long long first = static_cast<long long>(blockIdx.y) * chunk + ty;
+  auto row = [&](long long i, float2(&d)[4], const float2(&g)[4], float2(&u)[4]) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       float2 a, slope;
@@ -934,7 +929,37 @@ __global__ void __launch_bounds__(256, 3) gated_slope_kernel(const T* dh, long l
     }
     if (dz) {
       store8<T, TX == 32>(dz + i * lddz + col, left, true, u);  // rows start on 16-byte boundaries
-      store8<T, TX == 32>(dz + i * lddz + n + col, left, vec & 8, d);
+      store8<T, TX == 32>(dz + i * lddz + n + col, left, kVec || (vec & 8), d);
+    }
+  };
+  if (kVec && left >= 8) {  // (all of a warp's lanes, or all that have columns: n is a multiple of 8)
+    uint4 next[3];
+    auto fetch = [&](long long i) {
+      if (i >= end) return;
+      next[0] = __ldg(reinterpret_cast<const uint4*>(dh + i * lddh + col));
+      next[1] = __ldg(reinterpret_cast<const uint4*>(pre + i * ldpre + col));
+      next[2] = __ldg(reinterpret_cast<const uint4*>(pre + i * ldpre + n + col));
+    };
+    fetch(first);
+    for (long long i = first; i < end; i += TY) {
+      float2 d[4], g[4], u[4];
+      unpack16<T>(next[0], d);
+      unpack16<T>(next[1], g);
+      unpack16<T>(next[2], u);
+      fetch(i + TY);
+      row(i, d, g, u);
+    }
+  } else if (!kVec) {
+    // Which memory a vector may be read from.
+    const uintptr_t dh0 = reinterpret_cast<uintptr_t>(dh), dh1 = reinterpret_cast<uintptr_t>(dh + (m - 1) * lddh + n);
+    const uintptr_t pre0 = reinterpret_cast<uintptr_t>(pre), pre1 = reinterpret_cast<uintptr_t>(pre + (m - 1) * ldpre + 2 * n);
+#pragma unroll 2
+    for (long long i = first; i < end; i += TY) {
+      float2 d[4], g[4], u[4];
+      load8_anywhere(dh + i * lddh + col, left, vec & 1, dh0, dh1, d);
+      load8_anywhere(pre + i * ldpre + col, left, vec & 2, pre0, pre1, g);
+      load8_anywhere(pre + i * ldpre + n + col, left, vec & 4, pre0, pre1, u);
+      row(i, d, g, u);
     }
   }
   if (!part && !db) return;
@@ -1398,7 +1423,9 @@ cudaError_t run_gated_slope(const LinearGradCall& c, const GatedPlan& p, T* dz, 
   const bool whole = p.chunks == 1;
   const int tx = c.m <= kFewSlopeRows ? 4 : 32;
   const cudaError_t s = launch_chained(
-      tx == 4 ? gated_slope_kernel<T, kAct, 4> : gated_slope_kernel<T, kAct, 32>,
+      tx == 4     ? gated_slope_kernel<T, kAct, 4, false>
+      : vec == 15 ? gated_slope_kernel<T, kAct, 32, true>
+                  : gated_slope_kernel<T, kAct, 32, false>,
       dim3((c.n + 8 * tx - 1) / (8 * tx), p.chunks), 256, 0, stream, 0, static_cast<const T*>(c.dy), c.lddy,
       static_cast<const T*>(c.pre), c.ldpre, dz, pad8(2 * c.n), db && !whole ? part : nullptr, whole ? db : nullptr, c.m,
       c.n, p.chunk, vec);

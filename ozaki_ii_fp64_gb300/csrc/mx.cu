@@ -2,7 +2,7 @@
 //
 //   s = 2^max(floor(log2 max|x|) - 2, -127) over 32 consecutive columns,
 //   q = x / s rounded to e2m1 (half to even, 6 beyond),  x ~ s q
-//   y = act(x w^T + b) + r  of two such matrices
+//   y = act(x w^T + b) + r  or  act(x w^T + b) r  of two such matrices
 //
 // Every step of the quantisation is exact but the one rounding: s is a power of
 // two, so x / s is, and the conversion instruction rounds it.  The product runs
@@ -390,7 +390,10 @@ __device__ __forceinline__ void finish_direct(const uint32_t (&u)[32], const Epi
     if (e.res) {
       load32(static_cast<const T*>(e.res) + row * e.ldr + col0 + 16 * h, w);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) z[8 * h + i] = add2(z[8 * h + i], Pair<T>::unpack(w[i]));
+      for (int i = 0; i < 8; ++i) {
+        const float2 r = Pair<T>::unpack(w[i]);
+        z[8 * h + i] = e.times ? mul2(z[8 * h + i], r) : add2(z[8 * h + i], r);
+      }
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[i] = Pair<T>::pack(z[8 * h + i].x, z[8 * h + i].y);
@@ -582,7 +585,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         if (direct)
           finish_direct<T>(u, e, reinterpret_cast<const uint4*>(bias), row0 + lane, col0, p.m);
         else if (c < cols)
-          finish_rows<T>(
+          finish_rows<T, true>(
               [&](bool, float(&z)[32]) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i) z[i] = __uint_as_float(u[i]);
@@ -741,7 +744,7 @@ __global__ void __launch_bounds__(kMxFewThreads, 2)
   tc_fence_before();
   __syncthreads();
   cluster_sync();
-  join_few<T, 128>(smem, p.e, p.split, rank, j0, i0, min(NT, p.m - i0), p.n, kMxFewThreads);
+  join_few<T, 128, true>(smem, p.e, p.split, rank, j0, i0, min(NT, p.m - i0), p.n, kMxFewThreads);
   cluster_sync();  // peers have read this CTA's sums
   if (warp == 1) {
     tc_fence_after();
@@ -867,9 +870,24 @@ cudaError_t launch_mx_few(const MxLinearCall& c, const Epilogue& e, cudaStream_t
                         mx, p, c.flags);
 }
 
+// The product of an empty reduction: act(bias), and the residual or factor.
+template <typename T>
+__global__ void __launch_bounds__(256) mx_empty_kernel(int m, int n, const Epilogue e) {
+  chain_next();
+  chain_wait();
+  const long long all = static_cast<long long>(m) * n;
+  for (long long i = blockIdx.x * 256LL + threadIdx.x; i < all; i += gridDim.x * 256LL) {
+    const long long row = i / n;
+    const int col = static_cast<int>(i % n);
+    float y = activate(e.bias ? to_float(static_cast<const T*>(e.bias)[col]) : 0.f, e.act);
+    if (e.res) y = with_res<true>(y, to_float(static_cast<const T*>(e.res)[row * e.ldr + col]), e);
+    static_cast<T*>(e.out)[row * e.ldo + col] = from_float<T>(y);
+  }
+}
+
 template <typename T>
 cudaError_t mx_linear_t(const MxLinearCall& c, cudaStream_t stream) {
-  Epilogue e = {c.bias, c.res, c.ldr, nullptr, 0, c.y, c.ldy, c.act, 0};
+  Epilogue e = {c.bias, c.res, c.ldr, nullptr, 0, c.y, c.ldy, c.act, 0, c.times};
   e.vec = (e.bias && rows_aligned(e.bias, 0, 1) ? 1 : 0) | (e.res && rows_aligned(e.res, e.ldr, c.m) ? 2 : 0) |
           (rows_aligned(e.out, e.ldo, c.m) ? 8 : 0);
   // Rows of the output and the residual on 32-byte boundaries.
@@ -877,6 +895,11 @@ cudaError_t mx_linear_t(const MxLinearCall& c, cudaStream_t stream) {
     return (reinterpret_cast<uintptr_t>(p) & 31u) == 0 && (c.m <= 1 || (ld & 15) == 0);
   };
   if (wide(e.out, e.ldo) && (!e.res || wide(e.res, e.ldr))) e.vec |= 16;
+  if (c.k == 0) {
+    const long long all = static_cast<long long>(c.m) * c.n;
+    return launch_chained(mx_empty_kernel<T>, dim3(static_cast<unsigned>(std::min<long long>((all + 255) / 256, 4096))),
+                          256, 0, stream, 0, c.m, c.n, e);
+  }
   const long long squares = static_cast<long long>((c.m + 127) / 128) * ((c.n + 127) / 128);
   if (c.m <= 16) return launch_mx_few<T, 16>(c, e, stream);
   if (c.m <= 32) return launch_mx_few<T, 32>(c, e, stream);

@@ -25,6 +25,7 @@ struct Epilogue {
   long long ldo;
   int act;
   int vec;  // bits: 1 bias, 2 res, 4 pre, 8 out rows start on 16-byte boundaries; gated, 16 and 32: bias's, pre's second half
+  bool times;  // res multiplies act(z) (kTimes epilogues) instead of being added
 };
 
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_word,
@@ -280,10 +281,16 @@ __device__ __forceinline__ float4 load_cluster16(uint32_t addr) {
   return v;
 }
 
+// act(z) and the residual, or the factor, of its place.
+template <bool kTimes>
+__device__ __forceinline__ float with_res(float z, float r, const Epilogue& e) {
+  return kTimes && e.times ? z * r : z + r;
+}
+
 // One warp's 32 rows x 32 columns of accumulators, a row a lane, from
 // source(last, z) through the epilogue; the source is asked for the last time
 // with last = true.
-template <typename T, typename F>
+template <typename T, bool kTimes, typename F>
 __device__ __forceinline__ void finish_rows(F source, const uint4 (&res)[4], const Epilogue& e, uint8_t* stage,
                                             const uint4* bias, int row0, int col0, int m, int n) {
   const int lane = threadIdx.x & 31;
@@ -321,7 +328,7 @@ __device__ __forceinline__ void finish_rows(F source, const uint4 (&res)[4], con
       float r[8];
       unpack16<T>(*at, r);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) z[8 * c + i] += r[i];
+      for (int i = 0; i < 8; ++i) z[8 * c + i] = with_res<kTimes>(z[8 * c + i], r[i], e);
     }
     *at = pack16<T>(z + 8 * c);
   }
@@ -335,7 +342,7 @@ __device__ __forceinline__ void finish_rows(F source, const uint4 (&res)[4], con
 // CTA takes its share of the columns, kCols / split of them, every token, four
 // columns of a token at a time.  kCols = 64: a gated layer's, the gate in the
 // first 64 sums and up in the others.
-template <typename T, int kCols>
+template <typename T, int kCols, bool kTimes>
 __device__ __forceinline__ void join_few(const uint8_t* smem, const Epilogue& e, int split, int rank, int j0, int i0,
                                          int rows, int n, int threads) {
   const int width = kCols / 4 / split;
@@ -394,7 +401,7 @@ __device__ __forceinline__ void join_few(const uint8_t* smem, const Epilogue& e,
     if (e.res) {
       load4(static_cast<const T*>(e.res) + row * e.ldr + j, left, (e.vec & 2) != 0, v);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) z[q] += v[q];
+      for (int q = 0; q < 4; ++q) z[q] = with_res<kTimes>(z[q], v[q], e);
     }
     store4(static_cast<T*>(e.out) + row * e.ldo + j, z, left, (e.vec & 8) != 0);
   }

@@ -145,6 +145,11 @@ def test_of_nothing(oz):
     assert oz.gated_linear(rnd(1, 16, BF16, 4)[:0], rnd(8, 16, BF16, 5)).shape == (0, 4)
     dx, dw, db = oz.gated_linear_backward(rnd(1, 4, BF16, 6)[:0], rnd(1, 16, BF16, 7)[:0], rnd(8, 16, BF16, 8),
                                           rnd(1, 8, BF16, 9)[:0])
+    x, w = rnd(3, 16, BF16, 10), rnd(1, 16, BF16, 11)[:0]
+    empty = torch.empty(3, 0, dtype=BF16, device=DEV)
+    assert oz.gated_linear(x, w).shape == (3, 0)
+    gx, gw, gb = oz.gated_linear_backward(empty, x, w, empty)
+    assert gx.shape == (3, 16) and not gx.any() and gw.shape == (0, 16) and gb.shape == (0,)
     assert dx.shape == (0, 16) and not dw.any() and not db.any() and dw.shape == (8, 16) and db.shape == (8,)
 
 

@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 
 import mx_reference as ref
-from layer_reference import linear64, worst
+from layer_reference import TINY, linear64, worst
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -164,6 +164,25 @@ def test_product_activations(oz, act, m):
     product(oz, m, 200, 2300, BF16, act, bias=False, residual=True)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("m, k, n, pad", [(1, 200, 300, 0), (40, 300, 2048, 8), (500, 256, 2049, 0), (700, 300, 2304, 0),
+                                          (700, 300, 2304, 5)])
+def test_product_times_a_matrix(oz, m, k, n, pad, dtype):
+    # With the other half's product as the factor: a gated layer.
+    x, gate, up = rnd(m, k, dtype, 60, 0.5), rnd(n, k, dtype, 61, k ** -0.5), rnd(n, k, dtype, 62, k ** -0.5)
+    b = rnd(1, n, dtype, 63)[0]
+    xq, gq, uq = oz.mx_quantize(x), oz.mx_quantize(gate), oz.mx_quantize(up)
+    u = oz.mx_linear(xq, uq, dtype=dtype, out=rnd(m, n, dtype, 64, pad=pad))
+    h = oz.mx_linear(xq, gq, b, activation="silu", times=u)
+    a, tol, _, _ = linear64(oz.mx_dequantize(xq, dtype), oz.mx_dequantize(gq, dtype), b, None, "silu")
+    # tol is u |a| + (1 + u) e of the rounded a; the product has e |u|, an fp32 rounding and its own to the type.
+    want = a * u.double()
+    bound = tol * u.double().abs() + 2.0 ** -23 * want.abs() + TINY[dtype]
+    assert worst(h, want, bound) <= 1
+    assert oz.mx_linear(xq, gq, b, activation="silu", times=u, out=u) is u
+    assert torch.equal(u, h)
+
+
 def test_product_takes_every_scale_of_its_own_block(oz):
     # One element of a block is 1 and its scale a power of two that only this row and block have: an output says which
     # scales met.
@@ -199,6 +218,9 @@ def test_product_of_nothing(oz):
     y = oz.mx_linear(empty, weights, b, activation="relu")
     assert torch.equal(y, b.clamp(min=0).expand(3, 5))
     assert oz.mx_linear(oz.mx_quantize(rnd(1, 64, BF16, 2)[:0]), oz.mx_quantize(rnd(4, 64, BF16, 3))).shape == (0, 4)
+    t = rnd(3, 5, BF16, 4)
+    assert torch.equal(oz.mx_linear(empty, weights, b, times=t), (b.float() * t.float()).bfloat16())
+    assert torch.equal(oz.mx_linear(empty, weights, residual=t), t)
     assert oz.mx_dequantize(empty).shape == (3, 0)
 
 
