@@ -828,22 +828,6 @@ __global__ void __launch_bounds__(256, 4) slope_kernel(const T* dy, long long ld
   }
 }
 
-// The 16 bytes that lie `off` bytes (even, under 16) into lo and hi together.
-__device__ __forceinline__ uint4 shifted16(const uint4& lo, const uint4& hi, uint32_t off) {
-  uint32_t u[5];
-  switch (off >> 2) {
-    case 0: u[0] = lo.x, u[1] = lo.y, u[2] = lo.z, u[3] = lo.w, u[4] = hi.x; break;
-    case 1: u[0] = lo.y, u[1] = lo.z, u[2] = lo.w, u[3] = hi.x, u[4] = hi.y; break;
-    case 2: u[0] = lo.z, u[1] = lo.w, u[2] = hi.x, u[3] = hi.y, u[4] = hi.z; break;
-    default: u[0] = lo.w, u[1] = hi.x, u[2] = hi.y, u[3] = hi.z, u[4] = hi.w; break;
-  }
-  if (off & 2) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) u[i] = __funnelshift_r(u[i], u[i + 1], 16);
-  }
-  return make_uint4(u[0], u[1], u[2], u[3]);
-}
-
 // Eight consecutive elements of a matrix whose rows start anywhere, of which
 // `left` exist (0 past the end): from the two aligned vectors that they lie in,
 // where those are the matrix's own memory, begin to end.

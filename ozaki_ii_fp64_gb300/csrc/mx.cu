@@ -364,7 +364,8 @@ __device__ __forceinline__ void store32(void* p, const uint32_t (&v)[8]) {
 }
 
 // A warp's 32 rows x 32 columns of accumulators, a row a lane, where rows start
-// on 32-byte boundaries: straight from registers in 32-byte pieces.  (The MMAs
+// on 16-byte boundaries: straight from registers in pieces of 32 bytes, or of 16
+// where some row starts on no 32-byte boundary.  (The MMAs
 // and the copies that feed them take all of shared memory's bandwidth, 67 KB in
 // the 512 clocks of a stage; passing the outputs through it cost them a sixth.)
 template <typename T>
@@ -386,9 +387,15 @@ __device__ __forceinline__ void finish_direct(const uint32_t (&u)[32], const Epi
   activate_all(z, e.act);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    uint32_t w[8];
+    alignas(16) uint32_t w[8];
     if (e.res) {
-      load32(static_cast<const T*>(e.res) + row * e.ldr + col0 + 16 * h, w);
+      const T* p = static_cast<const T*>(e.res) + row * e.ldr + col0 + 16 * h;
+      if (e.vec & 16) {
+        load32(p, w);
+      } else {
+        *reinterpret_cast<uint4*>(w) = reinterpret_cast<const uint4*>(p)[0];
+        *reinterpret_cast<uint4*>(w + 4) = reinterpret_cast<const uint4*>(p)[1];
+      }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float2 r = Pair<T>::unpack(w[i]);
@@ -397,7 +404,13 @@ __device__ __forceinline__ void finish_direct(const uint32_t (&u)[32], const Epi
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[i] = Pair<T>::pack(z[8 * h + i].x, z[8 * h + i].y);
-    store32(static_cast<T*>(e.out) + row * e.ldo + col0 + 16 * h, w);
+    T* to = static_cast<T*>(e.out) + row * e.ldo + col0 + 16 * h;
+    if (e.vec & 16) {
+      store32(to, w);
+    } else {
+      reinterpret_cast<uint4*>(to)[0] = *reinterpret_cast<const uint4*>(w);
+      reinterpret_cast<uint4*>(to)[1] = *reinterpret_cast<const uint4*>(w + 4);
+    }
   }
 }
 
@@ -537,6 +550,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     const int ew = warp - 2, quarter = warp & 3, group = ew >> 2;
     uint8_t *stage = staging + ew * 2048, *bias = biases + ew * 64;
     const Epilogue& e = p.e;
+    const bool rows16 = (e.vec & 8) && (!e.res || (e.vec & 2));
     int n_tiles = 0;
     bool live = true;
     for (int t = pair; t < total && live; t += npairs, ++n_tiles) {
@@ -554,7 +568,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
       for (int h = 0; h < p.bn; h += 128) {
         const int c = (first ^ h) + group * 32;
         const int col0 = tn * p.bn + c;
-        const bool direct = (e.vec & 16) != 0 && c + 32 <= cols;
+        const bool direct = rows16 && c + 32 <= cols;
         uint4 res[4];
         if (c < cols) {
           if (e.res && !direct)

@@ -129,13 +129,30 @@ __device__ __forceinline__ void activate_all(float2 (&z)[N], int act) {
   }
 }
 
+// The 16 bytes that lie `off` bytes (even, under 16) into lo and hi together;
+// without a branch, for lanes whose off differ.
+__device__ __forceinline__ uint4 shifted16(const uint4& lo, const uint4& hi, uint32_t off) {
+  uint32_t w[7] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z};
+  const bool two = (off & 8) != 0, one = (off & 4) != 0;
+  const uint32_t past = two ? hi.w : hi.z;
+#pragma unroll
+  for (int i = 0; i < 5; ++i) w[i] = two ? w[i + 2] : w[i];
+  w[5] = two ? past : w[5];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) w[i] = one ? w[i + 1] : w[i];
+  const uint32_t bits = (off & 2) * 8;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], bits);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // A warp's 32 rows x 32 columns of 16-bit elements pass through its 2 KB of
 // shared memory (row r at byte 64 r, its 16-byte piece c at piece
 // c ^ (r / 2 % 4): no bank conflicts by rows or by pieces), so that a row moves
 // as one 64-byte run.  A lane's share on the way: piece lane % 4 of rows
-// 8 i + lane / 4; or, where rows do not start on 16-byte boundaries, word
-// lane % 16 of rows 2 i + lane / 16, between words where the row starts on an
-// odd element.
+// 8 i + lane / 4, in global memory between two aligned pieces where rows do not
+// start on 16-byte boundaries; or, of columns that the matrix ends within, word
+// lane % 16 of rows 2 i + lane / 16, element by element.
 __device__ __forceinline__ uint4* stage_piece(uint8_t* stage, int r, int c) {
   return reinterpret_cast<uint4*>(stage + r * 64) + (c ^ (r >> 1 & 3));
 }
@@ -147,48 +164,48 @@ template <typename T>
 __device__ __forceinline__ void read_rows(uint4 (&v)[4], const T* in, long long ld, int row0, int col0, int m, int n,
                                           bool vec) {
   const int lane = threadIdx.x & 31;
-  if (vec && col0 + 32 <= n) {
+  if (col0 + 32 <= n) {
+    // The memory that a vector may be read from: the matrix's.
+    const uintptr_t begin = reinterpret_cast<uintptr_t>(in), end = reinterpret_cast<uintptr_t>(in + (m - 1LL) * ld + n);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = row0 + 8 * i + (lane >> 2);
-      v[i] = r < m ? *reinterpret_cast<const uint4*>(in + r * ld + col0 + 8 * (lane & 3)) : make_uint4(0, 0, 0, 0);
+      const T* p = in + r * ld + col0 + 8 * (lane & 3);
+      v[i] = make_uint4(0, 0, 0, 0);
+      if (r >= m) continue;
+      if (vec) {
+        v[i] = *reinterpret_cast<const uint4*>(p);
+        continue;
+      }
+      const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 15u);
+      const uintptr_t from = reinterpret_cast<uintptr_t>(p) - off;
+      if (from >= begin && from + 32 <= end) {
+        v[i] = shifted16(*reinterpret_cast<const uint4*>(from), *reinterpret_cast<const uint4*>(from + 16), off);
+      } else {
+        uint32_t* w = reinterpret_cast<uint32_t*>(&v[i]);
+        const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[k] = q[2 * k] | (static_cast<uint32_t>(q[2 * k + 1]) << 16);
+      }
     }
     return;
   }
   uint32_t* w = reinterpret_cast<uint32_t*>(v);
   const uint16_t* p = reinterpret_cast<const uint16_t*>(in) + row0 * ld + col0;
   const int word = lane & 15;
-  if (col0 > 0 && col0 + 32 <= n) {  // the element before the run is the row's, too
-    // All loads first: the words, and for row `lane` the last element, which a
-    // row that starts on an odd element has in a 17th word.
-    const uint32_t last = row0 + lane < m ? p[lane * ld + 31] : 0;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int r = 2 * i + (lane >> 4);
-      const uintptr_t q = reinterpret_cast<uintptr_t>(p + r * ld) & ~uintptr_t(3);
-      w[i] = row0 + r < m ? *(reinterpret_cast<const uint32_t*>(q) + word) : 0;
-    }
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int r = 2 * i + (lane >> 4);
-      const uint32_t next = __shfl_down_sync(0xFFFFFFFFu, w[i], 1), tail = __shfl_sync(0xFFFFFFFFu, last, r);
-      if (reinterpret_cast<uintptr_t>(p + r * ld) & 2u) w[i] = __funnelshift_r(w[i], word == 15 ? tail : next, 16);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int r = 2 * i + (lane >> 4);
-      const uint16_t* q = p + r * ld + 2 * word;
-      const uint32_t a = row0 + r < m && col0 + 2 * word < n ? q[0] : 0;
-      const uint32_t b = row0 + r < m && col0 + 2 * word + 1 < n ? q[1] : 0;
-      w[i] = a | (b << 16);
-    }
+  for (int i = 0; i < 16; ++i) {
+    const int r = 2 * i + (lane >> 4);
+    const uint16_t* q = p + r * ld + 2 * word;
+    const uint32_t a = row0 + r < m && col0 + 2 * word < n ? q[0] : 0;
+    const uint32_t b = row0 + r < m && col0 + 2 * word + 1 < n ? q[1] : 0;
+    w[i] = a | (b << 16);
   }
 }
 
-__device__ __forceinline__ void stage_rows(const uint4 (&v)[4], uint8_t* stage, int col0, int n, bool vec) {
+__device__ __forceinline__ void stage_rows(const uint4 (&v)[4], uint8_t* stage, int col0, int n) {
   const int lane = threadIdx.x & 31;
-  if (vec && col0 + 32 <= n) {
+  if (col0 + 32 <= n) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) *stage_piece(stage, 8 * i + (lane >> 2), lane & 3) = v[i];
   } else {
@@ -212,30 +229,39 @@ __device__ __forceinline__ void write_rows(uint8_t* stage, T* out, long long ldo
     return;
   }
   uint16_t* p = reinterpret_cast<uint16_t*>(out) + row0 * ldo + col0;
-  const bool whole = col0 + 32 <= n;
-  const int word = lane & 15;
-#pragma unroll 1
-  for (int i0 = 0; i0 < 16; i0 += 4) {
-    uint32_t a[4], b[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) a[i] = *stage_word(stage, 2 * (i0 + i) + (lane >> 4), word);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) b[i] = __shfl_down_sync(0xFFFFFFFFu, a[i], 1);
-#pragma unroll
+  if (col0 + 32 <= n) {
+    // The whole 16-byte pieces of a row's run, `to` bytes in: three, or four of a
+    // row that starts on a boundary.  (By words, two rows at a time: 1000 x 2048 ->
+    // 4099 in 4 bits 13.2 us, so 11.9.)
+    const int slot = lane & 3;
+#pragma unroll 2
     for (int i = 0; i < 4; ++i) {
-      const int r = 2 * (i0 + i) + (lane >> 4);
+      const int r = 8 * i + (lane >> 2);
       uint16_t* q = p + r * ldo;
-      const bool odd = (reinterpret_cast<uintptr_t>(q) & 2u) != 0, in_m = row0 + r < m;
-      if (whole) {  // from an odd start: words of elements 2 word + 1 and 2 word + 2, and the two ends
-        const uint32_t both = odd ? __funnelshift_r(a[i], b[i], 16) : a[i];
-        if (in_m && !(odd && word == 15)) *reinterpret_cast<uint32_t*>(q + 2 * word + (odd ? 1 : 0)) = both;
-        if (in_m && odd && word == 15) q[31] = static_cast<uint16_t>(a[i] >> 16);
-        if (in_m && odd && word == 0) q[0] = static_cast<uint16_t>(a[i]);
-      } else {
-        if (in_m && col0 + 2 * word < n) q[2 * word] = static_cast<uint16_t>(a[i]);
-        if (in_m && col0 + 2 * word + 1 < n) q[2 * word + 1] = static_cast<uint16_t>(a[i] >> 16);
-      }
+      const uint32_t to = (0u - static_cast<uint32_t>(reinterpret_cast<uintptr_t>(q))) & 15u;
+      const uint4 v = shifted16(*stage_piece(stage, r, slot), *stage_piece(stage, r, (slot + 1) & 3), to);
+      if (row0 + r < m && (to == 0 || slot < 3)) *reinterpret_cast<uint4*>(q + to / 2 + 8 * slot) = v;
     }
+    // And the eight elements before and after them, eight lanes a row.
+#pragma unroll 4
+    for (int i = 0; i < 8; ++i) {
+      const int r = 4 * i + (lane >> 3), k = lane & 7;
+      uint16_t* q = p + r * ldo;
+      const int head = static_cast<int>(((0u - static_cast<uint32_t>(reinterpret_cast<uintptr_t>(q))) & 15u) / 2);
+      const int at = k < head ? k : 24 + k;
+      if (row0 + r < m && head != 0) q[at] = reinterpret_cast<const uint16_t*>(stage_piece(stage, r, at >> 3))[at & 7];
+    }
+    return;
+  }
+  const int word = lane & 15;
+#pragma unroll 4
+  for (int i = 0; i < 16; ++i) {
+    const int r = 2 * i + (lane >> 4);
+    const uint32_t a = *stage_word(stage, r, word);
+    uint16_t* q = p + r * ldo;
+    const bool in_m = row0 + r < m;
+    if (in_m && col0 + 2 * word < n) q[2 * word] = static_cast<uint16_t>(a);
+    if (in_m && col0 + 2 * word + 1 < n) q[2 * word + 1] = static_cast<uint16_t>(a >> 16);
   }
 }
 
@@ -316,7 +342,7 @@ __device__ __forceinline__ void finish_rows(F source, const uint4 (&res)[4], con
     __syncwarp();
   }
   if (e.res) {
-    stage_rows(res, stage, col0, n, (e.vec & 2) != 0);
+    stage_rows(res, stage, col0, n);
     __syncwarp();
   }
   take(true);
