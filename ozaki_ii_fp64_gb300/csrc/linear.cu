@@ -109,15 +109,17 @@ __device__ __forceinline__ uint32_t part_piece(int r, int c) {
   return static_cast<uint32_t>(r * 1024 + ((c ^ (r & 31)) << 4));
 }
 
-// The same for a gated tile: z the gate's accumulators, u the up projection's.
-template <typename T>
-__device__ __forceinline__ void finish_gated(float2 (&z)[16], float2 (&u)[16], const Epilogue& e, uint8_t* stage,
-                                             uint8_t* bias, int row0, int col0, int m, int n) {
+// The same for a gated tile, from source(half, v): the gate's accumulators, half
+// 0, and the up projection's.  One half's 32 values live at a time but for the
+// product, so that writing rows has registers left.
+template <typename T, typename F>
+__device__ __forceinline__ void finish_gated(F source, const Epilogue& e, uint8_t* stage, uint8_t* bias, int row0, int col0,
+                                             int m, int n) {
   const int lane = threadIdx.x & 31;
-  // One half's bias and rounded pre-activation.
-  auto half = [&](float2 (&v)[16], int at) {
+  auto take = [&](float2 (&v)[16], int half) {
+    source(half, v);
     if (e.bias) {  // the chunk's 32 values, for every lane
-      const uint16_t b = col0 + lane < n ? static_cast<const uint16_t*>(e.bias)[at + col0 + lane] : 0;
+      const uint16_t b = col0 + lane < n ? static_cast<const uint16_t*>(e.bias)[half * n + col0 + lane] : 0;
       __syncwarp();
       reinterpret_cast<uint16_t*>(bias)[lane] = b;
       __syncwarp();
@@ -129,24 +131,33 @@ __device__ __forceinline__ void finish_gated(float2 (&z)[16], float2 (&u)[16], c
         for (int i = 0; i < 4; ++i) v[4 * q + i] = add2(v[4 * q + i], f[i]);
       }
     }
-    if (e.pre) {
-#pragma unroll
-      for (int c = 0; c < 4; ++c) *stage_piece(stage, lane, c) = pack16<T>(v + 4 * c);
-      __syncwarp();
-      write_rows(stage, static_cast<T*>(e.pre) + at, e.ldpre, row0, col0, m, n, (e.vec & (at ? 32 : 4)) != 0);
-      __syncwarp();
-    }
   };
-  half(z, 0);
-  half(u, n);
+  auto put = [&](const float2 (&v)[16]) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) *stage_piece(stage, lane, c) = pack16<T>(v + 4 * c);
+    __syncwarp();
+  };
+  auto write = [&](void* to, long long ld, int at, int aligned) {
+    write_rows(stage, static_cast<T*>(to) + at, ld, row0, col0, m, n, (e.vec & aligned) != 0);
+    __syncwarp();
+  };
+  float2 z[16];
+  take(z, 0);
+  if (e.pre) {
+    put(z);
+    write(e.pre, e.ldpre, 0, 4);
+  }
   activate_all(z, e.act);
+  {
+    float2 u[16];
+    take(u, 1);
+    if (e.pre) put(u);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) z[i] = mul2(z[i], u[i]);
-#pragma unroll
-  for (int c = 0; c < 4; ++c) *stage_piece(stage, lane, c) = pack16<T>(z + 4 * c);
-  __syncwarp();
-  write_rows(stage, static_cast<T*>(e.out), e.ldo, row0, col0, m, n, (e.vec & 8) != 0);
-  __syncwarp();
+    for (int i = 0; i < 16; ++i) z[i] = mul2(z[i], u[i]);
+  }
+  if (e.pre) write(e.pre, e.ldpre, n, 32);
+  put(z);
+  write(e.out, e.ldo, 0, 8);
 }
 
 // kGated: B holds the rows of two layers, gate (n of them) and up (n more), and
@@ -360,20 +371,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           live = warp_wait(&tfull[buf], use & 1, abort_word, flags);  // c < 128: a warp's only chunk
           if (!live) break;
           tc_fence_after();
-          uint32_t a[32], b[32];
-          tmem_ld32(tcol + c, a);
-          tmem_ld32(tcol + width + c, b);
-          tmem_wait_ld();
-          float2 z[16], u[16];
+          finish_gated<T>(
+              [&](int half, float2(&v)[16]) {
+                uint32_t a[32];
+                tmem_ld32(tcol + (half ? width : 0) + c, a);
+                tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            z[i] = make_float2(__uint_as_float(a[2 * i]), __uint_as_float(a[2 * i + 1]));
-            u[i] = make_float2(__uint_as_float(b[2 * i]), __uint_as_float(b[2 * i + 1]));
-          }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(&tempty[buf], lead));
-          finish_gated<T>(z, u, e, stage, bias, row0, col0, p.m, p.n);
+                for (int i = 0; i < 16; ++i) v[i] = make_float2(__uint_as_float(a[2 * i]), __uint_as_float(a[2 * i + 1]));
+                if (half) {
+                  tc_fence_before();
+                  __syncwarp();
+                  if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(&tempty[buf], lead));
+                }
+              },
+              e, stage, bias, row0, col0, p.m, p.n);
           continue;
         }
         uint4 res[4];

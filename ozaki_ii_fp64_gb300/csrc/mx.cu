@@ -586,25 +586,33 @@ __global__ void __launch_bounds__(kMxThreads, 1)
           tc_fence_after();
           waited = true;
         }
-        uint32_t u[32];
-        if (c < cols) {
-          tmem_ld32(tcol + c, u);
-          tmem_wait_ld();
-        }
-        if (h == 0) {  // (BN = 128: the whole tile)
+        // The warp's sums of this half are in registers: of the first half (of BN =
+        // 128 the whole tile) the MMAs wait for that.
+        auto release = [&] {
+          if (h != 0) return;
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(&taken[buf], 0));
-        }
-        if (direct)
+        };
+        uint32_t u[32];
+        if (direct) {
+          tmem_ld32(tcol + c, u);
+          tmem_wait_ld();
+          release();
           finish_direct<T>(u, e, reinterpret_cast<const uint4*>(bias), row0 + lane, col0, p.m);
-        else if (c < cols)
+        } else if (c < cols) {
           finish_rows<T, true>(
               [&](bool, float(&z)[32]) {
+                tmem_ld32(tcol + c, u);
+                tmem_wait_ld();
+                release();
 #pragma unroll
                 for (int i = 0; i < 32; ++i) z[i] = __uint_as_float(u[i]);
               },
               res, e, stage, reinterpret_cast<const uint4*>(bias), row0, col0, p.m, p.n);
+        } else {
+          release();
+        }
       }
     }
   }
