@@ -109,12 +109,18 @@ __device__ __forceinline__ uint32_t part_piece(int r, int c) {
   return static_cast<uint32_t>(r * 1024 + ((c ^ (r & 31)) << 4));
 }
 
+// Whether a gated tile has an output whose rows have no alignment.
+__device__ __forceinline__ bool gated_together(const Epilogue& e) {
+  return (e.vec & 8) == 0 || (e.pre && (e.vec & 36) != 36);
+}
+
 // The same for a gated tile, from source(half, v): the gate's accumulators, half
 // 0, and the up projection's.  One half's 32 values live at a time but for the
-// product, so that writing rows has registers left.
+// product, so that writing rows has registers left.  `some`: whether this warp's
+// columns exist (a quarter's warps come together); the tile's end at `end`.
 template <typename T, typename F>
-__device__ __forceinline__ void finish_gated(F source, const Epilogue& e, uint8_t* stage, uint8_t* bias, int row0, int col0,
-                                             int m, int n) {
+__device__ __forceinline__ void finish_gated(F source, bool some, const Epilogue& e, uint8_t* stage, uint8_t* bias,
+                                             const Quarter& quarter, int row0, int col0, int m, int n, int end) {
   const int lane = threadIdx.x & 31;
   auto take = [&](float2 (&v)[16], int half) {
     source(half, v);
@@ -133,13 +139,20 @@ __device__ __forceinline__ void finish_gated(F source, const Epilogue& e, uint8_
     }
   };
   auto put = [&](const float2 (&v)[16]) {
+    if (!some) return;
 #pragma unroll
     for (int c = 0; c < 4; ++c) *stage_piece(stage, lane, c) = pack16<T>(v + 4 * c);
-    __syncwarp();
   };
   auto write = [&](void* to, long long ld, int at, int aligned) {
-    write_rows(stage, static_cast<T*>(to) + at, ld, row0, col0, m, n, (e.vec & aligned) != 0);
-    __syncwarp();
+    if (e.vec & aligned) {
+      __syncwarp();
+      if (some) write_rows(stage, static_cast<T*>(to) + at, ld, row0, col0, m, n, true);
+      __syncwarp();
+    } else {
+      quarter_sync(quarter);
+      write_together(quarter, static_cast<T*>(to) + at, ld, row0, col0 - 32 * quarter.group, m, end);
+      quarter_sync(quarter);
+    }
   };
   float2 z[16];
   take(z, 0);
@@ -364,29 +377,37 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;  // one tile
       }
       bool waited = false, live = true;
-#pragma unroll 1
-      for (int c = group * 32; c < cols; c += 128) {
-        const int col0 = tn * width + c;
-        if constexpr (kGated) {
-          live = warp_wait(&tfull[buf], use & 1, abort_word, flags);  // c < 128: a warp's only chunk
-          if (!live) break;
-          tc_fence_after();
+      if constexpr (kGated) {  // 128 columns or fewer: a chunk a warp
+        const int c = group * 32;
+        const bool some = c < cols, together = gated_together(e);
+        const Quarter q = {staging + (ew & 3) * 2048, quarter, group};
+        live = warp_wait(&tfull[buf], use & 1, abort_word, flags);
+        if (together) live = quarter_all(q, live);
+        if (!live) break;
+        tc_fence_after();
+        auto release = [&] {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(&tempty[buf], lead));
+        };
+        if (some || (together && cols > 0))
           finish_gated<T>(
               [&](int half, float2(&v)[16]) {
                 uint32_t a[32];
-                tmem_ld32(tcol + (half ? width : 0) + c, a);
+                tmem_ld32(tcol + (half ? width : 0) + (some ? c : 0), a);
                 tmem_wait_ld();
 #pragma unroll
                 for (int i = 0; i < 16; ++i) v[i] = make_float2(__uint_as_float(a[2 * i]), __uint_as_float(a[2 * i + 1]));
-                if (half) {
-                  tc_fence_before();
-                  __syncwarp();
-                  if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(&tempty[buf], lead));
-                }
+                if (half) release();
               },
-              e, stage, bias, row0, col0, p.m, p.n);
-          continue;
-        }
+              some, e, stage, bias, q, row0, tn * width + c, p.m, p.n, min(p.n, (tn + 1) * width));
+        else
+          release();
+        continue;
+      }
+#pragma unroll 1
+      for (int c = group * 32; c < cols; c += 128) {
+        const int col0 = tn * width + c;
         uint4 res[4];
         if (e.res)
           read_rows(res, static_cast<const T*>(e.res), e.ldr, row0, col0, p.m, p.n, (e.vec & 2) != 0);

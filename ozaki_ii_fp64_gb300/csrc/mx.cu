@@ -414,6 +414,48 @@ __device__ __forceinline__ void finish_direct(const uint32_t (&u)[32], const Epi
   }
 }
 
+// The same where the output's rows start on no 16-byte boundaries, from source(z),
+// by a quarter's warps together (`some`: whether this one's columns exist).
+template <typename T, typename F>
+__device__ __forceinline__ void finish_together(F source, bool some, const uint4 (&res)[4], const Epilogue& e,
+                                                uint8_t* stage, const uint4* bias, const Quarter& q, int row0, int col0,
+                                                int m, int n) {
+  const int lane = threadIdx.x & 31;
+  if (some && e.res) {
+    stage_rows(res, stage, col0, n);
+    __syncwarp();
+  }
+  float2 z[16];
+  source(z);
+  if (some) {
+    if (e.bias) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float2 b[4];
+        unpack16<T>(bias[k], b);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) z[4 * k + i] = add2(z[4 * k + i], b[i]);
+      }
+    }
+    activate_all(z, e.act);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      uint4* at = stage_piece(stage, lane, c);
+      if (e.res) {
+        float2 r[4];
+        unpack16<T>(*at, r);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          z[4 * c + i] = e.times ? mul2(z[4 * c + i], r[i]) : add2(z[4 * c + i], r[i]);
+      }
+      *at = pack16<T>(z + 4 * c);
+    }
+  }
+  quarter_sync(q);
+  write_together(q, static_cast<T*>(e.out), e.ldo, row0, col0 - 32 * q.group, m, n);
+  quarter_sync(q);
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kMxThreads, 1)
     mx_pair_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
@@ -550,7 +592,8 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     const int ew = warp - 2, quarter = warp & 3, group = ew >> 2;
     uint8_t *stage = staging + ew * 2048, *bias = biases + ew * 64;
     const Epilogue& e = p.e;
-    const bool rows16 = (e.vec & 8) && (!e.res || (e.vec & 2));
+    const bool rows16 = (e.vec & 8) && (!e.res || (e.vec & 2)), together = (e.vec & 8) == 0;
+    const Quarter q = {staging + (ew & 3) * 2048, quarter, group};
     int n_tiles = 0;
     bool live = true;
     for (int t = pair; t < total && live; t += npairs, ++n_tiles) {
@@ -582,6 +625,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         }
         if (!waited) {
           live = warp_wait(&tfull[buf], use & 1, abort_word, flags);
+          if (together) live = quarter_all(q, live);
           if (!live) break;
           tc_fence_after();
           waited = true;
@@ -600,6 +644,16 @@ __global__ void __launch_bounds__(kMxThreads, 1)
           tmem_wait_ld();
           release();
           finish_direct<T>(u, e, reinterpret_cast<const uint4*>(bias), row0 + lane, col0, p.m);
+        } else if (together && (first ^ h) < cols) {
+          finish_together<T>(
+              [&](float2(&z)[16]) {
+                tmem_ld32(tcol + c, u);
+                tmem_wait_ld();
+                release();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) z[i] = make_float2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
+              },
+              c < cols, res, e, stage, reinterpret_cast<const uint4*>(bias), q, row0, col0, p.m, p.n);
         } else if (c < cols) {
           finish_rows<T, true>(
               [&](bool, float(&z)[32]) {

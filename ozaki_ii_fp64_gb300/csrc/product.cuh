@@ -234,7 +234,6 @@ __device__ __forceinline__ void write_rows(uint8_t* stage, T* out, long long ldo
     // row that starts on a boundary.  Bound by instructions, so their addresses are
     // stepped: the places of a lane's rows, eight or four apart, differ by a
     // constant (the pieces' order comes from bits 1 and 2 of the row).
-    // (8192 x 192 -> 9449 gated, pre-activations kept: 294 us without, X.X.)
     const int rows = m - row0, l4 = lane >> 2, slot = lane & 3;
     uint16_t* q = p + l4 * ldo;
     const uint4 *a = stage_piece(stage, l4, slot), *b = stage_piece(stage, l4, (slot + 1) & 3);
@@ -267,6 +266,58 @@ __device__ __forceinline__ void write_rows(uint8_t* stage, T* out, long long ldo
     const bool in_m = row0 + r < m;
     if (in_m && col0 + 2 * word < n) q[2 * word] = static_cast<uint16_t>(a);
     if (in_m && col0 + 2 * word + 1 < n) q[2 * word + 1] = static_cast<uint16_t>(a >> 16);
+  }
+}
+
+// The four warps that hold the same 32 rows of a tile (a lane quarter of TMEM),
+// 128 columns together.  Where rows start on no 16-byte boundaries they write
+// them as one, in runs of 256 bytes: a run's first and last sector go out in part,
+// and a part of a sector takes the way to L2 that a whole one takes.  (8192 x 192
+// -> 9449 gated, the pre-activations kept, by runs of 64 bytes: 884 MB on that way
+// for 464 written.  15075 rows of it: 578 us, 380 by these.)
+struct Quarter {
+  uint8_t* staging;  // of its first warp; the next one's is kQuarterStride on
+  int id, group;     // quarter, and which of its warps
+};
+constexpr int kQuarterStride = 4 * 2048;
+__device__ __forceinline__ void quarter_sync(const Quarter& q) {
+  asm volatile("bar.sync %0, 128;" ::"r"(q.id + 1) : "memory");
+}
+// Whether all four say so: they give up a wait together or not at all, since
+// each would be missing from the others' barriers.
+__device__ __forceinline__ bool quarter_all(const Quarter& q, bool ok) {
+  uint32_t all;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 q, %1, 0;\n bar.red.and.pred p, %2, 128, q;\n selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(all)
+      : "r"(ok ? 1u : 0u), "r"(q.id + 1)
+      : "memory");
+  return all != 0;
+}
+
+// Rows row0 .. row0 + 31 of the quarter's columns from col0 on, up to 128 and
+// below `end`, staged by its warps, to memory of any alignment: eight rows a warp,
+// half a warp a row.
+template <typename T>
+__device__ __forceinline__ void write_together(const Quarter& q, T* out, long long ldo, int row0, int col0, int m, int end) {
+  const int lane = threadIdx.x & 31, slot = lane & 15, cols = min(128, end - col0);
+  const int first = q.group * 8 + (lane >> 4), rows = m - row0 - first, next = min(slot + 1, 15);
+  uint16_t* p = reinterpret_cast<uint16_t*>(out) + (row0 + first) * ldo + col0;
+  const uint8_t* at0 = q.staging + first * 64;  // rows go by two, whose pieces' order is i
+  const uint8_t *a = at0 + (slot >> 2) * kQuarterStride, *b = at0 + (next >> 2) * kQuarterStride;
+#pragma unroll
+  for (int i = 0; i < 4; ++i, p += 2 * ldo) {
+    // Elements to the first boundary, whole pieces after it, and the rest.
+    const int head = static_cast<int>(((0u - static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p))) & 15u) / 2);
+    const int whole = max(cols - head, 0) / 8;
+    const uint4 v = shifted16(*reinterpret_cast<const uint4*>(a + 128 * i + 16 * ((slot & 3) ^ i)),
+                              *reinterpret_cast<const uint4*>(b + 128 * i + 16 * ((next & 3) ^ i)), 2 * head);
+    if (2 * i < rows && slot < whole) *reinterpret_cast<uint4*>(p + head + 8 * slot) = v;
+    const int at = slot < 8 ? slot : head + 8 * whole + slot - 8, stop = slot < 8 ? min(head, cols) : cols;
+    const int piece = (at >> 3) & 15;
+    const uint16_t one = *reinterpret_cast<const uint16_t*>(at0 + (piece >> 2) * kQuarterStride + 128 * i +
+                                                            16 * ((piece & 3) ^ i) + 2 * (at & 7));
+    if (2 * i < rows && at < stop) p[at] = one;
   }
 }
 

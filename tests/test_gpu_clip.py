@@ -93,7 +93,7 @@ def test_dense_tensors_of_any_order(oz):
     check(oz, [rnd((30, 70), BF16, 1).t(), rnd((4, 5, 6), F32, 2).permute(2, 0, 1)], 1.0)
 
 
-@pytest.mark.parametrize("count", [48, 49, 960, 961, 2500])
+@pytest.mark.parametrize("count", [63, 64, 65, 256, 257, 960, 961, 2500])
 def test_long_lists(oz, count):
     base = rnd((count * 8 + 100,), F32, 3)
     grads = [base[8 * i:8 * i + 1 + i % 7] for i in range(count)]
