@@ -860,27 +860,29 @@ __global__ void __launch_bounds__(256, 4) slope_kernel(const T* dy, long long ld
   }
 }
 
-// Eight consecutive elements of a matrix whose rows start anywhere, of which
-// `left` exist (0 past the end): from the two aligned vectors that they lie in,
-// where those are the matrix's own memory, begin to end.
-template <typename T>
-__device__ __forceinline__ void load8_anywhere(const T* p, int left, bool vec, uintptr_t begin, uintptr_t end,
-                                               float2 (&v)[4]) {
-  const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 15u);
-  const uintptr_t from = reinterpret_cast<uintptr_t>(p) - off;
-  if (!vec && left >= 8 && from >= begin && from + 32 <= end) {
-    const uint4* at = reinterpret_cast<const uint4*>(from);
-    unpack16<T>(shifted16(__ldg(at), __ldg(at + 1), off), v);
-  } else {
-    load8(p, left, vec, v);
+// The aligned 16 bytes at `from`, of a matrix that lies from begin to end: what is
+// not its memory is not read.
+__device__ __forceinline__ uint4 load_aligned(uintptr_t from, uintptr_t begin, uintptr_t end) {
+  if (from >= begin && from + 16 <= end) return __ldg(reinterpret_cast<const uint4*>(from));
+  uint4 v = make_uint4(0, 0, 0, 0);
+  uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uintptr_t at = from + 2 * i;
+    if (at >= begin && at < end) w[i / 2] |= static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(at)) << (16 * (i & 1));
   }
+  return v;
+}
+__device__ __forceinline__ uint4 from_next_lane(const uint4& v) {
+  return make_uint4(__shfl_down_sync(0xFFFFFFFFu, v.x, 1), __shfl_down_sync(0xFFFFFFFFu, v.y, 1),
+                    __shfl_down_sync(0xFFFFFFFFu, v.z, 1), __shfl_down_sync(0xFFFFFFFFu, v.w, 1));
 }
 
-// Stores eight consecutive elements of which `left` exist.  A warp whose lanes'
-// elements follow each other (kRow) stores vectors from the first boundary on,
-// made of a lane's elements and the next one's, where p is on none; all of its
+// Stores eight consecutive elements of which `left` exist.  A warp whose first
+// kRow lanes' elements follow each other stores vectors from the first boundary
+// on, made of a lane's elements and the next one's, where p is on none; all of its
 // lanes call this.
-template <typename T, bool kRow>
+template <typename T, int kRow>
 __device__ __forceinline__ void store8(T* p, int left, bool vec, const float2 (&v)[4]) {
   const uint4 mine = pack16<T>(v);
   if (vec) {
@@ -888,16 +890,12 @@ __device__ __forceinline__ void store8(T* p, int left, bool vec, const float2 (&
       *reinterpret_cast<uint4*>(p) = mine;
       return;
     }
-  } else if constexpr (kRow) {
+  } else if constexpr (kRow > 0) {
     const int lane = threadIdx.x & 31;
     const uint32_t off = 16 - static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 15u);  // to the boundary
-    uint4 next;
-    next.x = __shfl_down_sync(0xFFFFFFFFu, mine.x, 1);
-    next.y = __shfl_down_sync(0xFFFFFFFFu, mine.y, 1);
-    next.z = __shfl_down_sync(0xFFFFFFFFu, mine.z, 1);
-    next.w = __shfl_down_sync(0xFFFFFFFFu, mine.w, 1);
+    const uint4 next = from_next_lane(mine);
     const int head = static_cast<int>(off) / 2;
-    const bool joins = lane < 31 && left >= 16;
+    const bool joins = lane < kRow - 1 && left >= 16;
     if (joins) *reinterpret_cast<uint4*>(p + head) = shifted16(mine, next, off);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {  // a head that the lane before does not take, a tail that does not join
@@ -916,20 +914,25 @@ __device__ __forceinline__ void store8(T* p, int left, bool vec, const float2 (&
 // dz = [dh u act'(g)  dh act(g)] of the gated layer, rounded (where dz is given;
 // rows of 2 n elements, lddz apart), and its column sums per chunk of rows as
 // slope_kernel forms them: to part ([chunk][2 n]) or db.  vec: bits 1 dh, 2 g,
-// 4 u start on 16-byte boundaries, 8 so does dz's second half; kVec: all do, and
-// the vectors of a thread's next row are on their way while it works on one.
+// 4 u start on 16-byte boundaries, 8 so does dz's second half.  Rows of a warp's
+// length (TX = 32) are a row ahead on their way: kWhole, where all of those do, as
+// they are; else as the aligned vectors that they lie in, one a lane, whose
+// elements a lane takes from its own and the next lane's, 31 lanes of them.
 // Bound by HBM, three matrices read and two written: 8192 x 8192 bf16 silu 102 us,
-// 6.6 TB/s (two rows ahead: 122, three: 140, in spilled registers).
-template <typename T, int kAct, int TX, bool kVec>
+// 6.6 TB/s (two rows ahead: 122, three: 140, in spilled registers); 11431 x 5330,
+// rows of no alignment, 302 us by two vectors a lane as they are needed, 186 by
+// the next lane's.
+template <typename T, int kAct, int TX, bool kWhole>
 __global__ void __launch_bounds__(256, 3) gated_slope_kernel(const T* dh, long long lddh, const T* pre, long long ldpre,
                                                              T* dz, long long lddz, float* part, T* db, int m, int n,
                                                              int chunk, int vec) {
-  constexpr int TY = 256 / TX, kCols = 8 * TX;
-  __shared__ float red[TY][kCols + 8];
+  constexpr bool kShifted = TX == 32 && !kWhole;
+  constexpr int TY = 256 / TX, kOwn = kShifted ? 31 : TX, kCols = 8 * kOwn;
+  __shared__ float red[TY][8 * TX + 8];
   chain_next();
   chain_wait();
   const int tx = threadIdx.x % TX, ty = threadIdx.x / TX;
-  const int col = blockIdx.x * kCols + tx * 8, left = n - col;
+  const int col = blockIdx.x * kCols + tx * 8, left = tx < kOwn ? n - col : 0;
   float2 sums[2][4] = {};
   const long long end = min(static_cast<long long>(m), (blockIdx.y + 1LL) * chunk);
   const long long first = static_cast<long long>(blockIdx.y) * chunk + ty;
@@ -944,38 +947,51 @@ __global__ void __launch_bounds__(256, 3) gated_slope_kernel(const T* dh, long l
       sums[1][q] = add2(sums[1][q], d[q]);
     }
     if (dz) {
-      store8<T, TX == 32>(dz + i * lddz + col, left, true, u);  // rows start on 16-byte boundaries
-      store8<T, TX == 32>(dz + i * lddz + n + col, left, kVec || (vec & 8), d);
+      constexpr int kRow = TX == 32 ? kOwn : 0;
+      store8<T, kRow>(dz + i * lddz + col, left, true, u);  // rows start on 16-byte boundaries
+      store8<T, kRow>(dz + i * lddz + n + col, left, kWhole || (vec & 8), d);
     }
   };
-  if (kVec && left >= 8) {  // (all of a warp's lanes, or all that have columns: n is a multiple of 8)
+  if constexpr (TX != 32) {
+    if (left > 0)
+      for (long long i = first; i < end; i += TY) {
+        float2 d[4], g[4], u[4];
+        load8(dh + i * lddh + col, left, vec & 1, d);
+        load8(pre + i * ldpre + col, left, vec & 2, g);
+        load8(pre + i * ldpre + n + col, left, vec & 4, u);
+        row(i, d, g, u);
+      }
+  } else {
+    const T* at[3] = {dh + col, pre + col, pre + n + col};
+    const uintptr_t begin[2] = {reinterpret_cast<uintptr_t>(dh), reinterpret_cast<uintptr_t>(pre)};
+    const uintptr_t stop[2] = {reinterpret_cast<uintptr_t>(dh + (m - 1) * lddh + n),
+                               reinterpret_cast<uintptr_t>(pre + (m - 1) * ldpre + 2 * n)};
     uint4 next[3];
     auto fetch = [&](long long i) {
-      if (i >= end) return;
-      next[0] = __ldg(reinterpret_cast<const uint4*>(dh + i * lddh + col));
-      next[1] = __ldg(reinterpret_cast<const uint4*>(pre + i * ldpre + col));
-      next[2] = __ldg(reinterpret_cast<const uint4*>(pre + i * ldpre + n + col));
+      if (i >= end || (kWhole && left < 8)) return;  // (n is a multiple of 8 then)
+#pragma unroll
+      for (int a = 0; a < 3; ++a) {
+        const T* p = at[a] + i * (a == 0 ? lddh : ldpre);
+        if constexpr (kWhole)
+          next[a] = __ldg(reinterpret_cast<const uint4*>(p));
+        else
+          next[a] = load_aligned(reinterpret_cast<uintptr_t>(p) & ~uintptr_t(15), begin[a != 0], stop[a != 0]);
+      }
     };
     fetch(first);
     for (long long i = first; i < end; i += TY) {
-      float2 d[4], g[4], u[4];
-      unpack16<T>(next[0], d);
-      unpack16<T>(next[1], g);
-      unpack16<T>(next[2], u);
+      float2 v[3][4];
+#pragma unroll
+      for (int a = 0; a < 3; ++a) {
+        uint4 mine = next[a];
+        if constexpr (!kWhole) {
+          const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(at[a] + i * (a == 0 ? lddh : ldpre))) & 15u;
+          mine = shifted16(mine, from_next_lane(mine), off);
+        }
+        unpack16<T>(mine, v[a]);
+      }
       fetch(i + TY);
-      row(i, d, g, u);
-    }
-  } else if (!kVec) {
-    // Which memory a vector may be read from.
-    const uintptr_t dh0 = reinterpret_cast<uintptr_t>(dh), dh1 = reinterpret_cast<uintptr_t>(dh + (m - 1) * lddh + n);
-    const uintptr_t pre0 = reinterpret_cast<uintptr_t>(pre), pre1 = reinterpret_cast<uintptr_t>(pre + (m - 1) * ldpre + 2 * n);
-#pragma unroll 2
-    for (long long i = first; i < end; i += TY) {
-      float2 d[4], g[4], u[4];
-      load8_anywhere(dh + i * lddh + col, left, vec & 1, dh0, dh1, d);
-      load8_anywhere(pre + i * ldpre + col, left, vec & 2, pre0, pre1, g);
-      load8_anywhere(pre + i * ldpre + n + col, left, vec & 4, pre0, pre1, u);
-      row(i, d, g, u);
+      if (!kWhole || left >= 8) row(i, v[0], v[1], v[2]);
     }
   }
   if (!part && !db) return;
@@ -1437,12 +1453,12 @@ cudaError_t run_gated_slope(const LinearGradCall& c, const GatedPlan& p, T* dz, 
   const int vec = (rows_aligned(c.dy, c.lddy, c.m) ? 1 : 0) | (pre ? 2 : 0) | (pre && half ? 4 : 0) | (half ? 8 : 0);
   T* db = static_cast<T*>(c.db);
   const bool whole = p.chunks == 1;
-  const int tx = c.m <= kFewSlopeRows ? 4 : 32;
+  const int tx = c.m <= kFewSlopeRows ? 4 : 32, cols = tx == 4 ? 32 : vec == 15 ? 256 : 248;
   const cudaError_t s = launch_chained(
       tx == 4     ? gated_slope_kernel<T, kAct, 4, false>
       : vec == 15 ? gated_slope_kernel<T, kAct, 32, true>
                   : gated_slope_kernel<T, kAct, 32, false>,
-      dim3((c.n + 8 * tx - 1) / (8 * tx), p.chunks), 256, 0, stream, 0, static_cast<const T*>(c.dy), c.lddy,
+      dim3((c.n + cols - 1) / cols, p.chunks), 256, 0, stream, 0, static_cast<const T*>(c.dy), c.lddy,
       static_cast<const T*>(c.pre), c.ldpre, dz, pad8(2 * c.n), db && !whole ? part : nullptr, whole ? db : nullptr, c.m,
       c.n, p.chunk, vec);
   if (s != cudaSuccess || !db || whole) return s;
