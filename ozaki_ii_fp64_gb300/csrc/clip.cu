@@ -7,8 +7,9 @@
 // No atomics: the same gradients give the same bits.  Squares and a warp's sum of
 // 2048 of them are fp32 (a chain of 40 roundings at most), everything after that
 // is fp64, whose rate is two additions a clock and SM.  Bound by HBM: each gradient is read twice, the second time in
-// the reverse order, so that what L2 still holds of the first pass (up to 129 MB)
-// is read from there, and written once.
+// the reverse order, so that what L2 still holds of the first pass is read from
+// there, and written once: 2.15 GB in 48 tensors 1000 us, 6.4 TB/s over the three; 100
+// MB 42 us.
 #include <algorithm>
 #include <atomic>
 #include <cstdint>
@@ -246,8 +247,10 @@ __global__ void __launch_bounds__(kThreads, 4)
 }
 
 // Both in one launch, for short lists of little memory: a cluster of 16 CTAs,
-// each with groups of kThreads that take chunks in turn; the CTAs' sums meet
-// through distributed shared memory.
+// each with groups of kThreads that take a chunk; the CTAs' sums meet through
+// distributed shared memory.  6 tensors of 1.1 MB in all: 6.1 us and 4 of the host,
+// 7.3 and 9.5 by two launches.  (With twice the chunks, in turn, 4 MB take 10.9 us,
+// 6.8 by two launches.)
 constexpr int kClusterCtas = 16, kClusterGroups = 4;
 constexpr int kClusterThreads = kClusterGroups * kThreads;
 template <int N>

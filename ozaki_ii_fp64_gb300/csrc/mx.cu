@@ -88,10 +88,11 @@ struct TilePart {
 // (1021 x 5003 fp32 has 160 of them: 12.8 us, by quarters 5.6), to a quarter of
 // one, the 32 rows of one byte column of its words.  A warp takes a row, a
 // lane eight columns of it, four lanes a block; the next rows of a warp (64
-// bytes a lane) are on their way while it works on as many.  kVec: rows start on 16-byte boundaries;
-// else their elements come one by one, a warp's side by side, and pass through
-// shared memory to the lanes that take eight.  A block with an infinity or a NaN
-// takes the scale NaN (255).
+// bytes a lane) are on their way while it works on as many.  kVec: rows start on
+// 16-byte boundaries; else their elements come one by one, a warp's side by side,
+// and pass through shared memory to the lanes that take eight.  A block with an
+// infinity or a NaN takes the scale NaN (255).  Bound by HBM: 16384 x 8192 bf16, 268
+// MB in and 71 out, 55 us, 6.2 TB/s (93 without rows ahead).
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(256, 4) mx_quantize_kernel(const T* x, long long ldx, int rows, int k, uint8_t* codes,
                                                              uint8_t* scales, int ktiles, int quarters) {
@@ -193,7 +194,8 @@ __global__ void __launch_bounds__(256, 4) mx_quantize_kernel(const T* x, long lo
 }
 
 // The values that codes and scales stand for: the same tiles and lanes, and
-// through shared memory where rows start on no 16-byte boundaries.
+// through shared memory where rows start on no 16-byte boundaries.  16384 x 8192
+// bf16, 71 MB in and 268 out, 54 us.
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(256) mx_dequantize_kernel(const uint8_t* codes, const uint8_t* scales, int ktiles,
                                                             int quarters, T* y, long long ldy, int rows, int k) {
@@ -272,6 +274,12 @@ __global__ void __launch_bounds__(256) mx_dequantize_kernel(const uint8_t* codes
 // 256 that share 64, the end of one and the start of the other.  The epilogue
 // takes the half with the shared columns first, and the next tile's MMAs start
 // once that half is in registers.
+//
+// Bound by shared memory (operands in and out), 560 clocks a stage against the
+// MMAs' 512, by the wait between a tile's last MMA and the next one's first (14 of
+// 186 us at 16 stages a tile) and by the outputs' way out: 8192 x 4096 -> 16384
+// bf16 160 us (6.9 PFLOP/s), with gelu_tanh 170; 8192 x 16384 -> 4096 144 (7.7),
+// in a short burst; a second of the first runs at 180, the power cap's clocks.
 // ---------------------------------------------------------------------------
 constexpr int kMxThreads = 32 * (3 + kEpiWarps);
 constexpr int kCodes = 128 * 128;                        // bytes of 128 rows of 256 codes
@@ -355,8 +363,8 @@ __device__ __forceinline__ void load32(const void* p, uint32_t (&v)[8]) {
                : "l"(p)
                : "memory");
 }
-// Without a place in L1, which nothing reads it from again: 8192 x 4096 -> 16384
-// takes 171 us, with one 180.
+// Without a place in L1, which nothing reads it from again: 9 us of the 180 that
+// 8192 x 4096 -> 16384 took with one.
 __device__ __forceinline__ void store32(void* p, const uint32_t (&v)[8]) {
   asm volatile("st.global.L1::no_allocate.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
                "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
@@ -365,9 +373,10 @@ __device__ __forceinline__ void store32(void* p, const uint32_t (&v)[8]) {
 
 // A warp's 32 rows x 32 columns of accumulators, a row a lane, where rows start
 // on 16-byte boundaries: straight from registers in pieces of 32 bytes, or of 16
-// where some row starts on no 32-byte boundary.  (The MMAs
-// and the copies that feed them take all of shared memory's bandwidth, 67 KB in
-// the 512 clocks of a stage; passing the outputs through it cost them a sixth.)
+// where some row starts on no 32-byte boundary.  (The MMAs and the copies that
+// feed them take all of shared memory's bandwidth, 67 KB in the 512 clocks of a
+// stage; passing the outputs through it, too, cost 8192 x 4096 -> 16384 6 of 186
+// us.)
 template <typename T>
 __device__ __forceinline__ void finish_direct(const uint32_t (&u)[32], const Epilogue& e, const uint4* bias,
                                               long long row, int col0, int m) {
@@ -685,7 +694,9 @@ __global__ void __launch_bounds__(kMxThreads, 1)
 //
 // As the kernel for few rows of linear.cu: the weights take the MMA's 128 rows,
 // the tokens its N = NT columns, a cluster of up to 16 CTAs shares the
-// reduction of 128 columns of D, and joins its fp32 sums in rank order.
+// reduction of 128 columns of D, and joins its fp32 sums in rank order.  Bound by
+// HBM and the start and end of a launch: 1 x 4096 -> 16384, 35.7 MB, 8.4 us from
+// HBM, 6.6 from L2.
 // ---------------------------------------------------------------------------
 template <int NT>
 struct MxFewCfg {
@@ -857,7 +868,9 @@ bool scale_map(CUtensorMap* map, const void* scales, int rows, int k) {
 }
 
 // CTAs of a pass over a matrix: its tiles, or their quarters where those do not
-// give every SM four.
+// give every SM four (bf16, us, quantised and read back, whole / quarters: 1024 x
+// 4096 6.8 + 4.9 / 3.5 + 3.8, 4096 x 4096 9.3 + 10.9 / 9.0 + 7.5, 8192 x 4096 15.0 +
+// 15.1 / 17.3 + 13.9, 16384 x 8192 55.6 + 53.3 / 70.2 + 54.9).
 long long tile_ctas(int rows, int k, int* quarters) {
   const long long tiles = static_cast<long long>((rows + 127) / 128) * k_tiles(k);
   *quarters = tiles < 152 * 4;
@@ -961,6 +974,21 @@ __global__ void __launch_bounds__(256) mx_empty_kernel(int m, int n, const Epilo
   }
 }
 
+// Whether the kernel for few rows takes a product.  The pairs' time is that of
+// their stages, 0.26 us each, whatever the rows up to 256; this one's shares the
+// stages over a cluster but grows with its rows.  Weights of 4096 rows from HBM,
+// us, few rows / pairs: 32 rows of 1024 columns 5.7 / 4.5, of 2048 5.8 / 5.7, of
+// 4096 6.6 / 8.0; 64 rows of 4096 8.4 / 8.1, of 8192 9.9 / 12.6; 128 rows of 4096
+// 11.2 / 8.3, of 8192 13.0 / 12.9, of 16384 15.4 / 21.9.  Above 128 rows its 128 x
+// 128 tiles have to leave SMs for a shared reduction (256 rows of 16384: 16.7 /
+// 22.0).
+bool few_rows(int m, int n, int kt) {
+  if (m <= 16) return true;
+  if (m <= 64) return kt >= (m <= 32 ? 8 : 17);
+  const long long squares = static_cast<long long>((m + 127) / 128) * ((n + 127) / 128);
+  return kt >= 32 && (m <= 128 || squares <= 76);
+}
+
 template <typename T>
 cudaError_t mx_linear_t(const MxLinearCall& c, cudaStream_t stream) {
   Epilogue e = {c.bias, c.res, c.ldr, nullptr, 0, c.y, c.ldy, c.act, 0, c.times};
@@ -976,16 +1004,19 @@ cudaError_t mx_linear_t(const MxLinearCall& c, cudaStream_t stream) {
     return launch_chained(mx_empty_kernel<T>, dim3(static_cast<unsigned>(std::min<long long>((all + 255) / 256, 4096))),
                           256, 0, stream, 0, c.m, c.n, e);
   }
-  const long long squares = static_cast<long long>((c.m + 127) / 128) * ((c.n + 127) / 128);
-  if (c.m <= 16) return launch_mx_few<T, 16>(c, e, stream);
-  if (c.m <= 32) return launch_mx_few<T, 32>(c, e, stream);
-  if (c.m <= 64) return launch_mx_few<T, 64>(c, e, stream);
-  if (c.m <= 128 || squares <= 76) return launch_mx_few<T, 128>(c, e, stream);
+  if (few_rows(c.m, c.n, k_tiles(c.k)))
+    return c.m <= 16   ? launch_mx_few<T, 16>(c, e, stream)
+           : c.m <= 32 ? launch_mx_few<T, 32>(c, e, stream)
+           : c.m <= 64 ? launch_mx_few<T, 64>(c, e, stream)
+                       : launch_mx_few<T, 128>(c, e, stream);
   int pairs = 0;
   const cudaError_t s = resident_pairs<T>(&pairs);
   if (s != cudaSuccess) return s;
   MxProduct p = {c.m, c.n, k_tiles(c.k), 256, {}, e};
   auto tiles = [&](int bn) { return static_cast<long long>((c.m + 255) / 256) * ((c.n + bn - 1) / bn); };
+  // Narrow tiles where every one of them has a pair of its own (1024 x 4096 -> 2048:
+  // 8.6 us, 9.0 by half as many wide ones); in two rounds they lose (1024 x 4096 ->
+  // 4096: 13.8, 11.1 by one round of wide ones).
   if (tiles(128) <= pairs) p.bn = 128;
   p.tiles = raster((c.m + 255) / 256, (c.n + p.bn - 1) / p.bn);
   CUtensorMap ma, mb, msa, msb;

@@ -157,6 +157,14 @@ def test_product_shapes(oz, shape, dtype):
     product(oz, m, k, n, dtype, bias=False)
 
 
+# Reductions that a cluster shares, unevenly, for every number of rows that it takes, and few rows of short ones.
+@pytest.mark.parametrize("m, k, n", [(16, 8200, 130), (30, 2048, 200), (30, 1700, 264), (32, 9000, 1000), (50, 4100, 77),
+                                     (64, 4352, 640), (60, 5000, 129), (100, 8200, 130), (128, 9001, 256), (90, 7000, 300),
+                                     (200, 8192, 136), (300, 16384, 300), (150, 20000, 64), (1000, 8192, 512)])
+def test_product_long_reductions(oz, m, k, n):
+    product(oz, m, k, n, BF16, "silu", residual=True)
+
+
 @pytest.mark.parametrize("act", ["none", "relu", "gelu", "gelu_tanh", "silu"])
 @pytest.mark.parametrize("m", [1, 40, 700])
 def test_product_activations(oz, act, m):
