@@ -1270,10 +1270,13 @@ Ready ready(int m, int n, int depth, const Matrix& a, bool a_mn, const Matrix& b
 // 76 tiles of 128 x 128 with a reduction worth sharing.  128 rows of 4096 ->
 // 4096 take it 15.5 us (pairs 18), 256 rows of 8192 -> 1024 15.7 (19.5); but
 // 256 rows of 4096 -> 16384 41.7 (30).
+// Of a gated layer up to 64 rows, whose sums it joins twice: 128 rows of 1024 -> 2 x
+// 2048 from HBM 10.4 us (pairs 8.2), of 4096 -> 2 x 8192 32 (30), 64 rows 8.1 (8.0)
+// and 28.4 (29.6).
 bool few_rows(const Product& p, bool gated = false) {
   const long long squares =
       static_cast<long long>((p.m + 127) / 128) * (gated ? (p.n + 63) / 64 : (p.n + 127) / 128);
-  return !p.a_mn && (p.m <= 128 || (squares <= 76 && p.kb >= 32));
+  return !p.a_mn && (p.m <= (gated ? 64 : 128) || (squares <= 76 && p.kb >= 32));
 }
 
 template <typename T, bool kGated = false>
