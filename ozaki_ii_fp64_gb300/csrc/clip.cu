@@ -3,13 +3,13 @@
 //   N = sqrt(sum over all tensors of g^2),  g <- g min(1, max_norm / (N + eps))
 //
 // Two launches: the sums of squares, a partial one for each CTA, then the
-// scaling, before which every CTA adds the partial sums up in the same order.
-// No atomics: the same gradients give the same bits.  Squares and a warp's sum of
-// 2048 of them are fp32 (a chain of 40 roundings at most), everything after that
-// is fp64, whose rate is two additions a clock and SM.  Bound by HBM: each gradient is read twice, the second time in
-// the reverse order, so that what L2 still holds of the first pass is read from
-// there, and written once: 2.15 GB in 48 tensors 1000 us, 6.4 TB/s over the three; 100
-// MB 42 us.
+// scaling, before which every CTA adds the partial sums up in the same order; one
+// for short lists of little memory.  No atomics: the same gradients give the same
+// bits.  Squares and a warp's sum of 2048 of them are fp32 (a chain of 40 roundings
+// at most), everything after that is fp64, whose rate is two additions a clock and
+// SM.  Bound by HBM: each gradient is read twice, the second time in the reverse
+// order, so that what L2 still holds of the first pass is read from there, and
+// written once: 2.15 GB in 48 tensors 1000 us, 6.4 TB/s over the three; 100 MB 42 us.
 #include <algorithm>
 #include <atomic>
 #include <cstdint>

@@ -24,7 +24,9 @@ struct Epilogue {
   void* out;
   long long ldo;
   int act;
-  int vec;  // bits: 1 bias, 2 res, 4 pre, 8 out rows start on 16-byte boundaries; gated, 16 and 32: bias's, pre's second half
+  // Bits: 1 bias, 2 res, 4 pre, 8 out rows start on 16-byte boundaries.  Gated: 16
+  // bias's, 32 pre's second half do; 4-bit product: 16 res and out rows on 32 bytes.
+  int vec;
   bool times;  // res multiplies act(z) (kTimes epilogues) instead of being added
 };
 

@@ -95,6 +95,17 @@ def test_shapes(oz, shape, dtype):
         assert worst(got, v, e) <= 1
 
 
+# Long reductions of few tiles, which two or four CTA pairs share; more than the kernel for few rows takes, and that kernel's.
+@pytest.mark.parametrize("m, k, n", [(256, 8192, 2600), (250, 6000, 2601), (130, 20000, 3000), (256, 3000, 2560), (100, 1500, 700),
+                                     (128, 9000, 136), (64, 9000, 136), (300, 16384, 1700), (512, 8192, 1300)])
+def test_long_reductions(oz, m, k, n):
+    x, w, b = rnd(m, k, BF16, 61), rnd(2 * n, k, BF16, 62, k ** -0.5), rnd(1, 2 * n, BF16, 63)[0]
+    h, pre = oz.gated_linear(x, w, b, activation="gelu", save_pre=True)
+    want, tol, z, tolz = gated64(x, w, b, "gelu")
+    assert worst(h, want, tol) <= 1 and worst(pre, z, tolz) <= 1
+    assert torch.equal(oz.gated_linear(x, w, b, activation="gelu"), h)
+
+
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("m", [1, 5, 200, 700])
 def test_activations(oz, act, m):
