@@ -76,8 +76,8 @@ __device__ __forceinline__ void load8(const T* p, int left, bool vec, float2 (&v
 // Bound by the MMAs (256 columns) or a CTA's loads (128): 8192 x 4096 -> 16384
 // bf16 with gelu_tanh, pre kept: 575 us in a short burst (1.91 PFLOP/s), 694 at
 // the clocks that the power cap leaves after seconds of it.  A launch costs 4 to
-// 6.5 us beyond its rounds, and rows of no alignment another 8 at 1000 x 2049 ->
-// 4099, f16 with a residual (35 us).
+// 6.5 us beyond its rounds; at 1000 x 2049 -> 4099, f16 with a residual (34 us),
+// the copies of both odd operands cost 8 and the odd rows of y and the residual 2.
 // ---------------------------------------------------------------------------
 constexpr int kRing = 192 * 1024;  // stages of two blocks of A and one or two of B: 8 or 6
 constexpr int kMaxStages = 8;
