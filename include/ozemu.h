@@ -545,8 +545,8 @@ size_t ozemu_linear_bytes(int m, int n, int k, const void* X, int ldx, const voi
  * dZ is rounded to the type for the two products (the tensor cores take
  * 16-bit operands): with an activation other than none and relu one rounding
  * more than dX and dW have from an unrounded dZ, a factor sqrt(2) of their error,
- * and in f16 an infinity beyond 65504.  db sums it unrounded.  m = 0 zeroes dW
- * and db, n = 0 zeroes dX. */
+ * and in f16 an infinity beyond 65504 and, below 2^-14, an error of up to 2^-25 as
+ * dY's own.  db sums it unrounded.  m = 0 zeroes dW and db, n = 0 zeroes dX. */
 int ozemu_linear_backward(int m, int n, int k, int type, const void* dY, int lddy, const void* X, int ldx,
                           const void* W, int ldw, int activation, const void* pre, int ldpre, void* dX, int lddx,
                           void* dW, int lddw, void* db, void* workspace, size_t workspace_bytes,
@@ -574,7 +574,10 @@ size_t ozemu_gated_linear_bytes(int m, int n, int k, const void* X, int ldx, con
  * G and U,
  *   dX = dZ W (m x k, lddx),  dW = dZ^T X (2n x k, lddw),  db = sum_i dZ_i (2n);
  * each of dX, dW, db may be NULL: not computed.  dZ is rounded to the type for
- * the two products, as in ozemu_linear_backward; db sums it unrounded.  m = 0
+ * the two products, as in ozemu_linear_backward; db sums it unrounded.  In f16 it
+ * is rounded times a power of two that brings its largest finite element to 2^14
+ * .. 2^15, which dX and dW have taken out of their fp32 sums: a product of three
+ * that leaves the type's range loses nothing where dX, dW do not leave it.  m = 0
  * zeroes dW and db, n = 0 zeroes dX. */
 int ozemu_gated_linear_backward(int m, int n, int k, int type, const void* dH, int lddh, const void* X, int ldx,
                                 const void* W, int ldw, int activation, const void* pre, int ldpre, void* dX, int lddx,

@@ -21,8 +21,13 @@
 // values would have: where dz has one (an activation other than none and relu),
 // the error of dx and dw against 64 bits, relative in 2-norm, goes from 1.7e-3
 // to 2.3e-3 in bf16 (8192 x 4096 -> 16384, gelu) and from 2.1e-4 to 2.9e-4 in
-// f16, and an f16 dz beyond 65504 is infinite.  Two 16-bit parts of dz would
-// avoid it for twice the MMAs of both products.  Sums in the tensor cores
+// f16.  Two 16-bit parts of dz would avoid it for twice the MMAs of both
+// products.  In f16 dz can leave the type's range where the gradients do not.
+// The gated layer's, products of three, are rounded times a power of two that
+// brings the largest of them to 2^14 .. 2^15, and dx and dw have it taken out of
+// their fp32 sums.  The plain layer's, dy times a slope, are rounded as they are:
+// beyond 65504 (a slope is up to 1.13) they are infinite, below 2^-14 they keep
+// 2^-25 absolutely, as dy itself does.  Sums in the tensor cores
 // differ from sums of fp32 roundings in the last bits: the forward product's
 // outputs by 1.4e-4 of them, bf16 roundings that fall the other way, at the
 // same error against 64 bits.
@@ -509,12 +514,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             store4(static_cast<T*>(e.out) + row * e.ldo + col, z[i], left, (e.vec & 8) != 0);
           }
         } else {
+          const float f = sums_scale(e);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const long long row = grow0 + r0 + 2 * i;
             if (row >= p.m) continue;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) z[i][k] += b[k];
+            for (int k = 0; k < 4; ++k) z[i][k] = z[i][k] * f + b[k];
             if (e.pre) store4(static_cast<T*>(e.pre) + row * e.ldpre + col, z[i], left, (e.vec & 4) != 0);
             activate_all(z[i], e.act);
             if (e.res) {
@@ -911,11 +917,108 @@ __device__ __forceinline__ void store8(T* p, int left, bool vec, const float2 (&
   }
 }
 
+// The largest magnitude of dz = [dh u act'(g)  dh act(g)], of its finite values,
+// for its scale: largest[CTA] of the grid's.  float16 only: the other type has
+// fp32's range.  A CTA takes a strip of columns (every gridDim.x-th), a warp a row
+// at a time, eight columns a lane: kVec, where rows start on 16-byte boundaries, 256
+// of them, as they are; else 248, as in gated_slope_kernel.  Bound by HBM: 8192 x
+// 8192 silu, 403 MB, 78 us (112 a row at a time); 8192 x 5330, rows of no alignment, 73.
+constexpr int kLargestCtas = 152 * 4;
+template <typename T, int kAct, bool kVec>
+__global__ void __launch_bounds__(256, 4) gated_largest_kernel(const T* dh, long long lddh, const T* pre, long long ldpre,
+                                                               float* largest, int m, int n) {
+  constexpr int kOwn = kVec ? 32 : 31;
+  __shared__ uint32_t red[8];
+  chain_next();
+  chain_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uintptr_t begin[2] = {reinterpret_cast<uintptr_t>(dh), reinterpret_cast<uintptr_t>(pre)};
+  const uintptr_t stop[2] = {reinterpret_cast<uintptr_t>(dh + (m - 1) * lddh + n),
+                             reinterpret_cast<uintptr_t>(pre + (m - 1) * ldpre + 2 * n)};
+  const int step = 8 * gridDim.y;
+  uint32_t most = 0;
+  for (long long col0 = blockIdx.x * 8LL * kOwn; col0 < n; col0 += gridDim.x * 8LL * kOwn) {
+    const int col = static_cast<int>(col0) + lane * 8, left = lane < kOwn ? n - col : 0;
+    const T* at[3] = {dh + col, pre + col, pre + n + col};
+#pragma unroll 1
+    for (int row = blockIdx.y * 8 + warp; row < m; row += 2 * step) {
+      uint4 u[2][3];  // two rows' loads before the first of them is needed
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int a = 0; a < 3; ++a) {
+          const T* p = at[a] + (row + static_cast<long long>(r) * step) * (a == 0 ? lddh : ldpre);
+          u[r][a] = make_uint4(0, 0, 0, 0);
+          if (row + static_cast<long long>(r) * step >= m) continue;
+          if constexpr (kVec) {  // (n is a multiple of 8)
+            if (left > 0) u[r][a] = __ldg(reinterpret_cast<const uint4*>(p));
+          } else {
+            u[r][a] = load_aligned(reinterpret_cast<uintptr_t>(p) & ~uintptr_t(15), begin[a != 0], stop[a != 0]);
+          }
+        }
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float2 v[3][4];
+#pragma unroll
+        for (int a = 0; a < 3; ++a) {
+          if constexpr (!kVec) {
+            const T* p = at[a] + (row + static_cast<long long>(r) * step) * (a == 0 ? lddh : ldpre);
+            u[r][a] = shifted16(u[r][a], from_next_lane(u[r][a]), static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 15u);
+          }
+          unpack16<T>(u[r][a], v[a]);
+        }
+        auto take = [&](float f, bool some) {
+          const uint32_t bits = __float_as_uint(f) & 0x7FFFFFFFu;
+          if (some && bits < 0x7F800000u) most = max(most, bits);
+        };
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float2 a, slope;
+          activation_and_slope2<kAct>(v[1][q], a, slope);
+          slope = mul2(mul2(v[0][q], v[2][q]), slope);
+          a = mul2(v[0][q], a);
+          take(slope.x, kVec || 2 * q < left);
+          take(a.x, kVec || 2 * q < left);
+          take(slope.y, kVec || 2 * q + 1 < left);
+          take(a.y, kVec || 2 * q + 1 < left);
+        }
+      }
+    }
+  }
+  most = __reduce_max_sync(0xFFFFFFFFu, most);
+  if (lane == 0) red[warp] = most;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) most = max(most, red[i]);
+    largest[blockIdx.y * gridDim.x + blockIdx.x] = __uint_as_float(most);
+  }
+}
+
+// The power of two that brings the largest of those (parts of them) to 2^14 ..
+// 2^15, the same for every thread of a CTA; 1 where all are 0.  The first CTA
+// leaves its inverse.
+__device__ __forceinline__ float gated_scale(const float* largest, int parts, float* inverse) {
+  __shared__ uint32_t red[8];
+  uint32_t most = 0;
+  for (int i = threadIdx.x; i < parts; i += 256) most = max(most, __float_as_uint(__ldcg(largest + i)));
+  most = __reduce_max_sync(0xFFFFFFFFu, most);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = most;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) most = max(most, red[i]);
+  // 2^s with s = 14 - floor(log2 most), within what has an inverse.
+  const int exponent = most == 0 ? 127 : min(max(268 - static_cast<int>(most >> 23), 1), 253);
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0)
+    *inverse = __uint_as_float(static_cast<uint32_t>(254 - exponent) << 23);
+  return __uint_as_float(static_cast<uint32_t>(exponent) << 23);
+}
+
 // dz = [dh u act'(g)  dh act(g)] of the gated layer, rounded (where dz is given;
-// rows of 2 n elements, lddz apart), and its column sums per chunk of rows as
-// slope_kernel forms them: to part ([chunk][2 n]) or db.  vec: bits 1 dh, 2 g,
-// 4 u start on 16-byte boundaries, 8 so does dz's second half.  Rows of a warp's
-// length (TX = 32) are a row ahead on their way: kWhole, where all of those do, as
+// rows of 2 n elements, lddz apart; float16 times gated_scale), and its column
+// sums per chunk of rows as slope_kernel forms them: to part ([chunk][2 n]) or db.
+// vec: bits 1 dh, 2 g, 4 u start on 16-byte boundaries, 8 so does dz's second
+// half.  Rows of a warp's length (TX = 32) are a row ahead on their way: kWhole, where all of those do, as
 // they are; else as the aligned vectors that they lie in, one a lane, whose
 // elements a lane takes from its own and the next lane's, 31 lanes of them.
 // Bound by HBM, three matrices read and two written: 8192 x 8192 bf16 silu 102 us,
@@ -925,12 +1028,18 @@ __device__ __forceinline__ void store8(T* p, int left, bool vec, const float2 (&
 template <typename T, int kAct, int TX, bool kWhole>
 __global__ void __launch_bounds__(256, 3) gated_slope_kernel(const T* dh, long long lddh, const T* pre, long long ldpre,
                                                              T* dz, long long lddz, float* part, T* db, int m, int n,
-                                                             int chunk, int vec) {
+                                                             int chunk, int vec, const float* largest, int parts,
+                                                             float* inverse) {
   constexpr bool kShifted = TX == 32 && !kWhole;
+  constexpr bool kScaled = !Pair<T>::kBf16;
   constexpr int TY = 256 / TX, kOwn = kShifted ? 31 : TX, kCols = 8 * kOwn;
   __shared__ float red[TY][8 * TX + 8];
   chain_next();
   chain_wait();
+  float scale = 1.f;
+  auto find_scale = [&] {
+    if (kScaled && dz) scale = gated_scale(largest, parts, inverse);
+  };
   const int tx = threadIdx.x % TX, ty = threadIdx.x / TX;
   const int col = blockIdx.x * kCols + tx * 8, left = tx < kOwn ? n - col : 0;
   float2 sums[2][4] = {};
@@ -947,12 +1056,20 @@ __global__ void __launch_bounds__(256, 3) gated_slope_kernel(const T* dh, long l
       sums[1][q] = add2(sums[1][q], d[q]);
     }
     if (dz) {
+      if constexpr (kScaled) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          u[q] = mul2(u[q], both(scale));
+          d[q] = mul2(d[q], both(scale));
+        }
+      }
       constexpr int kRow = TX == 32 ? kOwn : 0;
       store8<T, kRow>(dz + i * lddz + col, left, true, u);  // rows start on 16-byte boundaries
       store8<T, kRow>(dz + i * lddz + n + col, left, kWhole || (vec & 8), d);
     }
   };
   if constexpr (TX != 32) {
+    find_scale();
     if (left > 0)
       for (long long i = first; i < end; i += TY) {
         float2 d[4], g[4], u[4];
@@ -979,6 +1096,7 @@ __global__ void __launch_bounds__(256, 3) gated_slope_kernel(const T* dh, long l
       }
     };
     fetch(first);
+    find_scale();
     for (long long i = first; i < end; i += TY) {
       float2 v[3][4];
 #pragma unroll
@@ -1377,11 +1495,11 @@ cudaError_t run_slope(const LinearGradCall& c, const BackwardPlan& p, T* dz, flo
                         db, nullptr);
 }
 
-// dx = dz w and dw = dz^T x, with dz of n columns.
+// dx = dz w and dw = dz^T x, with dz of n columns, times a number in memory (NULL: 1).
 template <typename T>
 cudaError_t grad_products(const LinearGradCall& c, int n, const Matrix& dz, const Matrix& x, const Matrix& w,
-                          cudaStream_t stream) {
-  Epilogue to_dx = {nullptr, nullptr, 0, nullptr, 0, c.dx, c.lddx, kActNone, 0}, to_dw = to_dx;
+                          const float* scale, cudaStream_t stream) {
+  Epilogue to_dx = {nullptr, nullptr, 0, nullptr, 0, c.dx, c.lddx, kActNone, 0, false, scale}, to_dw = to_dx;
   to_dw.out = c.dw;
   to_dw.ldo = c.lddw;
   const bool want_dx = c.dx && c.m > 0 && c.k > 0, want_dw = c.dw && n > 0 && c.k > 0;
@@ -1420,7 +1538,7 @@ cudaError_t linear_backward_t(const LinearGradCall& c, cudaStream_t stream) {
     s = launch_chained(join_parts_kernel<T>, dim3((c.n + 31) / 32), 1024, 0, stream, 0, nullptr, 0, 0, c.n,
                        static_cast<T*>(c.db), nullptr);
   }
-  return s == cudaSuccess ? grad_products<T>(c, c.n, dz, x, w, stream) : s;
+  return s == cudaSuccess ? grad_products<T>(c, c.n, dz, x, w, nullptr, stream) : s;
 }
 
 // ------------------------------------------------------- the gated layer's
@@ -1438,6 +1556,8 @@ struct GatedPlan {
   int chunk, chunks;
   size_t dz, part, x, w;
 };
+// What the CTAs find largest, and, in a line of its own, the scale's inverse.
+constexpr size_t kScaleBytes = (kLargestCtas * sizeof(float) + 255) / 256 * 256 + 256;
 GatedPlan gated_plan(const LinearGradCall& c) {
   GatedPlan p;
   const size_t up = 255;
@@ -1451,19 +1571,33 @@ GatedPlan gated_plan(const LinearGradCall& c) {
 }
 
 template <typename T, int kAct>
-cudaError_t run_gated_slope(const LinearGradCall& c, const GatedPlan& p, T* dz, float* part, cudaStream_t stream) {
+cudaError_t run_gated_slope(const LinearGradCall& c, const GatedPlan& p, T* dz, float* part, float* largest, float* inverse,
+                            cudaStream_t stream) {
   const bool half = (c.n & 7) == 0, pre = rows_aligned(c.pre, c.ldpre, c.m);
   const int vec = (rows_aligned(c.dy, c.lddy, c.m) ? 1 : 0) | (pre ? 2 : 0) | (pre && half ? 4 : 0) | (half ? 8 : 0);
   T* db = static_cast<T*>(c.db);
   const bool whole = p.chunks == 1;
   const int tx = c.m <= kFewSlopeRows ? 4 : 32, cols = tx == 4 ? 32 : vec == 15 ? 256 : 248;
+  int parts = 0;
+  if constexpr (!Pair<T>::kBf16) {
+    if (dz) {
+      const bool whole_rows = (vec & 7) == 7;
+      const int across = std::min(kLargestCtas, (c.n - 1) / (whole_rows ? 256 : 248) + 1);
+      const int down = std::max(1, std::min(kLargestCtas / across, (c.m - 1) / 8 + 1));
+      parts = across * down;
+      const cudaError_t s = launch_chained(
+          whole_rows ? gated_largest_kernel<T, kAct, true> : gated_largest_kernel<T, kAct, false>, dim3(across, down), 256,
+          0, stream, 0, static_cast<const T*>(c.dy), c.lddy, static_cast<const T*>(c.pre), c.ldpre, largest, c.m, c.n);
+      if (s != cudaSuccess) return s;
+    }
+  }
   const cudaError_t s = launch_chained(
       tx == 4     ? gated_slope_kernel<T, kAct, 4, false>
       : vec == 15 ? gated_slope_kernel<T, kAct, 32, true>
                   : gated_slope_kernel<T, kAct, 32, false>,
       dim3((c.n + cols - 1) / cols, p.chunks), 256, 0, stream, 0, static_cast<const T*>(c.dy), c.lddy,
       static_cast<const T*>(c.pre), c.ldpre, dz, pad8(2 * c.n), db && !whole ? part : nullptr, whole ? db : nullptr, c.m,
-      c.n, p.chunk, vec);
+      c.n, p.chunk, vec, static_cast<const float*>(largest), parts, inverse);
   if (s != cudaSuccess || !db || whole) return s;
   return launch_chained(join_parts_kernel<T>, dim3((2 * c.n + 31) / 32), 1024, 0, stream, 0, part, p.chunks, p.chunks,
                         2 * c.n, db, nullptr);
@@ -1472,6 +1606,7 @@ cudaError_t run_gated_slope(const LinearGradCall& c, const GatedPlan& p, T* dz, 
 template <typename T>
 cudaError_t gated_backward_t(const LinearGradCall& c, cudaStream_t stream) {
   Matrix dz = {nullptr, pad8(2 * c.n), c.m, 2 * c.n}, x = {c.x, c.ldx, c.m, c.k}, w = {c.w, c.ldw, 2 * c.n, c.k};
+  float* inverse = nullptr;
   cudaError_t s = cudaSuccess;
   if (c.m > 0 && c.n > 0) {
     const GatedPlan plan = gated_plan(c);
@@ -1479,12 +1614,14 @@ cudaError_t gated_backward_t(const LinearGradCall& c, cudaStream_t stream) {
     T* own = c.dx || c.dw ? reinterpret_cast<T*>(ws) : nullptr;
     dz.p = own;
     float* part = reinterpret_cast<float*>(ws + plan.dz);
+    float* largest = reinterpret_cast<float*>(ws + plan.dz + plan.part + plan.x + plan.w);
+    if (!Pair<T>::kBf16 && own) inverse = largest + (kScaleBytes - 256) / sizeof(float);
     switch (c.act) {
-      case kActRelu: s = run_gated_slope<T, kActRelu>(c, plan, own, part, stream); break;
-      case kActGelu: s = run_gated_slope<T, kActGelu>(c, plan, own, part, stream); break;
-      case kActGeluTanh: s = run_gated_slope<T, kActGeluTanh>(c, plan, own, part, stream); break;
-      case kActSilu: s = run_gated_slope<T, kActSilu>(c, plan, own, part, stream); break;
-      default: s = run_gated_slope<T, kActNone>(c, plan, own, part, stream); break;
+      case kActRelu: s = run_gated_slope<T, kActRelu>(c, plan, own, part, largest, inverse, stream); break;
+      case kActGelu: s = run_gated_slope<T, kActGelu>(c, plan, own, part, largest, inverse, stream); break;
+      case kActGeluTanh: s = run_gated_slope<T, kActGeluTanh>(c, plan, own, part, largest, inverse, stream); break;
+      case kActSilu: s = run_gated_slope<T, kActSilu>(c, plan, own, part, largest, inverse, stream); break;
+      default: s = run_gated_slope<T, kActNone>(c, plan, own, part, largest, inverse, stream); break;
     }
     Matrix none = {nullptr, 0, 0, 0};
     if (s == cudaSuccess) s = align_operands(c.dw ? &x : &none, c.dx ? &w : &none, ws + plan.dz + plan.part, stream);
@@ -1492,7 +1629,7 @@ cudaError_t gated_backward_t(const LinearGradCall& c, cudaStream_t stream) {
     s = launch_chained(join_parts_kernel<T>, dim3((2 * c.n + 31) / 32), 1024, 0, stream, 0, nullptr, 0, 0, 2 * c.n,
                        static_cast<T*>(c.db), nullptr);
   }
-  return s == cudaSuccess ? grad_products<T>(c, 2 * c.n, dz, x, w, stream) : s;
+  return s == cudaSuccess ? grad_products<T>(c, 2 * c.n, dz, x, w, inverse, stream) : s;
 }
 
 }  // namespace
@@ -1524,7 +1661,7 @@ cudaError_t launch_gated_linear(const LinearCall& c, cudaStream_t stream) {
 
 size_t gated_linear_backward_workspace(const LinearGradCall& c) {
   const GatedPlan p = gated_plan(c);
-  return p.dz + p.part + p.x + p.w;
+  return p.dz + p.part + p.x + p.w + kScaleBytes;
 }
 
 cudaError_t launch_gated_linear_backward(const LinearGradCall& c, cudaStream_t stream) {

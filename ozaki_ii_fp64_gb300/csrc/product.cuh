@@ -28,7 +28,12 @@ struct Epilogue {
   // bias's, 32 pre's second half do; 4-bit product: 16 res and out rows on 32 bytes.
   int vec;
   bool times;  // res multiplies act(z) (kTimes epilogues) instead of being added
+  const float* scale;  // of the sums: a number in memory (NULL: 1), in plain epilogues
 };
+
+// That number, which a launch before this one wrote (by L2: a line in L1 may be
+// older than it).
+__device__ __forceinline__ float sums_scale(const Epilogue& e) { return e.scale ? __ldcg(e.scale) : 1.f; }
 
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_word,
                                           uint32_t* flags) {
@@ -381,6 +386,11 @@ __device__ __forceinline__ void finish_rows(F source, const uint4 (&res)[4], con
   float z[32];
   auto take = [&](bool last) {
     source(last, z);
+    if (!kTimes && e.scale) {
+      const float f = sums_scale(e);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) z[i] *= f;
+    }
     if (e.bias) {
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -474,6 +484,11 @@ __device__ __forceinline__ void join_few(const uint8_t* smem, const Epilogue& e,
       for (int q = 0; q < 4; ++q) z[q] *= u[q];
       store4(static_cast<T*>(e.out) + row * e.ldo + j, z, left, (e.vec & 8) != 0);
       continue;
+    }
+    if (!kTimes) {
+      const float f = sums_scale(e);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) z[q] *= f;
     }
     if (e.bias) {
       load4(static_cast<const T*>(e.bias) + j, left, e.vec & 1, v);
