@@ -628,8 +628,10 @@ int ozemu_mx_linear(int m, int n, int k, int type, const uint8_t* x_codes, const
  * the call returns: device pointers, numbers of elements (dense; up to 2^40)
  * and ozemu_types, which may differ.  outs[i] may be grads[i] itself, and
  * overlaps nothing else.  max_norm and eps >= 0, not both 0.  Squares and sums
- * of 2048 of them are fp32: gradients beyond 4e17 may give an infinite norm,
- * elements below 1e-23 do not count.  A NaN or an infinity goes through as the formula takes it. */
+ * of 2048 of them are fp32, scaled where they leave its range, so that finite
+ * gradients of any size have their norm; one beyond the largest float is infinite.
+ * A norm of infinity gives zeros, a NaN or an infinity goes through as the formula
+ * takes it (with an infinite max_norm, too: inf / inf is NaN). */
 int ozemu_clip_grad_norm(int count, const void* const* grads, const long long* sizes, const int* types,
                          void* const* outs, float max_norm, float eps, float* norm, void* workspace,
                          size_t workspace_bytes, cudaStream_t stream);

@@ -1033,5 +1033,5 @@ def clip_grad_norm(grads, max_norm, eps=1e-6, out=None, stream=None):
 
     out: as many tensors of the same sizes, types and strides that take the result; each may be its gradient itself
     (out=grads clips in place), and overlaps no other (ValueError).  A norm of infinity gives zeros (NaN where the
-    gradients are infinite), one of NaN gives NaN."""
+    gradients are infinite, and throughout with an infinite max_norm), one of NaN gives NaN."""
     return (_native or _layer_calls()).clip_grad_norm(grads, max_norm, eps, out, stream)

@@ -6,13 +6,15 @@
 // scaling, before which every CTA adds the partial sums up in the same order; one
 // for short lists of little memory.  No atomics: the same gradients give the same
 // bits.  Squares and a warp's sum of 2048 of them are fp32 (a chain of 40 roundings
-// at most), everything after that is fp64, whose rate is two additions a clock and
-// SM.  Bound by HBM: each gradient is read twice, the second time in the reverse
+// at most; scaled where they leave its range), everything after that is fp64, whose
+// rate is two additions a clock and SM.  Bound by HBM: each gradient is read twice, the second time in the reverse
 // order, so that what L2 still holds of the first pass is read from there, and
-// written once: 2.15 GB in 48 tensors 1000 us, 6.4 TB/s over the three; 100 MB 42 us.
+// written once: 2.15 GB in 48 tensors 1000 us, 6.4 TB/s over the three; 100 MB in
+// aligned tensors 45 us, packed without gaps 50.
 #include <algorithm>
 #include <atomic>
 #include <cstdint>
+#include <type_traits>
 
 #include "kernels.h"
 #include "layer.cuh"
@@ -102,8 +104,12 @@ struct Span {
   }
 };
 
-// A warp's share of a chunk's sum of squares, in every lane.
-__device__ __forceinline__ float chunk_squares(const Tensor& t, unsigned int chunk, int thread) {
+// Adds a warp's share of a chunk's sum of squares to its first lane's `sum`.  A
+// share that overflows fp32, or is below 2^-110, where its 2048 squares can lose
+// 2^-139 below the normal range, is formed again from elements times a power of
+// two: of 2^-80 the largest are below 2^48; of 2^100 those that are all below 2^-55
+// lie between 2^-49 and 2^45.  (Zeros come here, too.  An infinity or a NaN stays.)
+__device__ __forceinline__ void add_chunk_squares(const Tensor& t, unsigned int chunk, int thread, double& sum) {
   const Span span(t, chunk, thread);
   const uint4* from = reinterpret_cast<const uint4*>(t.g + span.at) + thread;
   uint4 v[kVectors];
@@ -114,26 +120,41 @@ __device__ __forceinline__ float chunk_squares(const Tensor& t, unsigned int chu
 #pragma unroll
     for (int j = 0; j < kVectors; ++j) v[j] = span.whole(j) ? from[j * kThreads] : make_uint4(0, 0, 0, 0);
   }
-  float2 s[2] = {};
-  with_type(t.type, [&](auto type) {
-    using T = decltype(type);
-    constexpr int kPairs = 8 / sizeof(T);
+  auto squares = [&](auto times, float power) {  // in every lane
+    float2 s[2] = {};
+    with_type(t.type, [&](auto type) {
+      using T = decltype(type);
+      constexpr int kPairs = 8 / sizeof(T);
 #pragma unroll
-    for (int j = 0; j < kVectors; ++j) {
-      float2 f[kPairs];
-      unpack16<T>(v[j], f);
+      for (int j = 0; j < kVectors; ++j) {
+        float2 f[kPairs];
+        unpack16<T>(v[j], f);
 #pragma unroll
-      for (int i = 0; i < kPairs; ++i) s[i & 1] = fma2(f[i], f[i], s[i & 1]);
-    }
-    span.template parts<T>(t, [&](long long at) {
-      const float f = to_float(*reinterpret_cast<const T*>(t.g + at));
-      s[0].x = fmaf(f, f, s[0].x);
+        for (int i = 0; i < kPairs; ++i) {
+          if constexpr (decltype(times)::value) f[i] = mul2(f[i], both(power));
+          s[i & 1] = fma2(f[i], f[i], s[i & 1]);
+        }
+      }
+      span.template parts<T>(t, [&](long long at) {
+        float f = to_float(*reinterpret_cast<const T*>(t.g + at));
+        if constexpr (decltype(times)::value) f *= power;
+        s[0].x = fmaf(f, f, s[0].x);
+      });
     });
-  });
-  float sum = (s[0].x + s[1].x) + (s[0].y + s[1].y);
+    float all = (s[0].x + s[1].x) + (s[0].y + s[1].y);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-  return sum;
+    for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
+    return all;
+  };
+  const float once = squares(std::false_type(), 1.f);
+  const bool first = (threadIdx.x & 31) == 0;
+  if (once >= 0x1p-110f && once <= 0x1.fffffep127f) {
+    if (first) sum += static_cast<double>(once);
+    return;
+  }
+  const bool small = once < 1.f;
+  const float again = squares(std::true_type(), small ? 0x1p100f : 0x1p-80f);
+  if (first) sum += static_cast<double>(again) * (small ? 0x1p-200 : 0x1p160);
 }
 
 // out = g factor on a chunk.
@@ -208,8 +229,7 @@ __global__ void __launch_bounds__(kThreads, 4) squares_kernel(const __grid_const
   double sum = 0.0;
   for (unsigned int c = blockIdx.x; c < g.chunks; c += gridDim.x) {
     const Tensor& t = g.t[tensor_of(g, c)];
-    const float more = chunk_squares(t, c - t.first, threadIdx.x);
-    if ((threadIdx.x & 31) == 0) sum += static_cast<double>(more);
+    add_chunk_squares(t, c - t.first, threadIdx.x, sum);
   }
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = sum;
   __syncthreads();
@@ -248,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 4)
 
 // Both in one launch, for short lists of little memory: a cluster of 16 CTAs,
 // each with groups of kThreads that take a chunk; the CTAs' sums meet through
-// distributed shared memory.  6 tensors of 1.1 MB in all: 6.1 us and 4 of the host,
+// distributed shared memory.  6 tensors of 1.1 MB in all: 6.4 us and 4 of the host,
 // 7.3 and 9.5 by two launches.  (With twice the chunks, in turn, 4 MB take 10.9 us,
 // 6.8 by two launches.)
 constexpr int kClusterCtas = 16, kClusterGroups = 4;
@@ -268,8 +288,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1)
 #pragma unroll 1
   for (unsigned int c = first; c < g.chunks; c += kTurn) {
     const Tensor& t = g.t[tensor_of(g, c)];
-    const float more = chunk_squares(t, c - t.first, thread);
-    if ((threadIdx.x & 31) == 0) sum += static_cast<double>(more);
+    add_chunk_squares(t, c - t.first, thread, sum);
   }
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = sum;
   __syncthreads();
