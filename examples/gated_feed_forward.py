@@ -71,13 +71,15 @@ class GatedFeedForward:
         return oz.mx_linear(oz.mx_quantize(a), down, residual=x)
 
     def decoder(self, x):
-        """(graph, output): a replay decodes what x holds then, into the output."""
+        """(graph, output): a replay decodes what x holds then, with the block's matrices as they were, into the output."""
         weights = self.four_bits()
         self.decode(x, weights)  # the first call on a device allocates
         torch.cuda.synchronize()
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph):
             y = self.decode(x, weights)
+        # A graph keeps no reference to what it reads from outside its own memory.
+        graph.reads = x, weights, list(self.params.values())
         return graph, y
 
 
