@@ -66,6 +66,8 @@ class FeedForward:
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph):
             step()
+        # A graph keeps no reference to the memory outside its own that it reads and writes.
+        graph.uses = x, h, a, y, list(p.values())
         return graph, y
 
 

@@ -74,3 +74,21 @@ def test_gated_decoder(monkeypatch):
         read[:] = read[-7:]  # of the captured step: x, the norm's parameters, three weights, the residual
         return graph
     check(read, make)
+
+
+def test_decoder(monkeypatch):
+    read = []
+
+    def norm(x, w, b, out):
+        read.extend(weakref.ref(t) for t in (x, w, b, out))
+
+    def linear(x, w, b, out, activation="none", residual=None):
+        read.extend(weakref.ref(t) for t in (x, w, b, out) + ((residual,) if residual is not None else ()))
+
+    example = load("feed_forward", types.SimpleNamespace(layer_norm=norm, linear=linear), monkeypatch)
+
+    def make():
+        block = example.FeedForward(8, 12, device="cpu")
+        graph, y = block.decoder(torch.zeros(1, 8, dtype=torch.bfloat16))
+        return graph
+    check(read, make)

@@ -43,3 +43,17 @@ def test_gated_decoder():
     torch.cuda.synchronize()
     assert torch.equal(y, want)
     assert all(bool((t == 255).all()) for t in kept)
+
+
+def test_decoder():
+    example = load("feed_forward")
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    x = torch.randn(1, 512, generator=gen, device="cuda").to(BF16)
+    want = example.FeedForward(512, 1024, seed=3).forward(x)[0]
+    graph, y = example.FeedForward(512, 1024, seed=3).decoder(x.clone())
+    gc.collect()
+    kept = others([2 * 512, 4 * 512, 2 * 1024, 2 * 512 * 1024])
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, want)
+    assert all(bool((t == 255).all()) for t in kept)
