@@ -937,6 +937,8 @@ class MXMatrix:
 
     @staticmethod
     def empty(rows, cols, device="cuda"):
+        if not (0 <= rows <= 1 << 26 and 0 <= cols <= 1 << 26):
+            raise ValueError("MXMatrix: expected from 0 to 2^26 rows and columns")
         at = (ozemu_mx_code_bytes(rows, cols) + 255) // 256 * 256
         return MXMatrix(_torch().empty(at + ozemu_mx_scale_bytes(rows, cols), dtype=_torch().uint8, device=device), rows,
                         cols)

@@ -172,3 +172,9 @@ def test_clip_grad_norm(oz, change, words):
 def test_clip_grad_norm_of_other_kinds(oz, call):
     with pytest.raises(TypeError):
         oz.clip_grad_norm(**call)
+
+
+@pytest.mark.parametrize("rows, cols", [(-1, 4), (4, -1), ((1 << 26) + 1, 4), (4, (1 << 26) + 1)])
+def test_mx_matrix_sizes(oz, rows, cols):
+    with pytest.raises(ValueError, match="expected from 0 to 2\\^26 rows and columns"):
+        oz.MXMatrix.empty(rows, cols, device="cpu")
