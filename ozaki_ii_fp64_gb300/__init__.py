@@ -990,7 +990,7 @@ def mx_quantize(x, out=None, stream=None):
     native = _native or _layer_calls()
     if out is None:
         return MXMatrix(native.mx_quantize(x, None, stream), *x.shape)
-    if _mx(out, "out").shape != tuple(x.shape):
+    if _mx(out, "out").shape != tuple(getattr(x, "shape", out.shape)):  # (what is no tensor is refused below)
         raise ValueError("out: expected an MXMatrix of x's size")
     native.mx_quantize(x, out.data, stream)
     return out

@@ -178,3 +178,8 @@ def test_clip_grad_norm_of_other_kinds(oz, call):
 def test_mx_matrix_sizes(oz, rows, cols):
     with pytest.raises(ValueError, match="expected from 0 to 2\\^26 rows and columns"):
         oz.MXMatrix.empty(rows, cols, device="cpu")
+
+
+def test_mx_quantize_into_nothing_of_a_kind(oz):
+    with pytest.raises(ValueError, match="x: expected a tensor"):
+        oz.mx_quantize(3, out=mx(oz, 2, 4))
