@@ -653,6 +653,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
           tmem_wait_ld();
           release();
           finish_direct<T>(u, e, reinterpret_cast<const uint4*>(bias), row0 + lane, col0, p.m);
+          __syncwarp();  // lanes past the last row are back for the next read of TMEM, a warp's
         } else if (together && (first ^ h) < cols) {
           finish_together<T>(
               [&](float2(&z)[16]) {
