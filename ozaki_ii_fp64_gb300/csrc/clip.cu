@@ -7,10 +7,10 @@
 // for short lists of little memory.  No atomics: the same gradients give the same
 // bits.  Squares and a warp's sum of 2048 of them are fp32 (a chain of 40 roundings
 // at most; scaled where they leave its range), everything after that is fp64, whose
-// rate is two additions a clock and SM.  Bound by HBM: each gradient is read twice, the second time in the reverse
-// order, so that what L2 still holds of the first pass is read from there, and
-// written once: 2.15 GB in 48 tensors 1000 us, 6.4 TB/s over the three; 100 MB in
-// aligned tensors 45 us, packed without gaps 50.
+// rate is two additions a clock and SM.  Bound by HBM: each gradient is read twice,
+// the second time in the reverse order, so that what L2 still holds of the first
+// pass is read from there, and written once: 2.15 GB in 48 tensors 1000 us, 6.4 TB/s
+// over the three; 100 MB in aligned tensors 45 us, packed without gaps 50.
 #include <algorithm>
 #include <atomic>
 #include <cstdint>
@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 4)
 
 // Both in one launch, for short lists of little memory: a cluster of 16 CTAs,
 // each with groups of kThreads that take a chunk; the CTAs' sums meet through
-// distributed shared memory.  6 tensors of 1.1 MB in all: 6.4 us and 4 of the host,
+// distributed shared memory.  6 tensors of 1.1 MB in all: 6.8 us and 4 of the host,
 // 7.3 and 9.5 by two launches.  (With twice the chunks, in turn, 4 MB take 10.9 us,
 // 6.8 by two launches.)
 constexpr int kClusterCtas = 16, kClusterGroups = 4;

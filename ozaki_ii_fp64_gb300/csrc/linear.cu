@@ -1024,7 +1024,8 @@ __device__ __forceinline__ float gated_scale(const float* largest, int parts, fl
 // Bound by HBM, three matrices read and two written: 8192 x 8192 bf16 silu 102 us,
 // 6.6 TB/s (two rows ahead: 122, three: 140, in spilled registers); 11431 x 5330,
 // rows of no alignment, 302 us by two vectors a lane as they are needed, 186 by
-// the next lane's.
+// the next lane's (which spills 8 to 44 bytes at the 80 registers of three CTAs an
+// SM, 64 with float16's scale).
 template <typename T, int kAct, int TX, bool kWhole>
 __global__ void __launch_bounds__(256, 3) gated_slope_kernel(const T* dh, long long lddh, const T* pre, long long ldpre,
                                                              T* dz, long long lddz, float* part, T* db, int m, int n,

@@ -276,9 +276,10 @@ __global__ void __launch_bounds__(256) mx_dequantize_kernel(const uint8_t* codes
 // once that half is in registers.
 //
 // Bound by shared memory (operands in and out), 560 clocks a stage against the
-// MMAs' 512, by the wait between a tile's last MMA and the next one's first (14 of
-// 186 us at 16 stages a tile) and by the outputs' way out: 8192 x 4096 -> 16384
-// bf16 160 us (6.9 PFLOP/s), with gelu_tanh 170; 8192 x 16384 -> 4096 144 (7.7),
+// MMAs' 512, by the wait between a tile's last MMA and the next one's first (14 us
+// at 16 stages a tile, when the whole took 186) and by the outputs' way out: 8192 x
+// 4096 -> 16384 bf16 160 us (6.9 PFLOP/s), with gelu_tanh 170, with a residual 186;
+// 8192 x 256 -> 8192 31, 45 and 76; 8192 x 16384 -> 4096 144 (7.6),
 // in a short burst; a second of the first runs at 180, the power cap's clocks.
 // ---------------------------------------------------------------------------
 constexpr int kMxThreads = 32 * (3 + kEpiWarps);
@@ -363,8 +364,8 @@ __device__ __forceinline__ void load32(const void* p, uint32_t (&v)[8]) {
                : "l"(p)
                : "memory");
 }
-// Without a place in L1, which nothing reads it from again: 9 us of the 180 that
-// 8192 x 4096 -> 16384 took with one.
+// Without a place in L1, which nothing reads it from again: 8192 x 4096 -> 16384
+// 180 us -> 171, before other steps.
 __device__ __forceinline__ void store32(void* p, const uint32_t (&v)[8]) {
   asm volatile("st.global.L1::no_allocate.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
                "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
@@ -375,8 +376,8 @@ __device__ __forceinline__ void store32(void* p, const uint32_t (&v)[8]) {
 // on 16-byte boundaries: straight from registers in pieces of 32 bytes, or of 16
 // where some row starts on no 32-byte boundary.  (The MMAs and the copies that
 // feed them take all of shared memory's bandwidth, 67 KB in the 512 clocks of a
-// stage; passing the outputs through it, too, cost 8192 x 4096 -> 16384 6 of 186
-// us.)
+// stage; without the outputs' way through it 8192 x 4096 -> 16384 went from 186 to
+// 180 us, before other steps.)
 template <typename T>
 __device__ __forceinline__ void finish_direct(const uint32_t (&u)[32], const Epilogue& e, const uint4* bias,
                                               long long row, int col0, int m) {
