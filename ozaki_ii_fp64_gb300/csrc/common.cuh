@@ -220,6 +220,9 @@ __device__ __forceinline__ uint32_t mapa_shared(const void* p, uint32_t rank) {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// The same in two steps, for what needs no memory of the others: that they run.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
@@ -286,7 +289,10 @@ __device__ __forceinline__ void tc_commit(uint64_t* bar) {
 }
 
 // Pair (2-SM) forms: allocation, MMA issued by the pair's first CTA, and a
-// commit that arrives on the same barrier in both CTAs.
+// commit that arrives on the same barrier in both CTAs.  The allocation is one of
+// both SMs' memories and may begin once both CTAs run (cluster_arrive at their
+// start, cluster_wait before it): begun by one CTA before the other's start, it can
+// wait for good.
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t* holder, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(holder)),
                "r"(ncols)

@@ -560,6 +560,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // round run while the epilogue drains the other.
   constexpr int kBufs = (NL <= 2 || NL == 4) ? 2 : 1;
 
+  cluster_arrive();
   if (warp == 0 && lane == 0) {
     for (int s = 0; s < kStages2; ++s) {
       mbar_init(&full[s], 1);   // armed by the first CTA with both CTAs' bytes
@@ -575,6 +576,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tmA);
     tma_prefetch_desc(&tmB);
   }
+  __syncwarp();
+  cluster_wait();  // both CTAs run
   if (warp == 1) {
     tmem_alloc_pair(tmem_holder, kTmemCols2);
     tmem_relinquish_pair();

@@ -217,6 +217,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     kb1 = min(kb0 + p.share, p.kb);
   };
 
+  cluster_arrive();
   if (warp == 0 && lane == 0) {
     for (int s = 0; s < stages; ++s) {
       mbar_init(&full[s], 1);   // armed by the first CTA with both CTAs' bytes
@@ -232,6 +233,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&ma0);
     tma_prefetch_desc(&mb0);
   }
+  __syncwarp();
+  cluster_wait();  // both CTAs run
   if (warp == 1) {
     tmem_alloc_pair(tmem_holder, 512);
     tmem_relinquish_pair();

@@ -489,6 +489,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
   const bool wide = p.bn == 256;
   const uint32_t second = wide ? kSecondAccumulator : 128;
 
+  cluster_arrive();
   if (warp == 0 && lane == 0) {
     for (int s = 0; s < kMxStages; ++s) {
       mbar_init(&full[s], 1);   // armed by the first CTA with both CTAs' bytes
@@ -506,6 +507,8 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     tma_prefetch_desc(&msa);
     tma_prefetch_desc(&msb);
   }
+  __syncwarp();
+  cluster_wait();  // both CTAs run
   if (warp == 1) {
     tmem_alloc_pair(tmem_holder, 512);
     tmem_relinquish_pair();
