@@ -517,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             store4(static_cast<T*>(e.out) + row * e.ldo + col, z[i], left, (e.vec & 8) != 0);
           }
         } else {
-          const float f = sums_scale(e);
+          const float f = e.scale ? sums_scale(e) : 1.f;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const long long row = grow0 + r0 + 2 * i;
@@ -581,7 +581,7 @@ struct FewProduct {
 
 // kGated: the MMA's 128 rows are 64 gate rows of the wide operand and the 64 up
 // rows that belong to the same outputs, so a CTA's sums hold both halves.
-template <typename T, int NT, bool kGated>
+template <typename T, int NT, bool kGated, bool kScaled>
 __global__ void __launch_bounds__(kFewThreads, 2)
     product_few_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap mx,
                        const __grid_constant__ FewProduct p, uint32_t* flags) {
@@ -708,7 +708,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   __syncthreads();
   cluster_sync();
 
-  join_few<T, kCols, false>(smem, p.e, p.split, rank, j0, i0, min(NT, p.m - i0), p.n, kFewThreads);
+  join_few<T, kCols, false, kScaled>(smem, p.e, p.split, rank, j0, i0, min(NT, p.m - i0), p.n, kFewThreads);
   cluster_sync();  // peers have read this CTA's sums
   if (warp == 1) {
     tc_fence_after();
@@ -1345,17 +1345,20 @@ cudaError_t launch_few(const Matrix& w, bool w_mn, const Matrix& x, FewProduct p
   CUtensorMap mw, mx;
   if (!make_map(&mw, w, Pair<T>::kBf16, w_mn || kGated ? kBlock : 2 * kBlock) || !make_map(&mx, x, Pair<T>::kBf16, NT))
     return cudaErrorInvalidValue;
-  auto kern = product_few_kernel<T, NT, kGated>;
-  static std::atomic<bool> ready[kMaxDev];
+  auto kern = product_few_kernel<T, NT, kGated, false>;
+  if constexpr (!Pair<T>::kBf16 && !kGated)
+    if (p.e.scale) kern = product_few_kernel<T, NT, kGated, true>;
+  static std::atomic<bool> known[2][kMaxDev];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= kMaxDev) return cudaErrorInvalidDevice;
-  if (!ready[dev]) {
+  std::atomic<bool>& ready = known[p.e.scale != nullptr][dev];
+  if (!ready) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, FewCfg<NT>::kSmem);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
-    ready[dev] = true;
+    ready = true;
   }
   const int across = kGated ? (p.n + 63) / 64 : (p.n + 127) / 128, down = (p.m + NT - 1) / NT;
   p.w_mn = w_mn;

@@ -836,7 +836,7 @@ __global__ void __launch_bounds__(kMxFewThreads, 2)
   tc_fence_before();
   __syncthreads();
   cluster_sync();
-  join_few<T, 128, true>(smem, p.e, p.split, rank, j0, i0, min(NT, p.m - i0), p.n, kMxFewThreads);
+  join_few<T, 128, true, false>(smem, p.e, p.split, rank, j0, i0, min(NT, p.m - i0), p.n, kMxFewThreads);
   cluster_sync();  // peers have read this CTA's sums
   if (warp == 1) {
     tc_fence_after();
